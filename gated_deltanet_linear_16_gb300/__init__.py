@@ -28,12 +28,17 @@ __all__ = [
     "gdn_decode_conv_norm_noalloc", "GDN_NOALLOC_MAX_KEY_HEADS", "gdn_decode_norm_q8",
     "gdn_gate_norm", "gdn_gate_norm_q8",
     "gdn_h_f32_to_f16", "gdn_h_f16_to_f32", "gdn_status_str", "gdn_last_cuda_error",
+    "GDNA_F32", "GDNA_F16", "GDNA_BF16", "GDNA_E4M3",
+    "GDNA_ROPE_PLAIN", "GDNA_ROPE_LINEAR", "GDNA_ROPE_NTK", "GDNA_ROPE_YARN",
+    "gdna_rope_table", "gdna_page_assign", "gdna_qk_norm_rope", "gdna_attn_workspace", "gdna_attn_decode",
 ]
 
 GDN_STATE_F32 = 0
 GDN_STATE_F16 = 1
 GDN_NOALLOC_MAX_KEY_HEADS = 16384     # batch * NK limit of gdn_decode_conv_norm_noalloc
 GDN_DEFAULT_WAIT_POLLS = 4194304      # default bound of the tensor-core kernels' MMA-completion waits
+GDNA_F32, GDNA_F16, GDNA_BF16, GDNA_E4M3 = 0, 1, 2, 3          # element types of the attention-layer calls
+GDNA_ROPE_PLAIN, GDNA_ROPE_LINEAR, GDNA_ROPE_NTK, GDNA_ROPE_YARN = 0, 1, 2, 3
 STATUS = {0: "GDN_OK", 1: "GDN_ERR_ARG", 2: "GDN_ERR_UNSUPPORTED", 3: "GDN_ERR_ALIGN",
           4: "GDN_ERR_ALIAS", 5: "GDN_ERR_CUDA"}
 
@@ -89,6 +94,17 @@ def _declare(lib):
                "gdn_decode_conv_norm_noalloc", "gdn_decode_norm_q8", "gdn_gate_norm", "gdn_gate_norm_q8",
                "gdn_h_f32_to_f16",
                "gdn_h_f16_to_f32"):
+        getattr(lib, fn).restype = i32
+    f64 = ctypes.c_double
+    lib.gdna_rope_table.argtypes = [P, i64, i32, f64, i32, f64, f64, f64, f64, f64]
+    lib.gdna_page_assign.argtypes = [P, P, P, i64, P, i64, P, P, P, P, P, P, P, i32, i64, i32, i32, P]
+    lib.gdna_qk_norm_rope.argtypes = [P, P, P, i32, P, P, f32, P, i64, i32, i32, P, P, P, P, P, P, i32, f32, f32,
+                                      i64, i32, i32, i32, i64, i32, i64, i64, i64, i64, i64, i64, i64, i64, i64, P]
+    lib.gdna_attn_workspace.argtypes = [i32, i32, i32, i32, i32]
+    lib.gdna_attn_decode.argtypes = [P, i32, P, P, P, i32, f32, f32, P, i64, P, f32, P, i32, P, P, i64,
+                                     i32, i32, i32, i32, i32, i64, i32, i32, i64, i64, i64, i64, i64, i64, i64, P]
+    lib.gdna_attn_workspace.restype = i64
+    for fn in ("gdna_rope_table", "gdna_page_assign", "gdna_qk_norm_rope", "gdna_attn_decode"):
         getattr(lib, fn).restype = i32
     lib.gdn_status_str.argtypes = [i32]
     lib.gdn_status_str.restype = ctypes.c_char_p
@@ -366,3 +382,94 @@ def gdn_status_str(status: int) -> str:
 
 def gdn_last_cuda_error() -> int:
     return load().gdn_last_cuda_error()
+
+
+# ------------------------------------------------------------------ attention layers (include/gdna.h)
+
+_GDNA_TYPES = {}            # torch dtype -> GDNA_*, filled on first use
+
+
+def _gdna_dtype(x, dtype):
+    """The GDNA_* code of a tensor's type, or the one given (needed for a raw address)."""
+    if dtype is not None:
+        return dtype
+    if isinstance(x, int):
+        raise ValueError("a dtype is required for a raw address")
+    if not _GDNA_TYPES:
+        import torch
+        _GDNA_TYPES.update({torch.float32: GDNA_F32, torch.float16: GDNA_F16, torch.bfloat16: GDNA_BF16,
+                            torch.float8_e4m3fn: GDNA_E4M3})
+    code = _GDNA_TYPES.get(x.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    return code
+
+
+def gdna_rope_table(table, *, n_pos, rot, base, kind=GDNA_ROPE_PLAIN, factor=1.0, original_len=0.0, beta_fast=32.0,
+                    beta_slow=1.0, amplitude=1.0):
+    """Cosines and sines of positions [0, n_pos) into a HOST fp32 tensor [n_pos, rot] (rot/2 cosines, then
+    rot/2 sines a row), computed in 64 bits; copy it to the GPU once."""
+    if not isinstance(table, int) and table.device.type != "cpu":
+        raise ValueError("gdna_rope_table fills host memory")
+    _check("gdna_rope_table", load().gdna_rope_table(_ptr(table), n_pos, rot, base, kind, factor, original_len,
+                                                     beta_fast, beta_slow, amplitude))
+
+
+def gdna_page_assign(cached, fresh, table, free_pages, free_head, kv_len, row_start, slots, positions, free_head_out,
+                     unserved, *, batch, rows, page_size, max_pages, n_free=None, table_stride=None, stream=None):
+    """Pages, slots and positions of a step's new tokens from the sequences' lengths.  See include/gdna.h."""
+    st = (_lib or load()).gdna_page_assign(
+        _ptr(cached), _ptr(fresh), _ptr(table), max_pages if table_stride is None else table_stride,
+        _ptr(free_pages), free_pages.numel() if n_free is None else n_free, _ptr(free_head), _ptr(kv_len),
+        _ptr(row_start), _ptr(slots), _ptr(positions), _ptr(free_head_out), _ptr(unserved), batch, rows, page_size,
+        max_pages, _stream(stream))
+    if st:
+        _check("gdna_page_assign", st)
+
+
+def gdna_qk_norm_rope(q, k, v, qn, kn, cos_sin, positions, slots, q_out, k_cache=None, v_cache=None, k_out=None, *,
+                      rows, nq, nkv, d, rot, n_pos, interleaved=False, eps=1e-6, pages=0, page_size=0, k_scale=1.0,
+                      v_scale=1.0, dtype=None, cache_dtype=None, q_stride=None, q_head_stride=None, k_stride=None,
+                      v_stride=None, q_out_stride=None, k_out_stride=None, page_stride=None, token_stride=None,
+                      head_stride=None, stream=None):
+    """Per-head RMS norm and rotary positions of q and k, and the cache's new rows, in one pass.  Strides default
+    to contiguous rows and a cache [pages, page_size, nkv, d].  See include/gdna.h."""
+    hk = nkv * d
+    token_stride = hk if token_stride is None else token_stride
+    st = (_lib or load()).gdna_qk_norm_rope(
+        _ptr(q), _ptr(k), _ptr(v), _gdna_dtype(k if q is None else q, dtype), _ptr(qn), _ptr(kn), eps, _ptr(cos_sin),
+        n_pos, rot, 1 if interleaved else 0, _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_out), _ptr(k_cache),
+        _ptr(v_cache), GDNA_F16 if k_cache is None else _gdna_dtype(k_cache, cache_dtype), k_scale, v_scale,
+        rows, nq, nkv, d, pages, page_size, nq * d if q_stride is None else q_stride,
+        d if q_head_stride is None else q_head_stride, hk if k_stride is None else k_stride,
+        hk if v_stride is None else v_stride, nq * d if q_out_stride is None else q_out_stride,
+        hk if k_out_stride is None else k_out_stride, page_size * hk if page_stride is None else page_stride,
+        token_stride, d if head_stride is None else head_stride, _stream(stream))
+    if st:
+        _check("gdna_qk_norm_rope", st)
+
+
+def gdna_attn_workspace(*, batch, q_len, nq, nkv, d) -> int:
+    """Bytes of device scratch that gdna_attn_decode needs for a shape (0: not supported)."""
+    return (_lib or load()).gdna_attn_workspace(batch, q_len, nq, nkv, d)
+
+
+def gdna_attn_decode(q, k_cache, v_cache, table, kv_len, out, workspace, *, batch, q_len=1, nq, nkv, d, pages,
+                     page_size, max_pages, gate=None, lse=None, scale=None, k_scale=1.0, v_scale=1.0, dtype=None,
+                     cache_dtype=None, out_dtype=None, workspace_bytes=None, table_stride=None, q_stride=None,
+                     gate_stride=None, gate_head_stride=None, out_stride=None, page_stride=None, token_stride=None,
+                     head_stride=None, stream=None):
+    """Attention of the q_len newest tokens of each sequence over its paged cache; scale defaults to 1/sqrt(d),
+    strides to contiguous rows and a cache [pages, page_size, nkv, d].  See include/gdna.h."""
+    hq, hk = nq * d, nkv * d
+    st = (_lib or load()).gdna_attn_decode(
+        _ptr(q), _gdna_dtype(q, dtype), _ptr(gate), _ptr(k_cache), _ptr(v_cache), _gdna_dtype(k_cache, cache_dtype),
+        k_scale, v_scale, _ptr(table), max_pages if table_stride is None else table_stride, _ptr(kv_len),
+        d ** -0.5 if scale is None else scale, _ptr(out), _gdna_dtype(out, out_dtype), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes,
+        batch, q_len, nq, nkv, d, pages, page_size, max_pages, hq if q_stride is None else q_stride,
+        hq if gate_stride is None else gate_stride, d if gate_head_stride is None else gate_head_stride,
+        hq if out_stride is None else out_stride, page_size * hk if page_stride is None else page_stride,
+        hk if token_stride is None else token_stride, d if head_stride is None else head_stride, _stream(stream))
+    if st:
+        _check("gdna_attn_decode", st)

@@ -3,7 +3,7 @@
 Each .cu translation unit is compiled in parallel to an object under
 ``_build/`` at the repository root, then linked into
 ``gated_deltanet_linear_16_gb300/libgdn.so`` (CUDA runtime linked statically,
-only the ``gdn_*`` symbols of include/gdn.h exported).  Rebuilds only when a
+only the symbols of include/gdn.h and include/gdna.h exported).  Rebuilds only when a
 source, the public header or the flags changed.
 """
 from __future__ import annotations
@@ -28,7 +28,8 @@ NVCC_FLAGS = ARCH + [
 ]
 LINK_FLAGS = ARCH + ["-shared", "-cudart", "static"]
 SOURCES = ["gdn_abi.cu", "gdn_decode.cu", "gdn_chunk2.cu", "gdn_conv_norm.cu", "gdn_prefill.cu", "gdn_convert.cu",
-           "gdn_noalloc.cu", "gdn_norm.cu", "gdn_prefill_tc.cu"]
+           "gdn_noalloc.cu", "gdn_norm.cu", "gdn_prefill_tc.cu",
+           "gdna_abi.cu", "gdna_pages.cu", "gdna_rope.cu", "gdna_attn.cu"]
 
 
 def nvcc() -> str:
@@ -41,7 +42,7 @@ def nvcc() -> str:
 def _stamp() -> str:
     h = hashlib.sha256()
     h.update(" ".join(NVCC_FLAGS + LINK_FLAGS).encode())
-    for name in sorted(os.listdir(CSRC)) + ["../../include/gdn.h"]:
+    for name in sorted(os.listdir(CSRC)) + ["../../include/gdn.h", "../../include/gdna.h"]:
         path = os.path.normpath(os.path.join(CSRC, name))
         if os.path.isfile(path):
             h.update(name.encode())

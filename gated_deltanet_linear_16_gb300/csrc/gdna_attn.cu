@@ -1,0 +1,233 @@
+// gdna_attn.cu -- paged decode attention (gdna_attn_decode): the general kernel,
+// the join of items that lie in several blocks, and the choice of kernel.
+#include "gdna_attn.cuh"
+
+namespace gdna {
+namespace {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// ------------------------------------------------------------------ general kernel
+//
+// Any D <= 256, any strides and alignment.  One key a thread for the scores, one
+// output column (or two) a thread for the sums; weights pass through shared
+// memory.  Correct for everything and made for nothing: the calls that matter
+// run on the tensor cores.
+constexpr int kThreads = 128;
+constexpr int kRows = 8;
+constexpr int kMaxD = 256;
+
+__global__ void __launch_bounds__(kThreads)
+attn_general(const AttnParams p)
+{
+    __shared__ float q[kRows][kMaxD];
+    __shared__ float weight[kRows][kThreads];
+    __shared__ int64_t place[kThreads];    // element offset of a key's head; -1: a page of zeros
+    __shared__ float red[kRows][kThreads / 32];
+    __shared__ int64_t scratch[kThreads / 32 + 2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x, D = p.d;
+    Run run = find_run(p, c, scratch);
+    Join join = {0, 0, 0, 0};
+    while (run.at < run.end) {
+        const Part part = next_part(p, run, c);
+        const int head = part.item / p.row_tiles, row0 = (part.item % p.row_tiles) * kRows;
+        __syncthreads();
+        for (int i = tid; i < kRows * D; i += kThreads) {
+            const int r = i / D, x = i - r * D, row = row0 + r;
+            float v = 0.f;
+            if (row < p.q_len * p.group)
+                v = load_elem(p.q, ((int64_t)part.seq * p.q_len + row / p.group) * p.q_stride +
+                                       ((int64_t)head * p.group + row % p.group) * D + x, p.dtype);
+            q[r][x] = v;
+        }
+        int seen[kRows];
+        float m[kRows], l[kRows], acc[kRows][2];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            seen[r] = keys_seen(p, part.keys, row0 + r);
+            m[r] = kNegInf;
+            l[r] = acc[r][0] = acc[r][1] = 0.f;
+        }
+        for (int64_t u = part.u0; u < part.u1; ++u) {
+            const int64_t key = u * kThreads + tid;
+            int64_t at = -1;
+            if (key < part.keys) {
+                const int64_t pg = key / p.cache.page_size;
+                const int64_t page = p.table[part.seq * p.table_stride + pg];
+                if (page >= 0 && page < p.cache.pages)
+                    at = page * p.cache.page_stride + (key - pg * p.cache.page_size) * p.cache.token_stride +
+                         head * p.cache.head_stride;
+            }
+            __syncthreads();               // the last unit's weights and places are used up; q is there
+            place[tid] = at;
+            float s[kRows];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) s[r] = 0.f;
+            if (at >= 0)
+                for (int x = 0; x < D; ++x) {
+                    const float k = load_elem(p.k, at + x, p.cache_dtype);
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r) s[r] = fmaf(q[r][x], k, s[r]);
+                }
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                s[r] = key < seen[r] ? s[r] * p.scale : kNegInf;
+                float top = s[r];
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+                if (lane == 0) red[r][warp] = top;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                const float top = fmaxf(m[r], fmaxf(fmaxf(red[r][0], red[r][1]), fmaxf(red[r][2], red[r][3])));
+                const float from = top == kNegInf ? 0.f : top, down = weight_of(m[r], from);
+                const float w = key < seen[r] ? exp2f(s[r] - from) : 0.f;
+                l[r] = l[r] * down + w;
+                acc[r][0] *= down;
+                acc[r][1] *= down;
+                m[r] = top;
+                weight[r][tid] = w;
+            }
+            __syncthreads();
+            const int here = (int)min((int64_t)kThreads, part.keys - u * kThreads);
+            for (int j = 0; j < here; ++j) {
+                if (place[j] < 0) continue;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int x = tid + e * kThreads;
+                    if (x >= D) break;
+                    const float v = load_elem(p.v, place[j] + x, p.cache_dtype);
+#pragma unroll
+                    for (int r = 0; r < kRows; ++r)     // a key a row does not see adds nothing, NaN or not
+                        if (u * kThreads + j < seen[r]) acc[r][e] = fmaf(weight[r][j], v, acc[r][e]);
+                }
+            }
+        }
+        // a row's sum over the block (m is the same in all threads)
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const float t = gdn::group_sum<32>(l[r]);
+            __syncthreads();
+            if (lane == 0) red[r][warp] = t;
+            __syncthreads();
+            l[r] = red[r][0] + red[r][1] + red[r][2] + red[r][3];
+        }
+        if (part.begins && part.ends) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                if (row0 + r >= p.q_len * p.group) break;
+                const float norm = l[r] == 0.f ? 0.f : p.v_scale / l[r];
+                for (int e = 0; e < 2; ++e)
+                    if (tid + e * kThreads < D)
+                        write_out(p, part.seq, head, row0 + r, tid + e * kThreads, l[r] == 0.f ? 0.f : acc[r][e] * norm);
+                if (tid == 0) write_lse(p, part.seq, head, row0 + r, m[r], l[r]);
+            }
+        } else {
+            float *to = part_of(p, 2 * c + (part.begins ? 1 : 0));
+            const int width = part_width(D);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+                for (int e = 0; e < 2; ++e)
+                    if (tid + e * kThreads < D) to[r * width + tid + e * kThreads] = acc[r][e];
+                if (tid == 0) { to[kRows * width + 2 * r] = m[r]; to[kRows * width + 2 * r + 1] = l[r]; }
+            }
+            if (part.begins) join = Join{part.seq, part.item, part.blocks, 0};
+        }
+    }
+    if (tid == 0) joins_of(p)[c] = join;
+}
+
+// ------------------------------------------------------------------ join
+//
+// Block (c, r): row r of the item that begins in block c and continues.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads)
+attn_join(const AttnParams p)
+{
+    __shared__ float weight[kMaxGrid];
+    __shared__ float red[kJoinThreads / 32];
+    __shared__ float sums[kJoinThreads * 4];
+    const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Join join = joins_of(p)[c];
+    if (join.parts == 0) return;
+    const int head = join.item / p.row_tiles, row = (join.item % p.row_tiles) * p.tile_rows + r;
+    if (row >= p.q_len * p.group) return;
+    const int width = part_width(p.d), n = join.parts;
+    auto part = [&](int i) { return part_of(p, 2 * (c + i) + (i == 0 ? 1 : 0)); };
+
+    float top = kNegInf;
+    for (int i = tid; i < n; i += kJoinThreads) {
+        weight[i] = part(i)[p.tile_rows * width + 2 * r];
+        top = fmaxf(top, weight[i]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, red[w]);
+    const float m = top;
+    if (top == kNegInf) top = 0.f;
+    float l = 0.f;
+    for (int i = tid; i < n; i += kJoinThreads) {
+        weight[i] = weight_of(weight[i], top);
+        l += weight[i] * part(i)[p.tile_rows * width + 2 * r + 1];
+    }
+    l = gdn::group_sum<32>(l);
+    __syncthreads();
+    if (lane == 0) red[warp] = l;
+    __syncthreads();
+    l = 0.f;
+    for (int w = 0; w < kJoinThreads / 32; ++w) l += red[w];
+
+    // columns four at a time, the parts dealt over what threads are left
+    const int quads = width / 4, lanes = kJoinThreads / quads;   // quads <= 64
+    const int x = tid % quads, first = tid / quads;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (first < lanes) {
+#pragma unroll 4
+        for (int i = first; i < n; i += lanes) {
+            const float4 v = __ldcs(reinterpret_cast<const float4 *>(part(i) + r * width) + x);
+            const float w = weight[i];
+            o.x = fmaf(w, v.x, o.x); o.y = fmaf(w, v.y, o.y); o.z = fmaf(w, v.z, o.z); o.w = fmaf(w, v.w, o.w);
+        }
+        reinterpret_cast<float4 *>(sums)[tid] = o;
+    }
+    __syncthreads();
+    const float norm = l == 0.f ? 0.f : p.v_scale / l;
+    for (int col = tid; col < p.d; col += kJoinThreads) {
+        float t = 0.f;
+        for (int g = 0; g < lanes; ++g) t += sums[(g * quads + (col >> 2)) * 4 + (col & 3)];
+        write_out(p, join.seq, head, row, col, l == 0.f ? 0.f : t * norm);
+    }
+    if (tid == 0) write_lse(p, join.seq, head, row, m, l);
+}
+
+// Query rows of a work item on the tensor cores.
+int tc_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+}  // namespace
+
+int64_t attn_workspace_bytes(int64_t rows, int d)
+{
+    return kMaxGrid * (int64_t)sizeof(Join) + 2 * kMaxGrid * part_floats(tc_rows(rows), d) * (int64_t)sizeof(float);
+}
+
+cudaError_t launch_attn_decode(const AttnParams &params, bool fast, cudaStream_t s)
+{
+    (void)fast;
+    AttnParams p = params;
+    p.unit = kThreads;
+    p.tile_rows = kRows;
+    p.row_tiles = (int)(((int64_t)p.q_len * p.group + kRows - 1) / kRows);
+    const int sms = gdn::sm_count();
+    p.grid = 4 * sms < kMaxGrid ? 4 * sms : kMaxGrid;
+    attn_general<<<p.grid, kThreads, 0, s>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    attn_join<<<dim3(p.grid, p.tile_rows), kJoinThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace gdna

@@ -1,0 +1,167 @@
+// gdna_attn.cuh -- what the attention kernels share: how the work is dealt out,
+// and where partial results lie (gdna_attn_decode).
+//
+// Work.  An item is one (sequence, key head, tile of query rows); its keys are cut
+// into units of `unit` keys (a sequence without keys has one empty unit, which
+// writes its zeros).  All units of all items stand in one row, item after item,
+// and every block takes an equal run of them: long and short sequences, few and
+// many heads balance without the host knowing a length.  A block finds its run
+// from kv_len alone (a prefix sum over the batch that every block repeats).
+//
+// Results.  An item that lies within one block's run is finished there.  One that
+// crosses blocks leaves in each a partial: rows x D fp32 sums and each row's
+// running maximum and sum.  A block has at most two of them, its first item
+// (slot 2c) and its last (slot 2c + 1; an item that begins in the block is always
+// its last), so the workspace is two slots a block however long the sequences.
+// Block c also leaves a Join: the item that begins in it and continues, and in
+// how many blocks.  attn_join adds those up in the blocks' order, so the result
+// does not depend on timing.
+#pragma once
+
+#include "gdna_internal.cuh"
+
+namespace gdna {
+
+constexpr int kMaxGrid = 608;              // blocks at most: workspace for two partials each
+
+struct Join {
+    int seq, item;                         // item within the sequence: key head * row_tiles + row tile
+    int parts;                             // blocks the item lies in; 0: nothing to join here
+    int pad;
+};
+
+__host__ __device__ __forceinline__ int part_width(int d) { return (d + 3) & ~3; }
+// floats of one partial: rows x D sums, then rows x (maximum, sum)
+__host__ __device__ __forceinline__ int64_t part_floats(int rows, int d) { return (int64_t)rows * (part_width(d) + 2); }
+
+__device__ __forceinline__ Join *joins_of(const AttnParams &p) { return static_cast<Join *>(p.workspace); }
+__device__ __forceinline__ float *part_of(const AttnParams &p, int slot)
+{
+    return reinterpret_cast<float *>(static_cast<Join *>(p.workspace) + kMaxGrid) +
+           slot * part_floats(p.tile_rows, p.d);
+}
+
+// Keys of sequence b in its cache.
+__device__ __forceinline__ int keys_of(const AttnParams &p, int b)
+{
+    const int64_t most = (int64_t)p.max_pages * p.cache.page_size;
+    return (int)min((int64_t)max(p.kv_len[b], 0), most);
+}
+__device__ __forceinline__ int64_t units_of(const AttnParams &p, int keys)
+{
+    return keys > 0 ? ((int64_t)keys + p.unit - 1) / p.unit : 1;
+}
+
+// A block's run of units, in the row of all units.
+struct Run {
+    int64_t at, end, share;                // [at, end): this block's; share: units of every block's run
+    int64_t base;                          // first unit of sequence `seq`
+    int seq;
+};
+
+// The run of block c.  All threads call it; `scratch` has blockDim.x / 32 + 2 int64.
+__device__ __forceinline__ Run find_run(const AttnParams &p, int c, int64_t *scratch)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int64_t items = (int64_t)p.nkv * p.row_tiles;
+    const int per = (p.batch + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += units_of(p, keys_of(p, b));
+    int64_t incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(kFull, incl, off);
+        if (lane >= off) incl += y;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) incl += scratch[w];
+        total += scratch[w];
+    }
+    Run r;
+    total *= items;
+    r.share = (total + p.grid - 1) / p.grid;
+    r.at = c * r.share;
+    r.end = min(r.at + r.share, total);
+    // the thread whose sequences hold unit `at` walks them
+    int64_t base = (incl - mine) * items;
+    if (mine > 0 && base <= r.at && r.at < incl * items) {
+        int b = b0;
+        for (;; ++b) {
+            const int64_t n = units_of(p, keys_of(p, b)) * items;
+            if (r.at < base + n) break;
+            base += n;
+        }
+        scratch[warps] = base;
+        scratch[warps + 1] = b;
+    }
+    __syncthreads();
+    r.base = scratch[warps];
+    r.seq = (int)scratch[warps + 1];
+    return r;
+}
+
+// One item's part in a run.
+struct Part {
+    int seq, item, keys;                   // as in Join; keys of the sequence
+    int64_t u0, u1;                        // units of the item
+    bool begins, ends;                     // the item's first / last unit is among them
+    int blocks;                            // where it begins and does not end: blocks it lies in
+};
+
+// The run's next part; advances it.
+__device__ __forceinline__ Part next_part(const AttnParams &p, Run &r, int c)
+{
+    const int64_t items = (int64_t)p.nkv * p.row_tiles;
+    Part t;
+    t.seq = r.seq;
+    t.keys = keys_of(p, r.seq);
+    const int64_t n = units_of(p, t.keys), off = r.at - r.base;
+    t.item = (int)(off / n);
+    t.u0 = off - t.item * n;
+    t.u1 = min(n, t.u0 + (r.end - r.at));
+    t.begins = t.u0 == 0;
+    t.ends = t.u1 == n;
+    t.blocks = t.begins && !t.ends ? (int)((r.base + (t.item + 1) * n - 1) / r.share) - c + 1 : 0;
+    r.at += t.u1 - t.u0;
+    if (t.ends && t.item == items - 1) { r.base += n * items; ++r.seq; }
+    return t;
+}
+
+// Query row `row` (token * group + head of the group) of a sequence sees this many keys.
+__device__ __forceinline__ int keys_seen(const AttnParams &p, int keys, int row)
+{
+    return row < p.q_len * p.group ? keys - (p.q_len - 1 - row / p.group) : 0;
+}
+
+// Element c of query row `row`: o is the normalised sum.
+__device__ __forceinline__ void write_out(const AttnParams &p, int seq, int head, int row, int c, float o)
+{
+    const int64_t r = (int64_t)seq * p.q_len + row / p.group;
+    const int64_t h = (int64_t)head * p.group + row % p.group;
+    if (p.gate != nullptr) {
+        const float g = load_elem(p.gate, r * p.gate_stride + h * p.gate_head_stride + c, p.dtype);
+        o = o / (1.0f + expf(-g));
+    }
+    store_elem(p.out, r * p.out_stride + h * p.d + c, p.out_dtype, o);
+}
+
+__device__ __forceinline__ void write_lse(const AttnParams &p, int seq, int head, int row, float m, float l)
+{
+    const int64_t r = (int64_t)seq * p.q_len + row / p.group;
+    // m is in units of log2
+    if (p.lse != nullptr)
+        p.lse[r * p.nq + (int64_t)head * p.group + row % p.group] =
+            l == 0.f ? -__int_as_float(0x7f800000) : m * 0.69314718055994531f + logf(l);
+}
+
+// A row's sums stand for exp2(m) times them; m of a row without keys is -inf.
+__device__ __forceinline__ float weight_of(float m, float top) { return m == -__int_as_float(0x7f800000) ? 0.f : exp2f(m - top); }
+
+// Instances of the tensor-core kernel, one translation unit per cache type.
+template <int CACHE> cudaError_t launch_attn_tc(const AttnParams &p, cudaStream_t s);
+
+}  // namespace gdna

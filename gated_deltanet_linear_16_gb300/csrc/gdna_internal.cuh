@@ -1,0 +1,111 @@
+// gdna_internal.cuh -- parameter blocks, launcher declarations and device
+// helpers shared by the attention-layer translation units (include/gdna.h).
+// Not part of the public ABI.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdn_internal.cuh"
+#include "gdna.h"
+
+namespace gdna {
+
+using gdn::kFull;
+
+// Where the cache's elements are: strides in elements.
+struct CacheLayout {
+    int64_t page_stride, token_stride, head_stride;
+    int64_t pages;
+    int page_size;
+};
+
+struct PageParams {
+    const int32_t *cached, *fresh;
+    int32_t *table;
+    int64_t table_stride;
+    const int32_t *free_pages;
+    int64_t n_free;
+    const int32_t *free_head;
+    int32_t *kv_len, *row_start;
+    int64_t *slots;
+    int32_t *positions, *free_head_out, *unserved;
+    int64_t rows;
+    int batch, page_size, max_pages;
+};
+
+struct RopeParams {
+    const void *q, *k, *v;
+    const float *qn, *kn, *cos_sin;
+    const int32_t *positions;
+    const int64_t *slots;
+    void *q_out, *k_out, *k_cache, *v_cache;
+    int64_t rows, n_pos;
+    int64_t q_stride, q_head_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    CacheLayout cache;
+    int dtype, cache_dtype, nq, nkv, d, rot, interleaved;
+    float eps, k_scale, v_scale;
+};
+
+struct AttnParams {
+    const void *q, *gate, *k, *v;
+    const int32_t *table, *kv_len;
+    void *out;
+    float *lse;
+    void *workspace;
+    int64_t table_stride, q_stride, gate_stride, gate_head_stride, out_stride;
+    CacheLayout cache;
+    int dtype, cache_dtype, out_dtype;
+    int batch, q_len, nq, nkv, group, d, max_pages;
+    float scale;            // scale * k_scale * log2(e): scores in units of log2
+    float v_scale;
+    // set by the launcher
+    int unit;               // keys of one unit of work
+    int tile_rows;          // query rows (token, head of the group) of one work item
+    int row_tiles;          // ceil(q_len * group / tile_rows)
+    int grid;               // blocks that share the work
+};
+
+cudaError_t launch_page_assign(const PageParams &p, cudaStream_t s);
+cudaError_t launch_qk_norm_rope(const RopeParams &p, bool fast, cudaStream_t s);
+cudaError_t launch_attn_decode(const AttnParams &p, bool fast, cudaStream_t s);
+int64_t attn_workspace_bytes(int64_t rows, int d);
+
+// ---------------------------------------------------------------- device helpers
+
+template <int DT> struct Elem;
+template <> struct Elem<GDNA_F32> { using type = float; };
+template <> struct Elem<GDNA_F16> { using type = __half; };
+template <> struct Elem<GDNA_BF16> { using type = __nv_bfloat16; };
+template <> struct Elem<GDNA_E4M3> { using type = __nv_fp8_storage_t; };
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__nv_fp8_storage_t x)
+{
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(x, __NV_E4M3)));
+}
+
+// One element of an array whose type is known at run time.
+__device__ __forceinline__ float load_elem(const void *p, int64_t i, int dtype)
+{
+    if (dtype == GDNA_F32) return static_cast<const float *>(p)[i];
+    if (dtype == GDNA_F16) return to_f32(static_cast<const __half *>(p)[i]);
+    if (dtype == GDNA_BF16) return to_f32(static_cast<const __nv_bfloat16 *>(p)[i]);
+    return to_f32(static_cast<const __nv_fp8_storage_t *>(p)[i]);
+}
+
+// The same, rounded to nearest even once (E4M3 saturates at +-448).
+__device__ __forceinline__ void store_elem(void *p, int64_t i, int dtype, float x)
+{
+    if (dtype == GDNA_F32) static_cast<float *>(p)[i] = x;
+    else if (dtype == GDNA_F16) static_cast<__half *>(p)[i] = __float2half_rn(x);
+    else if (dtype == GDNA_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
+    else static_cast<__nv_fp8_storage_t *>(p)[i] = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+}  // namespace gdna

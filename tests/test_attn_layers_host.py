@@ -1,0 +1,219 @@
+"""Checks of the attention-layer entry points that need no GPU: what they refuse, the workspace's size, and the
+host's table of cosines and sines against its definition in extended precision."""
+import ctypes
+import math
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_linear_16_gb300 as gdn
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "gdna.h")
+OK, ARG, UNSUP, ALIGN, ALIAS = 0, 1, 2, 3, 4
+G = 1 << 32
+A = [G * (i + 1) for i in range(20)]        # fake, far apart addresses: never dereferenced by a rejected call
+
+
+@pytest.fixture(scope="module")
+def built():
+    gdn.build()
+    return gdn.load()
+
+
+@pytest.fixture(scope="module")
+def lib(built):
+    if torch.cuda.is_available():
+        pytest.skip("fake-pointer validation tests run only on hosts without a GPU")
+    return built
+
+
+def test_header_and_exports_agree(built):
+    want = sorted(set(re.findall(r"GDN_API\s+[\w\s\*]*?\b(gdna_\w+)\s*\(", open(HEADER).read())))
+    assert want == ["gdna_attn_decode", "gdna_attn_workspace", "gdna_page_assign", "gdna_qk_norm_rope", "gdna_rope_table"]
+    out = subprocess.run(["nm", "-D", "--defined-only", gdn.library_path()], capture_output=True, text=True,
+                         check=True).stdout
+    assert sorted({x.split()[-1] for x in out.splitlines() if x.split()[-1].startswith("gdna_")}) == want
+    for name in want:
+        assert name in gdn.__all__ and hasattr(gdn, name)
+
+
+def test_the_headers_are_plain_c(built, tmp_path):
+    src = tmp_path / "t.c"
+    src.write_text('#include "gdna.h"\nint main(void) { return (int)sizeof(gdna_dtype) - (int)sizeof(int); }\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-fsyntax-only", "-I", os.path.dirname(HEADER), str(src)], check=True)
+
+
+def pages(lib, **kw):
+    a = dict(cached=A[0], fresh=A[1], table=A[2], stride=8, free=A[3], n_free=100, head=A[4], kv=A[5], start=A[6],
+             slots=A[7], pos=A[8], head_out=A[9], unserved=A[10], batch=4, rows=16, page=16, max_pages=8)
+    a.update(kw)
+    return lib.gdna_page_assign(a["cached"], a["fresh"], a["table"], a["stride"], a["free"], a["n_free"], a["head"],
+                                a["kv"], a["start"], a["slots"], a["pos"], a["head_out"], a["unserved"], a["batch"],
+                                a["rows"], a["page"], a["max_pages"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(batch=-1), ARG), (dict(rows=-1), ARG), (dict(page=0), ARG), (dict(max_pages=0), ARG), (dict(n_free=-1), ARG),
+    (dict(batch=(1 << 20) + 1), UNSUP), (dict(rows=1 << 31), UNSUP), (dict(n_free=1 << 31), UNSUP),
+    (dict(cached=None), ARG), (dict(fresh=None), ARG), (dict(table=None), ARG), (dict(free=None), ARG),
+    (dict(head=None), ARG), (dict(kv=None), ARG), (dict(start=None), ARG), (dict(slots=None), ARG), (dict(pos=None), ARG),
+    (dict(head_out=None), ARG), (dict(unserved=None), ARG), (dict(stride=7), ARG),
+    (dict(table=A[2] + 2), ALIGN), (dict(slots=A[7] + 4), ALIGN),
+    (dict(kv=A[0]), ALIAS), (dict(head_out=A[4]), ALIAS), (dict(start=A[5] + 12), ALIAS), (dict(slots=A[2] + 64), ALIAS),
+    (dict(unserved=A[3] + 396), ALIAS), (dict(batch=0), OK), (dict(batch=0, cached=None), OK)])
+def test_page_assign_refuses(lib, kw, want):
+    assert pages(lib, **kw) == want
+
+
+def rope(lib, **kw):
+    a = dict(q=A[0], k=A[1], v=A[2], dtype=0, qn=A[3], kn=A[4], eps=1e-6, cs=A[5], n_pos=100, rot=64, inter=0, pos=A[6],
+             slots=A[7], qo=A[8], ko=A[9], kc=A[10], vc=A[11], cdt=2, ks=1.0, vs=1.0, rows=8, nq=4, nkv=2, d=128,
+             pages=10, page=16, qs=512, qhs=128, kst=256, vst=256, qos=512, kos=256, ps=4096, ts=256, hs=128)
+    a.update(kw)
+    return lib.gdna_qk_norm_rope(a["q"], a["k"], a["v"], a["dtype"], a["qn"], a["kn"], a["eps"], a["cs"], a["n_pos"],
+                                 a["rot"], a["inter"], a["pos"], a["slots"], a["qo"], a["ko"], a["kc"], a["vc"], a["cdt"],
+                                 a["ks"], a["vs"], a["rows"], a["nq"], a["nkv"], a["d"], a["pages"], a["page"], a["qs"],
+                                 a["qhs"], a["kst"], a["vst"], a["qos"], a["kos"], a["ps"], a["ts"], a["hs"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), ARG), (dict(nq=-1), ARG), (dict(nkv=-1), ARG), (dict(nq=0, nkv=0), ARG), (dict(d=0), ARG),
+    (dict(d=257), UNSUP), (dict(dtype=3), UNSUP), (dict(dtype=9), UNSUP), (dict(cdt=0), UNSUP), (dict(cdt=7), UNSUP),
+    (dict(rot=63), ARG), (dict(rot=130), ARG), (dict(rot=-2), ARG), (dict(n_pos=0), ARG),
+    (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG), (dict(eps=float("inf")), ARG),
+    (dict(ks=0.0), ARG), (dict(vs=float("inf")), ARG), (dict(ks=-1.0), ARG), (dict(vs=float("nan")), ARG),
+    (dict(q=None), ARG), (dict(k=None), ARG), (dict(v=None), ARG), (dict(vc=None), ARG), (dict(cs=None), ARG),
+    (dict(pos=None), ARG), (dict(slots=None), ARG), (dict(qo=None), ARG), (dict(kc=None, vc=None, v=None, ko=None), ARG),
+    (dict(nkv=0, k=None, v=None, vc=None), ARG),                    # a cache and no keys
+    (dict(qs=511), ARG), (dict(qhs=127), ARG), (dict(kst=255), ARG), (dict(vst=1), ARG), (dict(qos=511), ARG),
+    (dict(kos=255), ARG), (dict(pages=0), ARG), (dict(page=0), ARG), (dict(pages=1 << 31), UNSUP),
+    (dict(ps=4095), ARG), (dict(ts=255), ARG), (dict(hs=127), ARG), (dict(ts=-256), ARG), (dict(ts=128, hs=128), ARG),
+    (dict(q=A[0] + 2), ALIGN), (dict(kc=A[10] + 1), ALIGN), (dict(slots=A[7] + 4), ALIGN), (dict(cs=A[5] + 1), ALIGN),
+    (dict(qo=A[0] + 16), ALIAS), (dict(qo=A[1]), ALIAS), (dict(ko=A[1]), ALIAS), (dict(kc=A[2]), ALIAS),
+    (dict(vc=A[10]), ALIAS), (dict(vc=A[10] + 64), ALIAS), (dict(qo=A[0], qhs=256, qs=1024), ALIAS),
+    (dict(qo=A[3]), ALIAS), (dict(ko=A[10]), ALIAS), (dict(qo=A[7]), ALIAS),
+    (dict(rows=0), OK), (dict(rows=0, q=None, k=None, v=None, vc=None), OK)])
+def test_qk_norm_rope_refuses(lib, kw, want):
+    assert rope(lib, **kw) == want
+
+
+def attn(lib, **kw):
+    a = dict(q=A[0], dtype=2, gate=A[1], k=A[2], v=A[3], cdt=2, ks=1.0, vs=1.0, table=A[4], tstride=8, kv=A[5], scale=0.1,
+             out=A[6], odt=2, lse=A[7], ws=A[8], wsb=1 << 30, batch=3, q_len=2, nq=8, nkv=2, d=128, pages=10, page=16,
+             max_pages=8, qs=1024, gs=1024, ghs=128, os=1024, ps=4096, ts=256, hs=128)
+    a.update(kw)
+    return lib.gdna_attn_decode(a["q"], a["dtype"], a["gate"], a["k"], a["v"], a["cdt"], a["ks"], a["vs"], a["table"],
+                                a["tstride"], a["kv"], a["scale"], a["out"], a["odt"], a["lse"], a["ws"], a["wsb"],
+                                a["batch"], a["q_len"], a["nq"], a["nkv"], a["d"], a["pages"], a["page"], a["max_pages"],
+                                a["qs"], a["gs"], a["ghs"], a["os"], a["ps"], a["ts"], a["hs"], None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(batch=-1), ARG), (dict(q_len=-1), ARG), (dict(nq=0), ARG), (dict(nkv=0), ARG), (dict(d=0), ARG),
+    (dict(max_pages=0), ARG), (dict(nq=9), UNSUP), (dict(d=257), UNSUP), (dict(dtype=3), UNSUP), (dict(odt=3), UNSUP),
+    (dict(cdt=0), UNSUP), (dict(cdt=4), UNSUP), (dict(batch=(1 << 20) + 1), UNSUP), (dict(q_len=1 << 22), UNSUP),
+    (dict(scale=0.0), ARG), (dict(scale=-1.0), ARG), (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG),
+    (dict(ks=0.0), ARG), (dict(vs=float("nan")), ARG), (dict(ks=1e-30, scale=1e-30), ARG),
+    (dict(q=None), ARG), (dict(k=None), ARG), (dict(v=None), ARG), (dict(table=None), ARG), (dict(kv=None), ARG),
+    (dict(out=None), ARG), (dict(ws=None), ARG), (dict(wsb=1000), ARG),
+    (dict(tstride=7), ARG), (dict(qs=1023), ARG), (dict(gs=1023), ARG), (dict(ghs=127), ARG), (dict(os=1023), ARG),
+    (dict(pages=0), ARG), (dict(page=0), ARG), (dict(ps=4095), ARG), (dict(ts=255), ARG), (dict(hs=100), ARG),
+    (dict(q=A[0] + 1), ALIGN), (dict(out=A[6] + 1), ALIGN), (dict(ws=A[8] + 8), ALIGN), (dict(lse=A[7] + 2), ALIGN),
+    (dict(k=A[2] + 1), ALIGN), (dict(kv=A[5] + 2), ALIGN),
+    (dict(out=A[0]), ALIAS), (dict(out=A[2] + 4096), ALIAS), (dict(lse=A[6] + 16), ALIAS), (dict(ws=A[4]), ALIAS),
+    (dict(out=A[1] + 128), ALIAS), (dict(lse=A[5]), ALIAS),
+    (dict(batch=0), OK), (dict(q_len=0), OK), (dict(batch=0, q=None, ws=None), OK)])
+def test_attn_decode_refuses(lib, kw, want):
+    assert attn(lib, **kw) == want
+
+
+def test_layouts_that_are_not_refused_reach_the_launch(lib):
+    """Heads first, K and V interleaved by page or by head: sound strides pass the checks (the launch then fails
+    without a GPU)."""
+    for kw in (dict(ps=4096, ts=128, hs=2048), dict(v=A[2] + 2 * 4096, ps=8192), dict(v=A[2] + 2 * 128, ps=8192, ts=512, hs=256),
+               dict(v=A[2])):
+        assert attn(lib, **kw) == 5, kw
+    assert rope(lib, vc=A[10] + 2 * 4096, ps=8192) == 5 and rope(lib, qo=A[0]) == 5
+
+
+def test_workspace_grows_with_rows_and_d(built):
+    size = lambda **kw: gdn.gdna_attn_workspace(**{**dict(batch=3, q_len=1, nq=8, nkv=2, d=128), **kw})   # noqa: E731
+    assert size() > 0 and size() == size(batch=1000) and size(nq=9) == 0 and size(d=257) == 0 and size(d=0) == 0
+    seen = [size(q_len=t) for t in (1, 2, 3, 5, 9, 17, 100)]
+    assert seen == sorted(seen) and size(d=256) > size(d=64)
+
+
+def table_of(**kw):
+    a = {**dict(n_pos=5, rot=64, base=1e4), **kw}
+    t = torch.full((a["n_pos"], a["rot"]), 7.0)
+    gdn.gdna_rope_table(t, **a)
+    return t.double().numpy()
+
+
+def want_table(n, freq, amplitude=1.0):
+    angle = np.asarray(n, np.longdouble)[:, None] * np.asarray(freq, np.longdouble)[None]
+    return np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float64) * amplitude
+
+
+def freqs(rot, base):
+    return np.array([np.longdouble(base) ** (np.longdouble(-2 * i) / rot) for i in range(rot // 2)])
+
+
+@pytest.mark.parametrize("rot,base", [(64, 1e4), (128, 1e6), (2, 1e4), (256, 5e5)])
+def test_rope_table(built, rot, base):
+    """Half a unit in the last place of fp32 (|entry| <= 1: 2^-25), and the 64-bit angle's error, n * 2^-52."""
+    got = table_of(n_pos=4000, rot=rot, base=base)
+    assert np.abs(got - want_table(range(4000), freqs(rot, base))).max() <= 2.0 ** -25 + 4000 * 2.0 ** -50
+
+
+def test_rope_table_far_positions(built):
+    n = 262144
+    got = table_of(n_pos=n, rot=8, base=1e4)
+    assert np.abs(got[-5:] - want_table(range(n - 5, n), freqs(8, 1e4))).max() <= 2.0 ** -25 + n * 2.0 ** -50
+
+
+def test_rope_scaling(built):
+    f = freqs(64, 1e4)
+    close = lambda kw, freq, amp=1.0: np.abs(table_of(n_pos=900, **kw) - want_table(range(900), freq, amp)).max() <= amp * 2e-7  # noqa: E731
+    assert close(dict(kind=gdn.GDNA_ROPE_LINEAR, factor=4.0), f / 4)
+    assert close(dict(kind=gdn.GDNA_ROPE_LINEAR, factor=1.0), f)
+    ntk = freqs(64, 1e4 * 8 ** (64 / 62))
+    assert close(dict(kind=gdn.GDNA_ROPE_NTK, factor=8.0), ntk)
+    assert ntk[0] == f[0] and abs(ntk[-1] * 8 / f[-1] - 1) < 1e-12       # the fastest kept, the slowest divided
+    # by parts: where a pair turns 32 times or more in 4096 positions it is kept, at one turn or less divided
+    low = math.floor(64 * math.log(4096 / (32 * 2 * math.pi)) / (2 * math.log(1e4)))
+    high = math.ceil(64 * math.log(4096 / (2 * math.pi)) / (2 * math.log(1e4)))
+    ramp = np.clip((np.arange(32) - low) / (high - low), 0, 1)
+    yarn = f * (1 - ramp) + f / 16 * ramp
+    assert yarn[0] == f[0] and yarn[-1] == f[-1] / 16 and ((yarn <= f) & (yarn >= f / 16)).all()
+    amp = 0.1 * math.log(16) + 1
+    assert close(dict(kind=gdn.GDNA_ROPE_YARN, factor=16.0, original_len=4096.0, amplitude=amp), yarn, amp)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(n_pos=-1), ARG), (dict(rot=0), ARG), (dict(rot=3), ARG), (dict(base=0.0), ARG), (dict(base=float("inf")), ARG),
+    (dict(amplitude=0.0), ARG), (dict(amplitude=float("nan")), ARG), (dict(kind=9), UNSUP),
+    (dict(kind=1, factor=0.5), ARG), (dict(kind=2, factor=float("nan")), ARG), (dict(kind=2, factor=2.0, rot=2), ARG),
+    (dict(kind=3, factor=2.0), ARG), (dict(kind=3, factor=2.0, original_len=100.0, beta_fast=1.0), ARG),
+    (dict(kind=3, factor=2.0, original_len=100.0, beta_slow=0.0), ARG), (dict(table=None), ARG), (dict(n_pos=0), OK)])
+def test_rope_table_refuses(built, kw, want):
+    buf = (ctypes.c_float * 400)()
+    a = dict(table=ctypes.addressof(buf), n_pos=4, rot=64, base=1e4, kind=0, factor=1.0, original_len=0.0, beta_fast=32.0,
+             beta_slow=1.0, amplitude=1.0)
+    a.update(kw)
+    assert built.gdna_rope_table(a["table"], a["n_pos"], a["rot"], a["base"], a["kind"], a["factor"], a["original_len"],
+                                 a["beta_fast"], a["beta_slow"], a["amplitude"]) == want
+    if want != OK:
+        assert not any(buf)
+
+
+def test_binding_refuses_other_types(built):
+    with pytest.raises(ValueError):
+        gdn.gdna_attn_decode(torch.zeros(4, dtype=torch.int32), 0, 0, 0, 0, 0, 0, batch=1, nq=1, nkv=1, d=4, pages=1,
+                             page_size=1, max_pages=1)
+    with pytest.raises(ValueError):
+        gdn.gdna_attn_decode(1 << 20, 0, 0, 0, 0, 0, 0, batch=1, nq=1, nkv=1, d=4, pages=1, page_size=1, max_pages=1)
