@@ -29,7 +29,8 @@ NVCC_FLAGS = ARCH + [
 LINK_FLAGS = ARCH + ["-shared", "-cudart", "static"]
 SOURCES = ["gdn_abi.cu", "gdn_decode.cu", "gdn_chunk2.cu", "gdn_conv_norm.cu", "gdn_prefill.cu", "gdn_convert.cu",
            "gdn_noalloc.cu", "gdn_norm.cu", "gdn_prefill_tc.cu",
-           "gdna_abi.cu", "gdna_pages.cu", "gdna_rope.cu", "gdna_attn.cu"]
+           "gdna_abi.cu", "gdna_pages.cu", "gdna_rope.cu", "gdna_attn.cu",
+           "gdna_attn_f16.cu", "gdna_attn_bf16.cu", "gdna_attn_e4m3.cu"]
 
 
 def nvcc() -> str:

@@ -214,9 +214,19 @@ int64_t attn_workspace_bytes(int64_t rows, int d)
     return kMaxGrid * (int64_t)sizeof(Join) + 2 * kMaxGrid * part_floats(tc_rows(rows), d) * (int64_t)sizeof(float);
 }
 
+cudaError_t launch_join(const AttnParams &p, cudaStream_t s)
+{
+    attn_join<<<dim3(p.grid, p.tile_rows), kJoinThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_attn_decode(const AttnParams &params, bool fast, cudaStream_t s)
 {
-    (void)fast;
+    if (fast) {
+        if (params.cache_dtype == GDNA_F16) return launch_attn_tc<GDNA_F16>(params, s);
+        if (params.cache_dtype == GDNA_BF16) return launch_attn_tc<GDNA_BF16>(params, s);
+        return launch_attn_tc<GDNA_E4M3>(params, s);
+    }
     AttnParams p = params;
     p.unit = kThreads;
     p.tile_rows = kRows;
@@ -224,10 +234,8 @@ cudaError_t launch_attn_decode(const AttnParams &params, bool fast, cudaStream_t
     const int sms = gdn::sm_count();
     p.grid = 4 * sms < kMaxGrid ? 4 * sms : kMaxGrid;
     attn_general<<<p.grid, kThreads, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    attn_join<<<dim3(p.grid, p.tile_rows), kJoinThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join(p, s);
 }
 
 }  // namespace gdna

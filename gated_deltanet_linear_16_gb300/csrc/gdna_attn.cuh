@@ -161,7 +161,10 @@ __device__ __forceinline__ void write_lse(const AttnParams &p, int seq, int head
 // A row's sums stand for exp2(m) times them; m of a row without keys is -inf.
 __device__ __forceinline__ float weight_of(float m, float top) { return m == -__int_as_float(0x7f800000) ? 0.f : exp2f(m - top); }
 
-// Instances of the tensor-core kernel, one translation unit per cache type.
+// Adds up the items that lie in several blocks, after the kernel that left them.
+cudaError_t launch_join(const AttnParams &p, cudaStream_t s);
+
+// The tensor-core kernels, one translation unit per cache type.
 template <int CACHE> cudaError_t launch_attn_tc(const AttnParams &p, cudaStream_t s);
 
 }  // namespace gdna

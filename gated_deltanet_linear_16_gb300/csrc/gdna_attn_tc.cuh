@@ -1,0 +1,583 @@
+// gdna_attn_tc.cuh -- paged decode attention on the tensor cores (head sizes 64,
+// 128 and 256): the kernel's template.  gdna_attn.cuh has the deal of the work and
+// the partial results.
+//
+// Mathematics.  With few query rows (8 to 64: the tokens and the group's heads) and
+// many keys, the keys take the side of the product that is 16 wide and the query
+// rows the side that is 8 wide:
+//
+//     S^T [16 keys x 8 rows]  = K [16 x D] . Q^T          D/16 products a row tile
+//     O^T [D x 8 rows]       += V^T [D x 16] . P^T        D/16 products a row tile
+//
+// so a row tile of 8 costs what it holds.  A warp takes 16 keys at a time with a
+// running maximum m and sum l for each row: S^T's columns are rows, so the maximum
+// over keys is three shuffles, and the rescale of O^T is by its own columns.  P^T
+// needs the transpose of what the first product leaves; an 8 x 8 register transpose
+// (movmatrix) does it, nothing passes through shared memory.
+//
+// Rounding.  K and V are exact in the products (E4M3 widens to fp16 exactly).  The
+// queries enter in as many 16-bit parts as their type needs (`q_parts`: x = hi + lo
+// [+ lower]), scaled by a power of two per row for fp16 products, so that no query
+// over- or underflows.  The weights exp2(s - m) <= 1 enter in two parts (hi + lo),
+// three where bf16 products give an fp32 output: with one part of bf16 the weights'
+// rounding (2^-9) would be as large as that of a bf16 output.  m, l, S and O are fp32.
+//
+// What a row does not see.  Masked scores are replaced, not added to.  Keys past the
+// sequence's end are not loaded (zeros stand for them).  The keys that some tokens see
+// and others do not (the last q_len - 1) may hold Inf or NaN values, and 0 * NaN would
+// carry them into rows that do not see them: there a tile with a non-finite V adds its
+// rows key by key instead.
+//
+// Data.  A warp (or the R warps that share keys, each with its own rows) has its own
+// ring of stages in shared memory, 16 keys of K and V each, filled by cp.async in
+// 16-byte pieces (a key's head is D contiguous elements; keys lie anywhere) and drained
+// without any barrier over the block.  Rows are padded by 16 bytes: eight rows of an
+// ldmatrix then start in eight different bank groups.
+#pragma once
+
+#include "gdna_attn.cuh"
+
+namespace gdna {
+namespace tc {
+
+constexpr int kKeys = 16;                  // keys of a step
+constexpr int kMaxStages = 8;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+__device__ __forceinline__ unsigned smem_addr(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void ldsm4(unsigned (&r)[4], unsigned addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(unsigned (&r)[4], unsigned addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// The transpose of an 8 x 8 matrix of 16-bit elements, one row of two a lane.
+__device__ __forceinline__ unsigned transpose8(unsigned x)
+{
+    unsigned y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void cp_async16(unsigned dst, const void *src, bool real)
+{
+    const int n = real ? 16 : 0;           // 0: sixteen zero bytes, nothing is read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// All but the newest `stages - 2` copy groups have landed.
+__device__ __forceinline__ void wait_stage(int stages)
+{
+    switch (stages) {
+    case 2: gdn::cp_async_wait<0>(); break;
+    case 3: gdn::cp_async_wait<1>(); break;
+    case 4: gdn::cp_async_wait<2>(); break;
+    case 5: gdn::cp_async_wait<3>(); break;
+    case 6: gdn::cp_async_wait<4>(); break;
+    case 7: gdn::cp_async_wait<5>(); break;
+    default: gdn::cp_async_wait<6>(); break;
+    }
+}
+
+// 16-bit operand type of the products: bf16 for a bf16 cache, else fp16.
+template <int CACHE> struct Op {
+    __device__ static unsigned pack(float a, float b)
+    {
+        __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<unsigned *>(&h);
+    }
+    __device__ static float2 unpack(unsigned u) { return __half22float2(*reinterpret_cast<__half2 *>(&u)); }
+    __device__ static void mma(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1)
+    {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+template <> struct Op<GDNA_BF16> {
+    __device__ static unsigned pack(float a, float b)
+    {
+        __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<unsigned *>(&h);
+    }
+    __device__ static float2 unpack(unsigned u)
+    {
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+    __device__ static void mma(float (&c)[4], const unsigned (&a)[4], unsigned b0, unsigned b1)
+    {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+
+// Two E4M3 values (16 bits) to two fp16, exactly.
+__device__ __forceinline__ unsigned widen2(unsigned short x)
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(x, __NV_E4M3);
+    return (unsigned)h.x | ((unsigned)h.y << 16);
+}
+
+template <int CACHE, int D, int NT, int R> struct Shape {
+    static constexpr int kElem = CACHE == GDNA_E4M3 ? 1 : 2;
+    static constexpr int kRowBytes = D * kElem;
+    static constexpr int kPitch = kRowBytes + 16;
+    static constexpr int kStage = 2 * kKeys * kPitch;          // K, then V
+    static constexpr int kWarps = (kRowBytes == 512 && R == 1) ? 2 : 4;
+    static constexpr int kKeyWarps = kWarps / R;
+    static constexpr int kRows = 8 * NT * R;
+    static constexpr int kQPitch = 2 * D + 16;
+    static constexpr int kSumPitch = D + 4;                    // floats
+};
+
+template <int CACHE, int D, int NT, int R>
+__global__ void __launch_bounds__(Shape<CACHE, D, NT, R>::kWarps * 32, 2)
+attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_parts)
+{
+    using S = Shape<CACHE, D, NT, R>;
+    using O = Op<CACHE>;
+    constexpr bool kF8 = CACHE == GDNA_E4M3;
+    constexpr int W = S::kWarps, TW = S::kKeyWarps, ROWS = S::kRows;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t scratch[W + 2];
+    __shared__ float row_scale[ROWS], warp_m[TW][ROWS], warp_l[TW][ROWS];
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+    const int tw = warp / R, rg = warp % R;                    // the keys it takes, the rows it takes
+    const int l4 = lane >> 2, c4 = lane & 3;
+    uint8_t *ring = smem + tw * stages * S::kStage;
+    uint8_t *qs = smem + TW * stages * S::kStage;
+    float *sums = reinterpret_cast<float *>(smem);             // after the keys: [TW][ROWS][kSumPitch]
+    const int group_rows = p.q_len * p.group;
+    const int64_t page_bytes = p.cache.page_stride * S::kElem, token_bytes = p.cache.token_stride * S::kElem;
+
+    Run run = find_run(p, c, scratch);
+    Join join = {0, 0, 0, 0};
+
+    while (run.at < run.end) {
+        const Part part = next_part(p, run, c);
+        const int head = part.item / p.row_tiles, row0 = (part.item % p.row_tiles) * ROWS;
+        const int steps = (int)(part.u1 - part.u0);
+        const int32_t *table = p.table + part.seq * p.table_stride;
+        const uint8_t *kb = static_cast<const uint8_t *>(p.k) + head * p.cache.head_stride * S::kElem;
+        const uint8_t *vb = static_cast<const uint8_t *>(p.v) + head * p.cache.head_stride * S::kElem;
+        __syncthreads();                   // the last part's sums and queries are used up
+
+        // page of the key that this lane looks up for a step; -1: none
+        auto first_key = [&](int i) { return (int64_t)((part.u0 + i) * TW + tw) * kKeys; };
+        auto page_of = [&](int i) {
+            const int64_t key = first_key(i) + (lane & 15);
+            return i < steps && key < part.keys ? __ldg(table + (unsigned)key / (unsigned)p.cache.page_size) : -1;
+        };
+        auto issue = [&](int i, int page) {
+            const unsigned key = (unsigned)first_key(i) + (lane & 15);
+            int64_t at = -1;
+            if ((unsigned)page < (unsigned)p.cache.pages)
+                at = page * page_bytes + (int64_t)(key % (unsigned)p.cache.page_size) * token_bytes;
+            uint8_t *st = ring + (i % stages) * S::kStage;
+            constexpr int kPieces = S::kRowBytes / 16;         // 16-byte pieces of a row: 4 .. 32
+            constexpr int kAtOnce = 32 / kPieces;              // rows of one instruction
+            constexpr int kMine = kKeys / R;                   // rows this warp copies
+            const int sub = lane / kPieces, piece = (lane % kPieces) * 16;
+#pragma unroll
+            for (int r = 0; r < kMine; r += kAtOnce) {
+                const int row = rg * kMine + r + sub;
+                const int64_t from = __shfl_sync(kFull, at, row & 15);
+                if (kAtOnce <= kMine || sub < kMine) {
+                    const unsigned dst = smem_addr(st + row * S::kPitch + piece);
+                    const int64_t o = from >= 0 ? from + piece : 0;
+                    cp_async16(dst, kb + o, from >= 0);
+                    cp_async16(dst + kKeys * S::kPitch, vb + o, from >= 0);
+                }
+            }
+        };
+        int page = page_of(0);
+        for (int i = 0; i < stages - 1; ++i) {
+            const int next = page_of(i + 1);
+            if (i < steps) issue(i, page);
+            gdn::cp_async_commit();
+            page = next;
+        }
+
+        // queries: 16-bit parts in shared memory (for E4M3 in the order in which its K comes, see below)
+        for (int r = warp; r < ROWS; r += W) {
+            const int row = row0 + r;
+            float x[D / 32];
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                x[j] = 0.f;
+                if (row < group_rows)
+                    x[j] = load_elem(p.q, ((int64_t)part.seq * p.q_len + row / p.group) * p.q_stride +
+                                              ((int64_t)head * p.group + row % p.group) * D + lane + 32 * j, p.dtype);
+                top = fmaxf(top, fabsf(x[j]));
+            }
+            float back = 1.f;
+            if constexpr (CACHE != GDNA_BF16) {                // largest element to 2^14 .. 2^15
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+                int e = (int)(__float_as_uint(top) >> 23) - 127;
+                e = top > 0.f && e < 128 ? max(e, -100) : 14;
+                const float up = __uint_as_float((unsigned)(127 + 14 - e) << 23);
+                back = __uint_as_float((unsigned)(127 - 14 + e) << 23);
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) x[j] *= up;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                int at = lane + 32 * j;
+                if constexpr (kF8) {
+                    // a 32-bit word of four E4M3 becomes two operand registers: slots 2q, 2q+1 and 8+2q, 8+2q+1
+                    const int q = (at & 15) >> 2, e = at & 3;
+                    at = (at & ~15) + (e < 2 ? 2 * q + e : 6 + 2 * q + e);
+                }
+                float rest = x[j];
+                for (int part_i = 0; part_i < q_parts; ++part_i) {
+                    const unsigned u = O::pack(rest, 0.f);
+                    *reinterpret_cast<uint16_t *>(qs + (part_i * ROWS + r) * S::kQPitch + at * 2) = (uint16_t)u;
+                    rest -= O::unpack(u).x;
+                }
+            }
+            if (lane == 0) row_scale[r] = p.scale * back;
+        }
+        __syncthreads();
+
+        // this lane's rows: rg * 8 NT + 8 t + 2 c4 + j
+        float m[NT][2], l[NT][2], rs[NT][2], o[D / 16][NT][4];
+        int seen[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = rg * 8 * NT + 8 * t + 2 * c4 + j;
+                m[t][j] = kNegInf;
+                l[t][j] = 0.f;
+                rs[t][j] = row_scale[r];
+                seen[t][j] = keys_seen(p, part.keys, row0 + r);
+            }
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[x][t][j] = 0.f;
+        const int all_see = part.keys - (p.q_len - 1);         // keys that every row sees
+        const unsigned q_at = smem_addr(qs + (rg * 8 * NT + (lane & 7)) * S::kQPitch + (lane >> 3) * 16);
+
+        for (int i = 0; i < steps; ++i) {
+            wait_stage(stages);
+            if constexpr (R == 1) __syncwarp();
+            else asm volatile("bar.sync %0, %1;" ::"r"(1 + tw), "n"(32 * R) : "memory");
+            // the stage that was used up a step ago takes the keys of stages - 1 steps ahead
+            {
+                const int ahead = i + stages - 1, next = page_of(ahead + 1);
+                if (ahead < steps) issue(ahead, page);
+                gdn::cp_async_commit();
+                page = next;
+            }
+            const int key0 = (int)first_key(i);
+            if (key0 >= part.keys) continue;
+            const unsigned ks = smem_addr(ring + (i % stages) * S::kStage);
+            const unsigned k_at = ks + (lane & 15) * S::kPitch + (lane >> 4) * 16;
+
+            // S^T: two chains of products a row tile
+            float s2[2][NT][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s2[h][t][j] = 0.f;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+                unsigned a[2][4];
+                if constexpr (kF8) {
+                    unsigned w[4];
+                    ldsm4(w, k_at + x * 32);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        a[h][0] = widen2((unsigned short)w[2 * h]);
+                        a[h][1] = widen2((unsigned short)w[2 * h + 1]);
+                        a[h][2] = widen2((unsigned short)(w[2 * h] >> 16));
+                        a[h][3] = widen2((unsigned short)(w[2 * h + 1] >> 16));
+                    }
+                } else {
+                    ldsm4(a[0], k_at + x * 64);
+                    ldsm4(a[1], k_at + x * 64 + 32);
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    for (int part_i = 0; part_i < q_parts; ++part_i) {
+                        unsigned b[4];
+                        ldsm4(b, q_at + (part_i * ROWS + 8 * t) * S::kQPitch + x * 64);
+                        O::mma(s2[0][t], a[0], b[0], b[1]);
+                        O::mma(s2[1][t], a[1], b[2], b[3]);
+                    }
+            }
+            // scores in units of log2, what a row does not see replaced
+            float w[NT][4];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[t][j] = (s2[0][t][j] + s2[1][t][j]) * rs[t][j & 1];
+            const bool edge = key0 + kKeys > all_see;
+            if (edge) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (key0 + l4 + (j >> 1) * 8 >= seen[t][j & 1]) w[t][j] = kNegInf;
+            }
+            bool moved = false;
+            float down[NT][2], from[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float top = fmaxf(w[t][j], w[t][j + 2]);
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+                    top = fmaxf(top, m[t][j]);
+                    moved |= top != m[t][j];
+                    from[t][j] = top == kNegInf ? 0.f : top;
+                    down[t][j] = weight_of(m[t][j], from[t][j]);
+                    m[t][j] = top;
+                }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[t][j] = exp2f(w[t][j] - from[t][j & 1]);
+            if (__any_sync(kFull, moved)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    l[t][0] *= down[t][0];
+                    l[t][1] *= down[t][1];
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[x][t][j] *= down[t][j & 1];
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                l[t][0] += w[t][0] + w[t][2];
+                l[t][1] += w[t][1] + w[t][3];
+            }
+
+            const uint8_t *vs = ring + (i % stages) * S::kStage + kKeys * S::kPitch;
+            bool plain = true;
+            if (edge && p.q_len > 1) {     // keys that some rows do not see: is every value finite?
+                bool odd = false;
+                for (int x = lane; x < kKeys * (S::kRowBytes / 16); x += 32) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(vs + x / (S::kRowBytes / 16) * S::kPitch +
+                                                                     x % (S::kRowBytes / 16) * 16);
+                    const unsigned words[4] = {u.x, u.y, u.z, u.w};
+                    // each element's all-ones exponent (E4M3: its one NaN pattern); a carry would pass a clear top bit
+                    constexpr unsigned kMask = kF8 ? 0x7f7f7f7fu : CACHE == GDNA_F16 ? 0x7c007c00u : 0x7f807f80u;
+                    constexpr unsigned kOne = kF8 ? 0x01010101u : CACHE == GDNA_F16 ? 0x04000400u : 0x00800080u;
+                    constexpr unsigned kTop = kF8 ? 0x80808080u : 0x80008000u;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) odd |= (((words[y] & kMask) + kOne) & kTop) != 0;
+                }
+                plain = !__any_sync(kFull, odd);
+            }
+            if (plain) {
+                unsigned b[3][NT][2];      // P^T in parts
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float r0 = w[t][2 * h], r1 = w[t][2 * h + 1];
+#pragma unroll
+                        for (int y = 0; y < 3; ++y) {
+                            const unsigned u = O::pack(r0, r1);
+                            const float2 back = O::unpack(u);
+                            r0 -= back.x;
+                            r1 -= back.y;
+                            b[y][t][h] = y < 2 || w_parts > 2 ? transpose8(u) : 0u;
+                        }
+                    }
+                const unsigned v_at = kF8 ? ks + (kKeys + (lane & 15)) * S::kPitch + (lane >> 4) * 16
+                                          : ks + (kKeys + (lane & 7) + (lane >> 4) * 8) * S::kPitch + ((lane >> 3) & 1) * 16;
+                if constexpr (kF8) {
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {
+                        unsigned u[4];
+                        ldsm4_trans(u, v_at + x * 32);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            // bytes of a word: keys 2c4, 2c4+1 of elements 2 l4, 2 l4 + 1
+                            const unsigned e0 = __byte_perm(u[2 * h], 0, 0x3120), e1 = __byte_perm(u[2 * h + 1], 0, 0x3120);
+                            const unsigned a[4] = {widen2((unsigned short)e0), widen2((unsigned short)(e0 >> 16)),
+                                                   widen2((unsigned short)e1), widen2((unsigned short)(e1 >> 16))};
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                O::mma(o[2 * x + h][t], a, b[0][t][0], b[0][t][1]);
+                                O::mma(o[2 * x + h][t], a, b[1][t][0], b[1][t][1]);
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        unsigned a[4];
+                        ldsm4_trans(a, v_at + x * 32);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            O::mma(o[x][t], a, b[0][t][0], b[0][t][1]);
+                            O::mma(o[x][t], a, b[1][t][0], b[1][t][1]);
+                            if (CACHE == GDNA_BF16 && w_parts > 2) O::mma(o[x][t], a, b[2][t][0], b[2][t][1]);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < kKeys; ++k) {
+                    float wk[NT][2];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            wk[t][j] = __shfl_sync(kFull, k < 8 ? w[t][j] : w[t][j + 2], (k & 7) * 4 + c4);
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int e = 16 * x + (kF8 ? 2 * l4 + h : l4 + 8 * h);
+                            const float v = load_elem(vs + k * S::kPitch, e, CACHE);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    if (key0 + k < seen[t][j]) o[x][t][2 * h + j] = fmaf(wk[t][j], v, o[x][t][2 * h + j]);
+                        }
+                }
+            }
+        }
+
+        // join the key warps' rows in shared memory, over the ring
+        gdn::cp_async_wait<0>();
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x = l[t][j];
+                x += __shfl_xor_sync(kFull, x, 4);
+                x += __shfl_xor_sync(kFull, x, 8);
+                x += __shfl_xor_sync(kFull, x, 16);
+                const int r = rg * 8 * NT + 8 * t + 2 * c4 + j;
+                if (l4 == 0) { warp_m[tw][r] = m[t][j]; warp_l[tw][r] = x; }
+#pragma unroll
+                for (int y = 0; y < D / 16; ++y)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        sums[(tw * ROWS + r) * S::kSumPitch + 16 * y + (kF8 ? 2 * l4 + h : l4 + 8 * h)] = o[y][t][2 * h + j];
+            }
+        __syncthreads();
+        const bool whole = part.begins && part.ends;
+        float *to = part_of(p, 2 * c + (part.begins ? 1 : 0));
+        for (int r = warp; r < ROWS; r += W) {
+            const int row = row0 + r;
+            if (row >= group_rows) break;
+            float top = kNegInf, total = 0.f, share[TW];
+#pragma unroll
+            for (int y = 0; y < TW; ++y) top = fmaxf(top, warp_m[y][r]);
+            const float mm = top;
+            if (top == kNegInf) top = 0.f;
+#pragma unroll
+            for (int y = 0; y < TW; ++y) {
+                share[y] = weight_of(warp_m[y][r], top);
+                total = fmaf(share[y], warp_l[y][r], total);
+            }
+            const float norm = total == 0.f ? 0.f : p.v_scale / total;
+#pragma unroll
+            for (int x0 = 0; x0 < D; x0 += 128) {
+                const int x = x0 + 4 * lane;
+                if (D < 128 && x >= D) break;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y < TW; ++y) {
+                    const float4 v = *reinterpret_cast<const float4 *>(sums + (y * ROWS + r) * S::kSumPitch + x);
+                    a.x = fmaf(share[y], v.x, a.x);
+                    a.y = fmaf(share[y], v.y, a.y);
+                    a.z = fmaf(share[y], v.z, a.z);
+                    a.w = fmaf(share[y], v.w, a.w);
+                }
+                if (whole) {
+                    write_out(p, part.seq, head, row, x, total == 0.f ? 0.f : a.x * norm);
+                    write_out(p, part.seq, head, row, x + 1, total == 0.f ? 0.f : a.y * norm);
+                    write_out(p, part.seq, head, row, x + 2, total == 0.f ? 0.f : a.z * norm);
+                    write_out(p, part.seq, head, row, x + 3, total == 0.f ? 0.f : a.w * norm);
+                } else {
+                    *reinterpret_cast<float4 *>(to + r * D + x) = a;
+                }
+            }
+            if (lane == 0) {
+                if (whole) write_lse(p, part.seq, head, row, mm, total);
+                else { to[ROWS * D + 2 * r] = mm; to[ROWS * D + 2 * r + 1] = total; }
+            }
+        }
+        if (part.begins && !part.ends) join = Join{part.seq, part.item, part.blocks, 0};
+    }
+    if (tid == 0) joins_of(p)[c] = join;
+}
+
+constexpr int kTwoPerSm = 111 * 1024;      // shared memory of a block of which two fit an SM
+constexpr int kOnePerSm = 224 * 1024;
+
+template <int CACHE, int D, int NT, int R>
+cudaError_t launch(AttnParams p, cudaStream_t s)
+{
+    using S = Shape<CACHE, D, NT, R>;
+    const bool bf16 = CACHE == GDNA_BF16;
+    // 16-bit parts that hold a query of its type: bf16 products have 8 bits a part, fp16 products 11
+    const int q_parts = p.dtype == GDNA_BF16 ? 1 : p.dtype == GDNA_F16 ? (bf16 ? 2 : 1) : (bf16 ? 3 : 2);
+    const int w_parts = bf16 && p.out_dtype == GDNA_F32 ? 3 : 2;
+    const int q_bytes = q_parts * S::kRows * S::kQPitch;
+    const int least = (S::kRows * S::kSumPitch * 4 + S::kStage - 1) / S::kStage;     // the sums lie over the ring
+    int stages = (kTwoPerSm - q_bytes) / (S::kKeyWarps * S::kStage);
+    if (stages < 3 || stages < least) stages = (kOnePerSm - q_bytes) / (S::kKeyWarps * S::kStage);
+    stages = stages > kMaxStages ? kMaxStages : stages;
+    static_assert(kOnePerSm - 3 * S::kRows * S::kQPitch >= S::kKeyWarps * S::kStage * 3 &&
+                  kOnePerSm - 3 * S::kRows * S::kQPitch >= S::kKeyWarps * S::kRows * S::kSumPitch * 4 + S::kKeyWarps * S::kStage,
+                  "three stages, and room for the sums, whatever the queries' type");
+    static_assert(kMaxStages * S::kStage >= S::kRows * S::kSumPitch * 4, "the sums lie over the ring");
+    const int bytes = S::kKeyWarps * stages * S::kStage + q_bytes;
+    p.unit = kKeys * S::kKeyWarps;
+    p.tile_rows = S::kRows;
+    p.row_tiles = (int)(((int64_t)p.q_len * p.group + S::kRows - 1) / S::kRows);
+    const int grid = gdn::sm_count() * (bytes <= kTwoPerSm ? 2 : 1);
+    p.grid = grid < kMaxGrid ? grid : kMaxGrid;
+    cudaError_t e = gdn::allow_dynamic_smem<&attn_tc<CACHE, D, NT, R>>(kOnePerSm);
+    if (e != cudaSuccess) return e;
+    attn_tc<CACHE, D, NT, R><<<p.grid, S::kWarps * 32, bytes, s>>>(p, stages, q_parts, w_parts);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join(p, s);
+}
+
+template <int CACHE, int D>
+cudaError_t by_rows(const AttnParams &p, cudaStream_t s)
+{
+    const int64_t rows = (int64_t)p.q_len * p.group;
+    if (rows <= 8) return launch<CACHE, D, 1, 1>(p, s);
+    if (rows <= 16) return launch<CACHE, D, 2, 1>(p, s);
+    if (rows <= 32) return launch<CACHE, D, 2, 2>(p, s);
+    return launch<CACHE, D, 2, 4>(p, s);
+}
+
+}  // namespace tc
+
+template <int CACHE> cudaError_t launch_attn_tc(const AttnParams &p, cudaStream_t s)
+{
+    return p.d == 64 ? tc::by_rows<CACHE, 64>(p, s) : p.d == 128 ? tc::by_rows<CACHE, 128>(p, s) : tc::by_rows<CACHE, 256>(p, s);
+}
+
+}  // namespace gdna
