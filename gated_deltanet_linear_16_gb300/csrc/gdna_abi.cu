@@ -270,6 +270,9 @@ GDN_API int gdna_attn_decode(const void *q, gdna_dtype dtype, const void *gate,
     p.dtype = dtype; p.cache_dtype = cache_dtype; p.out_dtype = out_dtype;
     p.batch = batch; p.q_len = q_len; p.nq = nq; p.nkv = nkv; p.group = nq / nkv; p.d = d; p.max_pages = max_pages;
     p.scale = scale2; p.v_scale = v_scale;
+    p.q_vec = rows_aligned(q, elem_size(dtype), 4 * elem_size(dtype), {q_stride, d});
+    p.gate_vec = rows_aligned(gate, elem_size(dtype), 4 * elem_size(dtype), {gate_stride, gate_head_stride});
+    p.out_vec = rows_aligned(out, elem_size(out_dtype), 4 * elem_size(out_dtype), {out_stride, d});
     // the tensor-core kernel copies a key's head in 16-byte pieces
     const int64_t e = elem_size(cache_dtype);
     const bool fast = (d == 64 || d == 128 || d == 256) &&

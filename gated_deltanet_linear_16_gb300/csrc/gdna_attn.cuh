@@ -149,13 +149,28 @@ __device__ __forceinline__ void write_out(const AttnParams &p, int seq, int head
     store_elem(p.out, r * p.out_stride + h * p.d + c, p.out_dtype, o);
 }
 
+// The natural logarithm of a row's softmax sum; m is in units of log2.
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l == 0.f ? -__int_as_float(0x7f800000) : m * 0.69314718055994531f + logf(l);
+}
 __device__ __forceinline__ void write_lse(const AttnParams &p, int seq, int head, int row, float m, float l)
 {
     const int64_t r = (int64_t)seq * p.q_len + row / p.group;
-    // m is in units of log2
-    if (p.lse != nullptr)
-        p.lse[r * p.nq + (int64_t)head * p.group + row % p.group] =
-            l == 0.f ? -__int_as_float(0x7f800000) : m * 0.69314718055994531f + logf(l);
+    if (p.lse != nullptr) p.lse[r * p.nq + (int64_t)head * p.group + row % p.group] = lse_of(m, l);
+}
+
+// Four sums of a row with softmax sum l to outputs.
+__device__ __forceinline__ void finish4(const AttnParams &p, float4 &a, float l, float4 gate)
+{
+    const float norm = l == 0.f ? 0.f : p.v_scale / l;
+    a = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a.x * norm, a.y * norm, a.z * norm, a.w * norm);
+    if (p.gate != nullptr) {
+        a.x = a.x / (1.0f + expf(-gate.x));
+        a.y = a.y / (1.0f + expf(-gate.y));
+        a.z = a.z / (1.0f + expf(-gate.z));
+        a.w = a.w / (1.0f + expf(-gate.w));
+    }
 }
 
 // A row's sums stand for exp2(m) times them; m of a row without keys is -inf.

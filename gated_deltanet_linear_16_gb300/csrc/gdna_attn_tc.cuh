@@ -136,6 +136,79 @@ template <int CACHE, int D, int NT, int R> struct Shape {
     static constexpr int kSumPitch = D + 4;                    // floats
 };
 
+// The query rows of an item into shared memory, in 16-bit parts.  Eight elements a lane,
+// several rows in flight.  For E4M3 the elements stand in the order in which K's come:
+// a 32-bit word of four becomes two operand registers, slots 2q, 2q+1 and 8+2q, 8+2q+1 of
+// the 16 that a product contracts.
+template <int CACHE, int D, int NT, int R>
+__device__ __forceinline__ void load_queries(const AttnParams &p, int seq, int head, int row0, int q_parts, uint8_t *qs,
+                                             float *row_scale)
+{
+    using S = Shape<CACHE, D, NT, R>;
+    using O = Op<CACHE>;
+    constexpr int ROWS = S::kRows, kLanes = D / 8, kPerWarp = 32 / kLanes;       // lanes of a row, rows of a warp
+    constexpr int kPasses = (ROWS + S::kWarps * kPerWarp - 1) / (S::kWarps * kPerWarp), kGo = kPasses < 4 ? kPasses : 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group_rows = p.q_len * p.group;
+    const int at = (lane % kLanes) * 8;
+#pragma unroll 1
+    for (int pass = 0; pass < kPasses; pass += kGo) {
+        float x[kGo][8];
+#pragma unroll
+        for (int k = 0; k < kGo; ++k) {
+            const int r = ((pass + k) * S::kWarps + warp) * kPerWarp + lane / kLanes, row = row0 + r;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
+            if (r < ROWS && row < group_rows) {
+                const int token = row / p.group;
+                const int64_t from = ((int64_t)seq * p.q_len + token) * p.q_stride +
+                                     ((int64_t)head * p.group + (row - token * p.group)) * D + at;
+                const float4 a = load4(p.q, from, p.dtype, p.q_vec), b = load4(p.q, from + 4, p.dtype, p.q_vec);
+                x[k][0] = a.x; x[k][1] = a.y; x[k][2] = a.z; x[k][3] = a.w;
+                x[k][4] = b.x; x[k][5] = b.y; x[k][6] = b.z; x[k][7] = b.w;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kGo; ++k) {
+            const int r = ((pass + k) * S::kWarps + warp) * kPerWarp + lane / kLanes;
+            float back = 1.f;
+            if constexpr (CACHE != GDNA_BF16) {                // fp16: the row's largest element to 2^14 .. 2^15
+                float top = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[k][j]));
+#pragma unroll
+                for (int off = kLanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+                int e = (int)(__float_as_uint(top) >> 23) - 127;
+                e = top > 0.f && e < 128 ? max(e, -100) : 14;
+                const float up = __uint_as_float((unsigned)(127 + 14 - e) << 23);
+                back = __uint_as_float((unsigned)(127 - 14 + e) << 23);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[k][j] *= up;
+            }
+            if (r < ROWS) {
+                for (int part = 0; part < q_parts; ++part) {
+                    unsigned u[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        u[j] = O::pack(x[k][2 * j], x[k][2 * j + 1]);
+                        const float2 f = O::unpack(u[j]);
+                        x[k][2 * j] -= f.x;
+                        x[k][2 * j + 1] -= f.y;
+                    }
+                    uint8_t *to = qs + (part * ROWS + r) * S::kQPitch;
+                    if constexpr (CACHE == GDNA_E4M3) {
+                        const int slot = (at & ~15) + (at & 8) / 2;
+                        *reinterpret_cast<uint2 *>(to + slot * 2) = make_uint2(u[0], u[2]);
+                        *reinterpret_cast<uint2 *>(to + (slot + 8) * 2) = make_uint2(u[1], u[3]);
+                    } else {
+                        *reinterpret_cast<uint4 *>(to + at * 2) = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                }
+                if (at == 0) row_scale[r] = p.scale * back;
+            }
+        }
+    }
+}
+
 template <int CACHE, int D, int NT, int R>
 __global__ void __launch_bounds__(Shape<CACHE, D, NT, R>::kWarps * 32, 2)
 attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_parts)
@@ -155,6 +228,7 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
     uint8_t *qs = smem + TW * stages * S::kStage;
     float *sums = reinterpret_cast<float *>(smem);             // after the keys: [TW][ROWS][kSumPitch]
     const int group_rows = p.q_len * p.group;
+    const bool in_page = p.cache.page_size % kKeys == 0;
     const int64_t page_bytes = p.cache.page_stride * S::kElem, token_bytes = p.cache.token_stride * S::kElem;
 
     Run run = find_run(p, c, scratch);
@@ -169,31 +243,43 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
         const uint8_t *vb = static_cast<const uint8_t *>(p.v) + head * p.cache.head_stride * S::kElem;
         __syncthreads();                   // the last part's sums and queries are used up
 
-        // page of the key that this lane looks up for a step; -1: none
-        auto first_key = [&](int i) { return (int64_t)((part.u0 + i) * TW + tw) * kKeys; };
+        // Page of a step's keys, looked up a step before it is needed; -1: none.  Where pages hold a
+        // multiple of 16 keys a step lies in one page and every lane looks up the same entry; else
+        // lane j looks up key j's.
+        auto first_key = [&](int i) { return (unsigned)((part.u0 + i) * TW + tw) * kKeys; };
         auto page_of = [&](int i) {
-            const int64_t key = first_key(i) + (lane & 15);
-            return i < steps && key < part.keys ? __ldg(table + (unsigned)key / (unsigned)p.cache.page_size) : -1;
+            const unsigned key = first_key(i) + (in_page ? 0 : lane & 15);
+            return i < steps && key < (unsigned)part.keys ? __ldg(table + key / (unsigned)p.cache.page_size) : -1;
         };
         auto issue = [&](int i, int page) {
-            const unsigned key = (unsigned)first_key(i) + (lane & 15);
-            int64_t at = -1;
-            if ((unsigned)page < (unsigned)p.cache.pages)
-                at = page * page_bytes + (int64_t)(key % (unsigned)p.cache.page_size) * token_bytes;
-            uint8_t *st = ring + (i % stages) * S::kStage;
             constexpr int kPieces = S::kRowBytes / 16;         // 16-byte pieces of a row: 4 .. 32
             constexpr int kAtOnce = 32 / kPieces;              // rows of one instruction
             constexpr int kMine = kKeys / R;                   // rows this warp copies
             const int sub = lane / kPieces, piece = (lane % kPieces) * 16;
+            const unsigned key0 = first_key(i), ps = (unsigned)p.cache.page_size;
+            const bool real = (unsigned)page < (unsigned)p.cache.pages;
+            const unsigned dst0 = smem_addr(ring + (i % stages) * S::kStage + (rg * kMine + sub) * S::kPitch + piece);
+            if (kAtOnce > kMine && sub >= kMine) return;       // (no shuffle below concerns these lanes)
+            if (in_page) {
+                int64_t at = real ? page * page_bytes + (int64_t)(key0 % ps + rg * kMine + sub) * token_bytes + piece : 0;
+                const int left = real ? part.keys - (int)key0 - rg * kMine - sub : 0;
 #pragma unroll
-            for (int r = 0; r < kMine; r += kAtOnce) {
-                const int row = rg * kMine + r + sub;
-                const int64_t from = __shfl_sync(kFull, at, row & 15);
-                if (kAtOnce <= kMine || sub < kMine) {
-                    const unsigned dst = smem_addr(st + row * S::kPitch + piece);
-                    const int64_t o = from >= 0 ? from + piece : 0;
-                    cp_async16(dst, kb + o, from >= 0);
-                    cp_async16(dst + kKeys * S::kPitch, vb + o, from >= 0);
+                for (int r = 0; r < kMine; r += kAtOnce) {
+                    const bool on = r < left;
+                    cp_async16(dst0 + r * S::kPitch, kb + (on ? at : 0), on);
+                    cp_async16(dst0 + (kKeys + r) * S::kPitch, vb + (on ? at : 0), on);
+                    at += kAtOnce * token_bytes;
+                }
+            } else {
+                const unsigned mask = kAtOnce > kMine ? (1u << (kMine * kPieces % 32)) - 1 : kFull;
+                const unsigned key = key0 + (lane & 15);
+                const int64_t at = real ? page * page_bytes + (int64_t)(key % ps) * token_bytes : -1;
+#pragma unroll
+                for (int r = 0; r < kMine; r += kAtOnce) {
+                    const int64_t from = __shfl_sync(mask, at, rg * kMine + r + sub);
+                    const bool on = from >= 0;
+                    cp_async16(dst0 + r * S::kPitch, kb + (on ? from + piece : 0), on);
+                    cp_async16(dst0 + (kKeys + r) * S::kPitch, vb + (on ? from + piece : 0), on);
                 }
             }
         };
@@ -205,47 +291,7 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
             page = next;
         }
 
-        // queries: 16-bit parts in shared memory (for E4M3 in the order in which its K comes, see below)
-        for (int r = warp; r < ROWS; r += W) {
-            const int row = row0 + r;
-            float x[D / 32];
-            float top = 0.f;
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                x[j] = 0.f;
-                if (row < group_rows)
-                    x[j] = load_elem(p.q, ((int64_t)part.seq * p.q_len + row / p.group) * p.q_stride +
-                                              ((int64_t)head * p.group + row % p.group) * D + lane + 32 * j, p.dtype);
-                top = fmaxf(top, fabsf(x[j]));
-            }
-            float back = 1.f;
-            if constexpr (CACHE != GDNA_BF16) {                // largest element to 2^14 .. 2^15
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
-                int e = (int)(__float_as_uint(top) >> 23) - 127;
-                e = top > 0.f && e < 128 ? max(e, -100) : 14;
-                const float up = __uint_as_float((unsigned)(127 + 14 - e) << 23);
-                back = __uint_as_float((unsigned)(127 - 14 + e) << 23);
-#pragma unroll
-                for (int j = 0; j < D / 32; ++j) x[j] *= up;
-            }
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                int at = lane + 32 * j;
-                if constexpr (kF8) {
-                    // a 32-bit word of four E4M3 becomes two operand registers: slots 2q, 2q+1 and 8+2q, 8+2q+1
-                    const int q = (at & 15) >> 2, e = at & 3;
-                    at = (at & ~15) + (e < 2 ? 2 * q + e : 6 + 2 * q + e);
-                }
-                float rest = x[j];
-                for (int part_i = 0; part_i < q_parts; ++part_i) {
-                    const unsigned u = O::pack(rest, 0.f);
-                    *reinterpret_cast<uint16_t *>(qs + (part_i * ROWS + r) * S::kQPitch + at * 2) = (uint16_t)u;
-                    rest -= O::unpack(u).x;
-                }
-            }
-            if (lane == 0) row_scale[r] = p.scale * back;
-        }
+        load_queries<CACHE, D, NT, R>(p, part.seq, head, row0, q_parts, qs, row_scale);
         __syncthreads();
 
         // this lane's rows: rg * 8 NT + 8 t + 2 c4 + j
@@ -294,31 +340,33 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s2[h][t][j] = 0.f;
+            for (int part_i = 0; part_i < q_parts; ++part_i) {
+                const unsigned q_now = q_at + part_i * ROWS * S::kQPitch;
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-                unsigned a[2][4];
-                if constexpr (kF8) {
-                    unsigned w[4];
-                    ldsm4(w, k_at + x * 32);
+                for (int x = 0; x < D / 32; ++x) {
+                    unsigned a[2][4];
+                    if constexpr (kF8) {
+                        unsigned w[4];
+                        ldsm4(w, k_at + x * 32);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        a[h][0] = widen2((unsigned short)w[2 * h]);
-                        a[h][1] = widen2((unsigned short)w[2 * h + 1]);
-                        a[h][2] = widen2((unsigned short)(w[2 * h] >> 16));
-                        a[h][3] = widen2((unsigned short)(w[2 * h + 1] >> 16));
+                        for (int h = 0; h < 2; ++h) {
+                            a[h][0] = widen2((unsigned short)w[2 * h]);
+                            a[h][1] = widen2((unsigned short)w[2 * h + 1]);
+                            a[h][2] = widen2((unsigned short)(w[2 * h] >> 16));
+                            a[h][3] = widen2((unsigned short)(w[2 * h + 1] >> 16));
+                        }
+                    } else {
+                        ldsm4(a[0], k_at + x * 64);
+                        ldsm4(a[1], k_at + x * 64 + 32);
                     }
-                } else {
-                    ldsm4(a[0], k_at + x * 64);
-                    ldsm4(a[1], k_at + x * 64 + 32);
-                }
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    for (int part_i = 0; part_i < q_parts; ++part_i) {
+                    for (int t = 0; t < NT; ++t) {
                         unsigned b[4];
-                        ldsm4(b, q_at + (part_i * ROWS + 8 * t) * S::kQPitch + x * 64);
+                        ldsm4(b, q_now + 8 * t * S::kQPitch + x * 64);
                         O::mma(s2[0][t], a[0], b[0], b[1]);
                         O::mma(s2[1][t], a[1], b[2], b[3]);
                     }
+                }
             }
             // scores in units of log2, what a row does not see replaced
             float w[NT][4];
@@ -401,40 +449,54 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                             const float2 back = O::unpack(u);
                             r0 -= back.x;
                             r1 -= back.y;
-                            b[y][t][h] = y < 2 || w_parts > 2 ? transpose8(u) : 0u;
+                            if (y < 2 || CACHE == GDNA_BF16) b[y][t][h] = transpose8(u);
                         }
                     }
                 const unsigned v_at = kF8 ? ks + (kKeys + (lane & 15)) * S::kPitch + (lane >> 4) * 16
                                           : ks + (kKeys + (lane & 7) + (lane >> 4) * 8) * S::kPitch + ((lane >> 3) & 1) * 16;
-                if constexpr (kF8) {
+                // the 16 x 16 blocks of V^T a few at a time: hi products of all, then lo products of all
+                constexpr int kBlocks = D * NT > 256 ? 2 : 4;                  // (registers)
+                auto block4 = [&](unsigned (&a)[kBlocks][4], int x0) {
+                    if constexpr (kF8) {
 #pragma unroll
-                    for (int x = 0; x < D / 32; ++x) {
-                        unsigned u[4];
-                        ldsm4_trans(u, v_at + x * 32);
+                        for (int x = 0; x < kBlocks / 2; ++x) {
+                            unsigned u[4];
+                            ldsm4_trans(u, v_at + (x0 / 2 + x) * 32);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            // bytes of a word: keys 2c4, 2c4+1 of elements 2 l4, 2 l4 + 1
-                            const unsigned e0 = __byte_perm(u[2 * h], 0, 0x3120), e1 = __byte_perm(u[2 * h + 1], 0, 0x3120);
-                            const unsigned a[4] = {widen2((unsigned short)e0), widen2((unsigned short)(e0 >> 16)),
-                                                   widen2((unsigned short)e1), widen2((unsigned short)(e1 >> 16))};
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) {
-                                O::mma(o[2 * x + h][t], a, b[0][t][0], b[0][t][1]);
-                                O::mma(o[2 * x + h][t], a, b[1][t][0], b[1][t][1]);
+                            for (int h = 0; h < 2; ++h) {
+                                // bytes of a word: keys 2c4, 2c4+1 of elements 2 l4, 2 l4 + 1
+                                const unsigned e0 = __byte_perm(u[2 * h], 0, 0x3120), e1 = __byte_perm(u[2 * h + 1], 0, 0x3120);
+                                a[2 * x + h][0] = widen2((unsigned short)e0);
+                                a[2 * x + h][1] = widen2((unsigned short)(e0 >> 16));
+                                a[2 * x + h][2] = widen2((unsigned short)e1);
+                                a[2 * x + h][3] = widen2((unsigned short)(e1 >> 16));
                             }
                         }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < kBlocks; ++x) ldsm4_trans(a[x], v_at + (x0 + x) * 32);
                     }
-                } else {
+                };
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        unsigned a[4];
-                        ldsm4_trans(a, v_at + x * 32);
+                for (int x0 = 0; x0 < D / 16; x0 += kBlocks) {
+                    unsigned a[kBlocks][4];
+                    block4(a, x0);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            O::mma(o[x][t], a, b[0][t][0], b[0][t][1]);
-                            O::mma(o[x][t], a, b[1][t][0], b[1][t][1]);
-                            if (CACHE == GDNA_BF16 && w_parts > 2) O::mma(o[x][t], a, b[2][t][0], b[2][t][1]);
-                        }
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int x = 0; x < kBlocks; ++x)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) O::mma(o[x0 + x][t], a[x], b[y][t][0], b[y][t][1]);
+                }
+                if (CACHE == GDNA_BF16 && w_parts > 2) {
+#pragma unroll
+                    for (int x0 = 0; x0 < D / 16; x0 += kBlocks) {
+                        unsigned a[kBlocks][4];
+                        block4(a, x0);
+#pragma unroll
+                        for (int x = 0; x < kBlocks; ++x)
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) O::mma(o[x0 + x][t], a[x], b[2][t][0], b[2][t][1]);
                     }
                 }
             } else {
@@ -484,27 +546,36 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
         __syncthreads();
         const bool whole = part.begins && part.ends;
         float *to = part_of(p, 2 * c + (part.begins ? 1 : 0));
-        for (int r = warp; r < ROWS; r += W) {
-            const int row = row0 + r;
-            if (row >= group_rows) break;
-            float top = kNegInf, total = 0.f, share[TW];
+        constexpr int kQuads = D / 4, kTasks = ROWS * kQuads / (W * 32), kGo = kTasks < 4 ? kTasks : 4;
+#pragma unroll 1
+        for (int k0 = 0; k0 < kTasks; k0 += kGo) {
+            float4 gate[kGo];
+            int64_t r_at[kGo], h_at[kGo];
 #pragma unroll
-            for (int y = 0; y < TW; ++y) top = fmaxf(top, warp_m[y][r]);
-            const float mm = top;
-            if (top == kNegInf) top = 0.f;
-#pragma unroll
-            for (int y = 0; y < TW; ++y) {
-                share[y] = weight_of(warp_m[y][r], top);
-                total = fmaf(share[y], warp_l[y][r], total);
+            for (int k = 0; k < kGo; ++k) {                    // every gate in flight
+                const int task = tid + (k0 + k) * W * 32, row = row0 + task / kQuads;
+                const int token = row / p.group;
+                r_at[k] = (int64_t)part.seq * p.q_len + token;
+                h_at[k] = (int64_t)head * p.group + (row - token * p.group);
+                gate[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (whole && p.gate != nullptr && row < group_rows)
+                    gate[k] = load4(p.gate, r_at[k] * p.gate_stride + h_at[k] * p.gate_head_stride + 4 * (task % kQuads),
+                                    p.dtype, p.gate_vec);
             }
-            const float norm = total == 0.f ? 0.f : p.v_scale / total;
 #pragma unroll
-            for (int x0 = 0; x0 < D; x0 += 128) {
-                const int x = x0 + 4 * lane;
-                if (D < 128 && x >= D) break;
+            for (int k = 0; k < kGo; ++k) {
+                const int task = tid + (k0 + k) * W * 32, r = task / kQuads, x = 4 * (task % kQuads);
+                if (row0 + r >= group_rows) continue;
+                float top = kNegInf, total = 0.f, share[TW];
+#pragma unroll
+                for (int y = 0; y < TW; ++y) top = fmaxf(top, warp_m[y][r]);
+                const float mm = top;
+                if (top == kNegInf) top = 0.f;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int y = 0; y < TW; ++y) {
+                    share[y] = weight_of(warp_m[y][r], top);
+                    total = fmaf(share[y], warp_l[y][r], total);
                     const float4 v = *reinterpret_cast<const float4 *>(sums + (y * ROWS + r) * S::kSumPitch + x);
                     a.x = fmaf(share[y], v.x, a.x);
                     a.y = fmaf(share[y], v.y, a.y);
@@ -512,17 +583,13 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                     a.w = fmaf(share[y], v.w, a.w);
                 }
                 if (whole) {
-                    write_out(p, part.seq, head, row, x, total == 0.f ? 0.f : a.x * norm);
-                    write_out(p, part.seq, head, row, x + 1, total == 0.f ? 0.f : a.y * norm);
-                    write_out(p, part.seq, head, row, x + 2, total == 0.f ? 0.f : a.z * norm);
-                    write_out(p, part.seq, head, row, x + 3, total == 0.f ? 0.f : a.w * norm);
+                    finish4(p, a, total, gate[k]);
+                    store4(p.out, r_at[k] * p.out_stride + h_at[k] * D + x, p.out_dtype, p.out_vec, a);
+                    if (x == 0 && p.lse != nullptr) p.lse[r_at[k] * p.nq + h_at[k]] = lse_of(mm, total);
                 } else {
                     *reinterpret_cast<float4 *>(to + r * D + x) = a;
+                    if (x == 0) { to[ROWS * D + 2 * r] = mm; to[ROWS * D + 2 * r + 1] = total; }
                 }
-            }
-            if (lane == 0) {
-                if (whole) write_lse(p, part.seq, head, row, mm, total);
-                else { to[ROWS * D + 2 * r] = mm; to[ROWS * D + 2 * r + 1] = total; }
             }
         }
         if (part.begins && !part.ends) join = Join{part.seq, part.item, part.blocks, 0};

@@ -62,6 +62,7 @@ struct AttnParams {
     int batch, q_len, nq, nkv, group, d, max_pages;
     float scale;            // scale * k_scale * log2(e): scores in units of log2
     float v_scale;
+    int q_vec, gate_vec, out_vec;   // rows and heads start on boundaries of four elements
     // set by the launcher
     int unit;               // keys of one unit of work
     int tile_rows;          // query rows (token, head of the group) of one work item
@@ -106,6 +107,45 @@ __device__ __forceinline__ void store_elem(void *p, int64_t i, int dtype, float 
     else if (dtype == GDNA_F16) static_cast<__half *>(p)[i] = __float2half_rn(x);
     else if (dtype == GDNA_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
     else static_cast<__nv_fp8_storage_t *>(p)[i] = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Four elements that follow one another; `vec`: they start on a boundary of four.
+__device__ __forceinline__ float4 load4(const void *p, int64_t i, int dtype, bool vec)
+{
+    if (!vec)
+        return make_float4(load_elem(p, i, dtype), load_elem(p, i + 1, dtype), load_elem(p, i + 2, dtype),
+                           load_elem(p, i + 3, dtype));
+    if (dtype == GDNA_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    if (dtype == GDNA_F16) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                       __uint_as_float(u.y & 0xffff0000u));
+}
+
+__device__ __forceinline__ void store4(void *p, int64_t i, int dtype, bool vec, float4 x)
+{
+    if (!vec) {
+        store_elem(p, i, dtype, x.x);
+        store_elem(p, i + 1, dtype, x.y);
+        store_elem(p, i + 2, dtype, x.z);
+        store_elem(p, i + 3, dtype, x.w);
+    } else if (dtype == GDNA_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = x;
+    } else {
+        uint2 u;
+        if (dtype == GDNA_F16) {
+            const __half2 a = __floats2half2_rn(x.x, x.y), b = __floats2half2_rn(x.z, x.w);
+            u = make_uint2(*reinterpret_cast<const unsigned *>(&a), *reinterpret_cast<const unsigned *>(&b));
+        } else {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+            u = make_uint2(*reinterpret_cast<const unsigned *>(&a), *reinterpret_cast<const unsigned *>(&b));
+        }
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) = u;
+    }
 }
 
 }  // namespace gdna
