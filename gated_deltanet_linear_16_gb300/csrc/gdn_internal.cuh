@@ -158,11 +158,11 @@ inline bool early_grid(unsigned grid, int ctas_per_sm)
 // Launch kern with programmatic stream serialisation when `early`, else as a
 // plain launch.  `early` only for a kernel instantiated with early_start<true>.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_early(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+cudaError_t launch_early(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t smem, cudaStream_t s,
                          bool early, Args &&...args)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(block, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;

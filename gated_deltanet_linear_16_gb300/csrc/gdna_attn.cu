@@ -150,6 +150,7 @@ attn_join(const AttnParams p)
     __shared__ float red[kJoinThreads / 32];
     __shared__ float sums[kJoinThreads * 4];
     const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    gdn::early_start<true>(nullptr, 0);
     const Join join = joins_of(p)[c];
     if (join.parts == 0) return;
     const int head = join.item / p.row_tiles, row = (join.item % p.row_tiles) * p.tile_rows + r;
@@ -216,8 +217,8 @@ int64_t attn_workspace_bytes(int64_t rows, int d)
 
 cudaError_t launch_join(const AttnParams &p, cudaStream_t s)
 {
-    attn_join<<<dim3(p.grid, p.tile_rows), kJoinThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    const int rows = p.q_len * p.group < p.tile_rows ? p.q_len * p.group : p.tile_rows;
+    return gdn::launch_early(attn_join, dim3(p.grid, rows), kJoinThreads, 0, s, true, p);
 }
 
 cudaError_t launch_attn_decode(const AttnParams &params, bool fast, cudaStream_t s)

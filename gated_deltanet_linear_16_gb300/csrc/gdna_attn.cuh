@@ -49,7 +49,13 @@ __device__ __forceinline__ int keys_of(const AttnParams &p, int b)
 }
 __device__ __forceinline__ int64_t units_of(const AttnParams &p, int keys)
 {
-    return keys > 0 ? ((int64_t)keys + p.unit - 1) / p.unit : 1;
+    return keys > 0 ? ((unsigned)keys + (unsigned)p.unit - 1) / (unsigned)p.unit : 1;
+}
+
+// a / b, in 32 bits where both fit (64-bit division is some hundred instructions).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b)
+{
+    return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((unsigned)a / (unsigned)b) : a / b;
 }
 
 // A block's run of units, in the row of all units.
@@ -83,7 +89,7 @@ __device__ __forceinline__ Run find_run(const AttnParams &p, int c, int64_t *scr
     }
     Run r;
     total *= items;
-    r.share = (total + p.grid - 1) / p.grid;
+    r.share = divide(total + p.grid - 1, p.grid);
     r.at = c * r.share;
     r.end = min(r.at + r.share, total);
     // the thread whose sequences hold unit `at` walks them
@@ -120,12 +126,12 @@ __device__ __forceinline__ Part next_part(const AttnParams &p, Run &r, int c)
     t.seq = r.seq;
     t.keys = keys_of(p, r.seq);
     const int64_t n = units_of(p, t.keys), off = r.at - r.base;
-    t.item = (int)(off / n);
+    t.item = (int)divide(off, n);
     t.u0 = off - t.item * n;
     t.u1 = min(n, t.u0 + (r.end - r.at));
     t.begins = t.u0 == 0;
     t.ends = t.u1 == n;
-    t.blocks = t.begins && !t.ends ? (int)((r.base + (t.item + 1) * n - 1) / r.share) - c + 1 : 0;
+    t.blocks = t.begins && !t.ends ? (int)divide(r.base + (t.item + 1) * n - 1, r.share) - c + 1 : 0;
     r.at += t.u1 - t.u0;
     if (t.ends && t.item == items - 1) { r.base += n * items; ++r.seq; }
     return t;
@@ -174,7 +180,13 @@ __device__ __forceinline__ void finish4(const AttnParams &p, float4 &a, float l,
 }
 
 // A row's sums stand for exp2(m) times them; m of a row without keys is -inf.
-__device__ __forceinline__ float weight_of(float m, float top) { return m == -__int_as_float(0x7f800000) ? 0.f : exp2f(m - top); }
+__device__ __forceinline__ float ex2(float x)              // 2^x, relative error below 2^-22
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float weight_of(float m, float top) { return m == -__int_as_float(0x7f800000) ? 0.f : ex2(m - top); }
 
 // Adds up the items that lie in several blocks, after the kernel that left them.
 cudaError_t launch_join(const AttnParams &p, cudaStream_t s);

@@ -11,16 +11,17 @@
 //
 // so a row tile of 8 costs what it holds.  A warp takes 16 keys at a time with a
 // running maximum m and sum l for each row: S^T's columns are rows, so the maximum
-// over keys is three shuffles, and the rescale of O^T is by its own columns.  P^T
+// over keys is three shuffles for each row, and the rescale of O^T is by its own columns.  P^T
 // needs the transpose of what the first product leaves; an 8 x 8 register transpose
 // (movmatrix) does it, nothing passes through shared memory.
 //
 // Rounding.  K and V are exact in the products (E4M3 widens to fp16 exactly).  The
 // queries enter in as many 16-bit parts as their type needs (`q_parts`: x = hi + lo
 // [+ lower]), scaled by a power of two per row for fp16 products, so that no query
-// over- or underflows.  The weights exp2(s - m) <= 1 enter in two parts (hi + lo),
-// three where bf16 products give an fp32 output: with one part of bf16 the weights'
-// rounding (2^-9) would be as large as that of a bf16 output.  m, l, S and O are fp32.
+// over- or underflows.  The weights exp2(s - m) <= 1 enter in as many parts as put
+// their rounding well below the output's (`w_parts`): bf16 products take two (one part's 2^-9
+// would be as large as a bf16 output's own), three for an fp32 output; fp16 products one
+// (2^-12), two for fp16 and fp32 outputs.  m, l, S and O are fp32.
 //
 // What a row does not see.  Masked scores are replaced, not added to.  Keys past the
 // sequence's end are not loaded (zeros stand for them).  The keys that some tokens see
@@ -40,7 +41,7 @@
 namespace gdna {
 namespace tc {
 
-constexpr int kKeys = 16;                  // keys of a step
+constexpr int kKeys = 16;                  // keys of a block: one side of a product
 constexpr int kMaxStages = 8;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -62,6 +63,11 @@ __device__ __forceinline__ unsigned transpose8(unsigned x)
     unsigned y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+__device__ __forceinline__ void lds16(unsigned (&r)[4], unsigned addr)
+{
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void cp_async16(unsigned dst, const void *src, bool real)
 {
@@ -128,7 +134,11 @@ template <int CACHE, int D, int NT, int R> struct Shape {
     static constexpr int kElem = CACHE == GDNA_E4M3 ? 1 : 2;
     static constexpr int kRowBytes = D * kElem;
     static constexpr int kPitch = kRowBytes + 16;
-    static constexpr int kStage = 2 * kKeys * kPitch;          // K, then V
+    // Blocks of 16 keys a step.  Short rows take two: the maximum's shuffles, the barrier and the
+    // addresses are then paid once for 32 keys.
+    static constexpr int kBlocks = kRowBytes <= 128 ? 2 : 1;
+    static constexpr int kStep = kKeys * kBlocks;
+    static constexpr int kStage = 2 * kStep * kPitch;          // K, then V
     static constexpr int kWarps = (kRowBytes == 512 && R == 1) ? 2 : 4;
     static constexpr int kKeyWarps = kWarps / R;
     static constexpr int kRows = 8 * NT * R;
@@ -216,7 +226,9 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
     using S = Shape<CACHE, D, NT, R>;
     using O = Op<CACHE>;
     constexpr bool kF8 = CACHE == GDNA_E4M3;
-    constexpr int W = S::kWarps, TW = S::kKeyWarps, ROWS = S::kRows;
+    constexpr int W = S::kWarps, TW = S::kKeyWarps, ROWS = S::kRows, KB = S::kBlocks;
+    // weight parts of the products proper; more follow in passes of their own
+    constexpr int kParts = kF8 ? 1 : 2;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t scratch[W + 2];
     __shared__ float row_scale[ROWS], warp_m[TW][ROWS], warp_l[TW][ROWS];
@@ -224,13 +236,15 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
     const int tw = warp / R, rg = warp % R;                    // the keys it takes, the rows it takes
     const int l4 = lane >> 2, c4 = lane & 3;
-    uint8_t *ring = smem + tw * stages * S::kStage;
+    const unsigned ring = smem_addr(smem) + tw * stages * S::kStage, ring_end = ring + stages * S::kStage;
     uint8_t *qs = smem + TW * stages * S::kStage;
     float *sums = reinterpret_cast<float *>(smem);             // after the keys: [TW][ROWS][kSumPitch]
     const int group_rows = p.q_len * p.group;
-    const bool in_page = p.cache.page_size % kKeys == 0;
+    const unsigned page_size = (unsigned)p.cache.page_size;
+    const bool in_page = page_size % kKeys == 0;               // a block of keys lies in one page
     const int64_t page_bytes = p.cache.page_stride * S::kElem, token_bytes = p.cache.token_stride * S::kElem;
 
+    gdn::early_start<true>(nullptr, 0);
     Run run = find_run(p, c, scratch);
     Join join = {0, 0, 0, 0};
 
@@ -238,59 +252,69 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
         const Part part = next_part(p, run, c);
         const int head = part.item / p.row_tiles, row0 = (part.item % p.row_tiles) * ROWS;
         const int steps = (int)(part.u1 - part.u0);
+        const unsigned keys = (unsigned)part.keys;
         const int32_t *table = p.table + part.seq * p.table_stride;
         const uint8_t *kb = static_cast<const uint8_t *>(p.k) + head * p.cache.head_stride * S::kElem;
         const uint8_t *vb = static_cast<const uint8_t *>(p.v) + head * p.cache.head_stride * S::kElem;
         __syncthreads();                   // the last part's sums and queries are used up
 
-        // Page of a step's keys, looked up a step before it is needed; -1: none.  Where pages hold a
-        // multiple of 16 keys a step lies in one page and every lane looks up the same entry; else
-        // lane j looks up key j's.
-        auto first_key = [&](int i) { return (unsigned)((part.u0 + i) * TW + tw) * kKeys; };
-        auto page_of = [&](int i) {
-            const unsigned key = first_key(i) + (in_page ? 0 : lane & 15);
-            return i < steps && key < (unsigned)part.keys ? __ldg(table + key / (unsigned)p.cache.page_size) : -1;
+        // Lane j looks up the page of key j of a step, a step before it is needed; -1: none.
+        const unsigned start = (unsigned)(part.u0 * TW + tw) * S::kStep;       // this warp's first key
+        unsigned look = start + lane % S::kStep;                               // the key to look up next
+        int ahead = 0;                                                         // its step
+        auto next_page = [&]() {
+            const int page = ahead < steps && look < keys ? __ldg(table + p.page_div.quotient(look)) : -1;
+            ++ahead;
+            look += TW * S::kStep;
+            return page;
         };
-        auto issue = [&](int i, int page) {
+        unsigned fill = start, fill_at = ring;                                 // the next step to copy: key, stage
+        auto issue = [&](int page) {
             constexpr int kPieces = S::kRowBytes / 16;         // 16-byte pieces of a row: 4 .. 32
             constexpr int kAtOnce = 32 / kPieces;              // rows of one instruction
-            constexpr int kMine = kKeys / R;                   // rows this warp copies
+            constexpr int kMine = S::kStep / R;                // rows this warp copies
+            static_assert(kAtOnce <= kMine && (kMine % kKeys == 0 || kKeys % kMine == 0), "whole instructions");
             const int sub = lane / kPieces, piece = (lane % kPieces) * 16;
-            const unsigned key0 = first_key(i), ps = (unsigned)p.cache.page_size;
-            const bool real = (unsigned)page < (unsigned)p.cache.pages;
-            const unsigned dst0 = smem_addr(ring + (i % stages) * S::kStage + (rg * kMine + sub) * S::kPitch + piece);
-            if (kAtOnce > kMine && sub >= kMine) return;       // (no shuffle below concerns these lanes)
+            const unsigned dst = fill_at + (rg * kMine + sub) * S::kPitch + piece;
+            const unsigned mine = fill + lane % S::kStep;
+            const unsigned place = mine - p.page_div.quotient(mine) * page_size;          // in its page
+            const int64_t at = (unsigned)page < (unsigned)p.cache.pages
+                                   ? page * page_bytes + (int64_t)place * token_bytes : -1;
             if (in_page) {
-                int64_t at = real ? page * page_bytes + (int64_t)(key0 % ps + rg * kMine + sub) * token_bytes + piece : 0;
-                const int left = real ? part.keys - (int)key0 - rg * kMine - sub : 0;
 #pragma unroll
-                for (int r = 0; r < kMine; r += kAtOnce) {
-                    const bool on = r < left;
-                    cp_async16(dst0 + r * S::kPitch, kb + (on ? at : 0), on);
-                    cp_async16(dst0 + (kKeys + r) * S::kPitch, vb + (on ? at : 0), on);
-                    at += kAtOnce * token_bytes;
+                for (int r0 = 0; r0 < kMine; r0 += kKeys) {    // a block: one address, then equal steps
+                    const int first = (rg * kMine + r0) / kKeys * kKeys, off = (rg * kMine + r0) % kKeys + sub;
+                    const int64_t block = __shfl_sync(kFull, at, first);
+                    int64_t from = block + off * token_bytes + piece;
+                    const int left = block >= 0 ? (int)(keys - fill) - first - off : 0;
+#pragma unroll
+                    for (int r = 0; r < kKeys && r < kMine; r += kAtOnce) {
+                        const bool on = r < left;
+                        cp_async16(dst + (r0 + r) * S::kPitch, kb + (on ? from : 0), on);
+                        cp_async16(dst + (S::kStep + r0 + r) * S::kPitch, vb + (on ? from : 0), on);
+                        from += kAtOnce * token_bytes;
+                    }
                 }
             } else {
-                const unsigned mask = kAtOnce > kMine ? (1u << (kMine * kPieces % 32)) - 1 : kFull;
-                const unsigned key = key0 + (lane & 15);
-                const int64_t at = real ? page * page_bytes + (int64_t)(key % ps) * token_bytes : -1;
 #pragma unroll
                 for (int r = 0; r < kMine; r += kAtOnce) {
-                    const int64_t from = __shfl_sync(mask, at, rg * kMine + r + sub);
+                    const int64_t from = __shfl_sync(kFull, at, rg * kMine + r + sub);
                     const bool on = from >= 0;
-                    cp_async16(dst0 + r * S::kPitch, kb + (on ? from + piece : 0), on);
-                    cp_async16(dst0 + (kKeys + r) * S::kPitch, vb + (on ? from + piece : 0), on);
+                    cp_async16(dst + r * S::kPitch, kb + (on ? from + piece : 0), on);
+                    cp_async16(dst + (S::kStep + r) * S::kPitch, vb + (on ? from + piece : 0), on);
                 }
             }
+            fill += TW * S::kStep;
+            fill_at += S::kStage;
+            if (fill_at == ring_end) fill_at = ring;
         };
-        int page = page_of(0);
+        int page = next_page();
         for (int i = 0; i < stages - 1; ++i) {
-            const int next = page_of(i + 1);
-            if (i < steps) issue(i, page);
+            const int next = next_page();
+            if (i < steps) issue(page);
             gdn::cp_async_commit();
             page = next;
         }
-
         load_queries<CACHE, D, NT, R>(p, part.seq, head, row0, q_parts, qs, row_scale);
         __syncthreads();
 
@@ -316,212 +340,249 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
         const int all_see = part.keys - (p.q_len - 1);         // keys that every row sees
         const unsigned q_at = smem_addr(qs + (rg * 8 * NT + (lane & 7)) * S::kQPitch + (lane >> 3) * 16);
 
+        unsigned ks = ring;                                    // the step's stage
+        int key0 = (int)start;
+#pragma unroll 1
         for (int i = 0; i < steps; ++i) {
             wait_stage(stages);
             if constexpr (R == 1) __syncwarp();
             else asm volatile("bar.sync %0, %1;" ::"r"(1 + tw), "n"(32 * R) : "memory");
             // the stage that was used up a step ago takes the keys of stages - 1 steps ahead
             {
-                const int ahead = i + stages - 1, next = page_of(ahead + 1);
-                if (ahead < steps) issue(ahead, page);
+                const int next = next_page();
+                if (i + stages - 1 < steps) issue(page);
                 gdn::cp_async_commit();
                 page = next;
             }
-            const int key0 = (int)first_key(i);
-            if (key0 >= part.keys) continue;
-            const unsigned ks = smem_addr(ring + (i % stages) * S::kStage);
-            const unsigned k_at = ks + (lane & 15) * S::kPitch + (lane >> 4) * 16;
+            if (key0 < part.keys) {
+                const unsigned k_at = ks + (lane & 15) * S::kPitch + (lane >> 4) * 16;
 
-            // S^T: two chains of products a row tile
-            float s2[2][NT][4];
+                // S^T: two chains of products a row tile and block
+                float s2[KB][2][NT][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                for (int y = 0; y < KB; ++y)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) s2[h][t][j] = 0.f;
-            for (int part_i = 0; part_i < q_parts; ++part_i) {
-                const unsigned q_now = q_at + part_i * ROWS * S::kQPitch;
+                        for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int x = 0; x < D / 32; ++x) {
-                    unsigned a[2][4];
-                    if constexpr (kF8) {
-                        unsigned w[4];
-                        ldsm4(w, k_at + x * 32);
+                            for (int j = 0; j < 4; ++j) s2[y][h][t][j] = 0.f;
+#pragma unroll 1
+                for (int part_i = 0; part_i < q_parts; ++part_i) {
+                    const unsigned q_now = q_at + part_i * ROWS * S::kQPitch;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            a[h][0] = widen2((unsigned short)w[2 * h]);
-                            a[h][1] = widen2((unsigned short)w[2 * h + 1]);
-                            a[h][2] = widen2((unsigned short)(w[2 * h] >> 16));
-                            a[h][3] = widen2((unsigned short)(w[2 * h + 1] >> 16));
-                        }
-                    } else {
-                        ldsm4(a[0], k_at + x * 64);
-                        ldsm4(a[1], k_at + x * 64 + 32);
-                    }
+                    for (int x = 0; x < D / 32; ++x) {
+                        unsigned b[NT][4];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        unsigned b[4];
-                        ldsm4(b, q_now + 8 * t * S::kQPitch + x * 64);
-                        O::mma(s2[0][t], a[0], b[0], b[1]);
-                        O::mma(s2[1][t], a[1], b[2], b[3]);
-                    }
-                }
-            }
-            // scores in units of log2, what a row does not see replaced
-            float w[NT][4];
+                        for (int t = 0; t < NT; ++t) ldsm4(b[t], q_now + 8 * t * S::kQPitch + x * 64);
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+                        for (int y = 0; y < KB; ++y) {
+                            unsigned a[2][4];
+                            if constexpr (kF8) {
+                                unsigned w[4];
+                                ldsm4(w, k_at + y * kKeys * S::kPitch + x * 32);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[t][j] = (s2[0][t][j] + s2[1][t][j]) * rs[t][j & 1];
-            const bool edge = key0 + kKeys > all_see;
-            if (edge) {
+                                for (int h = 0; h < 2; ++h) {
+                                    a[h][0] = widen2((unsigned short)w[2 * h]);
+                                    a[h][1] = widen2((unsigned short)w[2 * h + 1]);
+                                    a[h][2] = widen2((unsigned short)(w[2 * h] >> 16));
+                                    a[h][3] = widen2((unsigned short)(w[2 * h + 1] >> 16));
+                                }
+                            } else {
+                                ldsm4(a[0], k_at + y * kKeys * S::kPitch + x * 64);
+                                ldsm4(a[1], k_at + y * kKeys * S::kPitch + x * 64 + 32);
+                            }
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (key0 + l4 + (j >> 1) * 8 >= seen[t][j & 1]) w[t][j] = kNegInf;
-            }
-            bool moved = false;
-            float down[NT][2], from[NT][2];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float top = fmaxf(w[t][j], w[t][j + 2]);
-                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
-                    top = fmaxf(top, m[t][j]);
-                    moved |= top != m[t][j];
-                    from[t][j] = top == kNegInf ? 0.f : top;
-                    down[t][j] = weight_of(m[t][j], from[t][j]);
-                    m[t][j] = top;
-                }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[t][j] = exp2f(w[t][j] - from[t][j & 1]);
-            if (__any_sync(kFull, moved)) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    l[t][0] *= down[t][0];
-                    l[t][1] *= down[t][1];
-#pragma unroll
-                    for (int x = 0; x < D / 16; ++x)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) o[x][t][j] *= down[t][j & 1];
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                l[t][0] += w[t][0] + w[t][2];
-                l[t][1] += w[t][1] + w[t][3];
-            }
-
-            const uint8_t *vs = ring + (i % stages) * S::kStage + kKeys * S::kPitch;
-            bool plain = true;
-            if (edge && p.q_len > 1) {     // keys that some rows do not see: is every value finite?
-                bool odd = false;
-                for (int x = lane; x < kKeys * (S::kRowBytes / 16); x += 32) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(vs + x / (S::kRowBytes / 16) * S::kPitch +
-                                                                     x % (S::kRowBytes / 16) * 16);
-                    const unsigned words[4] = {u.x, u.y, u.z, u.w};
-                    // each element's all-ones exponent (E4M3: its one NaN pattern); a carry would pass a clear top bit
-                    constexpr unsigned kMask = kF8 ? 0x7f7f7f7fu : CACHE == GDNA_F16 ? 0x7c007c00u : 0x7f807f80u;
-                    constexpr unsigned kOne = kF8 ? 0x01010101u : CACHE == GDNA_F16 ? 0x04000400u : 0x00800080u;
-                    constexpr unsigned kTop = kF8 ? 0x80808080u : 0x80008000u;
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) odd |= (((words[y] & kMask) + kOne) & kTop) != 0;
-                }
-                plain = !__any_sync(kFull, odd);
-            }
-            if (plain) {
-                unsigned b[3][NT][2];      // P^T in parts
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float r0 = w[t][2 * h], r1 = w[t][2 * h + 1];
-#pragma unroll
-                        for (int y = 0; y < 3; ++y) {
-                            const unsigned u = O::pack(r0, r1);
-                            const float2 back = O::unpack(u);
-                            r0 -= back.x;
-                            r1 -= back.y;
-                            if (y < 2 || CACHE == GDNA_BF16) b[y][t][h] = transpose8(u);
-                        }
-                    }
-                const unsigned v_at = kF8 ? ks + (kKeys + (lane & 15)) * S::kPitch + (lane >> 4) * 16
-                                          : ks + (kKeys + (lane & 7) + (lane >> 4) * 8) * S::kPitch + ((lane >> 3) & 1) * 16;
-                // the 16 x 16 blocks of V^T a few at a time: hi products of all, then lo products of all
-                constexpr int kBlocks = D * NT > 256 ? 2 : 4;                  // (registers)
-                auto block4 = [&](unsigned (&a)[kBlocks][4], int x0) {
-                    if constexpr (kF8) {
-#pragma unroll
-                        for (int x = 0; x < kBlocks / 2; ++x) {
-                            unsigned u[4];
-                            ldsm4_trans(u, v_at + (x0 / 2 + x) * 32);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                // bytes of a word: keys 2c4, 2c4+1 of elements 2 l4, 2 l4 + 1
-                                const unsigned e0 = __byte_perm(u[2 * h], 0, 0x3120), e1 = __byte_perm(u[2 * h + 1], 0, 0x3120);
-                                a[2 * x + h][0] = widen2((unsigned short)e0);
-                                a[2 * x + h][1] = widen2((unsigned short)(e0 >> 16));
-                                a[2 * x + h][2] = widen2((unsigned short)e1);
-                                a[2 * x + h][3] = widen2((unsigned short)(e1 >> 16));
+                            for (int t = 0; t < NT; ++t) {
+                                O::mma(s2[y][0][t], a[0], b[t][0], b[t][1]);
+                                O::mma(s2[y][1][t], a[1], b[t][2], b[t][3]);
                             }
                         }
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < kBlocks; ++x) ldsm4_trans(a[x], v_at + (x0 + x) * 32);
-                    }
-                };
-#pragma unroll
-                for (int x0 = 0; x0 < D / 16; x0 += kBlocks) {
-                    unsigned a[kBlocks][4];
-                    block4(a, x0);
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-#pragma unroll
-                        for (int x = 0; x < kBlocks; ++x)
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) O::mma(o[x0 + x][t], a[x], b[y][t][0], b[y][t][1]);
-                }
-                if (CACHE == GDNA_BF16 && w_parts > 2) {
-#pragma unroll
-                    for (int x0 = 0; x0 < D / 16; x0 += kBlocks) {
-                        unsigned a[kBlocks][4];
-                        block4(a, x0);
-#pragma unroll
-                        for (int x = 0; x < kBlocks; ++x)
-#pragma unroll
-                            for (int t = 0; t < NT; ++t) O::mma(o[x0 + x][t], a[x], b[2][t][0], b[2][t][1]);
                     }
                 }
-            } else {
-#pragma unroll 1
-                for (int k = 0; k < kKeys; ++k) {
-                    float wk[NT][2];
+                // scores in units of log2, what a row does not see replaced
+                float w[KB][NT][4];
+#pragma unroll
+                for (int y = 0; y < KB; ++y)
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            wk[t][j] = __shfl_sync(kFull, k < 8 ? w[t][j] : w[t][j + 2], (k & 7) * 4 + c4);
+                        for (int j = 0; j < 4; ++j) w[y][t][j] = (s2[y][0][t][j] + s2[y][1][t][j]) * rs[t][j & 1];
+                const bool edge = key0 + S::kStep > all_see;
+                if (edge) {
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x)
+                    for (int y = 0; y < KB; ++y)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int e = 16 * x + (kF8 ? 2 * l4 + h : l4 + 8 * h);
-                            const float v = load_elem(vs + k * S::kPitch, e, CACHE);
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (key0 + y * kKeys + l4 + (j >> 1) * 8 >= seen[t][j & 1]) w[y][t][j] = kNegInf;
+                }
+                bool moved = false;
+                float top[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float x = fmaxf(w[0][t][j], w[0][t][j + 2]);
+#pragma unroll
+                        for (int y = 1; y < KB; ++y) x = fmaxf(x, fmaxf(w[y][t][j], w[y][t][j + 2]));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+                        top[t][j] = fmaxf(x, m[t][j]);
+                        moved |= top[t][j] != m[t][j];
+                    }
+                if (__any_sync(kFull, moved)) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        float down[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            down[j] = weight_of(m[t][j], top[t][j]);
+                            m[t][j] = top[t][j];
+                            l[t][j] *= down[j];
+                        }
+#pragma unroll
+                        for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[x][t][j] *= down[j & 1];
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float from = m[t][j] == kNegInf ? 0.f : m[t][j];
+#pragma unroll
+                        for (int y = 0; y < KB; ++y) {
+                            w[y][t][j] = ex2(w[y][t][j] - from);
+                            w[y][t][j + 2] = ex2(w[y][t][j + 2] - from);
+                            l[t][j] += w[y][t][j] + w[y][t][j + 2];
+                        }
+                    }
+
+                bool plain = true;
+                if (edge && p.q_len > 1) { // keys that some rows do not see: is every value finite?
+                    constexpr int kPieces = S::kRowBytes / 16;
+                    bool odd = false;
+                    for (int x = lane; x < S::kStep * kPieces; x += 32) {
+                        unsigned words[4];
+                        lds16(words, ks + (S::kStep + x / kPieces) * S::kPitch + x % kPieces * 16);
+                        // an element's all-ones exponent (E4M3: its one NaN) carries into its clear top bit
+                        constexpr unsigned kMask = kF8 ? 0x7f7f7f7fu : CACHE == GDNA_F16 ? 0x7c007c00u : 0x7f807f80u;
+                        constexpr unsigned kOne = kF8 ? 0x01010101u : CACHE == GDNA_F16 ? 0x04000400u : 0x00800080u;
+                        constexpr unsigned kTop = kF8 ? 0x80808080u : 0x80008000u;
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) odd |= (((words[y] & kMask) + kOne) & kTop) != 0;
+                    }
+                    plain = !__any_sync(kFull, odd);
+                }
+                if (plain) {
+#pragma unroll
+                    for (int y = 0; y < KB; ++y) {
+                        const unsigned vs = ks + (S::kStep + y * kKeys) * S::kPitch;
+                        const unsigned v_at = kF8 ? vs + (lane & 15) * S::kPitch + (lane >> 4) * 16
+                                                  : vs + ((lane & 7) + (lane >> 4) * 8) * S::kPitch + ((lane >> 3) & 1) * 16;
+                        float rest[NT][4];
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) rest[t][j] = w[y][t][j];
+                        auto next_part_of_weights = [&](unsigned (&b)[NT][2]) {
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const unsigned u = O::pack(rest[t][2 * h], rest[t][2 * h + 1]);
+                                    const float2 f = O::unpack(u);
+                                    rest[t][2 * h] -= f.x;
+                                    rest[t][2 * h + 1] -= f.y;
+                                    b[t][h] = transpose8(u);
+                                }
+                        };
+                        unsigned b[kParts][NT][2];
+#pragma unroll
+                        for (int z = 0; z < kParts; ++z) next_part_of_weights(b[z]);
+                        // the 16 x 16 blocks of V^T a few at a time: the first part's products of all, then the next's
+                        constexpr int kGo = D * NT > 256 ? 2 : 4;              // (registers)
+                        auto values = [&](unsigned (&a)[kGo][4], int x0) {
+                            if constexpr (kF8) {
+#pragma unroll
+                                for (int x = 0; x < kGo / 2; ++x) {
+                                    unsigned u[4];
+                                    ldsm4_trans(u, v_at + (x0 / 2 + x) * 32);
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        // bytes of a word: keys 2c4, 2c4+1 of elements 2 l4, 2 l4 + 1
+                                        const unsigned e0 = __byte_perm(u[2 * h], 0, 0x3120), e1 = __byte_perm(u[2 * h + 1], 0, 0x3120);
+                                        a[2 * x + h][0] = widen2((unsigned short)e0);
+                                        a[2 * x + h][1] = widen2((unsigned short)(e0 >> 16));
+                                        a[2 * x + h][2] = widen2((unsigned short)e1);
+                                        a[2 * x + h][3] = widen2((unsigned short)(e1 >> 16));
+                                    }
+                                }
+                            } else {
+#pragma unroll
+                                for (int x = 0; x < kGo; ++x) ldsm4_trans(a[x], v_at + (x0 + x) * 32);
+                            }
+                        };
+#pragma unroll
+                        for (int x0 = 0; x0 < D / 16; x0 += kGo) {
+                            unsigned a[kGo][4];
+                            values(a, x0);
+#pragma unroll
+                            for (int z = 0; z < kParts; ++z)
+#pragma unroll
+                                for (int x = 0; x < kGo; ++x)
+#pragma unroll
+                                    for (int t = 0; t < NT; ++t) O::mma(o[x0 + x][t], a[x], b[z][t][0], b[z][t][1]);
+                        }
+#pragma unroll 1
+                        for (int z = kParts; z < w_parts; ++z) {
+                            next_part_of_weights(b[0]);
+#pragma unroll
+                            for (int x0 = 0; x0 < D / 16; x0 += kGo) {
+                                unsigned a[kGo][4];
+                                values(a, x0);
+#pragma unroll
+                                for (int x = 0; x < kGo; ++x)
+#pragma unroll
+                                    for (int t = 0; t < NT; ++t) O::mma(o[x0 + x][t], a[x], b[0][t][0], b[0][t][1]);
+                            }
+                        }
+                    }
+                } else {
+                    const uint8_t *vs = smem + (ks - smem_addr(smem)) + S::kStep * S::kPitch;
+#pragma unroll
+                    for (int y = 0; y < KB; ++y)
+#pragma unroll 1
+                        for (int k = 0; k < kKeys; ++k) {
+                            float wk[NT][2];
 #pragma unroll
                             for (int t = 0; t < NT; ++t)
 #pragma unroll
                                 for (int j = 0; j < 2; ++j)
-                                    if (key0 + k < seen[t][j]) o[x][t][2 * h + j] = fmaf(wk[t][j], v, o[x][t][2 * h + j]);
+                                    wk[t][j] = __shfl_sync(kFull, k < 8 ? w[y][t][j] : w[y][t][j + 2], (k & 7) * 4 + c4);
+#pragma unroll
+                            for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int e = 16 * x + (kF8 ? 2 * l4 + h : l4 + 8 * h);
+                                    const float v = load_elem(vs + (y * kKeys + k) * S::kPitch, e, CACHE);
+#pragma unroll
+                                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                        for (int j = 0; j < 2; ++j)
+                                            if (key0 + y * kKeys + k < seen[t][j])
+                                                o[x][t][2 * h + j] = fmaf(wk[t][j], v, o[x][t][2 * h + j]);
+                                }
                         }
                 }
             }
+            key0 += TW * S::kStep;
+            ks += S::kStage;
+            if (ks == ring_end) ks = ring;
         }
 
         // join the key warps' rows in shared memory, over the ring
@@ -607,7 +668,8 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
     const bool bf16 = CACHE == GDNA_BF16;
     // 16-bit parts that hold a query of its type: bf16 products have 8 bits a part, fp16 products 11
     const int q_parts = p.dtype == GDNA_BF16 ? 1 : p.dtype == GDNA_F16 ? (bf16 ? 2 : 1) : (bf16 ? 3 : 2);
-    const int w_parts = bf16 && p.out_dtype == GDNA_F32 ? 3 : 2;
+    // and weights: to well below the output's rounding
+    const int w_parts = (bf16 ? 2 : 1) + (p.out_dtype == GDNA_F32 || (CACHE != GDNA_BF16 && p.out_dtype == GDNA_F16));
     const int q_bytes = q_parts * S::kRows * S::kQPitch;
     const int least = (S::kRows * S::kSumPitch * 4 + S::kStage - 1) / S::kStage;     // the sums lie over the ring
     int stages = (kTwoPerSm - q_bytes) / (S::kKeyWarps * S::kStage);
@@ -618,15 +680,15 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
                   "three stages, and room for the sums, whatever the queries' type");
     static_assert(kMaxStages * S::kStage >= S::kRows * S::kSumPitch * 4, "the sums lie over the ring");
     const int bytes = S::kKeyWarps * stages * S::kStage + q_bytes;
-    p.unit = kKeys * S::kKeyWarps;
+    p.unit = S::kStep * S::kKeyWarps;
+    p.page_div = Divisor::of((unsigned)p.cache.page_size);
     p.tile_rows = S::kRows;
     p.row_tiles = (int)(((int64_t)p.q_len * p.group + S::kRows - 1) / S::kRows);
     const int grid = gdn::sm_count() * (bytes <= kTwoPerSm ? 2 : 1);
     p.grid = grid < kMaxGrid ? grid : kMaxGrid;
     cudaError_t e = gdn::allow_dynamic_smem<&attn_tc<CACHE, D, NT, R>>(kOnePerSm);
     if (e != cudaSuccess) return e;
-    attn_tc<CACHE, D, NT, R><<<p.grid, S::kWarps * 32, bytes, s>>>(p, stages, q_parts, w_parts);
-    e = cudaGetLastError();
+    e = gdn::launch_early(attn_tc<CACHE, D, NT, R>, (unsigned)p.grid, S::kWarps * 32, bytes, s, true, p, stages, q_parts, w_parts);
     return e != cudaSuccess ? e : launch_join(p, s);
 }
 
@@ -635,7 +697,7 @@ cudaError_t by_rows(const AttnParams &p, cudaStream_t s)
 {
     const int64_t rows = (int64_t)p.q_len * p.group;
     if (rows <= 8) return launch<CACHE, D, 1, 1>(p, s);
-    if (rows <= 16) return launch<CACHE, D, 2, 1>(p, s);
+    if (rows <= 16) return launch<CACHE, D, 1, 2>(p, s);
     if (rows <= 32) return launch<CACHE, D, 2, 2>(p, s);
     return launch<CACHE, D, 2, 4>(p, s);
 }

@@ -23,6 +23,20 @@ struct CacheLayout {
     int page_size;
 };
 
+// Division of x < 2^31 by a fixed d >= 1 as a product: with 2^s >= d the quotient is
+// floor(x m / 2^(31+s)), m = ceil(2^(31+s) / d) < 2^32 (the error x (m d - 2^(31+s)) / (d 2^(31+s))
+// stays below 1 / d: Granlund and Montgomery, PLDI 1994).
+struct Divisor {
+    unsigned m, s;
+    static Divisor of(unsigned d)
+    {
+        unsigned s = 0;
+        while ((1ull << s) < d) ++s;
+        return Divisor{(unsigned)(((1ull << (31 + s)) + d - 1) / d), s};
+    }
+    __device__ __forceinline__ unsigned quotient(unsigned x) const { return (unsigned)(((uint64_t)x * m) >> (31 + s)); }
+};
+
 struct PageParams {
     const int32_t *cached, *fresh;
     int32_t *table;
@@ -68,6 +82,7 @@ struct AttnParams {
     int tile_rows;          // query rows (token, head of the group) of one work item
     int row_tiles;          // ceil(q_len * group / tile_rows)
     int grid;               // blocks that share the work
+    Divisor page_div;       // by the page size
 };
 
 cudaError_t launch_page_assign(const PageParams &p, cudaStream_t s);
