@@ -9,6 +9,7 @@
 #include "gdn.h"
 #include "gdn_internal.cuh"
 #include "gdn_tc.cuh"
+#include "gdna_internal.cuh"
 
 namespace gdn {
 
@@ -477,7 +478,11 @@ GDN_API int gdn_prefill_chunked(void *state, gdn_state_dtype state_dtype, int64_
 GDN_API int gdn_device_wait_timeouts(unsigned *count)
 {
     if (count == nullptr) return GDN_ERR_ARG;
-    return cuda_status(tc_wait_timeouts(count));
+    unsigned attention = 0;
+    cudaError_t e = tc_wait_timeouts(count);
+    if (e == cudaSuccess) e = gdna::attn_wait_timeouts(&attention);
+    *count += attention;
+    return cuda_status(e);
 }
 
 GDN_API void gdn_set_wait_polls(unsigned polls) { tc_set_wait_polls(polls); }

@@ -911,6 +911,10 @@ void tc_set_wait_polls(uint32_t polls)
 
 void tc_set_mma_wait_polls(uint32_t polls) { g_wait_polls.store(polls); }
 
+uint32_t tc_copy_wait_polls() { return g_copy_wait_polls.load(); }
+
+void *tensor_map_encoder() { return reinterpret_cast<void *>(encode_fn()); }
+
 cudaError_t tc_wait_timeouts(unsigned *count)
 {
     const cudaError_t e = cudaDeviceSynchronize();

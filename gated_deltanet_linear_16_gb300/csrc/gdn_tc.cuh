@@ -200,5 +200,9 @@ cudaError_t tc_wait_timeouts(unsigned *count);
 void tc_set_wait_polls(uint32_t polls);
 // The bound of the MMA waits alone (the tensor-copy waits keep theirs).
 void tc_set_mma_wait_polls(uint32_t polls);
+// The bound of the waits on tensor copies.
+uint32_t tc_copy_wait_polls();
+// cuTensorMapEncodeTiled (a PFN_cuTensorMapEncodeTiled_v12000), or null.
+void *tensor_map_encoder();
 
 }  // namespace gdn

@@ -210,6 +210,16 @@ int tc_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 
 
 }  // namespace
 
+cudaError_t attn_wait_timeouts(unsigned *count)
+{
+    unsigned n[3] = {0, 0, 0};
+    cudaError_t e = attn_wait_timeouts<GDNA_F16>(&n[0]);
+    if (e == cudaSuccess) e = attn_wait_timeouts<GDNA_BF16>(&n[1]);
+    if (e == cudaSuccess) e = attn_wait_timeouts<GDNA_E4M3>(&n[2]);
+    *count = n[0] + n[1] + n[2];
+    return e;
+}
+
 int64_t attn_workspace_bytes(int64_t rows, int d)
 {
     return kMaxGrid * (int64_t)sizeof(Join) + 2 * kMaxGrid * part_floats(tc_rows(rows), d) * (int64_t)sizeof(float);

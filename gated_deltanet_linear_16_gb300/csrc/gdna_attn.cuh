@@ -193,5 +193,7 @@ cudaError_t launch_join(const AttnParams &p, cudaStream_t s);
 
 // The tensor-core kernels, one translation unit per cache type.
 template <int CACHE> cudaError_t launch_attn_tc(const AttnParams &p, cudaStream_t s);
+// Bounded waits of theirs that ran out on the current device.
+template <int CACHE> cudaError_t attn_wait_timeouts(unsigned *count);
 
 }  // namespace gdna

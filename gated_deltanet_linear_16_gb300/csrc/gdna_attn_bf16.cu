@@ -3,4 +3,5 @@
 
 namespace gdna {
 template cudaError_t launch_attn_tc<GDNA_BF16>(const AttnParams &, cudaStream_t);
+template cudaError_t attn_wait_timeouts<GDNA_BF16>(unsigned *);
 }

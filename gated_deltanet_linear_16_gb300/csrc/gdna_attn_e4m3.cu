@@ -3,4 +3,5 @@
 
 namespace gdna {
 template cudaError_t launch_attn_tc<GDNA_E4M3>(const AttnParams &, cudaStream_t);
+template cudaError_t attn_wait_timeouts<GDNA_E4M3>(unsigned *);
 }

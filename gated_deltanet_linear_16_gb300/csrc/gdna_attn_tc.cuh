@@ -29,20 +29,30 @@
 // carry them into rows that do not see them: there a tile with a non-finite V adds its
 // rows key by key instead.
 //
-// Data.  A warp (or the R warps that share keys, each with its own rows) has its own
-// ring of stages in shared memory, 16 keys of K and V each, filled by cp.async in
-// 16-byte pieces (a key's head is D contiguous elements; keys lie anywhere) and drained
-// without any barrier over the block.  Rows are padded by 16 bytes: eight rows of an
-// ldmatrix then start in eight different bank groups.
+// Data.  A block is one producer warp and W consumer warps, one block an SM.  The
+// producer walks the block's parts on its own and keeps the rings full: it is already
+// copying the next item's keys while the consumers finish the last one's rows.  Each
+// consumer warp (or the R warps that share keys, each with its own rows) has a ring of
+// stages in shared memory, a step's K and V each, with a full and an empty mbarrier a
+// stage.  Rows lie in panels of 128 bytes with the 128-byte swizzle (64 with the 64-byte
+// one), so eight rows of an ldmatrix start in eight different bank groups.
+//   Where pages hold a multiple of 16 keys, a block of 16 keys lies in one page and a tensor
+// copy brings a panel of it: the (copy, consumer) pairs of a step are one lane each.
+// Otherwise the producer's lanes copy 16 bytes at a time (cp.async) to the same layout.
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
 #include "gdna_attn.cuh"
+#include "gdn_tc.cuh"
 
 namespace gdna {
 namespace tc {
 
 constexpr int kKeys = 16;                  // keys of a block: one side of a product
-constexpr int kMaxStages = 8;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ unsigned smem_addr(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
@@ -74,19 +84,28 @@ __device__ __forceinline__ void cp_async16(unsigned dst, const void *src, bool r
     const int n = real ? 16 : 0;           // 0: sixteen zero bytes, nothing is read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-// All but the newest `stages - 2` copy groups have landed.
-__device__ __forceinline__ void wait_stage(int stages)
+// A panel of 16 keys: {x, c1, c2, c3} are the map's coordinates.
+__device__ __forceinline__ void copy_panel(unsigned dst, const CUtensorMap *map, int x, int c1, int c2, int c3, unsigned bar)
 {
-    switch (stages) {
-    case 2: gdn::cp_async_wait<0>(); break;
-    case 3: gdn::cp_async_wait<1>(); break;
-    case 4: gdn::cp_async_wait<2>(); break;
-    case 5: gdn::cp_async_wait<3>(); break;
-    case 6: gdn::cp_async_wait<4>(); break;
-    case 7: gdn::cp_async_wait<5>(); break;
-    default: gdn::cp_async_wait<6>(); break;
-    }
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void arrive_expect(uint64_t *bar, unsigned bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+// One arrival once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void arrive_copies(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// Waits on the kernel's barriers that ran out on this device (each cache type's kernels have their own).
+static __device__ unsigned g_wait_timeouts;
 
 // 16-bit operand type of the products: bf16 for a bf16 cache, else fp16.
 template <int CACHE> struct Op {
@@ -132,18 +151,42 @@ __device__ __forceinline__ unsigned widen2(unsigned short x)
 
 template <int CACHE, int D, int NT, int R> struct Shape {
     static constexpr int kElem = CACHE == GDNA_E4M3 ? 1 : 2;
-    static constexpr int kRowBytes = D * kElem;
-    static constexpr int kPitch = kRowBytes + 16;
-    // Blocks of 16 keys a step.  Short rows take two: the maximum's shuffles, the barrier and the
-    // addresses are then paid once for 32 keys.
+    static constexpr int kRowBytes = D * kElem;                // 64, 128, 256 or 512
+    static constexpr int kPanel = kRowBytes < 128 ? kRowBytes : 128;           // bytes of a row in a panel
+    static constexpr int kPanels = kRowBytes / kPanel;
+    static constexpr int kPanelBytes = kKeys * kPanel;
+    static constexpr int kBlockBytes = kKeys * kRowBytes;      // K, or V, of a block
+    // Blocks of 16 keys a step.  Short rows take two: the maximum's shuffles, the barriers and the
+    // loop are then paid once for 32 keys.
     static constexpr int kBlocks = kRowBytes <= 128 ? 2 : 1;
     static constexpr int kStep = kKeys * kBlocks;
-    static constexpr int kStage = 2 * kStep * kPitch;          // K, then V
-    static constexpr int kWarps = (kRowBytes == 512 && R == 1) ? 2 : 4;
+    static constexpr int kStage = 2 * kBlocks * kBlockBytes;   // K's blocks, then V's
+    // Consumers: eight, with 168 registers each; four (255 registers) where two row tiles of a large
+    // head need them, or where eight rings of such long rows would hold one stage.
+    static constexpr int kWarps = (kRowBytes == 512 && R == 1) || (NT == 2 && D >= 128) ? 4 : 8;
     static constexpr int kKeyWarps = kWarps / R;
     static constexpr int kRows = 8 * NT * R;
+    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int kCopies = 2 * kBlocks * kPanels;      // tensor copies of a stage
     static constexpr int kQPitch = 2 * D + 16;
-    static constexpr int kSumPitch = D + 4;                    // floats
+    // the consumers' sums are added up some columns at a time
+    static constexpr int kColumns = kKeyWarps * kRows <= 64 ? 64 : 32;
+    static constexpr int kSumPitch = kColumns + 4;             // floats
+    static constexpr int kSumBytes = kKeyWarps * kRows * kSumPitch * 4;
+    static constexpr int kMaxStages = 6;
+    static_assert(kKeyWarps * kCopies <= 32, "a lane for each copy of a step");
+
+    // Swizzled place of byte `b` of row `r` in a block.
+    __device__ __forceinline__ static unsigned place(unsigned r, unsigned b)
+    {
+        if constexpr (kPanel == 128) return b / 128 * kPanelBytes + r * 128 + ((b % 128) ^ ((r & 7) << 4));
+        else return r * 64 + (b ^ (((r >> 1) & 3) << 4));
+    }
+    // From the place of (row, byte 0 or 16) to that of 32 x cols further on.
+    __device__ __forceinline__ static unsigned across(unsigned at, int x)
+    {
+        return (at ^ (unsigned)(32 * x % kPanel)) + 32 * x / kPanel * kPanelBytes;
+    }
 };
 
 // The query rows of an item into shared memory, in 16-bit parts.  Eight elements a lane,
@@ -219,9 +262,121 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, int seq, int h
     }
 }
 
+// How the tensor maps number the cache's dimensions after the elements of a head.
+struct MapDims {
+    int token, head, page;                 // 1 .. 3
+};
+
+// The producer warp: fills the consumers' rings, part after part.
 template <int CACHE, int D, int NT, int R>
-__global__ void __launch_bounds__(Shape<CACHE, D, NT, R>::kWarps * 32, 2)
-attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_parts)
+__device__ __forceinline__ void produce(const AttnParams &p, Run run, int c, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                        const MapDims dims, int stages, unsigned polls, uint8_t *smem,
+                                        uint64_t (*full)[Shape<CACHE, D, NT, R>::kKeyWarps],
+                                        uint64_t (*empty)[Shape<CACHE, D, NT, R>::kKeyWarps], int *gave_up)
+{
+    using S = Shape<CACHE, D, NT, R>;
+    constexpr int TW = S::kKeyWarps, KB = S::kBlocks;
+    const int lane = threadIdx.x & 31;
+    const unsigned page_size = (unsigned)p.cache.page_size, ring = smem_addr(smem);
+    int slot = 0, filled = 0;              // the next stage; stages filled so far, at most `stages`
+    unsigned phase = 1;                    // of its empty barrier: the first round finds all of them empty
+    bool ok = true;
+
+    if (dims.page != 0) {
+        // lane: the consumer it copies for, and which panel of which block of K or V
+        const int y = lane / S::kCopies, copy = lane % S::kCopies;
+        const bool mine = y < TW;
+        const int panel = copy % S::kPanels, block = copy / S::kPanels % KB, values = copy / (S::kPanels * KB);
+        const unsigned dst = ring + (mine ? y : 0) * stages * S::kStage + (values * KB + block) * S::kBlockBytes +
+                             panel * S::kPanelBytes;
+        const CUtensorMap *map = values ? &v_map : &k_map;
+        while (ok && run.at < run.end) {
+            const Part part = next_part(p, run, c);
+            const int head = part.item / p.row_tiles, steps = (int)(part.u1 - part.u0);
+            const int32_t *table = p.table + part.seq * p.table_stride;
+            unsigned key = (unsigned)((part.u0 * TW + y) * S::kStep + block * kKeys);
+            auto look_up = [&](int i) {    // the page of this lane's block; past the cache (zeros) if there is none
+                int page = i < steps && mine && key < (unsigned)part.keys ? __ldg(table + p.page_div.quotient(key)) : -1;
+                return (unsigned)page < (unsigned)p.cache.pages ? page : (int)p.cache.pages;
+            };
+            int page = look_up(0);
+            for (int i = 0; i < steps; ++i) {
+                const int token = (int)(key - p.page_div.quotient(min(key, 0x7fffffffu)) * page_size), at = page;
+                key += TW * S::kStep;
+                page = look_up(i + 1);
+                ok = __all_sync(kFull, !mine || gdn::tc::mbar_wait(&empty[slot][mine ? y : 0], phase, polls));
+                if (!ok) break;
+                if (mine && copy == 0) arrive_expect(&full[slot][y], S::kStage);
+                __syncwarp();
+                if (mine) {
+                    const int c1 = dims.token == 1 ? token : dims.head == 1 ? head : at;
+                    const int c2 = dims.token == 2 ? token : dims.head == 2 ? head : at;
+                    const int c3 = dims.token == 3 ? token : dims.head == 3 ? head : at;
+                    copy_panel(dst + slot * S::kStage, map, panel * (S::kPanel / S::kElem), c1, c2, c3, smem_addr(&full[slot][y]));
+                }
+                filled = min(filled + 1, stages);
+                if (++slot == stages) { slot = 0; phase ^= 1; }
+            }
+        }
+    } else {
+        const int64_t page_bytes = p.cache.page_stride * S::kElem, token_bytes = p.cache.token_stride * S::kElem;
+        constexpr int kPieces = S::kRowBytes / 16, kAtOnce = 32 / kPieces;     // 16-byte pieces of a row, rows at once
+        const int sub = lane / kPieces, piece = lane % kPieces * 16;
+        while (ok && run.at < run.end) {
+            const Part part = next_part(p, run, c);
+            const int head = part.item / p.row_tiles, steps = (int)(part.u1 - part.u0);
+            const int32_t *table = p.table + part.seq * p.table_stride;
+            const uint8_t *kb = static_cast<const uint8_t *>(p.k) + head * p.cache.head_stride * S::kElem;
+            const uint8_t *vb = static_cast<const uint8_t *>(p.v) + head * p.cache.head_stride * S::kElem;
+            unsigned key = (unsigned)(part.u0 * TW) * S::kStep + lane % S::kStep;      // the one this lane looks up
+            auto look_up = [&](int i) {
+                return i < steps && key < (unsigned)part.keys ? __ldg(table + p.page_div.quotient(key)) : -1;
+            };
+            int page = look_up(0);
+            for (int i = 0; i < steps; ++i) {
+                for (int y = 0; y < TW && ok; ++y) {
+                    int64_t at = -1;
+                    if ((unsigned)page < (unsigned)p.cache.pages)
+                        at = page * page_bytes + (int64_t)(key - p.page_div.quotient(key) * page_size) * token_bytes;
+                    key += S::kStep;
+                    page = look_up(y + 1 < TW ? i : i + 1);
+                    ok = __all_sync(kFull, gdn::tc::mbar_wait(&empty[slot][y], phase, polls));
+                    if (!ok) break;
+                    const unsigned to = ring + (y * stages + slot) * S::kStage;
+#pragma unroll 4
+                    for (int r = 0; r < S::kStep; r += kAtOnce) {
+                        const int row = r + sub;
+                        const int64_t from = __shfl_sync(kFull, at, row);
+                        const unsigned dst = to + row / kKeys * S::kBlockBytes + S::place(row % kKeys, piece);
+                        cp_async16(dst, kb + (from >= 0 ? from + piece : 0), from >= 0);
+                        cp_async16(dst + KB * S::kBlockBytes, vb + (from >= 0 ? from + piece : 0), from >= 0);
+                    }
+                    arrive_copies(&full[slot][y]);
+                }
+                if (!ok) break;
+                if (++slot == stages) { slot = 0; phase ^= 1; }
+            }
+        }
+        gdn::cp_async_wait<0>();
+    }
+    // No copy is left in flight when the block's memory is freed: consumers that kept up have waited for
+    // every stage; where a wait gave up, here or there, what was issued is waited for (again bounded).
+    __syncthreads();
+    if (!ok || *(volatile int *)gave_up != 0) {
+        const int y = lane < TW ? lane : 0;
+        for (int i = 0; i < filled; ++i) {
+            // a stage's last fill completes its full barrier's phase with the parity of the next empty wait
+            const int at = slot - 1 - i;
+            gdn::tc::mbar_wait(&full[at < 0 ? at + stages : at][y], at < 0 ? phase : phase ^ 1, GDN_DEFAULT_WAIT_POLLS);
+        }
+        if (lane == 0) atomicAdd(&g_wait_timeouts, 1u);
+    }
+}
+
+template <int CACHE, int D, int NT, int R>
+__global__ void __launch_bounds__(Shape<CACHE, D, NT, R>::kThreads, 1)
+attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+        const MapDims dims, const int stages, const int q_parts, const int w_parts, const unsigned polls)
 {
     using S = Shape<CACHE, D, NT, R>;
     using O = Op<CACHE>;
@@ -229,94 +384,52 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
     constexpr int W = S::kWarps, TW = S::kKeyWarps, ROWS = S::kRows, KB = S::kBlocks;
     // weight parts of the products proper; more follow in passes of their own
     constexpr int kParts = kF8 ? 1 : 2;
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t scratch[W + 2];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t scratch[W + 3];
     __shared__ float row_scale[ROWS], warp_m[TW][ROWS], warp_l[TW][ROWS];
+    __shared__ uint64_t full[S::kMaxStages][TW], empty[S::kMaxStages][TW];
+    __shared__ int gave_up;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+    uint8_t *smem = smem_raw + (-smem_addr(smem_raw) & 1023u);                 // the swizzle's period
+    uint8_t *qs = smem + TW * stages * S::kStage;
+    float *sums = reinterpret_cast<float *>(qs + q_parts * ROWS * S::kQPitch); // [TW][ROWS][kSumPitch]
+    const bool tensor_copies = dims.page != 0;
+
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i)
+            for (int y = 0; y < TW; ++y) {
+                gdn::tc::mbar_init(&full[i][y], tensor_copies ? 1 : 32);
+                gdn::tc::mbar_init(&empty[i][y], R);
+            }
+        gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    gdn::early_start<true>(nullptr, 0);
+    Run run = find_run(p, c, scratch);     // (synchronises: the barriers are set up)
+
+    if (warp == W) {
+        produce<CACHE, D, NT, R>(p, run, c, k_map, v_map, dims, stages, polls, smem, full, empty, &gave_up);
+        return;
+    }
+
     const int tw = warp / R, rg = warp % R;                    // the keys it takes, the rows it takes
     const int l4 = lane >> 2, c4 = lane & 3;
-    const unsigned ring = smem_addr(smem) + tw * stages * S::kStage, ring_end = ring + stages * S::kStage;
-    uint8_t *qs = smem + TW * stages * S::kStage;
-    float *sums = reinterpret_cast<float *>(smem);             // after the keys: [TW][ROWS][kSumPitch]
+    const unsigned ring = smem_addr(smem) + tw * stages * S::kStage;
     const int group_rows = p.q_len * p.group;
-    const unsigned page_size = (unsigned)p.cache.page_size;
-    const bool in_page = page_size % kKeys == 0;               // a block of keys lies in one page
-    const int64_t page_bytes = p.cache.page_stride * S::kElem, token_bytes = p.cache.token_stride * S::kElem;
-
-    gdn::early_start<true>(nullptr, 0);
-    Run run = find_run(p, c, scratch);
+    int slot = 0;
+    unsigned phase = 0;
+    bool ok = true;                        // every wait so far was in time
     Join join = {0, 0, 0, 0};
+    auto all_consumers = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory"); };
 
     while (run.at < run.end) {
         const Part part = next_part(p, run, c);
         const int head = part.item / p.row_tiles, row0 = (part.item % p.row_tiles) * ROWS;
         const int steps = (int)(part.u1 - part.u0);
-        const unsigned keys = (unsigned)part.keys;
-        const int32_t *table = p.table + part.seq * p.table_stride;
-        const uint8_t *kb = static_cast<const uint8_t *>(p.k) + head * p.cache.head_stride * S::kElem;
-        const uint8_t *vb = static_cast<const uint8_t *>(p.v) + head * p.cache.head_stride * S::kElem;
-        __syncthreads();                   // the last part's sums and queries are used up
-
-        // Lane j looks up the page of key j of a step, a step before it is needed; -1: none.
-        const unsigned start = (unsigned)(part.u0 * TW + tw) * S::kStep;       // this warp's first key
-        unsigned look = start + lane % S::kStep;                               // the key to look up next
-        int ahead = 0;                                                         // its step
-        auto next_page = [&]() {
-            const int page = ahead < steps && look < keys ? __ldg(table + p.page_div.quotient(look)) : -1;
-            ++ahead;
-            look += TW * S::kStep;
-            return page;
-        };
-        unsigned fill = start, fill_at = ring;                                 // the next step to copy: key, stage
-        auto issue = [&](int page) {
-            constexpr int kPieces = S::kRowBytes / 16;         // 16-byte pieces of a row: 4 .. 32
-            constexpr int kAtOnce = 32 / kPieces;              // rows of one instruction
-            constexpr int kMine = S::kStep / R;                // rows this warp copies
-            static_assert(kAtOnce <= kMine && (kMine % kKeys == 0 || kKeys % kMine == 0), "whole instructions");
-            const int sub = lane / kPieces, piece = (lane % kPieces) * 16;
-            const unsigned dst = fill_at + (rg * kMine + sub) * S::kPitch + piece;
-            const unsigned mine = fill + lane % S::kStep;
-            const unsigned place = mine - p.page_div.quotient(mine) * page_size;          // in its page
-            const int64_t at = (unsigned)page < (unsigned)p.cache.pages
-                                   ? page * page_bytes + (int64_t)place * token_bytes : -1;
-            if (in_page) {
-#pragma unroll
-                for (int r0 = 0; r0 < kMine; r0 += kKeys) {    // a block: one address, then equal steps
-                    const int first = (rg * kMine + r0) / kKeys * kKeys, off = (rg * kMine + r0) % kKeys + sub;
-                    const int64_t block = __shfl_sync(kFull, at, first);
-                    int64_t from = block + off * token_bytes + piece;
-                    const int left = block >= 0 ? (int)(keys - fill) - first - off : 0;
-#pragma unroll
-                    for (int r = 0; r < kKeys && r < kMine; r += kAtOnce) {
-                        const bool on = r < left;
-                        cp_async16(dst + (r0 + r) * S::kPitch, kb + (on ? from : 0), on);
-                        cp_async16(dst + (S::kStep + r0 + r) * S::kPitch, vb + (on ? from : 0), on);
-                        from += kAtOnce * token_bytes;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int r = 0; r < kMine; r += kAtOnce) {
-                    const int64_t from = __shfl_sync(kFull, at, rg * kMine + r + sub);
-                    const bool on = from >= 0;
-                    cp_async16(dst + r * S::kPitch, kb + (on ? from + piece : 0), on);
-                    cp_async16(dst + (S::kStep + r) * S::kPitch, vb + (on ? from + piece : 0), on);
-                }
-            }
-            fill += TW * S::kStep;
-            fill_at += S::kStage;
-            if (fill_at == ring_end) fill_at = ring;
-        };
-        int page = next_page();
-        for (int i = 0; i < stages - 1; ++i) {
-            const int next = next_page();
-            if (i < steps) issue(page);
-            gdn::cp_async_commit();
-            page = next;
-        }
         load_queries<CACHE, D, NT, R>(p, part.seq, head, row0, q_parts, qs, row_scale);
-        __syncthreads();
+        all_consumers();
 
         // this lane's rows: rg * 8 NT + 8 t + 2 c4 + j
         float m[NT][2], l[NT][2], rs[NT][2], o[D / 16][NT][4];
@@ -340,22 +453,24 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
         const int all_see = part.keys - (p.q_len - 1);         // keys that every row sees
         const unsigned q_at = smem_addr(qs + (rg * 8 * NT + (lane & 7)) * S::kQPitch + (lane >> 3) * 16);
 
-        unsigned ks = ring;                                    // the step's stage
-        int key0 = (int)start;
+        int key0 = (int)((part.u0 * TW + tw) * S::kStep);
 #pragma unroll 1
         for (int i = 0; i < steps; ++i) {
-            wait_stage(stages);
-            if constexpr (R == 1) __syncwarp();
-            else asm volatile("bar.sync %0, %1;" ::"r"(1 + tw), "n"(32 * R) : "memory");
-            // the stage that was used up a step ago takes the keys of stages - 1 steps ahead
-            {
-                const int next = next_page();
-                if (i + stages - 1 < steps) issue(page);
-                gdn::cp_async_commit();
-                page = next;
-            }
-            if (key0 < part.keys) {
-                const unsigned k_at = ks + (lane & 15) * S::kPitch + (lane >> 4) * 16;
+            ok = ok && __all_sync(kFull, gdn::tc::mbar_wait(&full[slot][tw], phase, polls));
+            const unsigned ks = ring + slot * S::kStage;
+            if (ok && key0 < part.keys) {
+                if (key0 + S::kStep > part.keys) {
+                    // past the sequence's end a page holds what it held before: 0 * NaN must not come of it
+                    for (int x = lane; x < S::kStep * (S::kRowBytes / 16); x += 32) {
+                        const int r = x / (S::kRowBytes / 16), b = x % (S::kRowBytes / 16) * 16;
+                        if (key0 + r >= part.keys)
+                            *reinterpret_cast<uint4 *>(smem + (ks - smem_addr(smem)) + (KB + r / kKeys) * S::kBlockBytes +
+                                                       S::place(r % kKeys, b)) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                const unsigned k_at = ks + S::place(lane & 15, (lane >> 4) * 16);
 
                 // S^T: two chains of products a row tile and block
                 float s2[KB][2][NT][4];
@@ -380,7 +495,7 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                             unsigned a[2][4];
                             if constexpr (kF8) {
                                 unsigned w[4];
-                                ldsm4(w, k_at + y * kKeys * S::kPitch + x * 32);
+                                ldsm4(w, S::across(k_at, x) + y * S::kBlockBytes);
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
                                     a[h][0] = widen2((unsigned short)w[2 * h]);
@@ -389,8 +504,8 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                                     a[h][3] = widen2((unsigned short)(w[2 * h + 1] >> 16));
                                 }
                             } else {
-                                ldsm4(a[0], k_at + y * kKeys * S::kPitch + x * 64);
-                                ldsm4(a[1], k_at + y * kKeys * S::kPitch + x * 64 + 32);
+                                ldsm4(a[0], S::across(k_at, 2 * x) + y * S::kBlockBytes);
+                                ldsm4(a[1], S::across(k_at, 2 * x + 1) + y * S::kBlockBytes);
                             }
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
@@ -464,11 +579,10 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
 
                 bool plain = true;
                 if (edge && p.q_len > 1) { // keys that some rows do not see: is every value finite?
-                    constexpr int kPieces = S::kRowBytes / 16;
                     bool odd = false;
-                    for (int x = lane; x < S::kStep * kPieces; x += 32) {
+                    for (int x = lane; x < S::kStep * (S::kRowBytes / 16); x += 32) {
                         unsigned words[4];
-                        lds16(words, ks + (S::kStep + x / kPieces) * S::kPitch + x % kPieces * 16);
+                        lds16(words, ks + KB * S::kBlockBytes + x * 16);
                         // an element's all-ones exponent (E4M3: its one NaN) carries into its clear top bit
                         constexpr unsigned kMask = kF8 ? 0x7f7f7f7fu : CACHE == GDNA_F16 ? 0x7c007c00u : 0x7f807f80u;
                         constexpr unsigned kOne = kF8 ? 0x01010101u : CACHE == GDNA_F16 ? 0x04000400u : 0x00800080u;
@@ -481,9 +595,9 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                 if (plain) {
 #pragma unroll
                     for (int y = 0; y < KB; ++y) {
-                        const unsigned vs = ks + (S::kStep + y * kKeys) * S::kPitch;
-                        const unsigned v_at = kF8 ? vs + (lane & 15) * S::kPitch + (lane >> 4) * 16
-                                                  : vs + ((lane & 7) + (lane >> 4) * 8) * S::kPitch + ((lane >> 3) & 1) * 16;
+                        const unsigned v_at = ks + (KB + y) * S::kBlockBytes +
+                                              (kF8 ? S::place(lane & 15, (lane >> 4) * 16)
+                                                   : S::place((lane & 7) + (lane >> 4) * 8, ((lane >> 3) & 1) * 16));
                         float rest[NT][4];
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
@@ -511,7 +625,7 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
 #pragma unroll
                                 for (int x = 0; x < kGo / 2; ++x) {
                                     unsigned u[4];
-                                    ldsm4_trans(u, v_at + (x0 / 2 + x) * 32);
+                                    ldsm4_trans(u, S::across(v_at, x0 / 2 + x));
 #pragma unroll
                                     for (int h = 0; h < 2; ++h) {
                                         // bytes of a word: keys 2c4, 2c4+1 of elements 2 l4, 2 l4 + 1
@@ -524,7 +638,7 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                                 }
                             } else {
 #pragma unroll
-                                for (int x = 0; x < kGo; ++x) ldsm4_trans(a[x], v_at + (x0 + x) * 32);
+                                for (int x = 0; x < kGo; ++x) ldsm4_trans(a[x], S::across(v_at, x0 + x));
                             }
                         };
 #pragma unroll
@@ -553,7 +667,7 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                         }
                     }
                 } else {
-                    const uint8_t *vs = smem + (ks - smem_addr(smem)) + S::kStep * S::kPitch;
+                    const uint8_t *vs = smem + (ks - smem_addr(smem)) + KB * S::kBlockBytes;
 #pragma unroll
                     for (int y = 0; y < KB; ++y)
 #pragma unroll 1
@@ -569,7 +683,7 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
                                     const int e = 16 * x + (kF8 ? 2 * l4 + h : l4 + 8 * h);
-                                    const float v = load_elem(vs + (y * kKeys + k) * S::kPitch, e, CACHE);
+                                    const float v = load_elem(vs + y * S::kBlockBytes + S::place(k, e * S::kElem), 0, CACHE);
 #pragma unroll
                                     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -581,13 +695,19 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                 }
             }
             key0 += TW * S::kStep;
-            ks += S::kStage;
-            if (ks == ring_end) ks = ring;
+            __syncwarp();
+            if (ok && lane == 0) arrive(&empty[slot][tw]);     // (after a failed wait nothing more may be copied)
+            if (++slot == stages) { slot = 0; phase ^= 1; }
+        }
+        if (!ok) {                         // copies that never came: the rows come out NaN
+#pragma unroll
+            for (int t = 0; t < NT; ++t) l[t][0] = l[t][1] = __int_as_float(0x7fc00000);
+            if (lane == 0) atomicExch(&gave_up, 1);
         }
 
-        // join the key warps' rows in shared memory, over the ring
-        gdn::cp_async_wait<0>();
-        __syncthreads();
+        // add up the key warps' rows, some columns at a time
+        const bool whole = part.begins && part.ends;
+        float *to = part_of(p, 2 * c + (part.begins ? 1 : 0));
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -598,36 +718,40 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                 x += __shfl_xor_sync(kFull, x, 16);
                 const int r = rg * 8 * NT + 8 * t + 2 * c4 + j;
                 if (l4 == 0) { warp_m[tw][r] = m[t][j]; warp_l[tw][r] = x; }
-#pragma unroll
-                for (int y = 0; y < D / 16; ++y)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        sums[(tw * ROWS + r) * S::kSumPitch + 16 * y + (kF8 ? 2 * l4 + h : l4 + 8 * h)] = o[y][t][2 * h + j];
             }
-        __syncthreads();
-        const bool whole = part.begins && part.ends;
-        float *to = part_of(p, 2 * c + (part.begins ? 1 : 0));
-        constexpr int kQuads = D / 4, kTasks = ROWS * kQuads / (W * 32), kGo = kTasks < 4 ? kTasks : 4;
-#pragma unroll 1
-        for (int k0 = 0; k0 < kTasks; k0 += kGo) {
-            float4 gate[kGo];
-            int64_t r_at[kGo], h_at[kGo];
+        constexpr int kQuads = S::kColumns / 4, kAll = ROWS * kQuads, kTasks = (kAll + W * 32 - 1) / (W * 32);
+        float4 gate[kTasks];
+        auto load_gates = [&](int x0) {
 #pragma unroll
-            for (int k = 0; k < kGo; ++k) {                    // every gate in flight
-                const int task = tid + (k0 + k) * W * 32, row = row0 + task / kQuads;
-                const int token = row / p.group;
-                r_at[k] = (int64_t)part.seq * p.q_len + token;
-                h_at[k] = (int64_t)head * p.group + (row - token * p.group);
-                gate[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (whole && p.gate != nullptr && row < group_rows)
-                    gate[k] = load4(p.gate, r_at[k] * p.gate_stride + h_at[k] * p.gate_head_stride + 4 * (task % kQuads),
-                                    p.dtype, p.gate_vec);
+            for (int k = 0; k < kTasks; ++k) {
+                const int task = tid + k * W * 32, row = row0 + task / kQuads;
+                if (whole && p.gate != nullptr && task < kAll && row < group_rows) {
+                    const int token = row / p.group;
+                    gate[k] = load4(p.gate, ((int64_t)part.seq * p.q_len + token) * p.gate_stride +
+                                                ((int64_t)head * p.group + (row - token * p.group)) * p.gate_head_stride +
+                                                x0 + 4 * (task % kQuads), p.dtype, p.gate_vec);
+                }
             }
+        };
+        load_gates(0);
 #pragma unroll
-            for (int k = 0; k < kGo; ++k) {
-                const int task = tid + (k0 + k) * W * 32, r = task / kQuads, x = 4 * (task % kQuads);
-                if (row0 + r >= group_rows) continue;
-                float top = kNegInf, total = 0.f, share[TW];
+        for (int x0 = 0; x0 < D; x0 += S::kColumns) {
+#pragma unroll
+            for (int y = x0 / 16; y < (x0 + S::kColumns) / 16; ++y)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            sums[(tw * ROWS + rg * 8 * NT + 8 * t + 2 * c4 + j) * S::kSumPitch + 16 * y - x0 +
+                                 (kF8 ? 2 * l4 + h : l4 + 8 * h)] = o[y][t][2 * h + j];
+            all_consumers();
+#pragma unroll
+            for (int k = 0; k < kTasks; ++k) {
+                const int task = tid + k * W * 32, r = task / kQuads, x = 4 * (task % kQuads);
+                if (task >= kAll || row0 + r >= group_rows) continue;
+                float top = kNegInf, total = 0.f;
 #pragma unroll
                 for (int y = 0; y < TW; ++y) top = fmaxf(top, warp_m[y][r]);
                 const float mm = top;
@@ -635,31 +759,66 @@ attn_tc(const AttnParams p, const int stages, const int q_parts, const int w_par
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int y = 0; y < TW; ++y) {
-                    share[y] = weight_of(warp_m[y][r], top);
-                    total = fmaf(share[y], warp_l[y][r], total);
+                    const float share = weight_of(warp_m[y][r], top);
+                    total = fmaf(share, warp_l[y][r], total);
                     const float4 v = *reinterpret_cast<const float4 *>(sums + (y * ROWS + r) * S::kSumPitch + x);
-                    a.x = fmaf(share[y], v.x, a.x);
-                    a.y = fmaf(share[y], v.y, a.y);
-                    a.z = fmaf(share[y], v.z, a.z);
-                    a.w = fmaf(share[y], v.w, a.w);
+                    a.x = fmaf(share, v.x, a.x);
+                    a.y = fmaf(share, v.y, a.y);
+                    a.z = fmaf(share, v.z, a.z);
+                    a.w = fmaf(share, v.w, a.w);
                 }
                 if (whole) {
+                    const int token = (row0 + r) / p.group;
+                    const int64_t r_at = (int64_t)part.seq * p.q_len + token;
+                    const int64_t h_at = (int64_t)head * p.group + (row0 + r - token * p.group);
                     finish4(p, a, total, gate[k]);
-                    store4(p.out, r_at[k] * p.out_stride + h_at[k] * D + x, p.out_dtype, p.out_vec, a);
-                    if (x == 0 && p.lse != nullptr) p.lse[r_at[k] * p.nq + h_at[k]] = lse_of(mm, total);
+                    store4(p.out, r_at * p.out_stride + h_at * D + x0 + x, p.out_dtype, p.out_vec, a);
+                    if (x0 + x == 0 && p.lse != nullptr) p.lse[r_at * p.nq + h_at] = lse_of(mm, total);
                 } else {
-                    *reinterpret_cast<float4 *>(to + r * D + x) = a;
-                    if (x == 0) { to[ROWS * D + 2 * r] = mm; to[ROWS * D + 2 * r + 1] = total; }
+                    *reinterpret_cast<float4 *>(to + r * D + x0 + x) = a;
+                    if (x0 + x == 0) { to[ROWS * D + 2 * r] = mm; to[ROWS * D + 2 * r + 1] = total; }
                 }
             }
+            if (x0 + S::kColumns < D) load_gates(x0 + S::kColumns);
+            all_consumers();
         }
         if (part.begins && !part.ends) join = Join{part.seq, part.item, part.blocks, 0};
     }
     if (tid == 0) joins_of(p)[c] = join;
+    __syncthreads();                       // (the producer looks whether all waits were in time)
 }
 
-constexpr int kTwoPerSm = 111 * 1024;      // shared memory of a block of which two fit an SM
-constexpr int kOnePerSm = 224 * 1024;
+constexpr int kSmemBytes = 224 * 1024;     // of a block, beside its static arrays
+
+// The 4-D map of the cache's K or V: the elements of a head, then (token, head, page) in the order of
+// their strides; box: 16 tokens x a panel.  False where the layout does not allow it.
+template <int CACHE, int D, int NT, int R>
+bool cache_map(const AttnParams &p, const void *base, CUtensorMap *map, MapDims *dims)
+{
+    using S = Shape<CACHE, D, NT, R>;
+    const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn::tensor_map_encoder());
+    if (encode == nullptr) return false;
+    struct Dim { int64_t stride, count; int box, *number; } d[3] = {
+        {p.cache.token_stride, p.cache.page_size, kKeys, &dims->token},
+        {p.cache.head_stride, p.nkv, 1, &dims->head},
+        {p.cache.page_stride, p.cache.pages, 1, &dims->page}};
+    std::sort(d, d + 3, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
+    cuuint64_t size[4] = {(cuuint64_t)D}, stride[3];
+    cuuint32_t box[4] = {(cuuint32_t)(S::kPanel / S::kElem)};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        const int64_t bytes = d[i].stride * S::kElem;
+        if (bytes <= 0 || bytes >= (int64_t{1} << 40)) return false;
+        size[i + 1] = (cuuint64_t)d[i].count;
+        stride[i] = (cuuint64_t)bytes;
+        box[i + 1] = (cuuint32_t)d[i].box;
+        *d[i].number = i + 1;
+    }
+    return encode(map, S::kElem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
+                  const_cast<void *>(base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  S::kPanel == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 template <int CACHE, int D, int NT, int R>
 cudaError_t launch(AttnParams p, cudaStream_t s)
@@ -670,25 +829,27 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
     const int q_parts = p.dtype == GDNA_BF16 ? 1 : p.dtype == GDNA_F16 ? (bf16 ? 2 : 1) : (bf16 ? 3 : 2);
     // and weights: to well below the output's rounding
     const int w_parts = (bf16 ? 2 : 1) + (p.out_dtype == GDNA_F32 || (CACHE != GDNA_BF16 && p.out_dtype == GDNA_F16));
-    const int q_bytes = q_parts * S::kRows * S::kQPitch;
-    const int least = (S::kRows * S::kSumPitch * 4 + S::kStage - 1) / S::kStage;     // the sums lie over the ring
-    int stages = (kTwoPerSm - q_bytes) / (S::kKeyWarps * S::kStage);
-    if (stages < 3 || stages < least) stages = (kOnePerSm - q_bytes) / (S::kKeyWarps * S::kStage);
-    stages = stages > kMaxStages ? kMaxStages : stages;
-    static_assert(kOnePerSm - 3 * S::kRows * S::kQPitch >= S::kKeyWarps * S::kStage * 3 &&
-                  kOnePerSm - 3 * S::kRows * S::kQPitch >= S::kKeyWarps * S::kRows * S::kSumPitch * 4 + S::kKeyWarps * S::kStage,
-                  "three stages, and room for the sums, whatever the queries' type");
-    static_assert(kMaxStages * S::kStage >= S::kRows * S::kSumPitch * 4, "the sums lie over the ring");
-    const int bytes = S::kKeyWarps * stages * S::kStage + q_bytes;
+    constexpr int kFixed = 1024 + S::kSumBytes;                // alignment of the ring; the sums
+    static_assert((kSmemBytes - kFixed - 3 * S::kRows * S::kQPitch) / (S::kKeyWarps * S::kStage) >= 2,
+                  "two stages whatever the queries' type");
+    const int fixed = kFixed + q_parts * S::kRows * S::kQPitch;
+    const int room = (kSmemBytes - fixed) / (S::kKeyWarps * S::kStage);
+    const int stages = room < S::kMaxStages ? room : S::kMaxStages;
     p.unit = S::kStep * S::kKeyWarps;
     p.page_div = Divisor::of((unsigned)p.cache.page_size);
     p.tile_rows = S::kRows;
     p.row_tiles = (int)(((int64_t)p.q_len * p.group + S::kRows - 1) / S::kRows);
-    const int grid = gdn::sm_count() * (bytes <= kTwoPerSm ? 2 : 1);
-    p.grid = grid < kMaxGrid ? grid : kMaxGrid;
-    cudaError_t e = gdn::allow_dynamic_smem<&attn_tc<CACHE, D, NT, R>>(kOnePerSm);
+    const int sms = gdn::sm_count();
+    p.grid = sms < kMaxGrid ? sms : kMaxGrid;
+    CUtensorMap k_map{}, v_map{};
+    MapDims dims{};
+    if (p.cache.page_size % kKeys != 0 || !cache_map<CACHE, D, NT, R>(p, p.k, &k_map, &dims) ||
+        !cache_map<CACHE, D, NT, R>(p, p.v, &v_map, &dims))
+        dims = MapDims{0, 0, 0};
+    cudaError_t e = gdn::allow_dynamic_smem<&attn_tc<CACHE, D, NT, R>>(kSmemBytes);
     if (e != cudaSuccess) return e;
-    e = gdn::launch_early(attn_tc<CACHE, D, NT, R>, (unsigned)p.grid, S::kWarps * 32, bytes, s, true, p, stages, q_parts, w_parts);
+    e = gdn::launch_early(attn_tc<CACHE, D, NT, R>, (unsigned)p.grid, S::kThreads, (size_t)(fixed + stages * S::kKeyWarps * S::kStage),
+                          s, true, p, k_map, v_map, dims, stages, q_parts, w_parts, gdn::tc_copy_wait_polls());
     return e != cudaSuccess ? e : launch_join(p, s);
 }
 
@@ -703,6 +864,11 @@ cudaError_t by_rows(const AttnParams &p, cudaStream_t s)
 }
 
 }  // namespace tc
+
+template <int CACHE> cudaError_t attn_wait_timeouts(unsigned *count)
+{
+    return cudaMemcpyFromSymbol(count, tc::g_wait_timeouts, sizeof(unsigned));
+}
 
 template <int CACHE> cudaError_t launch_attn_tc(const AttnParams &p, cudaStream_t s)
 {

@@ -88,6 +88,8 @@ struct AttnParams {
 cudaError_t launch_page_assign(const PageParams &p, cudaStream_t s);
 cudaError_t launch_qk_norm_rope(const RopeParams &p, bool fast, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnParams &p, bool fast, cudaStream_t s);
+// Bounded waits of the attention kernels that ran out on the current device.
+cudaError_t attn_wait_timeouts(unsigned *count);
 int64_t attn_workspace_bytes(int64_t rows, int d);
 
 // ---------------------------------------------------------------- device helpers
