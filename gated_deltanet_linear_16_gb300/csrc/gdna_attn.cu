@@ -24,12 +24,12 @@ attn_general(const AttnParams p)
     __shared__ float weight[kRows][kThreads];
     __shared__ int64_t place[kThreads];    // element offset of a key's head; -1: a page of zeros
     __shared__ float red[kRows][kThreads / 32];
-    __shared__ int64_t scratch[kThreads / 32 + 2];
+    __shared__ int64_t scratch[kThreads / 32 + 3];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x, D = p.d;
     Run run = find_run(p, c, scratch);
     Join join = {0, 0, 0, 0};
-    while (run.at < run.end) {
-        const Part part = next_part(p, run, c);
+    Part part;
+    while (next_part(p, run, c, part)) {
         const int head = part.item / p.row_tiles, row0 = (part.item % p.row_tiles) * kRows;
         __syncthreads();
         for (int i = tid; i < kRows * D; i += kThreads) {
@@ -140,69 +140,112 @@ attn_general(const AttnParams p)
 
 // ------------------------------------------------------------------ join
 //
-// Block (c, r): row r of the item that begins in block c and continues.
-constexpr int kJoinThreads = 256;
+// Block (c, r): row r of the item that begins in block c and continues.  All that it reads is a few
+// hundred KB from the L2, so what counts is the chain of latencies: the Join first, then every part's
+// maximum and sum, the first sums and the gate together.  The parts are dealt over the warps, a lane has
+// up to two groups of four columns.  Small blocks: there are as many as blocks times rows, and one wave
+// of them is to do.
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
+constexpr int kFirst = 4;                  // parts a warp asks for at once
 
 __global__ void __launch_bounds__(kJoinThreads)
 attn_join(const AttnParams p)
 {
     __shared__ float weight[kMaxGrid];
-    __shared__ float red[kJoinThreads / 32];
-    __shared__ float sums[kJoinThreads * 4];
+    __shared__ float red[kJoinWarps];
+    __shared__ float4 sums[kJoinWarps][64];
     const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int width = part_width(p.d), quads = width / 4;      // quads <= 64
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto part = [&](int i) { return part_of(p, 2 * (c + i) + (i == 0 ? 1 : 0)); };
+    auto ml = [&](int i) { return __ldcs(reinterpret_cast<const float2 *>(part(i) + p.tile_rows * width + 2 * r)); };
+    auto sum4 = [&](int i, int x) {
+        return i < 0 || x >= quads ? zero : __ldcs(reinterpret_cast<const float4 *>(part(i) + r * width) + x);
+    };
     gdn::early_start<true>(nullptr, 0);
     const Join join = joins_of(p)[c];
-    if (join.parts == 0) return;
-    const int head = join.item / p.row_tiles, row = (join.item % p.row_tiles) * p.tile_rows + r;
+    const int n = join.parts;
+    if (n == 0) return;
+    const float2 mine = tid < n ? ml(tid) : make_float2(kNegInf, 0.f);
+    float4 v[kFirst][2];
+#pragma unroll
+    for (int k = 0; k < kFirst; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[k][h] = sum4(warp + k * kJoinWarps < n ? warp + k * kJoinWarps : -1, lane + 32 * h);
+    const int head = join.item / p.row_tiles, row = (join.item - head * p.row_tiles) * p.tile_rows + r;
     if (row >= p.q_len * p.group) return;
-    const int width = part_width(p.d), n = join.parts;
-    auto part = [&](int i) { return part_of(p, 2 * (c + i) + (i == 0 ? 1 : 0)); };
+    const int token = row / p.group;
+    const int64_t r_at = (int64_t)join.seq * p.q_len + token, h_at = (int64_t)head * p.group + (row - token * p.group);
+    float4 gate = zero;
+    const bool four = p.d % 4 == 0;        // (else columns leave one by one)
+    if (four && tid < quads && p.gate != nullptr)
+        gate = load4(p.gate, r_at * p.gate_stride + h_at * p.gate_head_stride + 4 * tid, p.dtype, p.gate_vec);
 
-    float top = kNegInf;
-    for (int i = tid; i < n; i += kJoinThreads) {
-        weight[i] = part(i)[p.tile_rows * width + 2 * r];
-        top = fmaxf(top, weight[i]);
-    }
+    // the parts' maximum, then their weights and the row's sum
+    float top = mine.x;
+    for (int i = tid + kJoinThreads; i < n; i += kJoinThreads) top = fmaxf(top, ml(i).x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
     if (lane == 0) red[warp] = top;
     __syncthreads();
-    for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, red[w]);
-    const float m = top;
-    if (top == kNegInf) top = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, red[w]);
+    const float from = top == kNegInf ? 0.f : top;
     float l = 0.f;
     for (int i = tid; i < n; i += kJoinThreads) {
-        weight[i] = weight_of(weight[i], top);
-        l += weight[i] * part(i)[p.tile_rows * width + 2 * r + 1];
+        const float2 u = i == tid ? mine : ml(i);
+        weight[i] = weight_of(u.x, from);
+        l = fmaf(weight[i], u.y, l);
     }
     l = gdn::group_sum<32>(l);
     __syncthreads();
     if (lane == 0) red[warp] = l;
     __syncthreads();
     l = 0.f;
-    for (int w = 0; w < kJoinThreads / 32; ++w) l += red[w];
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) l += red[w];
 
-    // columns four at a time, the parts dealt over what threads are left
-    const int quads = width / 4, lanes = kJoinThreads / quads;   // quads <= 64
-    const int x = tid % quads, first = tid / quads;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (first < lanes) {
-#pragma unroll 4
-        for (int i = first; i < n; i += lanes) {
-            const float4 v = __ldcs(reinterpret_cast<const float4 *>(part(i) + r * width) + x);
-            const float w = weight[i];
-            o.x = fmaf(w, v.x, o.x); o.y = fmaf(w, v.y, o.y); o.z = fmaf(w, v.z, o.z); o.w = fmaf(w, v.w, o.w);
-        }
-        reinterpret_cast<float4 *>(sums)[tid] = o;
+    float4 o[2] = {zero, zero};
+    auto add = [&](int i, int h, float4 u) {
+        const float w = weight[i];
+        o[h].x = fmaf(w, u.x, o[h].x); o[h].y = fmaf(w, u.y, o[h].y);
+        o[h].z = fmaf(w, u.z, o[h].z); o[h].w = fmaf(w, u.w, o[h].w);
+    };
+    for (int i0 = warp; i0 < n; i0 += kFirst * kJoinWarps) {
+#pragma unroll
+        for (int k = 0; k < kFirst; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (i0 + k * kJoinWarps < n) add(i0 + k * kJoinWarps, h, v[k][h]);
+#pragma unroll
+        for (int k = 0; k < kFirst; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = i0 + (kFirst + k) * kJoinWarps;
+                v[k][h] = sum4(i < n ? i : -1, lane + 32 * h);
+            }
     }
+    sums[warp][lane] = o[0];
+    sums[warp][lane + 32] = o[1];
     __syncthreads();
     const float norm = l == 0.f ? 0.f : p.v_scale / l;
-    for (int col = tid; col < p.d; col += kJoinThreads) {
-        float t = 0.f;
-        for (int g = 0; g < lanes; ++g) t += sums[(g * quads + (col >> 2)) * 4 + (col & 3)];
-        write_out(p, join.seq, head, row, col, l == 0.f ? 0.f : t * norm);
+    if (tid < quads) {
+        float4 a = sums[0][tid];
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; ++w) {
+            const float4 u = sums[w][tid];
+            a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+        }
+        if (four) {
+            finish4(p, a, norm, gate);
+            store4(p.out, r_at * p.out_stride + h_at * p.d + 4 * tid, p.out_dtype, p.out_vec, a);
+        } else {
+            const float u[4] = {a.x, a.y, a.z, a.w};
+            for (int e = 0; e < 4 && 4 * tid + e < p.d; ++e)
+                write_out(p, join.seq, head, row, 4 * tid + e, norm == 0.f ? 0.f : u[e] * norm);
+        }
     }
-    if (tid == 0) write_lse(p, join.seq, head, row, m, l);
+    if (tid == 0) write_lse(p, join.seq, head, row, top, l);
 }
 
 // Query rows of a work item on the tensor cores.
@@ -228,6 +271,7 @@ int64_t attn_workspace_bytes(int64_t rows, int d)
 cudaError_t launch_join(const AttnParams &p, cudaStream_t s)
 {
     const int rows = p.q_len * p.group < p.tile_rows ? p.q_len * p.group : p.tile_rows;
+    if (p.grid < 2) return cudaSuccess;
     return gdn::launch_early(attn_join, dim3(p.grid, rows), kJoinThreads, 0, s, true, p);
 }
 
@@ -240,6 +284,7 @@ cudaError_t launch_attn_decode(const AttnParams &params, bool fast, cudaStream_t
     }
     AttnParams p = params;
     p.unit = kThreads;
+    p.lead = 0;
     p.tile_rows = kRows;
     p.row_tiles = (int)(((int64_t)p.q_len * p.group + kRows - 1) / kRows);
     const int sms = gdn::sm_count();

@@ -29,7 +29,7 @@
 // carry them into rows that do not see them: there a tile with a non-finite V adds its
 // rows key by key instead.
 //
-// Data.  A block is one producer warp and W consumer warps, one block an SM.  The
+// Data.  A block is one producer warp and W consumer warps.  The
 // producer walks the block's parts on its own and keeps the rings full: it is already
 // copying the next item's keys while the consumers finish the last one's rows.  Each
 // consumer warp (or the R warps that share keys, each with its own rows) has a ring of
@@ -54,6 +54,8 @@ namespace tc {
 
 constexpr int kKeys = 16;                  // keys of a block: one side of a product
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kSmemOne = 224 * 1024, kSmemTwo = 111 * 1024;      // of a block beside its static arrays: one, two an SM
+constexpr int kQueue = 8;                  // parts that the producer can be ahead: more than there are stages
 
 __device__ __forceinline__ unsigned smem_addr(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
 
@@ -91,6 +93,8 @@ __device__ __forceinline__ void copy_panel(unsigned dst, const CUtensorMap *map,
                  "[%0], [%1, {%2, %3, %4, %5}], [%6];"
                  ::"r"(dst), "l"(map), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
 }
+// A hint only: nothing is read.
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void arrive(uint64_t *bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -142,11 +146,12 @@ template <> struct Op<GDNA_BF16> {
     }
 };
 
-// Two E4M3 values (16 bits) to two fp16, exactly.
-__device__ __forceinline__ unsigned widen2(unsigned short x)
+// Four E4M3 values of a word to four fp16, exactly: the low two, the high two.
+__device__ __forceinline__ void widen4(unsigned x, unsigned &lo, unsigned &hi)
 {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(x, __NV_E4M3);
-    return (unsigned)h.x | ((unsigned)h.y << 16);
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(x));
 }
 
 template <int CACHE, int D, int NT, int R> struct Shape {
@@ -161,16 +166,22 @@ template <int CACHE, int D, int NT, int R> struct Shape {
     static constexpr int kBlocks = kRowBytes <= 128 ? 2 : 1;
     static constexpr int kStep = kKeys * kBlocks;
     static constexpr int kStage = 2 * kBlocks * kBlockBytes;   // K's blocks, then V's
-    // Consumers: eight, with 168 registers each; four (255 registers) where two row tiles of a large
-    // head need them, or where eight rings of such long rows would hold one stage.
-    static constexpr int kWarps = (kRowBytes == 512 && R == 1) || (NT == 2 && D >= 128) ? 4 : 8;
+    // Blocks on an SM.  Rows up to 256 bytes: two, so that one reads on while the other goes from an item to the
+    // next (256 requests over an E4M3 cache, D 128: 104 us against 119 with one block of eight consumers; 32 requests
+    // over a bf16 cache, D 128: 100.9 against 102.5).  Longer rows: one, whose rings hold more (262144 keys, D 256:
+    // 167 us against 177 with two).
+    static constexpr int kPerSm = kRowBytes <= 256 && !(NT == 2 && D >= 128) ? 2 : 1;
+    // Consumers: 168 registers each; four in a block (255 registers) where two row tiles of a large head need
+    // them, or where eight rings of such long rows would hold one stage.
+    static constexpr int kWarps = kPerSm == 2 || (kRowBytes == 512 && R == 1) || (NT == 2 && D >= 128) ? 4 : 8;
     static constexpr int kKeyWarps = kWarps / R;
     static constexpr int kRows = 8 * NT * R;
     static constexpr int kThreads = 32 * (kWarps + 1);
     static constexpr int kCopies = 2 * kBlocks * kPanels;      // tensor copies of a stage
     static constexpr int kQPitch = 2 * D + 16;
-    // the consumers' sums are added up some columns at a time
-    static constexpr int kColumns = kKeyWarps * kRows <= 64 ? 64 : 32;
+    // the consumers' sums are added up some columns at a time: 64 where three stages fit beside them
+    static constexpr int kSmem = kPerSm == 2 ? kSmemTwo : kSmemOne;
+    static constexpr int kColumns = 1024 + 3 * kKeyWarps * kStage + 2 * kRows * kQPitch + kKeyWarps * kRows * 68 * 4 <= kSmem ? 64 : 32;
     static constexpr int kSumPitch = kColumns + 4;             // floats
     static constexpr int kSumBytes = kKeyWarps * kRows * kSumPitch * 4;
     static constexpr int kMaxStages = 6;
@@ -189,37 +200,41 @@ template <int CACHE, int D, int NT, int R> struct Shape {
     }
 };
 
-// The query rows of an item into shared memory, in 16-bit parts.  Eight elements a lane,
-// several rows in flight.  For E4M3 the elements stand in the order in which K's come:
-// a 32-bit word of four becomes two operand registers, slots 2q, 2q+1 and 8+2q, 8+2q+1 of
-// the 16 that a product contracts.
-template <int CACHE, int D, int NT, int R>
-__device__ __forceinline__ void load_queries(const AttnParams &p, int seq, int head, int row0, int q_parts, uint8_t *qs,
-                                             float *row_scale)
-{
+// The query rows of an item, eight elements a lane: `fetch` brings the rows of some passes
+// into registers, `put` leaves them in shared memory in 16-bit parts.  For E4M3 the elements
+// stand in the order in which K's come: a 32-bit word of four becomes two operand registers,
+// slots 2q, 2q+1 and 8+2q, 8+2q+1 of the 16 that a product contracts.
+template <int CACHE, int D, int NT, int R> struct Queries {
     using S = Shape<CACHE, D, NT, R>;
     using O = Op<CACHE>;
-    constexpr int ROWS = S::kRows, kLanes = D / 8, kPerWarp = 32 / kLanes;       // lanes of a row, rows of a warp
-    constexpr int kPasses = (ROWS + S::kWarps * kPerWarp - 1) / (S::kWarps * kPerWarp), kGo = kPasses < 4 ? kPasses : 4;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group_rows = p.q_len * p.group;
-    const int at = (lane % kLanes) * 8;
-#pragma unroll 1
-    for (int pass = 0; pass < kPasses; pass += kGo) {
-        float x[kGo][8];
+    static constexpr int kRows = S::kRows, kLanes = D / 8, kPerWarp = 32 / kLanes;        // lanes of a row, rows of a warp
+    static constexpr int kPasses = (kRows + S::kWarps * kPerWarp - 1) / (S::kWarps * kPerWarp);
+    static constexpr int kGo = kPasses < 4 ? kPasses : 4;      // passes at once
+    float x[kGo][8];
+
+    __device__ __forceinline__ void fetch(const AttnParams &p, const Part &part, int pass)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const int head = part.item / p.row_tiles, row0 = (part.item - head * p.row_tiles) * kRows;
 #pragma unroll
         for (int k = 0; k < kGo; ++k) {
             const int r = ((pass + k) * S::kWarps + warp) * kPerWarp + lane / kLanes, row = row0 + r;
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
-            if (r < ROWS && row < group_rows) {
+            if (r < kRows && row < p.q_len * p.group) {
                 const int token = row / p.group;
-                const int64_t from = ((int64_t)seq * p.q_len + token) * p.q_stride +
-                                     ((int64_t)head * p.group + (row - token * p.group)) * D + at;
+                const int64_t from = ((int64_t)part.seq * p.q_len + token) * p.q_stride +
+                                     ((int64_t)head * p.group + (row - token * p.group)) * D + (lane % kLanes) * 8;
                 const float4 a = load4(p.q, from, p.dtype, p.q_vec), b = load4(p.q, from + 4, p.dtype, p.q_vec);
                 x[k][0] = a.x; x[k][1] = a.y; x[k][2] = a.z; x[k][3] = a.w;
                 x[k][4] = b.x; x[k][5] = b.y; x[k][6] = b.z; x[k][7] = b.w;
             }
         }
+    }
+
+    __device__ __forceinline__ void put(const AttnParams &p, int pass, int q_parts, uint8_t *qs, float *row_scale)
+    {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = (lane % kLanes) * 8;
 #pragma unroll
         for (int k = 0; k < kGo; ++k) {
             const int r = ((pass + k) * S::kWarps + warp) * kPerWarp + lane / kLanes;
@@ -237,7 +252,7 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, int seq, int h
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[k][j] *= up;
             }
-            if (r < ROWS) {
+            if (r < kRows) {
                 for (int part = 0; part < q_parts; ++part) {
                     unsigned u[4];
 #pragma unroll
@@ -247,7 +262,7 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, int seq, int h
                         x[k][2 * j] -= f.x;
                         x[k][2 * j + 1] -= f.y;
                     }
-                    uint8_t *to = qs + (part * ROWS + r) * S::kQPitch;
+                    uint8_t *to = qs + (part * kRows + r) * S::kQPitch;
                     if constexpr (CACHE == GDNA_E4M3) {
                         const int slot = (at & ~15) + (at & 8) / 2;
                         *reinterpret_cast<uint2 *>(to + slot * 2) = make_uint2(u[0], u[2]);
@@ -260,121 +275,185 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, int seq, int h
             }
         }
     }
-}
+};
 
 // How the tensor maps number the cache's dimensions after the elements of a head.
 struct MapDims {
     int token, head, page;                 // 1 .. 3
 };
 
-// The producer warp: fills the consumers' rings, part after part.
+// What the producer leaves behind: the next stage, the parity of its empty barrier's next wait, and how many of
+// the stages before it were filled (at most all).
+struct Ring {
+    int slot, filled;
+    unsigned phase;
+    bool ok;                               // every wait was in time
+};
+
+// The producer warp: fills the consumers' rings, part after part, and tells them the parts after the first, in
+// `queue`, as it comes to them; a part of no sequence ends them.
 template <int CACHE, int D, int NT, int R>
-__device__ __forceinline__ void produce(const AttnParams &p, Run run, int c, const CUtensorMap &k_map, const CUtensorMap &v_map,
+__device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, const CUtensorMap &k_map, const CUtensorMap &v_map,
                                         const MapDims dims, int stages, unsigned polls, uint8_t *smem,
                                         uint64_t (*full)[Shape<CACHE, D, NT, R>::kKeyWarps],
-                                        uint64_t (*empty)[Shape<CACHE, D, NT, R>::kKeyWarps], int *gave_up)
+                                        uint64_t (*empty)[Shape<CACHE, D, NT, R>::kKeyWarps], Part *queue, uint64_t *told)
 {
     using S = Shape<CACHE, D, NT, R>;
     constexpr int TW = S::kKeyWarps, KB = S::kBlocks;
     const int lane = threadIdx.x & 31;
     const unsigned page_size = (unsigned)p.cache.page_size, ring = smem_addr(smem);
-    int slot = 0, filled = 0;              // the next stage; stages filled so far, at most `stages`
-    unsigned phase = 1;                    // of its empty barrier: the first round finds all of them empty
+    int slot = 0, filled = 0, entered = 0;
+    unsigned phase = 1;                    // the first round finds all stages empty
     bool ok = true;
 
+    // The steps of the block's parts in order.  Pages are looked up a step before they are needed, also from
+    // one part to the next: a load's latency there would leave the rings dry.  What a stage's refill waits for
+    // is short for the same reason.
+    const int y = dims.page != 0 ? lane / S::kCopies : 0;      // the consumer this lane looks up for
+    const int copy = lane % S::kCopies;
+    const int panel = copy % S::kPanels, block = copy / S::kPanels % KB, values = copy / (S::kPanels * KB);
+    const unsigned first = dims.page != 0 ? y * S::kStep + block * kKeys : lane % S::kStep;      // its key of a unit
+    int left = 0, head = 0;                // steps of the part that are not looked up; its key head
+    unsigned key = 0, keys = 0;            // the key to look up next, the sequence's keys
+    const int32_t *table = nullptr;
+    Part part = {};
+    bool more = true, fresh = false;       // a step is left; a part was entered just now
+    auto enter = [&]() {                   // the next part
+        more = fresh = next_part(p, run, c, part);
+        if (!more) part.seq = -1;
+        if (lane == 0 && entered > 0) {
+            queue[entered % kQueue] = part;
+            arrive(&told[entered % kQueue]);
+        }
+        ++entered;
+        if (!more) return;
+        left = (int)(part.u1 - part.u0);
+        key = (unsigned)(part.u0 * TW) * S::kStep + first;
+        keys = (unsigned)part.keys;
+        table = p.table + part.seq * p.table_stride;
+        head = part.item / p.row_tiles;
+    };
+    auto warm = [&]() {                    // its query and gate rows on their way to the L2, before they are asked for
+        fresh = false;
+        const int elem = p.dtype == GDNA_F32 ? 4 : 2;
+        const int row0 = (part.item - head * p.row_tiles) * S::kRows, rows = min(S::kRows, p.q_len * p.group - row0);
+        for (int r = lane >> 2; r < rows; r += 8) {            // four lanes a row, a line of 128 bytes each at a time
+            const int row = row0 + r, token = row / p.group;
+            const int64_t n = (int64_t)part.seq * p.q_len + token, h = (int64_t)head * p.group + (row - token * p.group);
+            for (int at = (lane & 3) * 128; at < D * elem; at += 512) {
+                prefetch_l2(static_cast<const uint8_t *>(p.q) + (n * p.q_stride + h * D) * elem + at);
+                if (p.gate != nullptr)
+                    prefetch_l2(static_cast<const uint8_t *>(p.gate) + (n * p.gate_stride + h * p.gate_head_stride) * elem + at);
+            }
+        }
+    };
+    enter();
+
     if (dims.page != 0) {
-        // lane: the consumer it copies for, and which panel of which block of K or V
-        const int y = lane / S::kCopies, copy = lane % S::kCopies;
         const bool mine = y < TW;
-        const int panel = copy % S::kPanels, block = copy / S::kPanels % KB, values = copy / (S::kPanels * KB);
         const unsigned dst = ring + (mine ? y : 0) * stages * S::kStage + (values * KB + block) * S::kBlockBytes +
                              panel * S::kPanelBytes;
         const CUtensorMap *map = values ? &v_map : &k_map;
-        while (ok && run.at < run.end) {
-            const Part part = next_part(p, run, c);
-            const int head = part.item / p.row_tiles, steps = (int)(part.u1 - part.u0);
-            const int32_t *table = p.table + part.seq * p.table_stride;
-            unsigned key = (unsigned)((part.u0 * TW + y) * S::kStep + block * kKeys);
-            auto look_up = [&](int i) {    // the page of this lane's block; past the cache (zeros) if there is none
-                int page = i < steps && mine && key < (unsigned)part.keys ? __ldg(table + p.page_div.quotient(key)) : -1;
-                return (unsigned)page < (unsigned)p.cache.pages ? page : (int)p.cache.pages;
-            };
-            int page = look_up(0);
-            for (int i = 0; i < steps; ++i) {
-                const int token = (int)(key - p.page_div.quotient(min(key, 0x7fffffffu)) * page_size), at = page;
-                key += TW * S::kStep;
-                page = look_up(i + 1);
-                ok = __all_sync(kFull, !mine || gdn::tc::mbar_wait(&empty[slot][mine ? y : 0], phase, polls));
-                if (!ok) break;
-                if (mine && copy == 0) arrive_expect(&full[slot][y], S::kStage);
-                __syncwarp();
-                if (mine) {
-                    const int c1 = dims.token == 1 ? token : dims.head == 1 ? head : at;
-                    const int c2 = dims.token == 2 ? token : dims.head == 2 ? head : at;
-                    const int c3 = dims.token == 3 ? token : dims.head == 3 ? head : at;
-                    copy_panel(dst + slot * S::kStage, map, panel * (S::kPanel / S::kElem), c1, c2, c3, smem_addr(&full[slot][y]));
-                }
-                filled = min(filled + 1, stages);
-                if (++slot == stages) { slot = 0; phase ^= 1; }
+        int page = 0, token = 0;
+        auto look_up = [&]() {             // this lane's block of the step; past the cache (zeros) if there is none
+            page = -1;
+            token = 0;
+            if (mine && key < keys) {
+                const unsigned n = p.page_div.quotient(key);
+                token = (int)(key - n * page_size);
+                page = __ldg(table + n);
             }
+        };
+        if (more) look_up();
+        while (more) {
+            const int at = (unsigned)page < (unsigned)p.cache.pages ? page : (int)p.cache.pages;
+            const int c1 = dims.token == 1 ? token : dims.head == 1 ? head : at;
+            const int c2 = dims.token == 2 ? token : dims.head == 2 ? head : at;
+            const int c3 = dims.token == 3 ? token : dims.head == 3 ? head : at;
+            key += TW * S::kStep;
+            if (--left == 0) enter();
+            if (more) look_up();
+            ok = __all_sync(kFull, !mine || gdn::tc::mbar_wait(&empty[slot][mine ? y : 0], phase, polls));
+            if (!ok) break;
+            if (mine && copy == 0) arrive_expect(&full[slot][y], S::kStage);
+            __syncwarp();
+            if (mine)
+                copy_panel(dst + slot * S::kStage, map, panel * (S::kPanel / S::kElem), c1, c2, c3, smem_addr(&full[slot][y]));
+            filled = min(filled + 1, stages);
+            if (++slot == stages) { slot = 0; phase ^= 1; }
+            if (fresh) warm();
         }
     } else {
         const int64_t page_bytes = p.cache.page_stride * S::kElem, token_bytes = p.cache.token_stride * S::kElem;
         constexpr int kPieces = S::kRowBytes / 16, kAtOnce = 32 / kPieces;     // 16-byte pieces of a row, rows at once
         const int sub = lane / kPieces, piece = lane % kPieces * 16;
-        while (ok && run.at < run.end) {
-            const Part part = next_part(p, run, c);
-            const int head = part.item / p.row_tiles, steps = (int)(part.u1 - part.u0);
-            const int32_t *table = p.table + part.seq * p.table_stride;
-            const uint8_t *kb = static_cast<const uint8_t *>(p.k) + head * p.cache.head_stride * S::kElem;
-            const uint8_t *vb = static_cast<const uint8_t *>(p.v) + head * p.cache.head_stride * S::kElem;
-            unsigned key = (unsigned)(part.u0 * TW) * S::kStep + lane % S::kStep;      // the one this lane looks up
-            auto look_up = [&](int i) {
-                return i < steps && key < (unsigned)part.keys ? __ldg(table + p.page_div.quotient(key)) : -1;
-            };
-            int page = look_up(0);
-            for (int i = 0; i < steps; ++i) {
-                for (int y = 0; y < TW && ok; ++y) {
-                    int64_t at = -1;
-                    if ((unsigned)page < (unsigned)p.cache.pages)
-                        at = page * page_bytes + (int64_t)(key - p.page_div.quotient(key) * page_size) * token_bytes;
-                    key += S::kStep;
-                    page = look_up(y + 1 < TW ? i : i + 1);
-                    ok = __all_sync(kFull, gdn::tc::mbar_wait(&empty[slot][y], phase, polls));
-                    if (!ok) break;
-                    const unsigned to = ring + (y * stages + slot) * S::kStage;
-#pragma unroll 4
-                    for (int r = 0; r < S::kStep; r += kAtOnce) {
-                        const int row = r + sub;
-                        const int64_t from = __shfl_sync(kFull, at, row);
-                        const unsigned dst = to + row / kKeys * S::kBlockBytes + S::place(row % kKeys, piece);
-                        cp_async16(dst, kb + (from >= 0 ? from + piece : 0), from >= 0);
-                        cp_async16(dst + KB * S::kBlockBytes, vb + (from >= 0 ? from + piece : 0), from >= 0);
-                    }
-                    arrive_copies(&full[slot][y]);
-                }
-                if (!ok) break;
-                if (++slot == stages) { slot = 0; phase ^= 1; }
+        int page = -1;
+        unsigned place = 0;                // of the looked-up key in its page
+        auto look_up = [&]() {             // lane j: key j of a consumer's step
+            page = -1;
+            if (key < keys) {
+                const unsigned n = p.page_div.quotient(key);
+                place = key - n * page_size;
+                page = __ldg(table + n);
             }
+        };
+        if (more) look_up();
+        while (more && ok) {
+            const int64_t base = (int64_t)head * p.cache.head_stride * S::kElem;
+            const uint8_t *kb = static_cast<const uint8_t *>(p.k) + base, *vb = static_cast<const uint8_t *>(p.v) + base;
+            for (int z = 0; z < TW && ok; ++z) {
+                const int64_t at = (unsigned)page < (unsigned)p.cache.pages ? page * page_bytes + place * token_bytes : -1;
+                key += S::kStep;
+                if (z + 1 == TW && --left == 0) enter();
+                if (more) look_up();
+                ok = __all_sync(kFull, gdn::tc::mbar_wait(&empty[slot][z], phase, polls));
+                if (!ok) break;
+                const unsigned to = ring + (z * stages + slot) * S::kStage;
+#pragma unroll 4
+                for (int r = 0; r < S::kStep; r += kAtOnce) {
+                    const int row = r + sub;
+                    const int64_t from = __shfl_sync(kFull, at, row);
+                    const unsigned dst = to + row / kKeys * S::kBlockBytes + S::place(row % kKeys, piece);
+                    cp_async16(dst, kb + (from >= 0 ? from + piece : 0), from >= 0);
+                    cp_async16(dst + KB * S::kBlockBytes, vb + (from >= 0 ? from + piece : 0), from >= 0);
+                }
+                arrive_copies(&full[slot][z]);
+            }
+            if (++slot == stages) { slot = 0; phase ^= 1; }
+            if (fresh) warm();
         }
         gdn::cp_async_wait<0>();
     }
-    // No copy is left in flight when the block's memory is freed: consumers that kept up have waited for
-    // every stage; where a wait gave up, here or there, what was issued is waited for (again bounded).
-    __syncthreads();
-    if (!ok || *(volatile int *)gave_up != 0) {
-        const int y = lane < TW ? lane : 0;
-        for (int i = 0; i < filled; ++i) {
-            // a stage's last fill completes its full barrier's phase with the parity of the next empty wait
-            const int at = slot - 1 - i;
-            gdn::tc::mbar_wait(&full[at < 0 ? at + stages : at][y], at < 0 ? phase : phase ^ 1, GDN_DEFAULT_WAIT_POLLS);
+    return Ring{slot, filled, phase, ok};
+}
+
+// A wait gave up: NaN for every row of the block's parts.
+static __device__ __noinline__ void fill_nan(const AttnParams &p, Run run, int c, int rows)
+{
+    const float nan = __int_as_float(0x7fc00000);
+    Join join = {0, 0, 0, 0};
+    Part part;
+    while (next_part(p, run, c, part)) {
+        const int head = part.item / p.row_tiles, row0 = (part.item - head * p.row_tiles) * rows;
+        float *to = part_of(p, 2 * c + (part.begins ? 1 : 0));
+        for (int i = threadIdx.x; i < rows * p.d; i += blockDim.x) {
+            const int r = i / p.d, x = i - r * p.d;
+            if (row0 + r >= p.q_len * p.group) break;
+            if (part.begins && part.ends) {
+                write_out(p, part.seq, head, row0 + r, x, nan);
+                if (x == 0) write_lse(p, part.seq, head, row0 + r, nan, nan);
+            } else {
+                to[r * p.d + x] = nan;
+                if (x == 0) to[rows * p.d + 2 * r] = to[rows * p.d + 2 * r + 1] = nan;
+            }
         }
-        if (lane == 0) atomicAdd(&g_wait_timeouts, 1u);
+        if (part.begins && !part.ends) join = Join{part.seq, part.item, part.blocks, 0};
     }
+    if (threadIdx.x == 0) joins_of(p)[c] = join;
 }
 
 template <int CACHE, int D, int NT, int R>
-__global__ void __launch_bounds__(Shape<CACHE, D, NT, R>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<CACHE, D, NT, R>::kThreads, Shape<CACHE, D, NT, R>::kPerSm)
 attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
         const MapDims dims, const int stages, const int q_parts, const int w_parts, const unsigned polls)
 {
@@ -385,10 +464,14 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
     // weight parts of the products proper; more follow in passes of their own
     constexpr int kParts = kF8 ? 1 : 2;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t scratch[W + 3];
+    __shared__ int64_t scratch[W + 4];
     __shared__ float row_scale[ROWS], warp_m[TW][ROWS], warp_l[TW][ROWS];
     __shared__ uint64_t full[S::kMaxStages][TW], empty[S::kMaxStages][TW];
     __shared__ int gave_up;
+    __shared__ Part queue[kQueue];         // the part in hand and those after it
+    __shared__ uint64_t told[kQueue];
+    __shared__ Run whole_run;
+    __shared__ Join join;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
     uint8_t *smem = smem_raw + (-smem_addr(smem_raw) & 1023u);                 // the swizzle's period
@@ -402,6 +485,7 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                 gdn::tc::mbar_init(&full[i][y], tensor_copies ? 1 : 32);
                 gdn::tc::mbar_init(&empty[i][y], R);
             }
+        for (int i = 0; i < kQueue; ++i) gdn::tc::mbar_init(&told[i], 1);
         gave_up = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -410,7 +494,21 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
     Run run = find_run(p, c, scratch);     // (synchronises: the barriers are set up)
 
     if (warp == W) {
-        produce<CACHE, D, NT, R>(p, run, c, k_map, v_map, dims, stages, polls, smem, full, empty, &gave_up);
+        const Ring left = produce<CACHE, D, NT, R>(p, run, c, k_map, v_map, dims, stages, polls, smem, full, empty, queue, told);
+        if (!left.ok && lane == 0) gave_up = 1;
+        __syncthreads();
+        if (gave_up) {
+            // No copy is left in flight when the block's memory is freed: consumers that kept up have waited for
+            // every stage; else what was issued is waited for (again bounded).
+            for (int i = 0; i < left.filled; ++i) {
+                // a stage's last fill completes its full barrier's phase with the parity of the next empty wait
+                const int at = left.slot - 1 - i;
+                gdn::tc::mbar_wait(&full[at < 0 ? at + stages : at][lane < TW ? lane : 0], at < 0 ? left.phase : left.phase ^ 1,
+                                   GDN_DEFAULT_WAIT_POLLS);
+            }
+            if (lane == 0) atomicAdd(&g_wait_timeouts, 1u);
+            fill_nan(p, run, c, ROWS);
+        }
         return;
     }
 
@@ -421,15 +519,35 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
     int slot = 0;
     unsigned phase = 0;
     bool ok = true;                        // every wait so far was in time
-    Join join = {0, 0, 0, 0};
     auto all_consumers = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory"); };
+    auto all_agree = [&](bool x) {         // the same, and whether x holds for all
+        int y;
+        asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %1, 0;\n\tbar.red.and.pred b, 1, %2, a;\n\tselp.s32 %0, 1, 0, b;\n\t}"
+                     : "=r"(y) : "r"((int)x), "n"(32 * W) : "memory");
+        return y != 0;
+    };
+    Queries<CACHE, D, NT, R> queries;
+    {
+        Run r = run;
+        Part first;
+        if (!next_part(p, r, c, first)) first.seq = -1;
+        if (tid == 0) {
+            queue[0] = first;
+            whole_run = run;
+            join = Join{0, 0, 0, 0};
+        }
+    }
+    all_consumers();
 
-    while (run.at < run.end) {
-        const Part part = next_part(p, run, c);
-        const int head = part.item / p.row_tiles, row0 = (part.item % p.row_tiles) * ROWS;
-        const int steps = (int)(part.u1 - part.u0);
-        load_queries<CACHE, D, NT, R>(p, part.seq, head, row0, q_parts, qs, row_scale);
-        all_consumers();
+    for (int turn = 0; queue[turn % kQueue].seq >= 0; ++turn) {
+        const Part &part = queue[turn % kQueue];
+        const int steps = (int)(part.u1 - part.u0), keys = part.keys;
+        for (int pass = 0; pass < queries.kPasses; pass += queries.kGo) {
+            queries.fetch(p, part, pass);
+            queries.put(p, pass, q_parts, qs, row_scale);
+        }
+        all_consumers();                   // (and the last part is done with)
+        const int row0 = part.item % p.row_tiles * ROWS;
 
         // this lane's rows: rg * 8 NT + 8 t + 2 c4 + j
         float m[NT][2], l[NT][2], rs[NT][2], o[D / 16][NT][4];
@@ -442,7 +560,7 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                 m[t][j] = kNegInf;
                 l[t][j] = 0.f;
                 rs[t][j] = row_scale[r];
-                seen[t][j] = keys_seen(p, part.keys, row0 + r);
+                seen[t][j] = keys_seen(p, keys, row0 + r);
             }
 #pragma unroll
         for (int x = 0; x < D / 16; ++x)
@@ -450,7 +568,7 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[x][t][j] = 0.f;
-        const int all_see = part.keys - (p.q_len - 1);         // keys that every row sees
+        const int all_see = keys - (p.q_len - 1);         // keys that every row sees
         const unsigned q_at = smem_addr(qs + (rg * 8 * NT + (lane & 7)) * S::kQPitch + (lane >> 3) * 16);
 
         int key0 = (int)((part.u0 * TW + tw) * S::kStep);
@@ -458,12 +576,12 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
         for (int i = 0; i < steps; ++i) {
             ok = ok && __all_sync(kFull, gdn::tc::mbar_wait(&full[slot][tw], phase, polls));
             const unsigned ks = ring + slot * S::kStage;
-            if (ok && key0 < part.keys) {
-                if (key0 + S::kStep > part.keys) {
+            if (ok && key0 < keys) {
+                if (key0 + S::kStep > keys) {
                     // past the sequence's end a page holds what it held before: 0 * NaN must not come of it
                     for (int x = lane; x < S::kStep * (S::kRowBytes / 16); x += 32) {
                         const int r = x / (S::kRowBytes / 16), b = x % (S::kRowBytes / 16) * 16;
-                        if (key0 + r >= part.keys)
+                        if (key0 + r >= keys)
                             *reinterpret_cast<uint4 *>(smem + (ks - smem_addr(smem)) + (KB + r / kKeys) * S::kBlockBytes +
                                                        S::place(r % kKeys, b)) = make_uint4(0, 0, 0, 0);
                     }
@@ -498,10 +616,8 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                                 ldsm4(w, S::across(k_at, x) + y * S::kBlockBytes);
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) {
-                                    a[h][0] = widen2((unsigned short)w[2 * h]);
-                                    a[h][1] = widen2((unsigned short)w[2 * h + 1]);
-                                    a[h][2] = widen2((unsigned short)(w[2 * h] >> 16));
-                                    a[h][3] = widen2((unsigned short)(w[2 * h + 1] >> 16));
+                                    widen4(w[2 * h], a[h][0], a[h][2]);
+                                    widen4(w[2 * h + 1], a[h][1], a[h][3]);
                                 }
                             } else {
                                 ldsm4(a[0], S::across(k_at, 2 * x) + y * S::kBlockBytes);
@@ -629,11 +745,8 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
 #pragma unroll
                                     for (int h = 0; h < 2; ++h) {
                                         // bytes of a word: keys 2c4, 2c4+1 of elements 2 l4, 2 l4 + 1
-                                        const unsigned e0 = __byte_perm(u[2 * h], 0, 0x3120), e1 = __byte_perm(u[2 * h + 1], 0, 0x3120);
-                                        a[2 * x + h][0] = widen2((unsigned short)e0);
-                                        a[2 * x + h][1] = widen2((unsigned short)(e0 >> 16));
-                                        a[2 * x + h][2] = widen2((unsigned short)e1);
-                                        a[2 * x + h][3] = widen2((unsigned short)(e1 >> 16));
+                                        widen4(__byte_perm(u[2 * h], 0, 0x3120), a[2 * x + h][0], a[2 * x + h][1]);
+                                        widen4(__byte_perm(u[2 * h + 1], 0, 0x3120), a[2 * x + h][2], a[2 * x + h][3]);
                                     }
                                 }
                             } else {
@@ -699,15 +812,30 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
             if (ok && lane == 0) arrive(&empty[slot][tw]);     // (after a failed wait nothing more may be copied)
             if (++slot == stages) { slot = 0; phase ^= 1; }
         }
-        if (!ok) {                         // copies that never came: the rows come out NaN
-#pragma unroll
-            for (int t = 0; t < NT; ++t) l[t][0] = l[t][1] = __int_as_float(0x7fc00000);
-            if (lane == 0) atomicExch(&gave_up, 1);
-        }
+        // the part after this one was told (a barrier of `told` completes for every kQueue-th part; the first is not told)
+        const int after = (turn + 1) % kQueue;
+        ok = ok && __all_sync(kFull, gdn::tc::mbar_wait(&told[after], ((turn + 1) / kQueue - (after == 0)) & 1, polls));
 
-        // add up the key warps' rows, some columns at a time
+        // add up the key warps' rows, some columns at a time: a task is four columns of a row
         const bool whole = part.begins && part.ends;
+        const int head = part.item / p.row_tiles;
         float *to = part_of(p, 2 * c + (part.begins ? 1 : 0));
+        constexpr int kQuads = S::kColumns / 4, kAll = ROWS * kQuads, kTasks = (kAll + W * 32 - 1) / (W * 32);
+        constexpr int kGroups = D / S::kColumns;
+        // the gates of kAhead groups of columns are loaded together (their latency, once)
+        constexpr int kAhead = kGroups * kTasks <= 4 ? kGroups : kTasks <= 2 ? 2 : 1;
+        float4 gate[kAhead][kTasks];
+        float share[kTasks][TW], norm[kTasks];
+        int64_t out_at[kTasks], gate_at[kTasks];
+        bool real[kTasks];
+#pragma unroll
+        for (int k = 0; k < kTasks; ++k) {
+            const int task = tid + k * W * 32, r = task / kQuads, row = row0 + r, token = row / p.group;
+            const int64_t r_at = (int64_t)part.seq * p.q_len + token, h_at = (int64_t)head * p.group + (row - token * p.group);
+            real[k] = task < kAll && row < group_rows;
+            out_at[k] = whole ? r_at * p.out_stride + h_at * D + 4 * (task % kQuads) : r * D + 4 * (task % kQuads);
+            gate_at[k] = r_at * p.gate_stride + h_at * p.gate_head_stride + 4 * (task % kQuads);
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -719,23 +847,16 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                 const int r = rg * 8 * NT + 8 * t + 2 * c4 + j;
                 if (l4 == 0) { warp_m[tw][r] = m[t][j]; warp_l[tw][r] = x; }
             }
-        constexpr int kQuads = S::kColumns / 4, kAll = ROWS * kQuads, kTasks = (kAll + W * 32 - 1) / (W * 32);
-        float4 gate[kTasks];
-        auto load_gates = [&](int x0) {
-#pragma unroll
-            for (int k = 0; k < kTasks; ++k) {
-                const int task = tid + k * W * 32, row = row0 + task / kQuads;
-                if (whole && p.gate != nullptr && task < kAll && row < group_rows) {
-                    const int token = row / p.group;
-                    gate[k] = load4(p.gate, ((int64_t)part.seq * p.q_len + token) * p.gate_stride +
-                                                ((int64_t)head * p.group + (row - token * p.group)) * p.gate_head_stride +
-                                                x0 + 4 * (task % kQuads), p.dtype, p.gate_vec);
-                }
-            }
-        };
-        load_gates(0);
 #pragma unroll
         for (int x0 = 0; x0 < D; x0 += S::kColumns) {
+            if (x0 / S::kColumns % kAhead == 0 && whole && p.gate != nullptr) {
+#pragma unroll
+                for (int k = 0; k < kTasks; ++k)
+#pragma unroll
+                    for (int y = 0; y < kAhead; ++y)
+                        if (real[k]) gate[y][k] = load4(p.gate, gate_at[k] + x0 + y * S::kColumns, p.dtype, p.gate_vec);
+            }
+            if (x0 > 0) all_consumers();   // the last columns are added up
 #pragma unroll
             for (int y = x0 / 16; y < (x0 + S::kColumns) / 16; ++y)
 #pragma unroll
@@ -746,49 +867,62 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                         for (int h = 0; h < 2; ++h)
                             sums[(tw * ROWS + rg * 8 * NT + 8 * t + 2 * c4 + j) * S::kSumPitch + 16 * y - x0 +
                                  (kF8 ? 2 * l4 + h : l4 + 8 * h)] = o[y][t][2 * h + j];
-            all_consumers();
+            if (x0 > 0) {
+                all_consumers();
+            } else if (!all_agree(ok)) {
+                ok = false;
+                break;
+            } else {                       // each warp's share of a row
+#pragma unroll
+                for (int k = 0; k < kTasks; ++k) {
+                    const int task = tid + k * W * 32, r = task / kQuads;
+                    if (!real[k]) continue;
+                    float top = kNegInf, total = 0.f;
+#pragma unroll
+                    for (int y = 0; y < TW; ++y) top = fmaxf(top, warp_m[y][r]);
+                    const float from = top == kNegInf ? 0.f : top;
+#pragma unroll
+                    for (int y = 0; y < TW; ++y) {
+                        share[k][y] = weight_of(warp_m[y][r], from);
+                        total = fmaf(share[k][y], warp_l[y][r], total);
+                    }
+                    norm[k] = total == 0.f ? 0.f : p.v_scale / total;
+                    if (task % kQuads == 0) {
+                        if (!whole) { to[ROWS * D + 2 * r] = top; to[ROWS * D + 2 * r + 1] = total; }
+                        else if (p.lse != nullptr) write_lse(p, part.seq, head, row0 + r, top, total);
+                    }
+                }
+            }
 #pragma unroll
             for (int k = 0; k < kTasks; ++k) {
-                const int task = tid + k * W * 32, r = task / kQuads, x = 4 * (task % kQuads);
-                if (task >= kAll || row0 + r >= group_rows) continue;
-                float top = kNegInf, total = 0.f;
-#pragma unroll
-                for (int y = 0; y < TW; ++y) top = fmaxf(top, warp_m[y][r]);
-                const float mm = top;
-                if (top == kNegInf) top = 0.f;
+                const int task = tid + k * W * 32;
+                if (!real[k]) continue;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int y = 0; y < TW; ++y) {
-                    const float share = weight_of(warp_m[y][r], top);
-                    total = fmaf(share, warp_l[y][r], total);
-                    const float4 v = *reinterpret_cast<const float4 *>(sums + (y * ROWS + r) * S::kSumPitch + x);
-                    a.x = fmaf(share, v.x, a.x);
-                    a.y = fmaf(share, v.y, a.y);
-                    a.z = fmaf(share, v.z, a.z);
-                    a.w = fmaf(share, v.w, a.w);
+                    const float4 v = *reinterpret_cast<const float4 *>(sums + (y * ROWS + task / kQuads) * S::kSumPitch +
+                                                                       4 * (task % kQuads));
+                    a.x = fmaf(share[k][y], v.x, a.x);
+                    a.y = fmaf(share[k][y], v.y, a.y);
+                    a.z = fmaf(share[k][y], v.z, a.z);
+                    a.w = fmaf(share[k][y], v.w, a.w);
                 }
                 if (whole) {
-                    const int token = (row0 + r) / p.group;
-                    const int64_t r_at = (int64_t)part.seq * p.q_len + token;
-                    const int64_t h_at = (int64_t)head * p.group + (row0 + r - token * p.group);
-                    finish4(p, a, total, gate[k]);
-                    store4(p.out, r_at * p.out_stride + h_at * D + x0 + x, p.out_dtype, p.out_vec, a);
-                    if (x0 + x == 0 && p.lse != nullptr) p.lse[r_at * p.nq + h_at] = lse_of(mm, total);
+                    finish4(p, a, norm[k], gate[x0 / S::kColumns % kAhead][k]);
+                    store4(p.out, out_at[k] + x0, p.out_dtype, p.out_vec, a);
                 } else {
-                    *reinterpret_cast<float4 *>(to + r * D + x0 + x) = a;
-                    if (x0 + x == 0) { to[ROWS * D + 2 * r] = mm; to[ROWS * D + 2 * r + 1] = total; }
+                    *reinterpret_cast<float4 *>(to + out_at[k] + x0) = a;
                 }
             }
-            if (x0 + S::kColumns < D) load_gates(x0 + S::kColumns);
-            all_consumers();
         }
-        if (part.begins && !part.ends) join = Join{part.seq, part.item, part.blocks, 0};
+        if (!ok) break;                    // (for all consumers alike)
+        if (tid == 0 && part.begins && !part.ends) join = Join{part.seq, part.item, part.blocks, 0};
     }
-    if (tid == 0) joins_of(p)[c] = join;
-    __syncthreads();                       // (the producer looks whether all waits were in time)
+    if (!ok && tid == 0) gave_up = 1;
+    __syncthreads();
+    if (gave_up) fill_nan(p, whole_run, c, ROWS);
+    else if (tid == 0) joins_of(p)[c] = join;
 }
-
-constexpr int kSmemBytes = 224 * 1024;     // of a block, beside its static arrays
 
 // The 4-D map of the cache's K or V: the elements of a head, then (token, head, page) in the order of
 // their strides; box: 16 tokens x a panel.  False where the layout does not allow it.
@@ -817,7 +951,7 @@ bool cache_map(const AttnParams &p, const void *base, CUtensorMap *map, MapDims 
     return encode(map, S::kElem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
                   const_cast<void *>(base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   S::kPanel == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  S::kRowBytes >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int CACHE, int D, int NT, int R>
@@ -825,28 +959,34 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
 {
     using S = Shape<CACHE, D, NT, R>;
     const bool bf16 = CACHE == GDNA_BF16;
-    // 16-bit parts that hold a query of its type: bf16 products have 8 bits a part, fp16 products 11
-    const int q_parts = p.dtype == GDNA_BF16 ? 1 : p.dtype == GDNA_F16 ? (bf16 ? 2 : 1) : (bf16 ? 3 : 2);
+    // 16-bit parts of a query: what its type holds (bf16 products have 8 bits a part, fp16 products 11), but for an
+    // fp32 query, a bf16 cache and a 16-bit output two parts: the scores' 2^-17 is far below the output's rounding
+    const int q_parts = p.dtype == GDNA_BF16 ? 1 : p.dtype == GDNA_F16 ? (bf16 ? 2 : 1) : (bf16 ? (p.out_dtype == GDNA_F32 ? 3 : 2) : 2);
     // and weights: to well below the output's rounding
     const int w_parts = (bf16 ? 2 : 1) + (p.out_dtype == GDNA_F32 || (CACHE != GDNA_BF16 && p.out_dtype == GDNA_F16));
     constexpr int kFixed = 1024 + S::kSumBytes;                // alignment of the ring; the sums
-    static_assert((kSmemBytes - kFixed - 3 * S::kRows * S::kQPitch) / (S::kKeyWarps * S::kStage) >= 2,
+    constexpr int kSmem = S::kSmem;
+    static_assert((kSmem - kFixed - 3 * S::kRows * S::kQPitch) / (S::kKeyWarps * S::kStage) >= 2,
                   "two stages whatever the queries' type");
     const int fixed = kFixed + q_parts * S::kRows * S::kQPitch;
-    const int room = (kSmemBytes - fixed) / (S::kKeyWarps * S::kStage);
+    const int room = (kSmem - fixed) / (S::kKeyWarps * S::kStage);
     const int stages = room < S::kMaxStages ? room : S::kMaxStages;
     p.unit = S::kStep * S::kKeyWarps;
+    // what an item costs beside its keys (queries, adding up, output), in bytes of keys that the block could read
+    // meanwhile: measured best at 64 KB for 8 rows of 128, 256 KB for 16 rows of 256
+    const int cost = S::kRows * D < 4096 ? S::kRows * D * 64 : 256 * 1024;
+    p.lead = cost / (S::kKeyWarps * S::kStage);
     p.page_div = Divisor::of((unsigned)p.cache.page_size);
     p.tile_rows = S::kRows;
     p.row_tiles = (int)(((int64_t)p.q_len * p.group + S::kRows - 1) / S::kRows);
-    const int sms = gdn::sm_count();
-    p.grid = sms < kMaxGrid ? sms : kMaxGrid;
+    const int blocks = gdn::sm_count() * S::kPerSm;
+    p.grid = blocks < kMaxGrid ? blocks : kMaxGrid;
     CUtensorMap k_map{}, v_map{};
     MapDims dims{};
     if (p.cache.page_size % kKeys != 0 || !cache_map<CACHE, D, NT, R>(p, p.k, &k_map, &dims) ||
         !cache_map<CACHE, D, NT, R>(p, p.v, &v_map, &dims))
         dims = MapDims{0, 0, 0};
-    cudaError_t e = gdn::allow_dynamic_smem<&attn_tc<CACHE, D, NT, R>>(kSmemBytes);
+    cudaError_t e = gdn::allow_dynamic_smem<&attn_tc<CACHE, D, NT, R>>(kSmem);
     if (e != cudaSuccess) return e;
     e = gdn::launch_early(attn_tc<CACHE, D, NT, R>, (unsigned)p.grid, S::kThreads, (size_t)(fixed + stages * S::kKeyWarps * S::kStage),
                           s, true, p, k_map, v_map, dims, stages, q_parts, w_parts, gdn::tc_copy_wait_polls());

@@ -79,6 +79,7 @@ struct AttnParams {
     int q_vec, gate_vec, out_vec;   // rows and heads start on boundaries of four elements
     // set by the launcher
     int unit;               // keys of one unit of work
+    int lead;               // units that an item costs beside its keys
     int tile_rows;          // query rows (token, head of the group) of one work item
     int row_tiles;          // ceil(q_len * group / tile_rows)
     int grid;               // blocks that share the work

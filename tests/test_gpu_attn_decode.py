@@ -267,3 +267,30 @@ def test_inputs_on_any_boundary(cuda_lib):
 def test_empty_calls(cuda_lib):
     gdn.gdna_attn_decode(0, 0, 0, 0, 0, 0, 0, batch=0, nq=2, nkv=1, d=64, pages=1, page_size=1, max_pages=1, dtype=0,
                          cache_dtype=1, out_dtype=0, workspace_bytes=0)
+
+
+@pytest.mark.parametrize("d,cache,page", [(128, "bf16", 16), (256, "f16", 64), (64, "e4m3", 32), (128, "f16", 24)])
+def test_a_wait_that_gives_up(cuda_lib, d, cache, page):
+    """With no polls every bounded wait gives up at once: rows come out NaN, the event is counted, nothing hangs, and
+    the next call is whole again."""
+    s = make([3000, 70, 1], 6, 2, d, q_len=2, cache=cache, page=page, seed=6, k_scale=0.125 if cache == "e4m3" else 1.0)
+    out = torch.zeros((6, 6 * d), device="cuda")
+    lse = torch.zeros((36,), device="cuda")
+    before = gdn.gdn_device_wait_timeouts()
+    try:
+        gdn.gdn_set_wait_polls(0)
+        call(s, out, lse)
+    finally:
+        gdn.gdn_set_wait_polls(gdn.GDN_DEFAULT_WAIT_POLLS)
+    assert gdn.gdn_device_wait_timeouts() > before
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+    before = gdn.gdn_device_wait_timeouts()
+    check(s, "f32", gated=True)
+    assert gdn.gdn_device_wait_timeouts() == before
+
+
+@pytest.mark.parametrize("d,cache,page", [(128, "bf16", 16), (256, "f16", 64), (64, "e4m3", 32), (128, "f16", 24)])
+def test_no_wait_gives_up_in_a_healthy_run(cuda_lib, d, cache, page):
+    before = gdn.gdn_device_wait_timeouts()
+    check(make([9000, 70, 0, 4000] * 8, 6, 2, d, cache=cache, page=page, seed=6, k_scale=0.125 if cache == "e4m3" else 1.0))
+    assert gdn.gdn_device_wait_timeouts() == before
