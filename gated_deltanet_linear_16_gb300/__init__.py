@@ -136,10 +136,26 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_current_stream = None      # the current stream's address, once torch has CUDA up
+
+
+def _first_current_stream():
+    """torch.cuda.current_stream(), which brings CUDA up, and from then on the query behind it: building the
+    Stream object costs 3 us a call, as much as a launch."""
+    global _current_stream
+    import torch
+    address = torch.cuda.current_stream().cuda_stream
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is not None and device is not None and raw(device()) == address:
+        _current_stream = lambda: raw(device())     # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream   # noqa: E731
+    return address
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return (_current_stream or _first_current_stream)()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

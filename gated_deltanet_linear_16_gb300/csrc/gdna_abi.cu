@@ -207,7 +207,13 @@ GDN_API int gdna_qk_norm_rope(const void *q, const void *k, const void *v, gdna_
     p.dtype = dtype; p.cache_dtype = cache_dtype; p.nq = nq; p.nkv = nkv; p.d = d; p.rot = rot;
     p.interleaved = interleaved != 0;
     p.eps = eps; p.k_scale = k_scale; p.v_scale = v_scale;
-    const bool fast = false;
+    // the vector kernel moves four elements at a time, eight a lane with the rotated ones in whole lanes
+    const int64_t c = elem_size(cache_dtype);
+    const bool fast = (d == 64 || d == 128 || d == 256) && rot % 8 == 0 &&
+                      rows_aligned(q, e, 4 * e, {q_stride, q_head_stride}) && rows_aligned(k, e, 4 * e, {k_stride}) &&
+                      rows_aligned(v, e, 4 * e, {v_stride}) && rows_aligned(q_out, e, 4 * e, {q_out_stride}) &&
+                      rows_aligned(k_out, e, 4 * e, {k_out_stride}) && aligned(qn, 16) && aligned(kn, 16) && aligned(cos_sin, 16) &&
+                      (!caching || (rows_aligned(k_cache, c, 4 * c, {page_stride, token_stride, head_stride}) && aligned(v_cache, 4 * c)));
     return gdn::report_cuda_error(launch_qk_norm_rope(p, fast, (cudaStream_t)stream));
 }
 

@@ -49,6 +49,7 @@ struct PageParams {
     int32_t *positions, *free_head_out, *unserved;
     int64_t rows;
     int batch, page_size, max_pages;
+    Divisor page_div;       // by the page size (set by the launcher)
 };
 
 struct RopeParams {
@@ -62,6 +63,7 @@ struct RopeParams {
     CacheLayout cache;
     int dtype, cache_dtype, nq, nkv, d, rot, interleaved;
     float eps, k_scale, v_scale;
+    Divisor page_div;       // by the page size (set by the launcher)
 };
 
 struct AttnParams {
@@ -86,7 +88,7 @@ struct AttnParams {
     Divisor page_div;       // by the page size
 };
 
-cudaError_t launch_page_assign(const PageParams &p, cudaStream_t s);
+cudaError_t launch_page_assign(PageParams p, cudaStream_t s);
 cudaError_t launch_qk_norm_rope(const RopeParams &p, bool fast, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnParams &p, bool fast, cudaStream_t s);
 // Bounded waits of the attention kernels that ran out on the current device.

@@ -49,6 +49,7 @@ page_assign(const PageParams p)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t lo = (int64_t)blockIdx.x * kTile, hi = min(lo + kTile, p.rows);
     const bool last = blockIdx.x == gridDim.x - 1;
+    gdn::early_start<true>(nullptr, 0);
     const int64_t head = *p.free_head, P = p.page_size;
     if (tid == 0) { top = 0; refused = 0; }
 
@@ -63,7 +64,8 @@ page_assign(const PageParams p)
             c = max(p.cached[b], 0);
             f = max(p.fresh[b], 0);
         }
-        const int64_t have = (c + P - 1) / P, want = (c + f + P - 1) / P;
+        auto pages_of = [&](int64_t n) { return n > 0 ? (int64_t)p.page_div.quotient((unsigned)(n - 1)) + 1 : 0; };
+        const int64_t have = pages_of(c), want = c + f <= INT32_MAX ? pages_of(c + f) : INT32_MAX;
         const bool fits = f == 0 || (want <= p.max_pages && c + f <= INT32_MAX);
         const int64_t need = fits ? want - have : 0;
 
@@ -138,7 +140,7 @@ page_assign(const PageParams p)
             const int64_t at = e.cached + ((int64_t)r - e.start);
             pos = (int)min(at, (int64_t)INT32_MAX);
             if (e.first >= 0) {
-                const int64_t pg = at / P, in_page = at - pg * P;
+                const int64_t pg = p.page_div.quotient((unsigned)pos), in_page = pos - pg * P;
                 int32_t *entry = p.table + e.seq * p.table_stride + pg;
                 int64_t page;
                 if (pg < e.have) {
@@ -157,11 +159,11 @@ page_assign(const PageParams p)
 
 }  // namespace
 
-cudaError_t launch_page_assign(const PageParams &p, cudaStream_t s)
+cudaError_t launch_page_assign(PageParams p, cudaStream_t s)
 {
     const int64_t tiles = (p.rows + kTile - 1) / kTile;
-    page_assign<<<(unsigned)(tiles > 0 ? tiles : 1), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    p.page_div = Divisor::of((unsigned)p.page_size);
+    return gdn::launch_early(page_assign, (unsigned)(tiles > 0 ? tiles : 1), kThreads, 0, s, true, p);
 }
 
 }  // namespace gdna
