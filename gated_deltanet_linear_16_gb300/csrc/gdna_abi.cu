@@ -281,8 +281,7 @@ GDN_API int gdna_attn_decode(const void *q, gdna_dtype dtype, const void *gate,
     p.out_vec = rows_aligned(out, elem_size(out_dtype), 4 * elem_size(out_dtype), {out_stride, d});
     // the tensor-core kernel copies a key's head in 16-byte pieces
     const int64_t e = elem_size(cache_dtype);
-    const bool fast = (d == 64 || d == 128 || d == 256) &&
-                      rows_aligned(k_cache, e, 16, {page_stride, token_stride, head_stride}) && aligned(v_cache, 16);
+    const bool fast = d * e % 16 == 0 && rows_aligned(k_cache, e, 16, {page_stride, token_stride, head_stride}) && aligned(v_cache, 16);
     return gdn::report_cuda_error(launch_attn_decode(p, fast, (cudaStream_t)stream));
 }
 

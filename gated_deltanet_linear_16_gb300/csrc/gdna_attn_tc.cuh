@@ -1,5 +1,5 @@
 // gdna_attn_tc.cuh -- paged decode attention on the tensor cores (head sizes 64,
-// 128 and 256): the kernel's template.  gdna_attn.cuh has the deal of the work and
+// 128 and 256, and those in between): the kernel's template.  gdna_attn.cuh has the deal of the work and
 // the partial results.
 //
 // Mathematics.  With few query rows (8 to 64: the tokens and the group's heads) and
@@ -18,10 +18,9 @@
 // Rounding.  K and V are exact in the products (E4M3 widens to fp16 exactly).  The
 // queries enter in as many 16-bit parts as their type needs (`q_parts`: x = hi + lo
 // [+ lower]), scaled by a power of two per row for fp16 products, so that no query
-// over- or underflows.  The weights exp2(s - m) <= 1 enter in as many parts as put
-// their rounding well below the output's (`w_parts`): bf16 products take two (one part's 2^-9
-// would be as large as a bf16 output's own), three for an fp32 output; fp16 products one
-// (2^-12), two for fp16 and fp32 outputs.  m, l, S and O are fp32.
+// over- or underflows.  The weights exp2(s - m) <= 1 enter in two
+// parts, three where bf16 products give an fp32 output: one part's 2^-9 (2^-12 in fp16), relative to the largest
+// values, would show where sums cancel.  m, l, S and O are fp32.
 //
 // What a row does not see.  Masked scores are replaced, not added to.  Keys past the
 // sequence's end are not loaded (zeros stand for them).  The keys that some tokens see
@@ -29,16 +28,20 @@
 // carry them into rows that do not see them: there a tile with a non-finite V adds its
 // rows key by key instead.
 //
-// Data.  A block is one producer warp and W consumer warps.  The
-// producer walks the block's parts on its own and keeps the rings full: it is already
+// Data.  A block is some producer warps and W consumer warps.  A
+// producer walks the block's parts on its own and keeps its rings full: it is already
 // copying the next item's keys while the consumers finish the last one's rows.  Each
 // consumer warp (or the R warps that share keys, each with its own rows) has a ring of
 // stages in shared memory, a step's K and V each, with a full and an empty mbarrier a
 // stage.  Rows lie in panels of 128 bytes with the 128-byte swizzle (64 with the 64-byte
 // one), so eight rows of an ldmatrix start in eight different bank groups.
-//   Where pages hold a multiple of 16 keys, a block of 16 keys lies in one page and a tensor
-// copy brings a panel of it: the (copy, consumer) pairs of a step are one lane each.
-// Otherwise the producer's lanes copy 16 bytes at a time (cp.async) to the same layout.
+//   A tensor copy brings as many keys as surely lie in one page, 16 or a smaller power of two
+// that divides the page size, one lane a copy; 16 keys come with all panels of a head at once
+// (a producer pays some 40 ns a copy, one after the other).  Where that makes more than 32
+// copies (short pages), and for layouts that the encoder refuses, the producer's lanes copy 16
+// bytes at a time (cp.async) to the same places.
+// Head sizes in between run padded to the next of the three: a copy fills what lies past a
+// head with zeros.
 #pragma once
 
 #include <cuda.h>
@@ -86,12 +89,12 @@ __device__ __forceinline__ void cp_async16(unsigned dst, const void *src, bool r
     const int n = real ? 16 : 0;           // 0: sixteen zero bytes, nothing is read
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-// A panel of 16 keys: {x, c1, c2, c3} are the map's coordinates.
-__device__ __forceinline__ void copy_panel(unsigned dst, const CUtensorMap *map, int x, int c1, int c2, int c3, unsigned bar)
+// Some keys of a head, from element x on; the map's other dimension is the panel.
+__device__ __forceinline__ void copy_keys(unsigned dst, const CUtensorMap *map, int x, int token, int head, int page, unsigned bar)
 {
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4, %5}], [%6];"
-                 ::"r"(dst), "l"(map), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(token), "r"(0), "r"(head), "r"(page), "r"(bar) : "memory");
 }
 // A hint only: nothing is read.
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -161,23 +164,26 @@ template <int CACHE, int D, int NT, int R> struct Shape {
     static constexpr int kPanels = kRowBytes / kPanel;
     static constexpr int kPanelBytes = kKeys * kPanel;
     static constexpr int kBlockBytes = kKeys * kRowBytes;      // K, or V, of a block
-    // Blocks of 16 keys a step.  Short rows take two: the maximum's shuffles, the barriers and the
-    // loop are then paid once for 32 keys.
-    static constexpr int kBlocks = kRowBytes <= 128 ? 2 : 1;
+    // Blocks of 16 keys a step.  Two where three stages of them fit a ring: the maximum's shuffles, the
+    // barriers and the loop are then paid once for 32 keys (256 requests over an E4M3 cache: 158 us against
+    // 212; 32 rows, bf16, D 128: 88 against 106).
+    static constexpr int kBlocks = kRowBytes <= 128 || (kRowBytes == 256 && R >= 2) || R >= 4 ? 2 : 1;
     static constexpr int kStep = kKeys * kBlocks;
     static constexpr int kStage = 2 * kBlocks * kBlockBytes;   // K's blocks, then V's
     // Blocks on an SM.  Rows up to 256 bytes: two, so that one reads on while the other goes from an item to the
     // next (256 requests over an E4M3 cache, D 128: 104 us against 119 with one block of eight consumers; 32 requests
     // over a bf16 cache, D 128: 100.9 against 102.5).  Longer rows: one, whose rings hold more (262144 keys, D 256:
     // 167 us against 177 with two).
-    static constexpr int kPerSm = kRowBytes <= 256 && !(NT == 2 && D >= 128) ? 2 : 1;
-    // Consumers: 168 registers each; four in a block (255 registers) where two row tiles of a large head need
-    // them, or where eight rings of such long rows would hold one stage.
-    static constexpr int kWarps = kPerSm == 2 || (kRowBytes == 512 && R == 1) || (NT == 2 && D >= 128) ? 4 : 8;
+    static constexpr int kPerSm = kRowBytes <= 256 && R <= 4 ? 2 : 1;
+    // Consumers on an SM: eight, with 168 registers each; four (255 registers) where eight rings of such long rows
+    // would hold one stage.
+    static constexpr int kWarps = kPerSm == 2 || (kRowBytes == 512 && R == 1) ? 4 : 8;
     static constexpr int kKeyWarps = kWarps / R;
     static constexpr int kRows = 8 * NT * R;
-    static constexpr int kThreads = 32 * (kWarps + 1);
-    static constexpr int kCopies = 2 * kBlocks * kPanels;      // tensor copies of a stage
+    // Producers, each for its own rings: at most as many warps as leave the consumers their registers.
+    static constexpr int kProducers = kKeyWarps < (kPerSm == 2 ? 2 : 4) ? kKeyWarps : kPerSm == 2 ? 2 : 4;
+    static constexpr int kThreads = 32 * (kWarps + kProducers);
+    static constexpr int kCopies = 2 * kBlocks;                // blocks of K and V of a stage
     static constexpr int kQPitch = 2 * D + 16;
     // the consumers' sums are added up some columns at a time: 64 where three stages fit beside them
     static constexpr int kSmem = kPerSm == 2 ? kSmemTwo : kSmemOne;
@@ -185,7 +191,7 @@ template <int CACHE, int D, int NT, int R> struct Shape {
     static constexpr int kSumPitch = kColumns + 4;             // floats
     static constexpr int kSumBytes = kKeyWarps * kRows * kSumPitch * 4;
     static constexpr int kMaxStages = 6;
-    static_assert(kKeyWarps * kCopies <= 32, "a lane for each copy of a step");
+    static_assert(kKeyWarps * kCopies <= 32, "a lane for each block of a step");
 
     // Swizzled place of byte `b` of row `r` in a block.
     __device__ __forceinline__ static unsigned place(unsigned r, unsigned b)
@@ -221,10 +227,10 @@ template <int CACHE, int D, int NT, int R> struct Queries {
             const int r = ((pass + k) * S::kWarps + warp) * kPerWarp + lane / kLanes, row = row0 + r;
 #pragma unroll
             for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
-            if (r < kRows && row < p.q_len * p.group) {
+            if (r < kRows && row < p.q_len * p.group && (lane % kLanes) * 8 < p.d) {
                 const int token = row / p.group;
                 const int64_t from = ((int64_t)part.seq * p.q_len + token) * p.q_stride +
-                                     ((int64_t)head * p.group + (row - token * p.group)) * D + (lane % kLanes) * 8;
+                                     ((int64_t)head * p.group + (row - token * p.group)) * p.d + (lane % kLanes) * 8;
                 const float4 a = load4(p.q, from, p.dtype, p.q_vec), b = load4(p.q, from + 4, p.dtype, p.q_vec);
                 x[k][0] = a.x; x[k][1] = a.y; x[k][2] = a.z; x[k][3] = a.w;
                 x[k][4] = b.x; x[k][5] = b.y; x[k][6] = b.z; x[k][7] = b.w;
@@ -277,12 +283,13 @@ template <int CACHE, int D, int NT, int R> struct Queries {
     }
 };
 
-// How the tensor maps number the cache's dimensions after the elements of a head.
-struct MapDims {
-    int token, head, page;                 // 1 .. 3
+// The tensor copies: how many keys one brings (those that lie in one page wherever pages begin: 16, or a smaller power
+// of two that divides the page size; 0: no tensor copies), and in how many pieces a head comes.
+struct Copies {
+    int keys, pieces;
 };
 
-// What the producer leaves behind: the next stage, the parity of its empty barrier's next wait, and how many of
+// What a producer leaves behind: the next stage, the parity of its empty barrier's next wait, and how many of
 // the stages before it were filled (at most all).
 struct Ring {
     int slot, filled;
@@ -290,11 +297,11 @@ struct Ring {
     bool ok;                               // every wait was in time
 };
 
-// The producer warp: fills the consumers' rings, part after part, and tells them the parts after the first, in
-// `queue`, as it comes to them; a part of no sequence ends them.
+// Producer warp `who` of P: fills the rings of consumers who, who + P, .., part after part.  The first one tells
+// the consumers the parts after the first, in `queue`, as it comes to them; a part of no sequence ends them.
 template <int CACHE, int D, int NT, int R>
-__device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, const CUtensorMap &k_map, const CUtensorMap &v_map,
-                                        const MapDims dims, int stages, unsigned polls, uint8_t *smem,
+__device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, int who, int P, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                        const Copies copies, int stages, unsigned polls, uint8_t *smem,
                                         uint64_t (*full)[Shape<CACHE, D, NT, R>::kKeyWarps],
                                         uint64_t (*empty)[Shape<CACHE, D, NT, R>::kKeyWarps], Part *queue, uint64_t *told)
 {
@@ -309,10 +316,10 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, con
     // The steps of the block's parts in order.  Pages are looked up a step before they are needed, also from
     // one part to the next: a load's latency there would leave the rings dry.  What a stage's refill waits for
     // is short for the same reason.
-    const int y = dims.page != 0 ? lane / S::kCopies : 0;      // the consumer this lane looks up for
-    const int copy = lane % S::kCopies;
-    const int panel = copy % S::kPanels, block = copy / S::kPanels % KB, values = copy / (S::kPanels * KB);
-    const unsigned first = dims.page != 0 ? y * S::kStep + block * kKeys : lane % S::kStep;      // its key of a unit
+    // lane: a copy of a unit, some keys of a block of K or V for consumer y (or, without tensor copies, a key of each)
+    const int per = copies.keys != 0 ? S::kCopies * (kKeys / copies.keys) : 32;
+    const int y = who + lane / per * P, copy = lane % per, block = copy % KB, values = copy / KB % 2, row = copy / S::kCopies * copies.keys;
+    const unsigned first = copies.keys != 0 ? y * S::kStep + block * kKeys + row : who * S::kStep + lane % S::kStep;     // its key of a unit
     int left = 0, head = 0;                // steps of the part that are not looked up; its key head
     unsigned key = 0, keys = 0;            // the key to look up next, the sequence's keys
     const int32_t *table = nullptr;
@@ -321,7 +328,7 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, con
     auto enter = [&]() {                   // the next part
         more = fresh = next_part(p, run, c, part);
         if (!more) part.seq = -1;
-        if (lane == 0 && entered > 0) {
+        if (who == 0 && lane == 0 && entered > 0) {
             queue[entered % kQueue] = part;
             arrive(&told[entered % kQueue]);
         }
@@ -335,13 +342,14 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, con
     };
     auto warm = [&]() {                    // its query and gate rows on their way to the L2, before they are asked for
         fresh = false;
+        if (who != P - 1) return;
         const int elem = p.dtype == GDNA_F32 ? 4 : 2;
         const int row0 = (part.item - head * p.row_tiles) * S::kRows, rows = min(S::kRows, p.q_len * p.group - row0);
         for (int r = lane >> 2; r < rows; r += 8) {            // four lanes a row, a line of 128 bytes each at a time
             const int row = row0 + r, token = row / p.group;
             const int64_t n = (int64_t)part.seq * p.q_len + token, h = (int64_t)head * p.group + (row - token * p.group);
-            for (int at = (lane & 3) * 128; at < D * elem; at += 512) {
-                prefetch_l2(static_cast<const uint8_t *>(p.q) + (n * p.q_stride + h * D) * elem + at);
+            for (int at = (lane & 3) * 128; at < p.d * elem; at += 512) {
+                prefetch_l2(static_cast<const uint8_t *>(p.q) + (n * p.q_stride + h * p.d) * elem + at);
                 if (p.gate != nullptr)
                     prefetch_l2(static_cast<const uint8_t *>(p.gate) + (n * p.gate_stride + h * p.gate_head_stride) * elem + at);
             }
@@ -349,13 +357,12 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, con
     };
     enter();
 
-    if (dims.page != 0) {
+    if (copies.keys != 0) {
         const bool mine = y < TW;
-        const unsigned dst = ring + (mine ? y : 0) * stages * S::kStage + (values * KB + block) * S::kBlockBytes +
-                             panel * S::kPanelBytes;
+        const unsigned dst = ring + (mine ? y : 0) * stages * S::kStage + (values * KB + block) * S::kBlockBytes + row * S::kPanel;
         const CUtensorMap *map = values ? &v_map : &k_map;
         int page = 0, token = 0;
-        auto look_up = [&]() {             // this lane's block of the step; past the cache (zeros) if there is none
+        auto look_up = [&]() {             // past the cache (zeros) if there is no such page
             page = -1;
             token = 0;
             if (mine && key < keys) {
@@ -366,10 +373,7 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, con
         };
         if (more) look_up();
         while (more) {
-            const int at = (unsigned)page < (unsigned)p.cache.pages ? page : (int)p.cache.pages;
-            const int c1 = dims.token == 1 ? token : dims.head == 1 ? head : at;
-            const int c2 = dims.token == 2 ? token : dims.head == 2 ? head : at;
-            const int c3 = dims.token == 3 ? token : dims.head == 3 ? head : at;
+            const int at = (unsigned)page < (unsigned)p.cache.pages ? page : (int)p.cache.pages, from = token, of = head;
             key += TW * S::kStep;
             if (--left == 0) enter();
             if (more) look_up();
@@ -378,7 +382,9 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, con
             if (mine && copy == 0) arrive_expect(&full[slot][y], S::kStage);
             __syncwarp();
             if (mine)
-                copy_panel(dst + slot * S::kStage, map, panel * (S::kPanel / S::kElem), c1, c2, c3, smem_addr(&full[slot][y]));
+                for (int z = 0; z < copies.pieces; ++z)
+                    copy_keys(dst + slot * S::kStage + z * S::kPanelBytes, map, z * (S::kPanel / S::kElem), from, of, at,
+                              smem_addr(&full[slot][y]));
             filled = min(filled + 1, stages);
             if (++slot == stages) { slot = 0; phase ^= 1; }
             if (fresh) warm();
@@ -401,10 +407,11 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, con
         while (more && ok) {
             const int64_t base = (int64_t)head * p.cache.head_stride * S::kElem;
             const uint8_t *kb = static_cast<const uint8_t *>(p.k) + base, *vb = static_cast<const uint8_t *>(p.v) + base;
-            for (int z = 0; z < TW && ok; ++z) {
+            for (int z = who; z < TW && ok; z += P) {
                 const int64_t at = (unsigned)page < (unsigned)p.cache.pages ? page * page_bytes + place * token_bytes : -1;
-                key += S::kStep;
-                if (z + 1 == TW && --left == 0) enter();
+                const bool last = z + P >= TW;
+                key += (last ? TW - (z - who) : P) * S::kStep;
+                if (last && --left == 0) enter();
                 if (more) look_up();
                 ok = __all_sync(kFull, gdn::tc::mbar_wait(&empty[slot][z], phase, polls));
                 if (!ok) break;
@@ -413,9 +420,10 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, con
                 for (int r = 0; r < S::kStep; r += kAtOnce) {
                     const int row = r + sub;
                     const int64_t from = __shfl_sync(kFull, at, row);
+                    const bool on = from >= 0 && piece < p.d * S::kElem;
                     const unsigned dst = to + row / kKeys * S::kBlockBytes + S::place(row % kKeys, piece);
-                    cp_async16(dst, kb + (from >= 0 ? from + piece : 0), from >= 0);
-                    cp_async16(dst + KB * S::kBlockBytes, vb + (from >= 0 ? from + piece : 0), from >= 0);
+                    cp_async16(dst, kb + (on ? from + piece : 0), on);
+                    cp_async16(dst + KB * S::kBlockBytes, vb + (on ? from + piece : 0), on);
                 }
                 arrive_copies(&full[slot][z]);
             }
@@ -455,16 +463,15 @@ static __device__ __noinline__ void fill_nan(const AttnParams &p, Run run, int c
 template <int CACHE, int D, int NT, int R>
 __global__ void __launch_bounds__(Shape<CACHE, D, NT, R>::kThreads, Shape<CACHE, D, NT, R>::kPerSm)
 attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-        const MapDims dims, const int stages, const int q_parts, const int w_parts, const unsigned polls)
+        const Copies copies, const int stages, const int q_parts, const int w_parts, const unsigned polls)
 {
     using S = Shape<CACHE, D, NT, R>;
     using O = Op<CACHE>;
     constexpr bool kF8 = CACHE == GDNA_E4M3;
     constexpr int W = S::kWarps, TW = S::kKeyWarps, ROWS = S::kRows, KB = S::kBlocks;
-    // weight parts of the products proper; more follow in passes of their own
-    constexpr int kParts = kF8 ? 1 : 2;
+    constexpr int kParts = 2;              // of the weights; a third follows in a pass of its own
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t scratch[W + 4];
+    __shared__ int64_t scratch[S::kThreads / 32 + 3];
     __shared__ float row_scale[ROWS], warp_m[TW][ROWS], warp_l[TW][ROWS];
     __shared__ uint64_t full[S::kMaxStages][TW], empty[S::kMaxStages][TW];
     __shared__ int gave_up;
@@ -477,7 +484,7 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
     uint8_t *smem = smem_raw + (-smem_addr(smem_raw) & 1023u);                 // the swizzle's period
     uint8_t *qs = smem + TW * stages * S::kStage;
     float *sums = reinterpret_cast<float *>(qs + q_parts * ROWS * S::kQPitch); // [TW][ROWS][kSumPitch]
-    const bool tensor_copies = dims.page != 0;
+    const bool tensor_copies = copies.keys != 0;
 
     if (tid == 0) {
         for (int i = 0; i < stages; ++i)
@@ -493,20 +500,21 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
     gdn::early_start<true>(nullptr, 0);
     Run run = find_run(p, c, scratch);     // (synchronises: the barriers are set up)
 
-    if (warp == W) {
-        const Ring left = produce<CACHE, D, NT, R>(p, run, c, k_map, v_map, dims, stages, polls, smem, full, empty, queue, told);
+    if (warp >= W) {
+        const Ring left = produce<CACHE, D, NT, R>(p, run, c, warp - W, blockDim.x / 32 - W, k_map, v_map, copies, stages, polls, smem, full, empty, queue, told);
         if (!left.ok && lane == 0) gave_up = 1;
         __syncthreads();
         if (gave_up) {
             // No copy is left in flight when the block's memory is freed: consumers that kept up have waited for
             // every stage; else what was issued is waited for (again bounded).
+            const int mine = warp - W + lane * (blockDim.x / 32 - W), y = mine < TW ? mine : warp - W;
             for (int i = 0; i < left.filled; ++i) {
                 // a stage's last fill completes its full barrier's phase with the parity of the next empty wait
                 const int at = left.slot - 1 - i;
-                gdn::tc::mbar_wait(&full[at < 0 ? at + stages : at][lane < TW ? lane : 0], at < 0 ? left.phase : left.phase ^ 1,
+                gdn::tc::mbar_wait(&full[at < 0 ? at + stages : at][y], at < 0 ? left.phase : left.phase ^ 1,
                                    GDN_DEFAULT_WAIT_POLLS);
             }
-            if (lane == 0) atomicAdd(&g_wait_timeouts, 1u);
+            if (warp == W && lane == 0) atomicAdd(&g_wait_timeouts, 1u);
             fill_nan(p, run, c, ROWS);
         }
         return;
@@ -833,7 +841,7 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
             const int task = tid + k * W * 32, r = task / kQuads, row = row0 + r, token = row / p.group;
             const int64_t r_at = (int64_t)part.seq * p.q_len + token, h_at = (int64_t)head * p.group + (row - token * p.group);
             real[k] = task < kAll && row < group_rows;
-            out_at[k] = whole ? r_at * p.out_stride + h_at * D + 4 * (task % kQuads) : r * D + 4 * (task % kQuads);
+            out_at[k] = whole ? r_at * p.out_stride + h_at * p.d + 4 * (task % kQuads) : r * p.d + 4 * (task % kQuads);
             gate_at[k] = r_at * p.gate_stride + h_at * p.gate_head_stride + 4 * (task % kQuads);
         }
 #pragma unroll
@@ -849,12 +857,14 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
             }
 #pragma unroll
         for (int x0 = 0; x0 < D; x0 += S::kColumns) {
+            if (x0 >= p.d) break;
             if (x0 / S::kColumns % kAhead == 0 && whole && p.gate != nullptr) {
 #pragma unroll
                 for (int k = 0; k < kTasks; ++k)
 #pragma unroll
                     for (int y = 0; y < kAhead; ++y)
-                        if (real[k]) gate[y][k] = load4(p.gate, gate_at[k] + x0 + y * S::kColumns, p.dtype, p.gate_vec);
+                        if (real[k] && x0 + y * S::kColumns + 4 * ((tid + k * W * 32) % kQuads) < p.d)
+                            gate[y][k] = load4(p.gate, gate_at[k] + x0 + y * S::kColumns, p.dtype, p.gate_vec);
             }
             if (x0 > 0) all_consumers();   // the last columns are added up
 #pragma unroll
@@ -888,7 +898,7 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                     }
                     norm[k] = total == 0.f ? 0.f : p.v_scale / total;
                     if (task % kQuads == 0) {
-                        if (!whole) { to[ROWS * D + 2 * r] = top; to[ROWS * D + 2 * r + 1] = total; }
+                        if (!whole) { to[ROWS * p.d + 2 * r] = top; to[ROWS * p.d + 2 * r + 1] = total; }
                         else if (p.lse != nullptr) write_lse(p, part.seq, head, row0 + r, top, total);
                     }
                 }
@@ -896,7 +906,7 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
 #pragma unroll
             for (int k = 0; k < kTasks; ++k) {
                 const int task = tid + k * W * 32;
-                if (!real[k]) continue;
+                if (!real[k] || x0 + 4 * (task % kQuads) >= p.d) continue;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int y = 0; y < TW; ++y) {
@@ -924,34 +934,34 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
     else if (tid == 0) joins_of(p)[c] = join;
 }
 
-// The 4-D map of the cache's K or V: the elements of a head, then (token, head, page) in the order of
-// their strides; box: 16 tokens x a panel.  False where the layout does not allow it.
+// The map of the cache's K or V: elements of a panel, token, panel, head, page; box: `keys` tokens x all panels of a
+// head, which is how they lie in a stage.  Fewer than 16 keys, and a head that ends within a panel, come panel by
+// panel, the head's elements the first dimension and the panel none: what lies past the head is filled with zeros.  False where the encoder
+// refuses the layout.
 template <int CACHE, int D, int NT, int R>
-bool cache_map(const AttnParams &p, const void *base, CUtensorMap *map, MapDims *dims)
+bool cache_map(const AttnParams &p, const void *base, const Copies &copies, CUtensorMap *map)
 {
     using S = Shape<CACHE, D, NT, R>;
     const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn::tensor_map_encoder());
     if (encode == nullptr) return false;
-    struct Dim { int64_t stride, count; int box, *number; } d[3] = {
-        {p.cache.token_stride, p.cache.page_size, kKeys, &dims->token},
-        {p.cache.head_stride, p.nkv, 1, &dims->head},
-        {p.cache.page_stride, p.cache.pages, 1, &dims->page}};
-    std::sort(d, d + 3, [](const Dim &a, const Dim &b) { return a.stride < b.stride; });
-    cuuint64_t size[4] = {(cuuint64_t)D}, stride[3];
-    cuuint32_t box[4] = {(cuuint32_t)(S::kPanel / S::kElem)};
-    const cuuint32_t step[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 3; ++i) {
-        const int64_t bytes = d[i].stride * S::kElem;
+    constexpr int kPanelElems = S::kPanel / S::kElem;
+    const bool whole = copies.pieces == 1;
+    const int64_t strides[4] = {p.cache.token_stride, kPanelElems, p.cache.head_stride, p.cache.page_stride};
+    const cuuint64_t size[5] = {(cuuint64_t)(whole ? kPanelElems : p.d), (cuuint64_t)p.cache.page_size,
+                                (cuuint64_t)(whole ? p.d / kPanelElems : 1), (cuuint64_t)p.nkv, (cuuint64_t)p.cache.pages};
+    const cuuint32_t box[5] = {(cuuint32_t)kPanelElems, (cuuint32_t)copies.keys, (cuuint32_t)(whole ? S::kPanels : 1), 1, 1};
+    const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+    cuuint64_t stride[4];
+    for (int i = 0; i < 4; ++i) {
+        const int64_t bytes = strides[i] * S::kElem;
         if (bytes <= 0 || bytes >= (int64_t{1} << 40)) return false;
-        size[i + 1] = (cuuint64_t)d[i].count;
         stride[i] = (cuuint64_t)bytes;
-        box[i + 1] = (cuuint32_t)d[i].box;
-        *d[i].number = i + 1;
     }
-    return encode(map, S::kElem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
+    return encode(map, S::kElem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 5,
                   const_cast<void *>(base), size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   S::kPanel == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  S::kRowBytes >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  S::kRowBytes >= 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int CACHE, int D, int NT, int R>
@@ -962,8 +972,8 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
     // 16-bit parts of a query: what its type holds (bf16 products have 8 bits a part, fp16 products 11), but for an
     // fp32 query, a bf16 cache and a 16-bit output two parts: the scores' 2^-17 is far below the output's rounding
     const int q_parts = p.dtype == GDNA_BF16 ? 1 : p.dtype == GDNA_F16 ? (bf16 ? 2 : 1) : (bf16 ? (p.out_dtype == GDNA_F32 ? 3 : 2) : 2);
-    // and weights: to well below the output's rounding
-    const int w_parts = (bf16 ? 2 : 1) + (p.out_dtype == GDNA_F32 || (CACHE != GDNA_BF16 && p.out_dtype == GDNA_F16));
+    // and weights: 16 bits or more, 22 or more for an fp32 output
+    const int w_parts = bf16 && p.out_dtype == GDNA_F32 ? 3 : 2;
     constexpr int kFixed = 1024 + S::kSumBytes;                // alignment of the ring; the sums
     constexpr int kSmem = S::kSmem;
     static_assert((kSmem - kFixed - 3 * S::kRows * S::kQPitch) / (S::kKeyWarps * S::kStage) >= 2,
@@ -982,25 +992,46 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
     const int blocks = gdn::sm_count() * S::kPerSm;
     p.grid = blocks < kMaxGrid ? blocks : kMaxGrid;
     CUtensorMap k_map{}, v_map{};
-    MapDims dims{};
-    if (p.cache.page_size % kKeys != 0 || !cache_map<CACHE, D, NT, R>(p, p.k, &k_map, &dims) ||
-        !cache_map<CACHE, D, NT, R>(p, p.v, &v_map, &dims))
-        dims = MapDims{0, 0, 0};
+    Copies copies{p.cache.page_size & -p.cache.page_size, S::kPanels};
+    if (copies.keys >= kKeys) copies = Copies{kKeys, p.d * S::kElem % S::kPanel == 0 ? 1 : S::kPanels};
+    // Producers by the copies of a unit.  D 256, 262144 keys: with 8 copies 165 us by one warp, 167 by two; 64 (pages
+    // of a multiple of 8) 278 by one, 172 by two, 173 by four; 128 (of 4) 277 by two, 171 by four.  D 128, 32 requests:
+    // with 8 copies 101 by one, 102 by two; 32 107 and 102; cp.async 159 and 105.
+    const int lanes = S::kKeyWarps * S::kCopies * (kKeys / copies.keys);
+    int producers = lanes * copies.pieces <= 16 ? 1 : lanes * copies.pieces <= 64 ? 2 : 4;
+    if (producers > S::kProducers) producers = S::kProducers;
+    // a lane for each copy's key (all its pieces); else cp.async
+    if ((S::kKeyWarps + producers - 1) / producers * S::kCopies * (kKeys / copies.keys) > 32 ||
+        !cache_map<CACHE, D, NT, R>(p, p.k, copies, &k_map) || !cache_map<CACHE, D, NT, R>(p, p.v, copies, &v_map)) {
+        copies = Copies{0, 0};
+        producers = S::kPerSm == 2 && S::kProducers == 2 ? 2 : 1;
+    }
     cudaError_t e = gdn::allow_dynamic_smem<&attn_tc<CACHE, D, NT, R>>(kSmem);
     if (e != cudaSuccess) return e;
-    e = gdn::launch_early(attn_tc<CACHE, D, NT, R>, (unsigned)p.grid, S::kThreads, (size_t)(fixed + stages * S::kKeyWarps * S::kStage),
-                          s, true, p, k_map, v_map, dims, stages, q_parts, w_parts, gdn::tc_copy_wait_polls());
+    e = gdn::launch_early(attn_tc<CACHE, D, NT, R>, (unsigned)p.grid, 32 * (S::kWarps + producers), (size_t)(fixed + stages * S::kKeyWarps * S::kStage),
+                          s, true, p, k_map, v_map, copies, stages, q_parts, w_parts, gdn::tc_copy_wait_polls());
     return e != cudaSuccess ? e : launch_join(p, s);
 }
 
 template <int CACHE, int D>
 cudaError_t by_rows(const AttnParams &p, cudaStream_t s)
 {
+    // Eight rows a warp and as many warps to a ring as the rows need: the kernel is bound by each warp's chain of
+    // latencies, and more warps hide it (32 rows of 16 heads on one key head, bf16, D 128: 88 us against 127 with 16 rows
+    // a warp).  Sixteen where every warp of a ring would widen the same E4M3 keys again (256 requests, 16 rows, D 128:
+    // 153 us against 181), and for more than 32 rows of D <= 128: every warp reads all its ring's keys from shared
+    // memory, which eight of them could not do fast enough.
     const int64_t rows = (int64_t)p.q_len * p.group;
     if (rows <= 8) return launch<CACHE, D, 1, 1>(p, s);
-    if (rows <= 16) return launch<CACHE, D, 1, 2>(p, s);
-    if (rows <= 32) return launch<CACHE, D, 2, 2>(p, s);
-    return launch<CACHE, D, 2, 4>(p, s);
+    if constexpr (CACHE == GDNA_E4M3 && D <= 128) {
+        if (rows <= 16) return launch<CACHE, D, 2, 1>(p, s);
+        if (rows <= 32) return launch<CACHE, D, 2, 2>(p, s);
+    } else {
+        if (rows <= 16) return launch<CACHE, D, 1, 2>(p, s);
+        if (rows <= 32) return launch<CACHE, D, 1, 4>(p, s);
+    }
+    if constexpr (D == 256) return launch<CACHE, D, 1, 8>(p, s);
+    else return launch<CACHE, D, 2, 4>(p, s);
 }
 
 }  // namespace tc
@@ -1012,7 +1043,7 @@ template <int CACHE> cudaError_t attn_wait_timeouts(unsigned *count)
 
 template <int CACHE> cudaError_t launch_attn_tc(const AttnParams &p, cudaStream_t s)
 {
-    return p.d == 64 ? tc::by_rows<CACHE, 64>(p, s) : p.d == 128 ? tc::by_rows<CACHE, 128>(p, s) : tc::by_rows<CACHE, 256>(p, s);
+    return p.d <= 64 ? tc::by_rows<CACHE, 64>(p, s) : p.d <= 128 ? tc::by_rows<CACHE, 128>(p, s) : tc::by_rows<CACHE, 256>(p, s);
 }
 
 }  // namespace gdna

@@ -294,3 +294,20 @@ def test_no_wait_gives_up_in_a_healthy_run(cuda_lib, d, cache, page):
     before = gdn.gdn_device_wait_timeouts()
     check(make([9000, 70, 0, 4000] * 8, 6, 2, d, cache=cache, page=page, seed=6, k_scale=0.125 if cache == "e4m3" else 1.0))
     assert gdn.gdn_device_wait_timeouts() == before
+
+
+@pytest.mark.parametrize("page", [2, 4, 6, 8, 12, 40, 100, 128])
+@pytest.mark.parametrize("d,cache", [(64, "f16"), (128, "bf16"), (256, "bf16"), (64, "e4m3"), (128, "e4m3"), (112, "f16")])
+def test_page_sizes(cuda_lib, page, d, cache):
+    """Blocks of 16 keys that lie in one page, in 2, 4 or 8 pieces of pages."""
+    check(make([2000, 5, 0, 333], 6, 2, d, page=page, cache=cache, seed=page, k_scale=0.125 if cache == "e4m3" else 1.0))
+
+
+@pytest.mark.parametrize("d", [8, 16, 32, 40, 48, 72, 104, 136, 160, 192, 200, 248])
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group", [3, 12, 50])
+def test_head_sizes_in_between(cuda_lib, d, cache, group):
+    """Head sizes that run padded to 64, 128 or 256, whole and in parts."""
+    s = make([700, 3, 64, 9], 2 * group, 2, d, q_len=2, cache=cache, layout="padded", seed=d, dtype="f32",
+             k_scale=0.125 if cache == "e4m3" else 1.0)
+    check(s, "f32" if group == 3 else "bf16", gated=True)
