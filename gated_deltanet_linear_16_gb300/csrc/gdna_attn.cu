@@ -176,10 +176,10 @@ attn_join(const AttnParams p)
     if (row >= p.q_len * p.group) return;
     const int token = row / p.group;
     const int64_t r_at = (int64_t)join.seq * p.q_len + token, h_at = (int64_t)head * p.group + (row - token * p.group);
-    float4 gate = zero;
+    uint4 gate = make_uint4(0u, 0u, 0u, 0u);
     const bool four = p.d % 4 == 0;        // (else columns leave one by one)
     if (four && tid < quads && p.gate != nullptr)
-        gate = load4(p.gate, r_at * p.gate_stride + h_at * p.gate_head_stride + 4 * tid, p.dtype, p.gate_vec);
+        gate = ask4(p.gate, r_at * p.gate_stride + h_at * p.gate_head_stride + 4 * tid, p.dtype, p.gate_vec);
 
     // the parts' maximum, then their weights and the row's sum
     float top = mine.x;
@@ -237,7 +237,7 @@ attn_join(const AttnParams p)
             a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
         }
         if (four) {
-            finish4(p, a, norm, gate);
+            finish4(p, a, norm, got4(gate, p.dtype, p.gate_vec));
             store4(p.out, r_at * p.out_stride + h_at * p.d + 4 * tid, p.out_dtype, p.out_vec, a);
         } else {
             const float u[4] = {a.x, a.y, a.z, a.w};

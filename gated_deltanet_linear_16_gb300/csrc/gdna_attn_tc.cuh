@@ -90,11 +90,21 @@ __device__ __forceinline__ void cp_async16(unsigned dst, const void *src, bool r
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 // Some keys of a head, from element x on; the map's other dimension is the panel.
-__device__ __forceinline__ void copy_keys(unsigned dst, const CUtensorMap *map, int x, int token, int head, int page, unsigned bar)
+// Keys that are read once are the first to leave the L2 (`policy`), which has the program's code, block table and
+// activations to keep (two-token verify: 74.6 us against 80.9).
+__device__ __forceinline__ void copy_keys(unsigned dst, const CUtensorMap *map, int x, int token, int head, int page, unsigned bar,
+                                          uint64_t policy)
 {
-    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-                 ::"r"(dst), "l"(map), "r"(x), "r"(token), "r"(0), "r"(head), "r"(page), "r"(bar) : "memory");
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+                 "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(token), "r"(0), "r"(head), "r"(page), "r"(bar), "l"(policy) : "memory");
+}
+__device__ __forceinline__ uint64_t keep_policy(bool once)
+{
+    uint64_t policy;
+    if (once) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
 }
 // A hint only: nothing is read.
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -216,7 +226,7 @@ template <int CACHE, int D, int NT, int R> struct Queries {
     static constexpr int kRows = S::kRows, kLanes = D / 8, kPerWarp = 32 / kLanes;        // lanes of a row, rows of a warp
     static constexpr int kPasses = (kRows + S::kWarps * kPerWarp - 1) / (S::kWarps * kPerWarp);
     static constexpr int kGo = kPasses < 4 ? kPasses : 4;      // passes at once
-    float x[kGo][8];
+    uint4 raw[kGo][2];
 
     __device__ __forceinline__ void fetch(const AttnParams &p, const Part &part, int pass)
     {
@@ -225,15 +235,13 @@ template <int CACHE, int D, int NT, int R> struct Queries {
 #pragma unroll
         for (int k = 0; k < kGo; ++k) {
             const int r = ((pass + k) * S::kWarps + warp) * kPerWarp + lane / kLanes, row = row0 + r;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[k][j] = 0.f;
+            raw[k][0] = raw[k][1] = make_uint4(0u, 0u, 0u, 0u);
             if (r < kRows && row < p.q_len * p.group && (lane % kLanes) * 8 < p.d) {
                 const int token = row / p.group;
                 const int64_t from = ((int64_t)part.seq * p.q_len + token) * p.q_stride +
                                      ((int64_t)head * p.group + (row - token * p.group)) * p.d + (lane % kLanes) * 8;
-                const float4 a = load4(p.q, from, p.dtype, p.q_vec), b = load4(p.q, from + 4, p.dtype, p.q_vec);
-                x[k][0] = a.x; x[k][1] = a.y; x[k][2] = a.z; x[k][3] = a.w;
-                x[k][4] = b.x; x[k][5] = b.y; x[k][6] = b.z; x[k][7] = b.w;
+                raw[k][0] = ask4(p.q, from, p.dtype, p.q_vec);
+                raw[k][1] = ask4(p.q, from + 4, p.dtype, p.q_vec);
             }
         }
     }
@@ -244,11 +252,13 @@ template <int CACHE, int D, int NT, int R> struct Queries {
 #pragma unroll
         for (int k = 0; k < kGo; ++k) {
             const int r = ((pass + k) * S::kWarps + warp) * kPerWarp + lane / kLanes;
-            float back = 1.f;
+            float back = 1.f, x[8];
+            const float4 a = got4(raw[k][0], p.dtype, p.q_vec), b = got4(raw[k][1], p.dtype, p.q_vec);
+            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
             if constexpr (CACHE != GDNA_BF16) {                // fp16: the row's largest element to 2^14 .. 2^15
                 float top = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[k][j]));
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
 #pragma unroll
                 for (int off = kLanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
                 int e = (int)(__float_as_uint(top) >> 23) - 127;
@@ -256,17 +266,17 @@ template <int CACHE, int D, int NT, int R> struct Queries {
                 const float up = __uint_as_float((unsigned)(127 + 14 - e) << 23);
                 back = __uint_as_float((unsigned)(127 - 14 + e) << 23);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[k][j] *= up;
+                for (int j = 0; j < 8; ++j) x[j] *= up;
             }
             if (r < kRows) {
                 for (int part = 0; part < q_parts; ++part) {
                     unsigned u[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        u[j] = O::pack(x[k][2 * j], x[k][2 * j + 1]);
+                        u[j] = O::pack(x[2 * j], x[2 * j + 1]);
                         const float2 f = O::unpack(u[j]);
-                        x[k][2 * j] -= f.x;
-                        x[k][2 * j + 1] -= f.y;
+                        x[2 * j] -= f.x;
+                        x[2 * j + 1] -= f.y;
                     }
                     uint8_t *to = qs + (part * kRows + r) * S::kQPitch;
                     if constexpr (CACHE == GDNA_E4M3) {
@@ -359,6 +369,7 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, int
 
     if (copies.keys != 0) {
         const bool mine = y < TW;
+        const uint64_t policy = keep_policy(p.row_tiles == 1);
         const unsigned dst = ring + (mine ? y : 0) * stages * S::kStage + (values * KB + block) * S::kBlockBytes + row * S::kPanel;
         const CUtensorMap *map = values ? &v_map : &k_map;
         int page = 0, token = 0;
@@ -384,7 +395,7 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, int
             if (mine)
                 for (int z = 0; z < copies.pieces; ++z)
                     copy_keys(dst + slot * S::kStage + z * S::kPanelBytes, map, z * (S::kPanel / S::kElem), from, of, at,
-                              smem_addr(&full[slot][y]));
+                              smem_addr(&full[slot][y]), policy);
             filled = min(filled + 1, stages);
             if (++slot == stages) { slot = 0; phase ^= 1; }
             if (fresh) warm();
@@ -829,10 +840,6 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
         const int head = part.item / p.row_tiles;
         float *to = part_of(p, 2 * c + (part.begins ? 1 : 0));
         constexpr int kQuads = S::kColumns / 4, kAll = ROWS * kQuads, kTasks = (kAll + W * 32 - 1) / (W * 32);
-        constexpr int kGroups = D / S::kColumns;
-        // the gates of kAhead groups of columns are loaded together (their latency, once)
-        constexpr int kAhead = kGroups * kTasks <= 4 ? kGroups : kTasks <= 2 ? 2 : 1;
-        float4 gate[kAhead][kTasks];
         float share[kTasks][TW], norm[kTasks];
         int64_t out_at[kTasks], gate_at[kTasks];
         bool real[kTasks];
@@ -858,13 +865,12 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
 #pragma unroll
         for (int x0 = 0; x0 < D; x0 += S::kColumns) {
             if (x0 >= p.d) break;
-            if (x0 / S::kColumns % kAhead == 0 && whole && p.gate != nullptr) {
+            uint4 gate[kTasks];
 #pragma unroll
-                for (int k = 0; k < kTasks; ++k)
-#pragma unroll
-                    for (int y = 0; y < kAhead; ++y)
-                        if (real[k] && x0 + y * S::kColumns + 4 * ((tid + k * W * 32) % kQuads) < p.d)
-                            gate[y][k] = load4(p.gate, gate_at[k] + x0 + y * S::kColumns, p.dtype, p.gate_vec);
+            for (int k = 0; k < kTasks; ++k) {
+                gate[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (whole && p.gate != nullptr && real[k] && x0 + 4 * ((tid + k * W * 32) % kQuads) < p.d)
+                    gate[k] = ask4(p.gate, gate_at[k] + x0, p.dtype, p.gate_vec);
             }
             if (x0 > 0) all_consumers();   // the last columns are added up
 #pragma unroll
@@ -877,16 +883,14 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                         for (int h = 0; h < 2; ++h)
                             sums[(tw * ROWS + rg * 8 * NT + 8 * t + 2 * c4 + j) * S::kSumPitch + 16 * y - x0 +
                                  (kF8 ? 2 * l4 + h : l4 + 8 * h)] = o[y][t][2 * h + j];
-            if (x0 > 0) {
-                all_consumers();
-            } else if (!all_agree(ok)) {
-                ok = false;
-                break;
-            } else {                       // each warp's share of a row
+            if (x0 > 0) all_consumers();
+            else ok = all_agree(ok);
+            if (!ok) break;
 #pragma unroll
-                for (int k = 0; k < kTasks; ++k) {
-                    const int task = tid + k * W * 32, r = task / kQuads;
-                    if (!real[k]) continue;
+            for (int k = 0; k < kTasks; ++k) {
+                const int task = tid + k * W * 32, r = task / kQuads;
+                if (!real[k]) continue;
+                if (x0 == 0) {             // each warp's share of a row
                     float top = kNegInf, total = 0.f;
 #pragma unroll
                     for (int y = 0; y < TW; ++y) top = fmaxf(top, warp_m[y][r]);
@@ -902,23 +906,18 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                         else if (p.lse != nullptr) write_lse(p, part.seq, head, row0 + r, top, total);
                     }
                 }
-            }
-#pragma unroll
-            for (int k = 0; k < kTasks; ++k) {
-                const int task = tid + k * W * 32;
-                if (!real[k] || x0 + 4 * (task % kQuads) >= p.d) continue;
+                if (x0 + 4 * (task % kQuads) >= p.d) continue;
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int y = 0; y < TW; ++y) {
-                    const float4 v = *reinterpret_cast<const float4 *>(sums + (y * ROWS + task / kQuads) * S::kSumPitch +
-                                                                       4 * (task % kQuads));
+                    const float4 v = *reinterpret_cast<const float4 *>(sums + (y * ROWS + r) * S::kSumPitch + 4 * (task % kQuads));
                     a.x = fmaf(share[k][y], v.x, a.x);
                     a.y = fmaf(share[k][y], v.y, a.y);
                     a.z = fmaf(share[k][y], v.z, a.z);
                     a.w = fmaf(share[k][y], v.w, a.w);
                 }
                 if (whole) {
-                    finish4(p, a, norm[k], gate[x0 / S::kColumns % kAhead][k]);
+                    finish4(p, a, norm[k], got4(gate[k], p.dtype, p.gate_vec));
                     store4(p.out, out_at[k] + x0, p.out_dtype, p.out_vec, a);
                 } else {
                     *reinterpret_cast<float4 *>(to + out_at[k] + x0) = a;

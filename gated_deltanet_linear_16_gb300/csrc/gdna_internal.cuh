@@ -129,14 +129,22 @@ __device__ __forceinline__ void store_elem(void *p, int64_t i, int dtype, float 
     else static_cast<__nv_fp8_storage_t *>(p)[i] = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
 
-// Four elements that follow one another; `vec`: they start on a boundary of four.
-__device__ __forceinline__ float4 load4(const void *p, int64_t i, int dtype, bool vec)
+// Four elements that follow one another, as they lie in memory (`vec`: they start on a boundary of four; else as
+// fp32), so that several can be on their way before the first is looked at.
+__device__ __forceinline__ uint4 ask4(const void *p, int64_t i, int dtype, bool vec)
 {
     if (!vec)
-        return make_float4(load_elem(p, i, dtype), load_elem(p, i + 1, dtype), load_elem(p, i + 2, dtype),
-                           load_elem(p, i + 3, dtype));
-    if (dtype == GDNA_F32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+        return make_uint4(__float_as_uint(load_elem(p, i, dtype)), __float_as_uint(load_elem(p, i + 1, dtype)),
+                          __float_as_uint(load_elem(p, i + 2, dtype)), __float_as_uint(load_elem(p, i + 3, dtype)));
+    if (dtype == GDNA_F32) return *reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
     const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    return make_uint4(u.x, u.y, 0u, 0u);
+}
+// What ask4 brought.
+__device__ __forceinline__ float4 got4(uint4 u, int dtype, bool vec)
+{
+    if (!vec || dtype == GDNA_F32)
+        return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
     if (dtype == GDNA_F16) {
         const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
         const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
