@@ -97,12 +97,6 @@ int64_t attn_workspace_bytes(int64_t rows, int d);
 
 // ---------------------------------------------------------------- device helpers
 
-template <int DT> struct Elem;
-template <> struct Elem<GDNA_F32> { using type = float; };
-template <> struct Elem<GDNA_F16> { using type = __half; };
-template <> struct Elem<GDNA_BF16> { using type = __nv_bfloat16; };
-template <> struct Elem<GDNA_E4M3> { using type = __nv_fp8_storage_t; };
-
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

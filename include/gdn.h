@@ -84,8 +84,8 @@ extern "C" {
 #define GDN_ERR_CUDA 5         /* the CUDA launch failed (see gdn_last_cuda_error) */
 /* There is no timeout status: no kernel of the library waits on a flag, a
  * counter or another block (only on its own barriers, copy groups and, in
- * gdn_prefill_chunked, the completion of its own MMAs and tensor copies,
- * bounded waits counted by gdn_device_wait_timeouts).  A
+ * gdn_prefill_chunked and gdna.h's attention, the completion of its own MMAs
+ * and tensor copies, bounded waits counted by gdn_device_wait_timeouts).  A
  * base, stride or pitch that rules out the 16-byte vector kernels is not an
  * error either: the general kernel runs instead (GDN_ERR_ALIGN is only for a
  * pointer not aligned to its own element size). */
@@ -373,7 +373,8 @@ GDN_API int gdn_prefill_chunked(void *state, gdn_state_dtype state_dtype, int64_
  * gdn_device_wait_timeouts -- how many times, on the current device since
  * the library was loaded, a tensor-core kernel's bounded wait for its own
  * MMAs or tensor copies ran out (the kernel then stops and writes NaN to its
- * state; 0 in every healthy run).  Synchronises the current device first.  No
+ * state, or, for the attention of gdna.h, to its output rows; 0 in every
+ * healthy run).  Synchronises the current device first.  No
  * counterpart on the source pages: a health check of this library's kernels.
  *   count        host pointer, written.
  *   Errors: GDN_ERR_ARG (count NULL), GDN_ERR_CUDA.

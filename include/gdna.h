@@ -195,12 +195,18 @@ GDN_API int64_t gdna_attn_workspace(int batch, int q_len, int nq, int nkv, int d
  *   workspace    device scratch of workspace_bytes >= gdna_attn_workspace(),
  *                16-byte aligned; any content, and none is kept.  Calls that
  *                can overlap on the GPU need separate ones.
- *   NQ must be a multiple of NKV (GDN_ERR_UNSUPPORTED).  1 <= D <= 256.  Head
- *   sizes 64, 128 and 256 on 16-byte aligned caches run on the tensor cores; any
- *   other call runs a general kernel with the same results up to rounding.
+ *   NQ must be a multiple of NKV (GDN_ERR_UNSUPPORTED).  1 <= D <= 256.  Heads of
+ *   a multiple of 16 bytes on 16-byte aligned caches (bases and strides) run on
+ *   the tensor cores; any other call runs a general kernel, some ten times
+ *   slower, with the same results up to rounding.  Page sizes that 16 divides are
+ *   the fastest, multiples of 8 and of 4 nearly so.
  *   Scores, softmax sums and outputs are held in fp32; queries and weights enter
- *   the products in as many 16-bit parts as their type needs.  Results do not
- *   depend on timing.
+ *   the products in two or three 16-bit parts where one would show in the output.
+ *   A value or key that is not finite shows in the rows that see it.  Results do
+ *   not depend on timing.
+ *   The tensor-core kernels' waits for their own copies are bounded
+ *   (gdn_set_wait_polls); where one runs out the rows of that block come out NaN
+ *   and gdn_device_wait_timeouts counts it.
  */
 GDN_API int gdna_attn_decode(const void *q, gdna_dtype dtype, const void *gate,
                              const void *k_cache, const void *v_cache, gdna_dtype cache_dtype,
