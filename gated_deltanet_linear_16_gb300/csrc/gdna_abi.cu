@@ -38,6 +38,18 @@ int check_operand(const Operand &o, Span *span)
     return span->hi > span->lo ? GDN_OK : GDN_ERR_ARG;
 }
 
+// Rows that lie side by side in wider rows (q, k and v of one projection, say): same stride, and neither's columns
+// reach into the other's.
+bool side_by_side(const Operand &a, const Operand &b)
+{
+    const uint64_t stride = (uint64_t)a.stride * (uint64_t)a.elem;
+    if (a.rows <= 1 || b.rows <= 1 || stride == 0 || stride != (uint64_t)b.stride * (uint64_t)b.elem) return false;
+    const uint64_t la = (uint64_t)a.len * (uint64_t)a.elem, lb = (uint64_t)b.len * (uint64_t)b.elem;
+    const uint64_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+    const uint64_t off = pb >= pa ? (pb - pa) % stride : (stride - (pa - pb) % stride) % stride;   // of b's columns in a's rows
+    return off >= la && off + lb <= stride;
+}
+
 // Every operand is sound; outputs (the first n_out) overlap nothing else, except
 // the pair (may_a, may_b) if it is given.
 int check_operands(const Operand *ops, int n, int n_out, int may_a = -1, int may_b = -1)
@@ -49,7 +61,8 @@ int check_operands(const Operand *ops, int n, int n_out, int may_a = -1, int may
     }
     for (int i = 0; i < n_out; ++i)
         for (int j = 0; j < n; ++j)
-            if (j != i && !((i == may_a && j == may_b) || (i == may_b && j == may_a)) && overlap(spans[i], spans[j]))
+            if (j != i && !((i == may_a && j == may_b) || (i == may_b && j == may_a)) && overlap(spans[i], spans[j]) &&
+                !side_by_side(ops[i], ops[j]))
                 return GDN_ERR_ALIAS;
     return GDN_OK;
 }
@@ -245,6 +258,10 @@ GDN_API int gdna_attn_decode(const void *q, gdna_dtype dtype, const void *gate,
     if ((int64_t)q_len * nq > (1 << 24) || batch > (1 << 20) || rows > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     if (gate != nullptr && gate_head_stride < d) return GDN_ERR_ARG;
     if (rows == 0) return GDN_OK;
+    // the row of all units of work (16 keys at least each, and what an item costs beside them) is counted in 64 bits
+    const double most = ((double)max_pages * (page_size > 0 ? page_size : 0) / 16 + 64) * batch * nkv *
+                        ((double)q_len * (nq / nkv) / 8 + 1);
+    if (most > 4e18) return GDN_ERR_UNSUPPORTED;
     AttnParams p{};
     p.cache = CacheLayout{page_stride, token_stride, head_stride, pages, page_size};
     Operand ops[10];

@@ -24,6 +24,7 @@
 
 namespace gdna {
 
+constexpr int kMaxKeys = INT32_MAX - 4095; // so that a step past a sequence's end is an int
 constexpr int kMaxGrid = 608;              // blocks at most: workspace for two partials each
 
 struct Join {
@@ -46,7 +47,7 @@ __device__ __forceinline__ float *part_of(const AttnParams &p, int slot)
 // Keys of sequence b in its cache.
 __device__ __forceinline__ int keys_of(const AttnParams &p, int b)
 {
-    const int64_t most = (int64_t)p.max_pages * p.cache.page_size;
+    const int64_t most = min((int64_t)p.max_pages * p.cache.page_size, (int64_t)kMaxKeys);
     return (int)min((int64_t)max(p.kv_len[b], 0), most);
 }
 // Places of an item in the row: its units behind its lead.

@@ -146,8 +146,9 @@ GDN_API int gdna_page_assign(const int32_t *cached, const int32_t *fresh, int32_
  *                and rounded to nearest even once; E4M3 saturates at +-448.
  *                Two rows with the same slot: either may be kept.
  *   q_out may be q itself (same base, strides q_stride and q_head_stride = D);
- *   otherwise an output overlapping any operand is GDN_ERR_ALIAS.  k_cache and
- *   v_cache may be interleaved in one buffer.
+ *   otherwise an output overlapping any operand is GDN_ERR_ALIAS.  Rows of one
+ *   stride that lie side by side (q, k and v of one projection) do not overlap,
+ *   and k_cache and v_cache may be interleaved in one buffer.
  *   1 <= D <= 256, rot even and <= D, norms and rotations in fp32.
  */
 GDN_API int gdna_qk_norm_rope(const void *q, const void *k, const void *v, gdna_dtype dtype,
@@ -185,7 +186,7 @@ GDN_API int64_t gdna_attn_workspace(int batch, int q_len, int nq, int nkv, int d
  *                length are not read.  A page number outside [0, pages) reads as
  *                a page of zeros.
  *   kv_len       [batch] int32.  Below 0 counts as 0; above max_pages *
- *                page_size as that.
+ *                page_size (or 2^31 - 4096) as that.
  *   scale        finite; > 0 (usually 1/sqrt(D)).
  *   out          [batch*q_len] rows of NQ*D, stride out_stride, type out_dtype
  *                (F32, F16 or BF16), rounded once.

@@ -140,6 +140,21 @@ def test_layouts_that_are_not_refused_reach_the_launch(lib):
     assert rope(lib, vc=A[10] + 2 * 4096, ps=8192) == 5 and rope(lib, qo=A[0]) == 5
 
 
+def test_rows_side_by_side_are_no_alias(lib):
+    """q in place in the rows of one projection [q | k | v]; columns that reach into each other are refused."""
+    packed = dict(qs=1024, kst=1024, vst=1024, qos=1024, qo=A[0], k=A[0] + 512 * 4, v=A[0] + 768 * 4)
+    assert rope(lib, **packed) == 5
+    assert rope(lib, **{**packed, "k": A[0] + 511 * 4}) == ALIAS
+    assert rope(lib, **{**packed, "v": A[0] + 769 * 4}) == ALIAS
+    assert rope(lib, **{**packed, "kst": 1028}) == ALIAS
+    assert attn(lib, out=A[0] + 2 * 1024, qs=2048, os=2048) == 5 and attn(lib, out=A[0] + 2 * 1023, qs=2048, os=2048) == ALIAS
+
+
+def test_more_work_than_64_bits_count_is_refused(lib):
+    assert attn(lib, batch=1 << 20, q_len=1, nq=1 << 24, nkv=1 << 24, d=1, page=(1 << 31) - 1, max_pages=(1 << 31) - 1,
+                pages=1, hs=1, ts=1 << 24, ps=1 << 56, qs=1 << 24, gs=1 << 24, ghs=1, os=1 << 24, tstride=1 << 31) == UNSUP
+
+
 def test_workspace_grows_with_rows_and_d(built):
     size = lambda **kw: gdn.gdna_attn_workspace(**{**dict(batch=3, q_len=1, nq=8, nkv=2, d=128), **kw})   # noqa: E731
     assert size() > 0 and size() == size(batch=1000) and size(nq=9) == 0 and size(d=257) == 0 and size(d=0) == 0

@@ -201,3 +201,23 @@ def test_slots_past_32_bits(cuda_lib):
 
 def test_another_stream(cuda_lib):
     case(31, 6, 2, 128, 64, seed=4, stream=torch.cuda.Stream())
+
+
+def test_in_place_in_one_projection(cuda_lib):
+    """q rotated where it lies in rows [q | k | v]; k and v read from the same rows."""
+    rows, nq, nkv, d = 9, 4, 2, 64
+    qkv = torch.randn((rows, (nq + 2 * nkv) * d), device="cuda")
+    before = qkv.clone()
+    table = torch.randn((10, d), device="cuda")
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    c, plain = Cache(3, 4, nkv, d, "f16"), Cache(3, 4, nkv, d, "f16")
+    slots = torch.arange(rows, device="cuda")
+    w = qkv.stride(0)
+    args = dict(rows=rows, nq=nq, nkv=nkv, d=d, rot=d, n_pos=10, q_stride=w, k_stride=w, v_stride=w)
+    out = torch.empty((rows, nq * d), device="cuda")
+    gdn.gdna_qk_norm_rope(before, before[:, nq * d:], before[:, (nq + nkv) * d:], None, None, table, pos, slots, out,
+                          *plain.addresses(), **args, **plain.args())
+    gdn.gdna_qk_norm_rope(qkv, qkv[:, nq * d:], qkv[:, (nq + nkv) * d:], None, None, table, pos, slots, qkv,
+                          *c.addresses(), q_out_stride=w, **args, **c.args())
+    assert torch.equal(qkv[:, :nq * d], out) and torch.equal(qkv[:, nq * d:], before[:, nq * d:])
+    assert torch.equal(c.buf.view(torch.int16), plain.buf.view(torch.int16))
