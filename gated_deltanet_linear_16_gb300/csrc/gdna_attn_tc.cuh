@@ -862,16 +862,27 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                 const int r = rg * 8 * NT + 8 * t + 2 * c4 + j;
                 if (l4 == 0) { warp_m[tw][r] = m[t][j]; warp_l[tw][r] = x; }
             }
+        // The gates of all columns are asked for at once where they are few registers, so that their latency is paid
+        // once an item (111 requests of 5-139 keys, 10/5 heads of 256: 26.4 us against 27.5); else some columns at a time.
+        constexpr int kChunks = D / S::kColumns;
+        constexpr bool kAtOnce = kTasks * kChunks <= 4;
+        uint4 gate[kAtOnce ? kChunks : 1][kTasks];
+        auto ask_gates = [&](uint4 (&to)[kTasks], int x0) {
+#pragma unroll
+            for (int k = 0; k < kTasks; ++k) {
+                to[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (whole && p.gate != nullptr && real[k] && x0 + 4 * ((tid + k * W * 32) % kQuads) < p.d)
+                    to[k] = ask4(p.gate, gate_at[k] + x0, p.dtype, p.gate_vec);
+            }
+        };
+        if constexpr (kAtOnce)
+#pragma unroll
+            for (int y = 0; y < kChunks; ++y) ask_gates(gate[y], y * S::kColumns);
 #pragma unroll
         for (int x0 = 0; x0 < D; x0 += S::kColumns) {
             if (x0 >= p.d) break;
-            uint4 gate[kTasks];
-#pragma unroll
-            for (int k = 0; k < kTasks; ++k) {
-                gate[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (whole && p.gate != nullptr && real[k] && x0 + 4 * ((tid + k * W * 32) % kQuads) < p.d)
-                    gate[k] = ask4(p.gate, gate_at[k] + x0, p.dtype, p.gate_vec);
-            }
+            const int gx = kAtOnce ? x0 / S::kColumns : 0;
+            if constexpr (!kAtOnce) ask_gates(gate[0], x0);
             if (x0 > 0) all_consumers();   // the last columns are added up
 #pragma unroll
             for (int y = x0 / 16; y < (x0 + S::kColumns) / 16; ++y)
@@ -917,7 +928,7 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                     a.w = fmaf(share[k][y], v.w, a.w);
                 }
                 if (whole) {
-                    finish4(p, a, norm[k], got4(gate[k], p.dtype, p.gate_vec));
+                    finish4(p, a, norm[k], got4(gate[gx][k], p.dtype, p.gate_vec));
                     store4(p.out, out_at[k] + x0, p.out_dtype, p.out_vec, a);
                 } else {
                     *reinterpret_cast<float4 *>(to + out_at[k] + x0) = a;
