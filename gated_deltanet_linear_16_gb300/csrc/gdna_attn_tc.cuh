@@ -58,7 +58,11 @@ namespace tc {
 constexpr int kKeys = 16;                  // keys of a block: one side of a product
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr int kSmemOne = 224 * 1024, kSmemTwo = 111 * 1024;      // of a block beside its static arrays: one, two an SM
-constexpr int kQueue = 8;                  // parts that the producer can be ahead: more than there are stages
+constexpr int kMaxStages = 6;              // of a ring
+// Slots of the parts in hand.  The producer tells part n + 1 before it waits for the release of step n - stages.  With one
+// step a part, step n - 1 - stages is then known to be released, but its part may still be added up: stages + 3 parts, from
+// that one to n + 1, need a slot each.
+constexpr int kQueue = kMaxStages + 3;
 
 __device__ __forceinline__ unsigned smem_addr(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
 
@@ -200,7 +204,6 @@ template <int CACHE, int D, int NT, int R> struct Shape {
     static constexpr int kColumns = 1024 + 3 * kKeyWarps * kStage + 2 * kRows * kQPitch + kKeyWarps * kRows * 68 * 4 <= kSmem ? 64 : 32;
     static constexpr int kSumPitch = kColumns + 4;             // floats
     static constexpr int kSumBytes = kKeyWarps * kRows * kSumPitch * 4;
-    static constexpr int kMaxStages = 6;
     static_assert(kKeyWarps * kCopies <= 32, "a lane for each block of a step");
 
     // Swizzled place of byte `b` of row `r` in a block.
@@ -484,7 +487,7 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t scratch[S::kThreads / 32 + 3];
     __shared__ float row_scale[ROWS], warp_m[TW][ROWS], warp_l[TW][ROWS];
-    __shared__ uint64_t full[S::kMaxStages][TW], empty[S::kMaxStages][TW];
+    __shared__ uint64_t full[kMaxStages][TW], empty[kMaxStages][TW];
     __shared__ int gave_up;
     __shared__ Part queue[kQueue];         // the part in hand and those after it
     __shared__ uint64_t told[kQueue];
@@ -990,7 +993,7 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
                   "two stages whatever the queries' type");
     const int fixed = kFixed + q_parts * S::kRows * S::kQPitch;
     const int room = (kSmem - fixed) / (S::kKeyWarps * S::kStage);
-    const int stages = room < S::kMaxStages ? room : S::kMaxStages;
+    const int stages = room < kMaxStages ? room : kMaxStages;
     p.unit = S::kStep * S::kKeyWarps;
     // what an item costs beside its keys (queries, adding up, output), in bytes of keys that the block could read
     // meanwhile: measured best at 64 KB for 8 rows of 128, 256 KB for 16 rows of 256

@@ -232,3 +232,20 @@ def test_binding_refuses_other_types(built):
                              page_size=1, max_pages=1)
     with pytest.raises(ValueError):
         gdn.gdna_attn_decode(1 << 20, 0, 0, 0, 0, 0, 0, batch=1, nq=1, nkv=1, d=4, pages=1, page_size=1, max_pages=1)
+
+
+def test_the_queue_of_parts_holds_every_part_in_use():
+    """The tensor-core attention kernel's producer runs ahead of the consumers: a replay of the two, with one step a part
+    (the furthest it gets), finds no part told into the slot of one that is still being added up."""
+    source = open(os.path.join(os.path.dirname(HEADER), "..", "gated_deltanet_linear_16_gb300", "csrc", "gdna_attn_tc.cuh")).read()
+    most = int(re.search(r"constexpr int kMaxStages = (\d+);", source)[1])
+    slots = eval(re.search(r"constexpr int kQueue = ([^;]+);", source)[1], {"kMaxStages": most})
+    for stages in range(2, most + 1):
+        for in_use in range(100):                       # its step is released, its rows are being added up
+            step = 0
+            while True:
+                told = step + 1                         # before the wait for the step's stage
+                assert told <= in_use or told % slots != in_use % slots, (stages, in_use, told)
+                if step - stages > in_use:              # that stage is not released yet
+                    break
+                step += 1

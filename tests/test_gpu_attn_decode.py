@@ -311,3 +311,24 @@ def test_head_sizes_in_between(cuda_lib, d, cache, group):
     s = make([700, 3, 64, 9], 2 * group, 2, d, q_len=2, cache=cache, layout="padded", seed=d, dtype="f32",
              k_scale=0.125 if cache == "e4m3" else 1.0)
     check(s, "f32" if group == 3 else "bf16", gated=True)
+
+
+@pytest.mark.parametrize("page", [8, 16, 24])
+@pytest.mark.parametrize("d,cache,nq,nkv,q_len,batch,longest", [
+    (64, "e4m3", 8, 8, 1, 500, 128), (64, "f16", 72, 6, 1, 560, 64), (64, "bf16", 48, 8, 3, 420, 64),
+    (48, "f16", 20, 20, 9, 200, 40), (64, "e4m3", 18, 6, 8, 560, 64), (128, "e4m3", 64, 8, 5, 420, 40),
+    (256, "e4m3", 48, 4, 3, 420, 30)])
+def test_many_short_items_a_block(cuda_lib, page, d, cache, nq, nkv, q_len, batch, longest):
+    """Blocks that take ten items and more of one step each, in the shapes whose rings are deepest: every row's output and
+    log-sum-exp is its own, and nothing lands in front of either array."""
+    rng = np.random.default_rng(page * d + batch)
+    lens = rng.integers(1, longest + 1, batch)
+    lens[rng.random(batch) < 0.05] = 0
+    s = make(lens.tolist(), nq, nkv, d, q_len=q_len, cache=cache, page=page, seed=page, k_scale=0.125 if cache == "e4m3" else 1.0)
+    rows = batch * q_len
+    check(s, "f32")
+    before = 40 * nq                                    # room for the row of a sequence -1 and more
+    whole, out = guarded(rows, nq * d, nq * d, "f32", before=before * d)
+    lse = torch.full((before + rows * nq + before,), 77.0, device="cuda")
+    call(s, out, lse[before:])
+    assert intact(whole, out) and (lse[:before] == 77.0).all() and (lse[before + rows * nq:] == 77.0).all()
