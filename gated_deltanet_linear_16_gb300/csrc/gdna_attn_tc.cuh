@@ -20,7 +20,11 @@
 // [+ lower]), scaled by a power of two per row for fp16 products, so that no query
 // over- or underflows.  The weights exp2(s - m) <= 1 enter in two
 // parts, three where bf16 products give an fp32 output: one part's 2^-9 (2^-12 in fp16), relative to the largest
-// values, would show where sums cancel.  m, l, S and O are fp32.
+// values, would show where sums cancel.  For fp16 products they are lifted by 2^15, and with them l and O, until a part is
+// added up: fp16's steps end at 2^-24, and one key far ahead of the others (a first token that all attend to) whose value is
+// near zero leaves the output to weights that small.  Lifted, a weight is held to 2^-40 of the row's largest, or to 2^-22 of
+// itself (500 keys, f16, the first 16 nats ahead and its value zero: 6e-6 of the output's norm, 1e-1 without).
+// m, l, S and O are fp32.
 //
 // What a row does not see.  Masked scores are replaced, not added to.  Keys past the
 // sequence's end are not loaded (zeros stand for them).  The keys that some tokens see
@@ -128,8 +132,9 @@ __device__ __forceinline__ void arrive_copies(uint64_t *bar)
 // Waits on the kernel's barriers that ran out on this device (each cache type's kernels have their own).
 static __device__ unsigned g_wait_timeouts;
 
-// 16-bit operand type of the products: bf16 for a bf16 cache, else fp16.
+// 16-bit operand type of the products: bf16 for a bf16 cache, else fp16.  kLift: what weights are multiplied by for it.
 template <int CACHE> struct Op {
+    static constexpr float kLift = 32768.f;
     __device__ static unsigned pack(float a, float b)
     {
         __half2 h = __floats2half2_rn(a, b);
@@ -145,6 +150,7 @@ template <int CACHE> struct Op {
     }
 };
 template <> struct Op<GDNA_BF16> {
+    static constexpr float kLift = 1.f;
     __device__ static unsigned pack(float a, float b)
     {
         __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
@@ -709,8 +715,8 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                         const float from = m[t][j] == kNegInf ? 0.f : m[t][j];
 #pragma unroll
                         for (int y = 0; y < KB; ++y) {
-                            w[y][t][j] = ex2(w[y][t][j] - from);
-                            w[y][t][j + 2] = ex2(w[y][t][j + 2] - from);
+                            w[y][t][j] = O::kLift * ex2(w[y][t][j] - from);
+                            w[y][t][j + 2] = O::kLift * ex2(w[y][t][j + 2] - from);
                             l[t][j] += w[y][t][j] + w[y][t][j + 2];
                         }
                     }
@@ -911,7 +917,7 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
                     const float from = top == kNegInf ? 0.f : top;
 #pragma unroll
                     for (int y = 0; y < TW; ++y) {
-                        share[k][y] = weight_of(warp_m[y][r], from);
+                        share[k][y] = weight_of(warp_m[y][r], from) * (1.f / O::kLift);
                         total = fmaf(share[k][y], warp_l[y][r], total);
                     }
                     norm[k] = total == 0.f ? 0.f : p.v_scale / total;
@@ -985,7 +991,8 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
     // 16-bit parts of a query: what its type holds (bf16 products have 8 bits a part, fp16 products 11), but for an
     // fp32 query, a bf16 cache and a 16-bit output two parts: the scores' 2^-17 is far below the output's rounding
     const int q_parts = p.dtype == GDNA_BF16 ? 1 : p.dtype == GDNA_F16 ? (bf16 ? 2 : 1) : (bf16 ? (p.out_dtype == GDNA_F32 ? 3 : 2) : 2);
-    // and weights: 16 bits or more, 22 or more for an fp32 output
+    // and weights: two fp16 parts hold 22 bits (down to 2^-40 of the row's largest), two bf16 parts 16, three 24 for an fp32
+    // output
     const int w_parts = bf16 && p.out_dtype == GDNA_F32 ? 3 : 2;
     constexpr int kFixed = 1024 + S::kSumBytes;                // alignment of the ring; the sums
     constexpr int kSmem = S::kSmem;

@@ -332,3 +332,44 @@ def test_many_short_items_a_block(cuda_lib, page, d, cache, nq, nkv, q_len, batc
     lse = torch.full((before + rows * nq + before,), 77.0, device="cuda")
     call(s, out, lse[before:])
     assert intact(whole, out) and (lse[:before] == 77.0).all() and (lse[before + rows * nq:] == 77.0).all()
+
+
+@pytest.mark.parametrize("cache", ["f16", "e4m3", "bf16"])
+@pytest.mark.parametrize("d,group", [(128, 32), (64, 20), (64, 3), (128, 12), (256, 40)])
+@pytest.mark.parametrize("ahead", [10.0, 14.0, 18.0])
+@pytest.mark.parametrize("worth", [0.0, 0.01])
+def test_small_weights_beside_a_large_one(cuda_lib, cache, d, group, ahead, worth):
+    """A first key `ahead` nats above the others, with a value near zero: the output is what the small weights bring.
+    The bound is relative to sum w |v| / l, which is as small, and beside it a weight's last place: 2^-40 of the row's largest
+    (8 sqrt(n) of them, their roundings independent).  Enough items that most lie within one block."""
+    nkv, n, batch = 4, 500, 80
+    rng = torch.Generator().manual_seed(d + group)
+    u = 0.1 * (1.0 - 2.0 * torch.randint(0, 2, (nkv, d), generator=rng))
+    s = make([n] * batch, nkv * group, nkv, d, dtype="f32", cache=cache, seed=group, k_scale=0.125 if cache == "e4m3" else 1.0)
+    q = u[None, :, None, :] + 0.005 * torch.randn((batch, nkv, group, d), generator=rng)
+    s["q"] = q.reshape(batch, -1).cuda()
+    first, at = s["table"][:, 0].cpu().long(), torch.zeros(batch, dtype=torch.long)
+    k0 = (ahead / (s["scale"] * (u * u).sum(-1, keepdim=True)) * u).expand(batch, nkv, d)
+    v0 = worth * torch.randn((batch, nkv, d), generator=rng)
+    for which, mine, x in (("k", s["keys"], k0), ("v", s["values"], v0)):
+        stored = s["store"].put(which, first, at, x / s["k_scale"]) * s["k_scale"]
+        for b in range(batch):
+            mine[b][0] = stored[b]
+    out = torch.zeros((batch, nkv * group * d), device="cuda")
+    lse = torch.zeros((batch * nkv * group,), device="cuda")
+    call(s, out, lse)
+    rows = s["q"].double().view(batch, nkv, group, d)
+    k, v = (torch.tensor(np.stack(x), device="cuda") for x in (s["keys"], s["values"]))
+    scores = torch.einsum("bhgd,bnhd->bhgn", rows, k) * s["scale"]
+    w = torch.softmax(scores, -1)
+    flat = lambda x: x.reshape(batch, nkv * group, -1).cpu().numpy()               # noqa: E731
+    want, around = (flat(torch.einsum("bhgn,bnhd->bhgd", w, x)) for x in (v, v.abs()))
+    size = flat(torch.einsum("bhgd,bnhd->bhgn", rows.abs(), k.abs()).amax(-1) * s["scale"])
+    vmax = flat(v.abs().amax((1, 3))[:, :, None].expand(batch, nkv, group))
+    want_lse = flat(torch.logsumexp(scores, -1))[..., 0]
+    score = (8 * np.sqrt(d) * E32 + 2.0 ** -20) * size
+    tol = around * (2 * score + 2.0 ** -20 + (8 * np.sqrt(n) + 32) * E32) + 8 * np.sqrt(n) * 2.0 ** -40 * vmax
+    miss = np.abs(f64(out).reshape(want.shape) - want) - tol
+    assert (miss <= 0).all(), (miss.max(), np.abs(want).max())
+    lim = score[..., 0] + (8 * np.sqrt(n) + 8) * E32 + 4 * E32 * np.abs(want_lse)
+    assert (np.abs(f64(lse).reshape(want_lse.shape) - want_lse) <= lim).all()
