@@ -21,6 +21,16 @@ struct Span {
     uintptr_t lo, hi;
 };
 
+constexpr int64_t kMostElems = INT64_MAX / 16;             // of an array: its bytes are an int64, with room to add
+
+// Elements from the first to the last of `heads` heads of d, `stride` apart; more than kMostElems counts as one more.
+int64_t heads_len(int64_t heads, int64_t stride, int64_t d)
+{
+    if (heads <= 0) return 0;
+    if (heads > 1 && stride > (kMostElems - d) / (heads - 1)) return kMostElems + 1;
+    return (heads > 1 ? (heads - 1) * stride : 0) + d;
+}
+
 bool overlap(const Span &a, const Span &b) { return a.lo < b.hi && b.lo < a.hi; }
 bool aligned(const void *p, int64_t a) { return (uintptr_t)p % (uintptr_t)a == 0; }
 
@@ -31,7 +41,7 @@ int check_operand(const Operand &o, Span *span)
     if (o.p == nullptr) return GDN_ERR_ARG;
     if (o.rows > 1 && o.stride < o.len) return GDN_ERR_ARG;
     if (!aligned(o.p, o.elem)) return GDN_ERR_ALIGN;
-    if (o.rows > 1 && o.rows - 1 > (INT64_MAX / 16 - o.len) / o.stride) return GDN_ERR_ARG;
+    if (o.len > kMostElems || (o.rows > 1 && o.rows - 1 > (kMostElems - o.len) / o.stride)) return GDN_ERR_ARG;
     const int64_t elems = (o.rows > 1 ? (o.rows - 1) * o.stride : 0) + o.len;
     span->lo = (uintptr_t)o.p;
     span->hi = span->lo + (uintptr_t)elems * (uintptr_t)o.elem;
@@ -87,7 +97,7 @@ int check_cache(const void *k, const void *v, int dtype, const CacheLayout &c, i
         for (int i = 0; i < n; ++i) {
             if (dims[i].count <= 1) continue;
             if (dims[i].stride < *extent) return false;
-            if (dims[i].count - 1 > (INT64_MAX / 16 - *extent) / dims[i].stride) return false;
+            if (dims[i].count - 1 > (kMostElems - *extent) / dims[i].stride) return false;
             *extent += (dims[i].count - 1) * dims[i].stride;
         }
         return true;
@@ -193,7 +203,7 @@ GDN_API int gdna_qk_norm_rope(const void *q, const void *k, const void *v, gdna_
     const int n_out = n;
     // q_out on top of q, row for row and head for head, is the in-place call
     const bool in_place = q_out == q && q_head_stride == d && (q_out_stride == q_stride || rows == 1);
-    const int64_t q_len = nq > 0 ? (nq - 1) * q_head_stride + d : 0;
+    const int64_t q_len = heads_len(nq, q_head_stride, d);
     if (in_place) {
         if (rows > 1 && q_stride < hq) return GDN_ERR_ARG;
     } else {
@@ -280,7 +290,7 @@ GDN_API int gdna_attn_decode(const void *q, gdna_dtype dtype, const void *gate,
     ops[n++] = {table, batch, max_pages, table_stride, 4};
     ops[n++] = {kv_len, 1, batch, batch, 4};
     if (gate != nullptr)
-        ops[n++] = {gate, rows, (nq - 1) * gate_head_stride + d, gate_stride, elem_size(dtype)};
+        ops[n++] = {gate, rows, heads_len(nq, gate_head_stride, d), gate_stride, elem_size(dtype)};
     st = check_operands(ops, n, n_out);
     if (st != GDN_OK) return st;
     if (workspace_bytes < need) return GDN_ERR_ARG;

@@ -249,3 +249,13 @@ def test_the_queue_of_parts_holds_every_part_in_use():
                 if step - stages > in_use:              # that stage is not released yet
                     break
                 step += 1
+
+
+@pytest.mark.parametrize("stride", [1 << 60, 1 << 62, (1 << 63) - 1, (1 << 63) // 3 + 1])
+def test_head_strides_whose_products_pass_64_bits_are_refused(lib, stride):
+    """The last head's offset, and an array's bytes, are counted without wrapping."""
+    for rows in (1, 2):
+        assert rope(lib, qhs=stride, qs=stride, rows=rows) == ARG
+        assert attn(lib, ghs=stride, gs=stride, batch=rows, q_len=1) == ARG
+    assert rope(lib, qhs=stride, nq=1, qs=128) == 5                       # one head: the stride is not used
+    assert attn(lib, ghs=stride, gs=128, nq=1, nkv=1) == 5
