@@ -237,6 +237,8 @@ GDN_API int gdna_qk_norm_rope(const void *q, const void *k, const void *v, gdna_
                       rows_aligned(v, e, 4 * e, {v_stride}) && rows_aligned(q_out, e, 4 * e, {q_out_stride}) &&
                       rows_aligned(k_out, e, 4 * e, {k_out_stride}) && aligned(qn, 16) && aligned(kn, 16) && aligned(cos_sin, 16) &&
                       (!caching || (rows_aligned(k_cache, c, 4 * c, {page_stride, token_stride, head_stride}) && aligned(v_cache, 4 * c)));
+    // the general kernel's blocks of eight heads are counted in 31 bits
+    if (!fast && rows * (nq + (v != nullptr ? 2 : 1) * (int64_t)nkv) > 8 * (int64_t)INT32_MAX) return GDN_ERR_UNSUPPORTED;
     return gdn::report_cuda_error(launch_qk_norm_rope(p, fast, (cudaStream_t)stream));
 }
 

@@ -149,7 +149,11 @@ GDN_API int gdna_page_assign(const int32_t *cached, const int32_t *fresh, int32_
  *   otherwise an output overlapping any operand is GDN_ERR_ALIAS.  Rows of one
  *   stride that lie side by side (q, k and v of one projection) do not overlap,
  *   and k_cache and v_cache may be interleaved in one buffer.
- *   1 <= D <= 256, rot even and <= D, norms and rotations in fp32.
+ *   1 <= D <= 256, rot even and <= D, norms and rotations in fp32.  Head sizes
+ *   64, 128 and 256 with rot a multiple of 8, on boundaries of four elements, run
+ *   a vector kernel; any other call runs a general one, two to three times slower, which
+ *   takes at most 2^34 - 8 heads (rows * (NQ + NKV + NKV)) a call
+ *   (GDN_ERR_UNSUPPORTED).
  */
 GDN_API int gdna_qk_norm_rope(const void *q, const void *k, const void *v, gdna_dtype dtype,
                               const float *qn, const float *kn, float eps,

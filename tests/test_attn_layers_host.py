@@ -259,3 +259,15 @@ def test_head_strides_whose_products_pass_64_bits_are_refused(lib, stride):
         assert attn(lib, ghs=stride, gs=stride, batch=rows, q_len=1) == ARG
     assert rope(lib, qhs=stride, nq=1, qs=128) == 5                       # one head: the stride is not used
     assert attn(lib, ghs=stride, gs=128, nq=1, nkv=1) == 5
+
+
+def test_more_heads_than_the_general_kernel_counts_are_refused(lib):
+    """2^20 heads of 2^14 rows are 2^34, of 2^17 rows 2^37: more blocks of eight than a grid has."""
+    far = [(1 << 45) * (i + 1) for i in range(5)]
+    big = dict(q=far[0], k=None, v=None, qo=far[1], ko=None, kc=None, vc=None, cs=far[2], pos=far[3], slots=far[4], qn=None,
+               kn=None, d=1, rot=0, nq=1 << 20, nkv=0, qs=1 << 20, qhs=1, qos=1 << 20)
+    for rows in (1 << 14, 1 << 15, 1 << 17):
+        assert rope(lib, **big, rows=rows) == UNSUP
+    assert rope(lib, **big, rows=(1 << 14) - 1) == 5
+    vec = {**big, "d": 64, "qhs": 64, "qs": 1 << 26, "qos": 1 << 26}      # the vector kernel: blocks of rows
+    assert rope(lib, **vec, rows=1 << 14) == 5
