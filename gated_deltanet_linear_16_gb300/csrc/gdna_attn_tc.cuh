@@ -334,7 +334,8 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, int
 
     // The steps of the block's parts in order.  Pages are looked up a step before they are needed, also from
     // one part to the next: a load's latency there would leave the rings dry.  What a stage's refill waits for
-    // is short for the same reason.
+    // is short for the same reason.  The table is read by plain loads: the call before this one may still write it when
+    // this kernel becomes resident, so it is not read-only for the kernel's life.
     // lane: a copy of a unit, some keys of a block of K or V for consumer y (or, without tensor copies, a key of each)
     const int per = copies.keys != 0 ? S::kCopies * (kKeys / copies.keys) : 32;
     const int y = who + lane / per * P, copy = lane % per, block = copy % KB, values = copy / KB % 2, row = copy / S::kCopies * copies.keys;
@@ -388,7 +389,7 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, int
             if (mine && key < keys) {
                 const unsigned n = p.page_div.quotient(key);
                 token = (int)(key - n * page_size);
-                page = __ldg(table + n);
+                page = table[n];
             }
         };
         if (more) look_up();
@@ -420,7 +421,7 @@ __device__ __forceinline__ Ring produce(const AttnParams &p, Run run, int c, int
             if (key < keys) {
                 const unsigned n = p.page_div.quotient(key);
                 place = key - n * page_size;
-                page = __ldg(table + n);
+                page = table[n];
             }
         };
         if (more) look_up();

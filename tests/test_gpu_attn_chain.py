@@ -84,3 +84,33 @@ def test_steps_of_two_tokens(cuda_lib, d, page, kind):
         # a stored key may round to the other neighbour where the fp32 rotation and the 64-bit one straddle a tie
         # (2^-8 of a value for bf16, rarely); the attention itself is far nearer
         assert (np.abs(f64(out) - want) <= 2.0 ** -9 * np.maximum(vmax, 1)).all()
+
+
+@pytest.mark.parametrize("page,d", [(16, 128), (8, 64), (5, 128)])
+def test_a_table_written_just_before_it_is_read(cuda_lib, page, d):
+    """Page assignment and attention back to back, no wait between them, into a table whose entries the last turn left
+    pointing elsewhere: every turn reads the pages that its own assignment wrote.  (Keys are zero and a page's values its
+    number, so a row is the mean of its pages.)"""
+    batch, nq, turns, held = 96, 4, 24, 2
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pages = 1021
+    kc = torch.zeros((pages, page, 1, d), dtype=torch.float16, device="cuda")
+    vc = torch.zeros_like(kc) + torch.arange(pages, device="cuda", dtype=torch.float16)[:, None, None, None]
+    free = [torch.randperm(pages, generator=torch.Generator().manual_seed(i)).to(**i32) for i in range(turns)]
+    table = torch.zeros((batch, held), **i32)
+    cached, fresh, head = torch.zeros(batch, **i32), torch.full((batch,), held * page, **i32), torch.zeros(1, **i32)
+    kv_len, start, head_out, unserved = torch.zeros(batch, **i32), torch.zeros(batch + 1, **i32), torch.zeros(1, **i32), torch.zeros(1, **i32)
+    rows = batch * held * page
+    slots, pos = torch.zeros(rows, dtype=torch.int64, device="cuda"), torch.zeros(rows, **i32)
+    q = torch.randn((batch, nq * d), device="cuda")
+    out = torch.zeros((turns, batch, nq * d), device="cuda")
+    ws = torch.empty(gdn.gdna_attn_workspace(batch=batch, q_len=1, nq=nq, nkv=1, d=d), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(turns):
+        gdn.gdna_page_assign(cached, fresh, table, free[i], head, kv_len, start, slots, pos, head_out, unserved, batch=batch,
+                             rows=rows, page_size=page, max_pages=held)
+        gdn.gdna_attn_decode(q, kc, vc, table, kv_len, out[i], ws, batch=batch, nq=nq, nkv=1, d=d, pages=pages,
+                             page_size=page, max_pages=held)
+    for i in range(turns):
+        want = free[i][:batch * held].view(batch, held).double().mean(1)
+        assert (out[i].double() - want[:, None]).abs().max() <= 2.0 ** -19 * pages
