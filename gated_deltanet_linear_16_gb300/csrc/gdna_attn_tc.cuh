@@ -989,9 +989,12 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
 {
     using S = Shape<CACHE, D, NT, R>;
     const bool bf16 = CACHE == GDNA_BF16;
-    // 16-bit parts of a query: what its type holds (bf16 products have 8 bits a part, fp16 products 11), but for an
-    // fp32 query, a bf16 cache and a 16-bit output two parts: the scores' 2^-17 is far below the output's rounding
-    const int q_parts = p.dtype == GDNA_BF16 ? 1 : p.dtype == GDNA_F16 ? (bf16 ? 2 : 1) : (bf16 ? (p.out_dtype == GDNA_F32 ? 3 : 2) : 2);
+    // 16-bit parts of a query: what its type holds (bf16 products have 8 bits a part, fp16 products 11).  An fp32 query over
+    // a bf16 cache needs three; two, where nothing but a bf16 output shows it: its scores are then off by up to 2^-17 of
+    // sum |q_i k_i| * scale, which moves a weight less than the keys' own 2^-9 did when they were stored.  32 requests, two
+    // against three parts: 8 rows of 128 99 against 101 us, 16 rows 61 against 70, 12 rows of 256 74 against 86.
+    const bool coarse = p.out_dtype == GDNA_BF16 && p.lse == nullptr;
+    const int q_parts = p.dtype == GDNA_BF16 ? 1 : p.dtype == GDNA_F16 ? (bf16 ? 2 : 1) : (bf16 && !coarse ? 3 : 2);
     // and weights: two fp16 parts hold 22 bits (down to 2^-40 of the row's largest), two bf16 parts 16, three 24 for an fp32
     // output
     const int w_parts = bf16 && p.out_dtype == GDNA_F32 ? 3 : 2;

@@ -207,8 +207,10 @@ GDN_API int64_t gdna_attn_workspace(int batch, int q_len, int nq, int nkv, int d
  *   the fastest, multiples of 8 and of 4 nearly so.
  *   Scores, softmax sums and outputs are held in fp32; queries and weights enter
  *   the products in two or three 16-bit parts where one would show in the output.
- *   On the tensor cores a weight over an F16 or E4M3 cache is held to 2^-22 of
- *   itself or 2^-40 of its row's largest, whichever is more.
+ *   On the tensor cores an F32 query over a BF16 cache keeps 16 bits where out is
+ *   BF16 and lse NULL, else all 24; a weight over an F16 or E4M3 cache is held to
+ *   2^-22 of itself or 2^-40 of its row's largest, whichever is more, over a BF16
+ *   cache to 2^-16 of itself (F32 out: 2^-24).
  *   A value or key that is not finite shows in the rows that see it.  Results do
  *   not depend on timing.
  *   The tensor-core kernels' waits for their own copies are bounded

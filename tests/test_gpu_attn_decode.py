@@ -2,7 +2,8 @@
 
 Bounds, with e = 2^-24 and S the largest sum |q_i k_i| * scale of a row.  A score is
 a sum of D products in fp32 whose roundings are independent (8 standard deviations:
-8 sqrt(D) e S), of queries in 16-bit parts that hold 20 bits or more (2^-20 S); both
+8 sqrt(D) e S), of queries in 16-bit parts that hold 20 bits or more (2^-20 S; fp32 queries over a bf16 cache with a
+bf16 output and no log-sum-exp hold 16: no case here has that form with scores where it shows); both
 its maximum and its own error enter a weight.  Weights enter the products in parts of
 16 bits or more (2^-16, 2^-20 with an fp32 output), the sums over n keys add 8 sqrt(n) e,
 the running maximum's rescales a few e more.  All of it scales max |v|; the output's
@@ -373,3 +374,40 @@ def test_small_weights_beside_a_large_one(cuda_lib, cache, d, group, ahead, wort
     assert (miss <= 0).all(), (miss.max(), np.abs(want).max())
     lim = score[..., 0] + (8 * np.sqrt(n) + 8) * E32 + 4 * E32 * np.abs(want_lse)
     assert (np.abs(f64(lse).reshape(want_lse.shape) - want_lse) <= lim).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f16"])
+@pytest.mark.parametrize("d,group", [(64, 1), (128, 3), (256, 12), (128, 40)])
+@pytest.mark.parametrize("out_type", ["f32", "f16", "bf16"])
+def test_bits_of_an_fp32_query(cuda_lib, cache, d, group, out_type):
+    """Scores of hundreds that hang on the last bits of fp32 queries.  A query has two elements, x and y, the first key picks
+    x, the second y: a score is one element times the scale, exact but for the query's parts (2^-23), the scale in units of
+    log2, its product and the subtraction of the maximum: 8 roundings of 2^-24.  The log-sum-exp shows the error itself, with
+    its own 4 roundings; a weight of two keys a quarter of it."""
+    batch, nkv, scale = 3, 2, 512.0
+    s = make([2, 1, 2], nkv * group, nkv, d, dtype="f32", cache=cache, seed=d)
+    # x's rest after two bf16 parts is nearly half a unit of the second: 2^-17 (1 - 2^-5)
+    x, y = 1.0 + 2.0 ** -8 - 2.0 ** -16 + 2.0 ** -17 - 2.0 ** -22, 1.0 + 2.0 ** -9
+    q = torch.zeros((batch, nkv * group, d))
+    q[..., 0], q[..., 1] = x, y
+    rest = q[0, 0, 0] - q[0, 0, 0].bfloat16().float()
+    assert abs(rest - rest.bfloat16().float()) > 2.0 ** -17.2
+    s.update(scale=scale, q=q.view(batch, -1).cuda())
+    for b, n in enumerate(s["lens"]):
+        for j in range(n):
+            key = torch.zeros((1, nkv, d))
+            key[..., j] = 1.0
+            value = torch.full((1, nkv, d), 1.0 - 2.0 * j)
+            at = s["table"][b, :1].cpu().long(), torch.tensor([j])
+            s["keys"][b][j] = s["store"].put("k", *at, key)[0]
+            s["values"][b][j] = s["store"].put("v", *at, value)[0]
+    out = torch.zeros((batch, nkv * group * d), dtype=TYPES[out_type], device="cuda")
+    lse = torch.zeros((batch * nkv * group,), device="cuda")
+    call(s, out, lse)
+    want, want_lse, size, _ = attention64(q.double().numpy(), s["keys"], s["values"], s["lens"], 1, scale)
+    off = np.abs(f64(lse).reshape(want_lse.shape) - want_lse)
+    assert (off <= 12 * E32 * size[..., 0]).all(), (off / size[..., 0]).max()
+    part = 2.0 ** -20 if out_type == "f32" else 2.0 ** -16
+    tol = 2 * 0.25 * 2 * 8 * E32 * size + part + 32 * E32 + HALF_ULP[out_type] * 1.001 * np.abs(want) + HALF_STEP0[out_type]
+    miss = np.abs(f64(out).reshape(want.shape) - want) - tol
+    assert (miss <= 0).all(), miss.max()
