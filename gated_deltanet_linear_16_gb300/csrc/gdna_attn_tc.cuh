@@ -42,8 +42,8 @@
 //   A tensor copy brings as many keys as surely lie in one page, 16 or a smaller power of two
 // that divides the page size, one lane a copy; 16 keys come with all panels of a head at once
 // (a producer pays some 40 ns a copy, one after the other).  Where that makes more than 32
-// copies (short pages), and for layouts that the encoder refuses, the producer's lanes copy 16
-// bytes at a time (cp.async) to the same places.
+// copies (short pages), for heads that end within their only panel, and for layouts that the
+// encoder refuses, the producer's lanes copy 16 bytes at a time (cp.async) to the same places.
 // Head sizes in between run padded to the next of the three: a copy fills what lies past a
 // head with zeros.
 #pragma once
@@ -955,9 +955,9 @@ attn_tc(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __g
 }
 
 // The map of the cache's K or V: elements of a panel, token, panel, head, page; box: `keys` tokens x all panels of a
-// head, which is how they lie in a stage.  Fewer than 16 keys, and a head that ends within a panel, come panel by
-// panel, the head's elements the first dimension and the panel none: what lies past the head is filled with zeros.  False where the encoder
-// refuses the layout.
+// head, which is how they lie in a stage.  Fewer than 16 keys, and a head of several panels that ends within one, come
+// panel by panel, the head's elements the first dimension and the panel none: what lies past the head is filled with
+// zeros.  False where the encoder refuses the layout.
 template <int CACHE, int D, int NT, int R>
 bool cache_map(const AttnParams &p, const void *base, const Copies &copies, CUtensorMap *map)
 {
@@ -965,7 +965,7 @@ bool cache_map(const AttnParams &p, const void *base, const Copies &copies, CUte
     const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn::tensor_map_encoder());
     if (encode == nullptr) return false;
     constexpr int kPanelElems = S::kPanel / S::kElem;
-    const bool whole = copies.pieces == 1;
+    const bool whole = copies.pieces == 1;                     // (its panels are full: `launch`)
     const int64_t strides[4] = {p.cache.token_stride, kPanelElems, p.cache.head_stride, p.cache.page_stride};
     const cuuint64_t size[5] = {(cuuint64_t)(whole ? kPanelElems : p.d), (cuuint64_t)p.cache.page_size,
                                 (cuuint64_t)(whole ? p.d / kPanelElems : 1), (cuuint64_t)p.nkv, (cuuint64_t)p.cache.pages};
@@ -1024,8 +1024,10 @@ cudaError_t launch(AttnParams p, cudaStream_t s)
     const int lanes = S::kKeyWarps * S::kCopies * (kKeys / copies.keys);
     int producers = lanes * copies.pieces <= 16 ? 1 : lanes * copies.pieces <= 64 ? 2 : 4;
     if (producers > S::kProducers) producers = S::kProducers;
-    // a lane for each copy's key (all its pieces); else cp.async
-    if ((S::kKeyWarps + producers - 1) / producers * S::kCopies * (kKeys / copies.keys) > 32 ||
+    // a lane for each copy's key (all its pieces); else cp.async.  A head that ends within its only panel as well: tensor
+    // copies that fill the rest took 71 us against 67 for 32 requests of bf16 heads of 48, 137 against 133 and 136 against
+    // 127 for 256 requests of E4M3 heads of 96 and 80 (and 48 against 54 for bf16 heads of 32, not taken apart).
+    if ((S::kPanels == 1 && p.d * S::kElem % S::kPanel != 0) || (S::kKeyWarps + producers - 1) / producers * S::kCopies * (kKeys / copies.keys) > 32 ||
         !cache_map<CACHE, D, NT, R>(p, p.k, copies, &k_map) || !cache_map<CACHE, D, NT, R>(p, p.v, copies, &v_map)) {
         copies = Copies{0, 0};
         producers = S::kPerSm == 2 && S::kProducers == 2 ? 2 : 1;

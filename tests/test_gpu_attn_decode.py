@@ -8,6 +8,8 @@ its maximum and its own error enter a weight.  Weights enter the products in par
 16 bits or more (2^-16, 2^-20 with an fp32 output), the sums over n keys add 8 sqrt(n) e,
 the running maximum's rescales a few e more.  All of it scales max |v|; the output's
 type adds half a unit in its last place."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -411,3 +413,46 @@ def test_bits_of_an_fp32_query(cuda_lib, cache, d, group, out_type):
     tol = 2 * 0.25 * 2 * 8 * E32 * size + part + 32 * E32 + HALF_ULP[out_type] * 1.001 * np.abs(want) + HALF_STEP0[out_type]
     miss = np.abs(f64(out).reshape(want.shape) - want) - tol
     assert (miss <= 0).all(), miss.max()
+
+
+class KernelNode(ctypes.Structure):
+    """The driver's CUDA_KERNEL_NODE_PARAMS."""
+    _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3), ("shared", ctypes.c_uint),
+                ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p), ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+
+def launched_blocks(s):
+    """Threads of a block of each kernel that a call launches, from a capture that is not run."""
+    cu = ctypes.CDLL("libcuda.so.1")
+    stream = torch.cuda.Stream()
+    call(s, torch.zeros((len(s["lens"]) * s["q_len"], s["nq"] * s["d"]), device="cuda"))
+    out = torch.zeros((len(s["lens"]) * s["q_len"], s["nq"] * s["d"]), device="cuda")
+    ws = torch.empty(gdn.gdna_attn_workspace(batch=len(s["lens"]), q_len=s["q_len"], nq=s["nq"], nkv=s["nkv"], d=s["d"]),
+                     dtype=torch.uint8, device="cuda")
+    lens = torch.tensor(s["lens"], dtype=torch.int32, device="cuda")
+    kp, vp = s["store"].addresses()
+    torch.cuda.synchronize()
+    handle, graph, n = ctypes.c_void_p(stream.cuda_stream), ctypes.c_void_p(), ctypes.c_size_t(8)
+    assert cu.cuStreamBeginCapture_v2(handle, 2) == 0
+    gdn.gdna_attn_decode(s["q"], kp, vp, s["table"], lens, out, ws, batch=len(s["lens"]), q_len=s["q_len"], nq=s["nq"],
+                         nkv=s["nkv"], d=s["d"], max_pages=s["max_pages"], table_stride=s["table"].stride(0),
+                         q_stride=s["q"].stride(0), stream=stream, **s["store"].args())
+    assert cu.cuStreamEndCapture(handle, ctypes.byref(graph)) == 0
+    nodes, threads = (ctypes.c_void_p * 8)(), []
+    assert cu.cuGraphGetNodes(graph, nodes, ctypes.byref(n)) == 0
+    for node in nodes[:n.value]:
+        params = KernelNode()
+        assert cu.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(params)) == 0
+        threads.append(params.block[0])
+    assert cu.cuGraphDestroy(graph) == 0
+    return sorted(threads)
+
+
+@pytest.mark.parametrize("cache,full,sizes", [("bf16", 64, (8, 16, 32, 40, 48, 56)), ("f16", 64, (24,)), ("e4m3", 64, (16, 32, 48)),
+                                              ("e4m3", 128, (80, 96, 112))])
+def test_how_heads_of_one_panel_are_copied(cuda_lib, cache, full, sizes):
+    """A head that fills its panel comes by tensor copies, which one warp issues; one that ends within it 16 bytes at a time,
+    by two."""
+    assert launched_blocks(make([100, 7], 6, 2, full, cache=cache)) == [128, 160]            # the join, the kernel
+    for d in sizes:
+        assert launched_blocks(make([100, 7], 6, 2, d, cache=cache)) == [128, 192], d
