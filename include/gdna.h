@@ -12,7 +12,9 @@
  * Conventions are gdn.h's: device pointers the caller owns, strides in ELEMENTS,
  * asynchronous on `stream`, nothing allocated, arguments checked on the host
  * before anything is launched, status codes GDN_OK / GDN_ERR_*.  Sizes of zero
- * (batch, rows, q_len) are valid empty calls.  Values that live on the device
+ * (batch, rows, q_len) are valid empty calls: no CUDA call is made and nothing
+ * is written (but for gdna_page_assign with rows 0 and a batch, whose lengths,
+ * starts, head and count are).  Values that live on the device
  * (lengths, page numbers, positions, slots) cannot be checked on the host; the
  * kernels check them, and each entry point says what an invalid one does.  No
  * such value makes a kernel leave its buffers.
@@ -107,6 +109,9 @@ GDN_API int gdna_rope_table(float *table, int64_t n_pos, int rot, double base, g
  *   pages have run out; from the first that runs out of pages on, only sequences
  *   that need no page are served.  A sequence that is not served takes no page.
  *   A negative entry of the table or of free_pages gives slot -1.
+ *   A batch of 0 is an empty call like any other: no output is written, whatever
+ *   `rows`.  A caller that swaps two head buffers each step does not swap them
+ *   then, and has no row to store.
  *   No output may overlap another operand (pass two buffers in turn for
  *   free_head).  Results do not depend on timing.
  *   Limits: batch <= 2^20, page_size, max_pages >= 1, rows < 2^31 - 4096

@@ -168,3 +168,23 @@ def test_empty_calls_and_another_stream(cuda_lib):
     rows = int(fresh.sum())
     got = run(cached, fresh, table, free, head, rows, 16, 40, stream=torch.cuda.Stream())
     compare(got, walk(cached, fresh, table, free, head, rows, 16, 40), head)
+
+
+@pytest.mark.parametrize("rows", [0, 5])
+def test_a_batch_of_zero_writes_nothing(cuda_lib, rows):
+    """An empty call, as the header says: the head stays where the caller has it, and no slot, start or count changes."""
+    outs = [torch.full((8,), -9, dtype=torch.int64 if i == 2 else torch.int32, device="cuda") for i in range(6)]
+    ins = [torch.full((8,), 3, dtype=torch.int32, device="cuda") for _ in range(5)]
+    kv_len, start, slots, positions, head_out, unserved = outs
+    cached, fresh, table, free, head = ins
+    gdn.gdna_page_assign(cached, fresh, table, free, head, kv_len, start, slots, positions, head_out, unserved, batch=0,
+                         rows=rows, page_size=16, max_pages=1)
+    torch.cuda.synchronize()
+    assert all((x == -9).all() for x in outs) and all((x == 3).all() for x in ins)
+
+
+def test_a_batch_without_new_tokens_or_rows(cuda_lib):
+    """rows 0 with a batch is a call: lengths, starts, head and count are written."""
+    got = run(np.array([5, 0, 40]), np.array([0, 0, 0]), np.array([[4, -1, -1], [-1, -1, -1], [5, 6, 7]]), np.array([9, 8]), 1, 0, 16, 3)
+    assert got["kv_len"].tolist() == [5, 0, 40] and got["row_start"].tolist() == [0, 0, 0, 0]
+    assert got["head"][0] == 1 and got["unserved"][0] == 0
