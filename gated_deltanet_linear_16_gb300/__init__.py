@@ -403,6 +403,17 @@ def gdn_last_cuda_error() -> int:
 # ------------------------------------------------------------------ attention layers (include/gdna.h)
 
 _GDNA_TYPES = {}            # torch dtype -> GDNA_*, filled on first use
+_I32 = _I64 = _F32 = None   # torch's, set with it
+
+
+def _gdna_types():
+    global _I32, _I64, _F32
+    if not _GDNA_TYPES:
+        import torch
+        _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+        _GDNA_TYPES.update({torch.float32: GDNA_F32, torch.float16: GDNA_F16, torch.bfloat16: GDNA_BF16,
+                            torch.float8_e4m3fn: GDNA_E4M3})
+    return _GDNA_TYPES
 
 
 def _gdna_dtype(x, dtype):
@@ -411,33 +422,46 @@ def _gdna_dtype(x, dtype):
         return dtype
     if isinstance(x, int):
         raise ValueError("a dtype is required for a raw address")
-    if not _GDNA_TYPES:
-        import torch
-        _GDNA_TYPES.update({torch.float32: GDNA_F32, torch.float16: GDNA_F16, torch.bfloat16: GDNA_BF16,
-                            torch.float8_e4m3fn: GDNA_E4M3})
     code = _GDNA_TYPES.get(x.dtype)
     if code is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
     return code
 
 
+def _at(x, dtype, name):
+    """_ptr of an operand whose type the call lays down (None: whatever it is): another one would be read, or written past
+    its end, as if it had that type.  A raw address is taken at its word."""
+    if x is None or x.__class__ is int:
+        return x
+    if dtype is None or x.dtype is dtype:
+        return x.data_ptr()
+    raise ValueError(f"{name} is {x.dtype}, not {dtype}")
+
+
 def gdna_rope_table(table, *, n_pos, rot, base, kind=GDNA_ROPE_PLAIN, factor=1.0, original_len=0.0, beta_fast=32.0,
                     beta_slow=1.0, amplitude=1.0):
     """Cosines and sines of positions [0, n_pos) into a HOST fp32 tensor [n_pos, rot] (rot/2 cosines, then
     rot/2 sines a row), computed in 64 bits; copy it to the GPU once."""
+    _GDNA_TYPES or _gdna_types()
     if not isinstance(table, int) and table.device.type != "cpu":
         raise ValueError("gdna_rope_table fills host memory")
-    _check("gdna_rope_table", load().gdna_rope_table(_ptr(table), n_pos, rot, base, kind, factor, original_len,
+    _check("gdna_rope_table", load().gdna_rope_table(_at(table, _F32, "table"), n_pos, rot, base, kind, factor, original_len,
                                                      beta_fast, beta_slow, amplitude))
 
 
 def gdna_page_assign(cached, fresh, table, free_pages, free_head, kv_len, row_start, slots, positions, free_head_out,
                      unserved, *, batch, rows, page_size, max_pages, n_free=None, table_stride=None, stream=None):
-    """Pages, slots and positions of a step's new tokens from the sequences' lengths.  See include/gdna.h."""
+    """Pages, slots and positions of a step's new tokens from the sequences' lengths.  All int32, slots (where there are
+    rows) int64.  See include/gdna.h."""
+    _GDNA_TYPES or _gdna_types()
+    i32 = _I32
     st = (_lib or load()).gdna_page_assign(
-        _ptr(cached), _ptr(fresh), _ptr(table), max_pages if table_stride is None else table_stride,
-        _ptr(free_pages), free_pages.numel() if n_free is None else n_free, _ptr(free_head), _ptr(kv_len),
-        _ptr(row_start), _ptr(slots), _ptr(positions), _ptr(free_head_out), _ptr(unserved), batch, rows, page_size,
+        _at(cached, i32, "cached"), _at(fresh, i32, "fresh"), _at(table, i32, "table"),
+        max_pages if table_stride is None else table_stride,
+        _at(free_pages, i32, "free_pages"), free_pages.numel() if n_free is None else n_free,
+        _at(free_head, i32, "free_head"), _at(kv_len, i32, "kv_len"), _at(row_start, i32, "row_start"),
+        _at(slots, _I64 if rows else None, "slots"), _at(positions, i32, "positions"),
+        _at(free_head_out, i32, "free_head_out"), _at(unserved, i32, "unserved"), batch, rows, page_size,
         max_pages, _stream(stream))
     if st:
         _check("gdna_page_assign", st)
@@ -448,14 +472,23 @@ def gdna_qk_norm_rope(q, k, v, qn, kn, cos_sin, positions, slots, q_out, k_cache
                       v_scale=1.0, dtype=None, cache_dtype=None, q_stride=None, q_head_stride=None, k_stride=None,
                       v_stride=None, q_out_stride=None, k_out_stride=None, page_stride=None, token_stride=None,
                       head_stride=None, stream=None):
-    """Per-head RMS norm and rotary positions of q and k, and the cache's new rows, in one pass.  Strides default
-    to contiguous rows and a cache [pages, page_size, nkv, d].  See include/gdna.h."""
+    """Per-head RMS norm and rotary positions of q and k, and the cache's new rows, in one pass.  q, k, v, q_out and k_out
+    have one type and the caches one (unless `dtype`, `cache_dtype` say which), norms and cos_sin are fp32, positions
+    int32, slots int64.  Strides default to contiguous rows and a cache [pages, page_size, nkv, d].  See include/gdna.h."""
+    _GDNA_TYPES or _gdna_types()
     hk = nkv * d
     token_stride = hk if token_stride is None else token_stride
+    lead = k if q is None else q
+    code = _gdna_dtype(lead, dtype)
+    t = lead.dtype if dtype is None else None
+    cache_code = GDNA_F16 if k_cache is None else _gdna_dtype(k_cache, cache_dtype)
+    c = k_cache.dtype if cache_dtype is None and k_cache is not None else None
+    f32 = _F32
     st = (_lib or load()).gdna_qk_norm_rope(
-        _ptr(q), _ptr(k), _ptr(v), _gdna_dtype(k if q is None else q, dtype), _ptr(qn), _ptr(kn), eps, _ptr(cos_sin),
-        n_pos, rot, 1 if interleaved else 0, _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_out), _ptr(k_cache),
-        _ptr(v_cache), GDNA_F16 if k_cache is None else _gdna_dtype(k_cache, cache_dtype), k_scale, v_scale,
+        _at(q, t, "q"), _at(k, t, "k"), _at(v, t, "v"), code, _at(qn, f32, "qn"), _at(kn, f32, "kn"), eps,
+        _at(cos_sin, f32, "cos_sin"), n_pos, rot, 1 if interleaved else 0, _at(positions, _I32, "positions"),
+        _at(slots, _I64, "slots"), _at(q_out, t, "q_out"), _at(k_out, t, "k_out"), _at(k_cache, c, "k_cache"),
+        _at(v_cache, c, "v_cache"), cache_code, k_scale, v_scale,
         rows, nq, nkv, d, pages, page_size, nq * d if q_stride is None else q_stride,
         d if q_head_stride is None else q_head_stride, hk if k_stride is None else k_stride,
         hk if v_stride is None else v_stride, nq * d if q_out_stride is None else q_out_stride,
@@ -476,12 +509,17 @@ def gdna_attn_decode(q, k_cache, v_cache, table, kv_len, out, workspace, *, batc
                      gate_stride=None, gate_head_stride=None, out_stride=None, page_stride=None, token_stride=None,
                      head_stride=None, stream=None):
     """Attention of the q_len newest tokens of each sequence over its paged cache; scale defaults to 1/sqrt(d),
-    strides to contiguous rows and a cache [pages, page_size, nkv, d].  See include/gdna.h."""
+    strides to contiguous rows and a cache [pages, page_size, nkv, d].  gate has q's type and v_cache k_cache's (unless
+    `dtype`, `cache_dtype` say which), table and kv_len are int32, lse fp32.  See include/gdna.h."""
+    _GDNA_TYPES or _gdna_types()
     hq, hk = nq * d, nkv * d
+    code, cache_code = _gdna_dtype(q, dtype), _gdna_dtype(k_cache, cache_dtype)
+    c = k_cache.dtype if cache_dtype is None else None
     st = (_lib or load()).gdna_attn_decode(
-        _ptr(q), _gdna_dtype(q, dtype), _ptr(gate), _ptr(k_cache), _ptr(v_cache), _gdna_dtype(k_cache, cache_dtype),
-        k_scale, v_scale, _ptr(table), max_pages if table_stride is None else table_stride, _ptr(kv_len),
-        d ** -0.5 if scale is None else scale, _ptr(out), _gdna_dtype(out, out_dtype), _ptr(lse), _ptr(workspace),
+        _ptr(q), code, _at(gate, q.dtype if dtype is None else None, "gate"), _ptr(k_cache), _at(v_cache, c, "v_cache"),
+        cache_code, k_scale, v_scale, _at(table, _I32, "table"), max_pages if table_stride is None else table_stride,
+        _at(kv_len, _I32, "kv_len"), d ** -0.5 if scale is None else scale, _ptr(out), _gdna_dtype(out, out_dtype),
+        _at(lse, _F32, "lse"), _ptr(workspace),
         workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes,
         batch, q_len, nq, nkv, d, pages, page_size, max_pages, hq if q_stride is None else q_stride,
         hq if gate_stride is None else gate_stride, d if gate_head_stride is None else gate_head_stride,

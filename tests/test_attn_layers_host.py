@@ -271,3 +271,59 @@ def test_more_heads_than_the_general_kernel_counts_are_refused(lib):
     assert rope(lib, **big, rows=(1 << 14) - 1) == 5
     vec = {**big, "d": 64, "qhs": 64, "qs": 1 << 26, "qos": 1 << 26}      # the vector kernel: blocks of rows
     assert rope(lib, **vec, rows=1 << 14) == 5
+
+
+I32, I64, F16, BF16, F32, F64 = torch.int32, torch.int64, torch.float16, torch.bfloat16, torch.float32, torch.float64
+
+
+def binding_refuses(call, types, name, wrong):
+    """A call whose operands have these types, but for one: the binding says which, and the library is not asked."""
+    host = {n: torch.zeros(64, dtype=wrong if n == name else t) for n, t in types.items()}
+    with pytest.raises(ValueError, match=rf"^{name} is {wrong}"):
+        call(host)
+
+
+@pytest.mark.parametrize("name,wrong", [(n, I64) for n in ("cached", "fresh", "table", "free_pages", "free_head", "kv_len",
+                                                           "row_start", "positions", "free_head_out", "unserved")] + [("slots", I32)])
+def test_page_assign_checks_types(built, name, wrong):
+    types = {n: I32 for n in ("cached", "fresh", "table", "free_pages", "free_head", "kv_len", "row_start", "slots", "positions",
+                              "free_head_out", "unserved")}
+    types["slots"] = I64
+    binding_refuses(lambda x: gdn.gdna_page_assign(**x, batch=2, rows=4, page_size=4, max_pages=4, stream=0), types, name, wrong)
+
+
+@pytest.mark.parametrize("name,wrong", [("k", BF16), ("v", F16), ("q_out", BF16), ("k_out", F16), ("qn", BF16), ("kn", F64),
+                                        ("cos_sin", F64), ("positions", I64), ("slots", I32), ("v_cache", BF16)])
+def test_qk_norm_rope_checks_types(built, name, wrong):
+    types = dict(q=F32, k=F32, v=F32, qn=F32, kn=F32, cos_sin=F32, positions=I32, slots=I64, q_out=F32, k_out=F32, k_cache=F16,
+                 v_cache=F16)
+    binding_refuses(lambda x: gdn.gdna_qk_norm_rope(**x, rows=1, nq=2, nkv=1, d=8, rot=4, n_pos=8, pages=2, page_size=4, stream=0),
+                    types, name, wrong)
+
+
+@pytest.mark.parametrize("name,wrong", [("gate", F32), ("v_cache", BF16), ("table", I64), ("kv_len", I64), ("lse", BF16)])
+def test_attn_decode_checks_types(built, name, wrong):
+    types = dict(q=BF16, k_cache=F16, v_cache=F16, table=I32, kv_len=I32, out=BF16, workspace=torch.uint8, gate=BF16, lse=F32)
+    binding_refuses(lambda x: gdn.gdna_attn_decode(**x, batch=1, nq=2, nkv=1, d=8, pages=2, page_size=4, max_pages=2, stream=0),
+                    types, name, wrong)
+
+
+def test_rope_table_checks_types(built):
+    with pytest.raises(ValueError, match="^table is torch.float64"):
+        gdn.gdna_rope_table(torch.zeros((4, 8), dtype=F64), n_pos=4, rot=8, base=1e4)
+
+
+def test_given_types_and_raw_addresses_are_taken_at_their_word(lib):
+    """With `dtype` and `cache_dtype` the operands are what the caller says, as for raw addresses; the call then reaches the
+    launch, which fails without a GPU."""
+    raw = torch.zeros(1 << 22, dtype=torch.uint8)
+    at = lambda i: raw[i << 18:(i + 1) << 18]                                      # noqa: E731
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.gdna_attn_decode(at(0), at(1), at(2), at(3).view(I32), raw.data_ptr() + (4 << 18), at(5), at(6).data_ptr(), gate=at(13),
+                             batch=1, nq=2, nkv=1, d=8, pages=2, page_size=4, max_pages=2, stream=0, dtype=2, cache_dtype=3,
+                             out_dtype=0, workspace_bytes=1 << 40)
+    assert e.value.status == 5
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.gdna_qk_norm_rope(at(0), at(1), at(2), None, None, None, None, at(3).view(I64), at(4), at(5), at(6), rows=1, nq=2, nkv=1,
+                              d=8, rot=0, n_pos=0, pages=2, page_size=4, stream=0, dtype=1, cache_dtype=3)
+    assert e.value.status == 5
