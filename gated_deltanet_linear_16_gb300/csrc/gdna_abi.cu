@@ -82,6 +82,12 @@ bool plain_type(int dtype) { return dtype == GDNA_F32 || dtype == GDNA_F16 || dt
 bool cache_type(int dtype) { return dtype == GDNA_F16 || dtype == GDNA_BF16 || dtype == GDNA_E4M3; }
 bool sound_scale(float x) { return std::isfinite(x) && x > 0.f; }
 
+// An attention item is (key head, tile of 8 query rows or more); the rows of a sequence and all its items are int32.
+bool countable(int batch, int q_len, int nq)
+{
+    return (int64_t)q_len * nq <= (1 << 24) && batch <= (1 << 20) && (int64_t)batch * q_len <= INT32_MAX;
+}
+
 // The cache's strides keep its (page, token, head) vectors apart, and K's from V's
 // where the two share a buffer.  `span` is the elements of one array.
 int check_cache(const void *k, const void *v, int dtype, const CacheLayout &c, int nkv, int d, Operand *ok, Operand *ov)
@@ -244,7 +250,9 @@ GDN_API int gdna_qk_norm_rope(const void *q, const void *k, const void *v, gdna_
 
 GDN_API int64_t gdna_attn_workspace(int batch, int q_len, int nq, int nkv, int d)
 {
-    if (batch < 0 || q_len < 0 || nq <= 0 || nkv <= 0 || nq % nkv != 0 || d <= 0 || d > 256) return 0;
+    if (batch < 0 || q_len < 0 || nq <= 0 || nkv <= 0 || nq % nkv != 0 || d <= 0 || d > 256 ||
+        !countable(batch, q_len, nq))
+        return 0;
     return attn_workspace_bytes((int64_t)q_len * (nq / nkv), d);
 }
 
@@ -266,8 +274,7 @@ GDN_API int gdna_attn_decode(const void *q, gdna_dtype dtype, const void *gate,
     const float scale2 = (float)((double)scale * k_scale * 1.4426950408889634);
     if (!sound_scale(scale2)) return GDN_ERR_ARG;
     const int64_t rows = (int64_t)batch * q_len, hq = (int64_t)nq * d;
-    // an item is (key head, tile of 8 query rows or more); rows of a sequence and all items are int32
-    if ((int64_t)q_len * nq > (1 << 24) || batch > (1 << 20) || rows > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (!countable(batch, q_len, nq)) return GDN_ERR_UNSUPPORTED;
     if (gate != nullptr && gate_head_stride < d) return GDN_ERR_ARG;
     if (rows == 0) return GDN_OK;
     // the row of all units of work (16 keys at least each, and what an item costs beside them) is counted in 64 bits

@@ -327,3 +327,12 @@ def test_given_types_and_raw_addresses_are_taken_at_their_word(lib):
         gdn.gdna_qk_norm_rope(at(0), at(1), at(2), None, None, None, None, at(3).view(I64), at(4), at(5), at(6), rows=1, nq=2, nkv=1,
                               d=8, rot=0, n_pos=0, pages=2, page_size=4, stream=0, dtype=1, cache_dtype=3)
     assert e.value.status == 5
+
+
+@pytest.mark.parametrize("kw", [dict(batch=(1 << 20) + 1), dict(q_len=1 << 22), dict(nq=1 << 25), dict(batch=1 << 20, q_len=1 << 12)])
+def test_the_workspace_of_a_shape_that_is_refused_is_zero(lib, kw):
+    """gdna_attn_workspace says 0 for what gdna_attn_decode refuses."""
+    shape = {**dict(batch=3, q_len=2, nq=8, nkv=2, d=128), **kw}
+    rows = shape["nq"] * 128
+    assert attn(lib, **shape, qs=rows, gs=rows, os=rows) == UNSUP
+    assert gdn.gdna_attn_workspace(**shape) == 0
