@@ -207,7 +207,7 @@ GDN_API int64_t gdna_attn_workspace(int batch, int q_len, int nq, int nkv, int d
  *                can overlap on the GPU need separate ones.
  *   NQ must be a multiple of NKV (GDN_ERR_UNSUPPORTED).  1 <= D <= 256.  Heads of
  *   a multiple of 16 bytes on 16-byte aligned caches (bases and strides) run on
- *   the tensor cores; any other call runs a general kernel, some ten times
+ *   the tensor cores; any other call runs a general kernel, six to fifty times
  *   slower, with the same results up to rounding.  Page sizes that 16 divides are
  *   the fastest, multiples of 8 and of 4 nearly so.
  *   Scores, softmax sums and outputs are held in fp32; queries and weights enter
