@@ -31,6 +31,7 @@ __all__ = [
     "GDNA_F32", "GDNA_F16", "GDNA_BF16", "GDNA_E4M3",
     "GDNA_ROPE_PLAIN", "GDNA_ROPE_LINEAR", "GDNA_ROPE_NTK", "GDNA_ROPE_YARN",
     "gdna_rope_table", "gdna_page_assign", "gdna_qk_norm_rope", "gdna_attn_workspace", "gdna_attn_decode",
+    "gdnb_residual_norm", "gdnb_attn_prompt_workspace", "gdnb_attn_prompt", "gdnb_attn_shared_workspace", "gdnb_attn_shared",
 ]
 
 GDN_STATE_F32 = 0
@@ -105,6 +106,17 @@ def _declare(lib):
                                      i32, i32, i32, i32, i32, i64, i32, i32, i64, i64, i64, i64, i64, i64, i64, P]
     lib.gdna_attn_workspace.restype = i64
     for fn in ("gdna_rope_table", "gdna_page_assign", "gdna_qk_norm_rope", "gdna_attn_decode"):
+        getattr(lib, fn).restype = i32
+    lib.gdnb_residual_norm.argtypes = [P, i32, P, i32, P, P, P, f32, f32, P, P, i32, i64, i32, i64, i64, i64, i64, i64, P]
+    lib.gdnb_attn_prompt_workspace.argtypes = [i64, i32, i32, i32, i32]
+    lib.gdnb_attn_shared_workspace.argtypes = [i32, i32, i32, i32, i32, i32]
+    lib.gdnb_attn_prompt.argtypes = [P, i32, P, P, P, i32, f32, f32, P, i64, P, P, f32, P, i32, P, i64,
+                                     i64, i32, i32, i32, i32, i64, i32, i32, i64, i64, i64, i64, i64, i64, i64, P]
+    lib.gdnb_attn_shared.argtypes = [P, i32, P, P, P, i32, f32, f32, P, i32, P, i64, P, P, i64, P, f32, P, i32, P, i64,
+                                     i32, i32, i32, i32, i32, i64, i32, i32, i32, i64, i64, i64, i64, i64, i64, i64, P]
+    for fn in ("gdnb_attn_prompt_workspace", "gdnb_attn_shared_workspace"):
+        getattr(lib, fn).restype = i64
+    for fn in ("gdnb_residual_norm", "gdnb_attn_prompt", "gdnb_attn_shared"):
         getattr(lib, fn).restype = i32
     lib.gdn_status_str.argtypes = [i32]
     lib.gdn_status_str.restype = ctypes.c_char_p
@@ -527,3 +539,88 @@ def gdna_attn_decode(q, k_cache, v_cache, table, kv_len, out, workspace, *, batc
         hk if token_stride is None else token_stride, d if head_stride is None else head_stride, _stream(stream))
     if st:
         _check("gdna_attn_decode", st)
+
+
+# ------------------------------------------------------------------ decoder blocks (include/gdnb.h)
+
+def gdnb_residual_norm(x, y, x_out, h, *, rows, c, gate=None, post=None, pre=None, scale=1.0, eps=1e-6, x_dtype=None,
+                       y_dtype=None, h_dtype=None, x_stride=None, y_stride=None, gate_stride=0, x_out_stride=None,
+                       h_stride=None, stream=None):
+    """The norm after a block, its gate and residual scale, and the norm before the next: x_out = x + scale * gate * (post *
+    y / rms(y)), h = pre * x_out / rms(x_out).  y None: h of x alone; x_out or h None: not written.  gate (y's type) has one
+    row for all (gate_stride 0) or `rows`; weights are fp32.  See include/gdnb.h."""
+    _GDNA_TYPES or _gdna_types()
+    xd = _gdna_dtype(x, x_dtype)
+    yd = xd if y is None else _gdna_dtype(y, y_dtype)
+    hd = xd if h is None else _gdna_dtype(h, h_dtype)
+    st = (_lib or load()).gdnb_residual_norm(
+        _ptr(x), xd, _ptr(y), yd, _at(gate, y.dtype if y is not None and y_dtype is None else None, "gate"),
+        _at(post, _F32, "post"), _at(pre, _F32, "pre"), scale, eps,
+        _at(x_out, x.dtype if x_dtype is None else None, "x_out"), _ptr(h), hd, rows, c,
+        c if x_stride is None else x_stride, c if y_stride is None else y_stride, gate_stride,
+        c if x_out_stride is None else x_out_stride, c if h_stride is None else h_stride, _stream(stream))
+    if st:
+        _check("gdnb_residual_norm", st)
+
+
+def gdnb_attn_prompt_workspace(*, rows, batch, nq, nkv, d) -> int:
+    """Bytes of device scratch that gdnb_attn_prompt needs for a shape (0: not supported)."""
+    return (_lib or load()).gdnb_attn_prompt_workspace(rows, batch, nq, nkv, d)
+
+
+def gdnb_attn_prompt(q, k_cache, v_cache, row_start, kv_len, out, workspace, *, rows, batch, nq, nkv, d, table=None, pages=1,
+                     page_size=1, max_pages=1, gate=None, scale=None, k_scale=1.0, v_scale=1.0, dtype=None, cache_dtype=None,
+                     out_dtype=None, workspace_bytes=None, table_stride=None, q_stride=None, gate_stride=None,
+                     gate_head_stride=None, out_stride=None, page_stride=None, token_stride=None, head_stride=None,
+                     stream=None):
+    """Causal attention of packed sequences, rows row_start[b] .. row_start[b + 1] - 1 each, over the paged cache, or
+    (table None) over keys in rows like the queries'.  scale defaults to 1/sqrt(d), strides to contiguous rows and a cache
+    [pages, page_size, nkv, d].  gate has q's type and v_cache k_cache's (unless `dtype`, `cache_dtype` say which),
+    row_start, kv_len and table are int32.  See include/gdnb.h."""
+    _GDNA_TYPES or _gdna_types()
+    hq, hk = nq * d, nkv * d
+    code, cache_code = _gdna_dtype(q, dtype), _gdna_dtype(k_cache, cache_dtype)
+    st = (_lib or load()).gdnb_attn_prompt(
+        _ptr(q), code, _at(gate, q.dtype if dtype is None else None, "gate"), _ptr(k_cache),
+        _at(v_cache, k_cache.dtype if cache_dtype is None else None, "v_cache"), cache_code, k_scale, v_scale,
+        _at(table, _I32, "table"), max_pages if table_stride is None else table_stride, _at(row_start, _I32, "row_start"),
+        _at(kv_len, _I32, "kv_len"), d ** -0.5 if scale is None else scale, _ptr(out), _gdna_dtype(out, out_dtype),
+        _ptr(workspace), workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes,
+        rows, batch, nq, nkv, d, pages, page_size, max_pages, hq if q_stride is None else q_stride,
+        hq if gate_stride is None else gate_stride, d if gate_head_stride is None else gate_head_stride,
+        hq if out_stride is None else out_stride, page_size * hk if page_stride is None else page_stride,
+        hk if token_stride is None else token_stride, d if head_stride is None else head_stride, _stream(stream))
+    if st:
+        _check("gdnb_attn_prompt", st)
+
+
+def gdnb_attn_shared_workspace(*, batch, q_len, nq, nkv, d, groups=1) -> int:
+    """Bytes of device scratch that gdnb_attn_shared needs for a shape (0: not supported)."""
+    return (_lib or load()).gdnb_attn_shared_workspace(batch, groups, q_len, nq, nkv, d)
+
+
+def gdnb_attn_shared(q, k_cache, v_cache, shared_table, shared_len, table, kv_len, out, workspace, *, batch, q_len=1, nq, nkv,
+                     d, pages, page_size, max_shared_pages, max_pages, group_start=None, groups=1, gate=None, scale=None,
+                     k_scale=1.0, v_scale=1.0, dtype=None, cache_dtype=None, out_dtype=None, workspace_bytes=None,
+                     shared_stride=None, table_stride=None, q_stride=None, gate_stride=None, gate_head_stride=None,
+                     out_stride=None, page_stride=None, token_stride=None, head_stride=None, stream=None):
+    """gdna_attn_decode for requests that begin alike: group g is requests group_start[g] .. group_start[g + 1] - 1 (None:
+    one group of all), whose tokens see shared_len[g] keys in the pages of shared_table's row g before their own.  All int32.
+    See include/gdnb.h."""
+    _GDNA_TYPES or _gdna_types()
+    hq, hk = nq * d, nkv * d
+    code, cache_code = _gdna_dtype(q, dtype), _gdna_dtype(k_cache, cache_dtype)
+    st = (_lib or load()).gdnb_attn_shared(
+        _ptr(q), code, _at(gate, q.dtype if dtype is None else None, "gate"), _ptr(k_cache),
+        _at(v_cache, k_cache.dtype if cache_dtype is None else None, "v_cache"), cache_code, k_scale, v_scale,
+        _at(group_start, _I32, "group_start"), groups, _at(shared_table, _I32, "shared_table"),
+        max_shared_pages if shared_stride is None else shared_stride, _at(shared_len, _I32, "shared_len"),
+        _at(table, _I32, "table"), max_pages if table_stride is None else table_stride, _at(kv_len, _I32, "kv_len"),
+        d ** -0.5 if scale is None else scale, _ptr(out), _gdna_dtype(out, out_dtype), _ptr(workspace),
+        workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes, batch, q_len, nq, nkv, d,
+        pages, page_size, max_shared_pages, max_pages, hq if q_stride is None else q_stride,
+        hq if gate_stride is None else gate_stride, d if gate_head_stride is None else gate_head_stride,
+        hq if out_stride is None else out_stride, page_size * hk if page_stride is None else page_stride,
+        hk if token_stride is None else token_stride, d if head_stride is None else head_stride, _stream(stream))
+    if st:
+        _check("gdnb_attn_shared", st)

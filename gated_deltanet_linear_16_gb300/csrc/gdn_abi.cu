@@ -9,7 +9,7 @@
 #include "gdn.h"
 #include "gdn_internal.cuh"
 #include "gdn_tc.cuh"
-#include "gdna_internal.cuh"
+#include "gdnb_internal.cuh"
 
 namespace gdn {
 
@@ -478,10 +478,11 @@ GDN_API int gdn_prefill_chunked(void *state, gdn_state_dtype state_dtype, int64_
 GDN_API int gdn_device_wait_timeouts(unsigned *count)
 {
     if (count == nullptr) return GDN_ERR_ARG;
-    unsigned attention = 0;
+    unsigned attention = 0, prompts = 0;
     cudaError_t e = tc_wait_timeouts(count);
     if (e == cudaSuccess) e = gdna::attn_wait_timeouts(&attention);
-    *count += attention;
+    if (e == cudaSuccess) e = gdnb::flash_wait_timeouts(&prompts);
+    *count += attention + prompts;
     return cuda_status(e);
 }
 

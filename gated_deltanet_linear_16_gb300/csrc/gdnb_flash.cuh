@@ -1,0 +1,1199 @@
+// gdnb_flash.cuh -- attention of many query rows over one list of keys each, on the
+// fifth-generation tensor cores: the kernel behind gdnb_attn_prompt (a segment is a
+// sequence, causal) and behind the prefix of gdnb_attn_shared (a segment is a group
+// of requests, every row sees every key).
+//
+// Mathematics.  A tile is 128 or 256 rows (token, head of the group) of a segment that read
+// the same key head.  One pass over its keys, 128 at a time:
+//     S = Q K^T,  m' = max(m, rowmax S),  P = exp2(scale2 S - scale2 m'),  l += rowsum P,  O += P V
+// with O rescaled by exp2(scale2 (m - m')) only where a row's maximum has grown by more than
+// kSlack (in log2): until then P may exceed 1, which costs nothing while it fits its type.  A row of S is one
+// thread's (tensor memory gives a thread its lane), so maximum and sum need no shuffles.
+//
+// Where things are.  S of a block is 128 columns of tensor memory, and P takes the first 64 of
+// them as the A operand of the second product; O stays in tensor memory for the whole tile.  D <= 128:
+// two row tiles of 128 with an S each: one tile's softmax runs under the other's products.
+// D = 256: O takes half of tensor memory, so one row tile, and two S that alternate: S of the next
+// block is computed before P V of this one.  Q stays in shared memory; K and V come through one ring
+// of stages of 128 keys x 128 columns (32 KB; 64 columns for D = 64), rows in panels of 128
+// bytes with the 128-byte swizzle: K-major for the first product, and read along the other
+// direction (N-major) for the second.
+//
+// Who does what (512 threads, one block an SM, persistent).  Warps 0-7: softmax, rescale, output, and the
+// queries' way into shared memory.  Warp 8 issues products, warp 10 deals out work, warps 12-15 fill
+// the ring, a stage each in turn, by tensor copies or by loads (E4M3, odd pages and layouts).
+//
+// Work.  With many tiles a block takes every grid-th one, longest first within a sequence and in alternating
+// direction, so that neighbours read the same keys at the same time and loads even out.  With
+// fewer than two tiles a block, the tiles' costs (keys, and a lead for what a tile costs beside them) stand in one row
+// and every block takes an equal run of it: a tile that lies in several blocks leaves partial
+// results that join_parts adds up.  No host knowledge of lengths is needed for either.
+//
+// Rounding.  Products are of 16-bit operands with fp32 sums: keys and values exactly (E4M3 widens to fp16), queries in
+// `PARTS` parts (x = hi + lo), for fp16 products scaled by a power of two a row where their type has a
+// wider range.  A weight enters in one part: 2^-8 (2^-11 in fp16) of itself, of the order of
+// the 16-bit output's own rounding.  For fp16 products weights are lifted by 2^kLift, so that one far below
+// its row's largest keeps its bits (fp16's steps end at 2^-24).  m, l, S and O are fp32.
+//
+// What a row does not see.  Masked scores are replaced.  In blocks where some row does not see all
+// keys, values that are not finite are taken out of V (0 x NaN) and the first such key of each column is noted: the rows
+// that see it come out NaN in that column, the others clean.  Keys past the end count as zeros.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "gdn_tc.cuh"
+#include "gdnb_internal.cuh"
+
+namespace gdnb {
+namespace flash {
+
+using gdn::kFull;
+namespace tc = gdn::tc;
+
+constexpr int kKeys = 128;                 // keys of a block
+constexpr int kThreads = 512;
+constexpr int kMaxGrid = 160;              // blocks that share the work, at most
+constexpr int kItems = 4;                  // slots of the work queue
+constexpr int kCopyWarps = 4;
+constexpr int kLead = 256;                 // what a tile costs beside its keys, in keys: queries, first products, output
+constexpr int kLeastChunk = 768;           // a block's run of the row of costs, at least
+constexpr int kMostKeys = INT32_MAX - 4095;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// ------------------------------------------------------------------ work
+
+struct Segment {
+    int64_t row0;
+    int n, kv;                             // tokens, keys
+};
+
+__device__ __forceinline__ Segment segment(const FlashParams &p, int b)
+{
+    Segment s;
+    int64_t r0 = 0, r1 = p.rows;
+    if (p.row_start != nullptr) {
+        r0 = min(max((int64_t)p.row_start[b] * p.row_mult, (int64_t)0), p.rows);
+        r1 = min(max((int64_t)p.row_start[b + 1] * p.row_mult, r0), p.rows);
+    }
+    s.row0 = r0;
+    s.n = (int)(r1 - r0);
+    int64_t most = p.table == nullptr ? (int64_t)s.n : (int64_t)p.max_pages * p.cache.page_size;
+    if (most > kMostKeys) most = kMostKeys;
+    s.kv = p.kv_len == nullptr ? (int)most : (int)min((int64_t)max(p.kv_len[b], 0), most);
+    return s;
+}
+
+// Tiles of a segment for one head, and where their costs begin.
+struct Tiles {
+    int64_t count;                         // tiles
+    int64_t base;                          // cost of a tile beside its own tokens
+    int64_t cost;                          // of all
+    int step;                              // tokens a tile adds (0: every tile sees all keys)
+    int n, kv;
+};
+__device__ __forceinline__ Tiles tiles_of(const FlashParams &p, const Segment &s)
+{
+    Tiles t;
+    t.n = s.n;
+    t.kv = s.kv;
+    t.count = ((int64_t)s.n + p.tile_tokens - 1) / p.tile_tokens;
+    t.step = p.causal ? p.tile_tokens : 0;
+    t.base = kLead + (p.causal ? max(s.kv - s.n, 0) : s.kv);
+    t.cost = t.count * t.base;
+    if (p.causal && t.count > 0) t.cost += (int64_t)t.step * (t.count * (t.count - 1) / 2) + s.n;
+    return t;
+}
+__device__ __forceinline__ int64_t cost_before(const Tiles &t, int64_t tau)       // of tiles [0, tau), tau < count
+{
+    return tau * t.base + (int64_t)t.step * (tau * (tau + 1) / 2);
+}
+__device__ __forceinline__ int64_t cost_of(const FlashParams &p, const Tiles &t, int64_t tau)
+{
+    return t.base + (p.causal ? min((tau + 1) * t.step, (int64_t)t.n) : 0);
+}
+// Keys that tile tau's last token sees, and its blocks.
+__device__ __forceinline__ int keys_of(const FlashParams &p, const Tiles &t, int64_t tau)
+{
+    if (!p.causal) return t.kv;
+    const int64_t k = t.kv - (int64_t)t.n + min((tau + 1) * (int64_t)p.tile_tokens, (int64_t)t.n);
+    return k < 0 ? 0 : (int)k;
+}
+// Blocks of a tile that stand before place `x` of its cost.
+__device__ __forceinline__ int blocks_before(int64_t x, int blocks)
+{
+    if (x <= kLead) return 0;
+    const int64_t b = (x - kLead) / kKeys;
+    return b < blocks ? (int)b : blocks;
+}
+// The tile in which place `y` of a head's costs lies.
+__device__ __forceinline__ int64_t tile_at(const Tiles &t, int64_t y)
+{
+    int64_t tau;
+    if (t.step == 0) {
+        tau = y / t.base;
+    } else {                               // tau (base + step/2) + step/2 tau^2 <= y
+        const double h = 0.5 * t.step, b = (double)t.base + h;
+        tau = (int64_t)((sqrt(b * b + 4.0 * h * (double)y) - b) / (2.0 * h));
+    }
+    if (tau < 0) tau = 0;
+    if (tau > t.count - 1) tau = t.count - 1;
+    while (tau > 0 && cost_before(t, tau) > y) --tau;
+    while (tau + 1 < t.count && cost_before(t, tau + 1) <= y) ++tau;
+    return tau;
+}
+
+// Sums over all segments, by all threads of the block.
+struct Totals {
+    int64_t cost, tiles;
+};
+__device__ __forceinline__ Totals totals(const FlashParams &p, int64_t (*red)[2])
+{
+    int64_t cost = 0, tiles = 0;
+    for (int b = threadIdx.x; b < p.segs; b += blockDim.x) {
+        const Tiles t = tiles_of(p, segment(p, b));
+        cost += t.cost;
+        tiles += t.count;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        cost += __shfl_xor_sync(kFull, cost, off);
+        tiles += __shfl_xor_sync(kFull, tiles, off);
+    }
+    if ((threadIdx.x & 31) == 0) { red[threadIdx.x >> 5][0] = cost; red[threadIdx.x >> 5][1] = tiles; }
+    __syncthreads();
+    Totals all{0, 0};
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) { all.cost += red[w][0]; all.tiles += red[w][1]; }
+    all.cost *= p.nkv;
+    all.tiles *= p.nkv;
+    // starts that go back, so that segments overlap: there may be more tiles than partial results have room
+    if (p.all_parts && all.tiles > p.most_tiles) all = Totals{0, 0};
+    return all;
+}
+__device__ __forceinline__ bool whole_tiles(const FlashParams &p, const Totals &all)
+{
+    return !p.all_parts && (all.tiles >= 2 * (int64_t)p.grid || all.tiles > p.most_tiles);
+}
+// Cost of a block's run.
+__device__ __forceinline__ int64_t run_of(const FlashParams &p, const Totals &all)
+{
+    const int64_t even = (all.cost + p.grid - 1) / p.grid;
+    return even < kLeastChunk ? kLeastChunk : even;
+}
+
+// A segment's place in the row of all (costs and tiles before it), found 32 at a time by one warp.
+struct Place {
+    int seg;                               // p.segs: none
+    int64_t cost, tiles;                   // before the segment, over all heads
+    Tiles t;
+};
+// The segment in which place x of the costs (BY_COST; else tile x) lies, from segment `seg` on, before which `cost`
+// and `tiles` stand.
+template <bool BY_COST>
+__device__ __forceinline__ Place find(const FlashParams &p, int seg, int64_t cost, int64_t tiles, int64_t x)
+{
+    const int lane = threadIdx.x & 31;
+    for (; seg < p.segs; seg += 32) {
+        Tiles t{};
+        if (seg + lane < p.segs) t = tiles_of(p, segment(p, seg + lane));
+        int64_t c = t.cost * p.nkv, n = t.count * p.nkv;
+        const int64_t c0 = c, n0 = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t u = __shfl_up_sync(kFull, c, off), v = __shfl_up_sync(kFull, n, off);
+            if (lane >= off) { c += u; n += v; }
+        }
+        const bool past = BY_COST ? cost + c > x : tiles + n > x;
+        const unsigned hit = __ballot_sync(kFull, past);
+        const int at = hit ? __ffs(hit) - 1 : 31;
+        if (hit) {
+            Place r;
+            r.seg = seg + at;
+            r.cost = cost + __shfl_sync(kFull, c - c0, at);
+            r.tiles = tiles + __shfl_sync(kFull, n - n0, at);
+            r.t.count = __shfl_sync(kFull, t.count, at);
+            r.t.base = __shfl_sync(kFull, t.base, at);
+            r.t.cost = __shfl_sync(kFull, t.cost, at);
+            r.t.step = __shfl_sync(kFull, t.step, at);
+            r.t.n = __shfl_sync(kFull, t.n, at);
+            r.t.kv = __shfl_sync(kFull, t.kv, at);
+            return r;
+        }
+        cost += __shfl_sync(kFull, c, 31);
+        tiles += __shfl_sync(kFull, n, 31);
+    }
+    Place none{};
+    none.seg = p.segs;
+    return none;
+}
+
+// A block's piece of work: some key blocks of a tile.
+struct Item {
+    int64_t row0;                          // first row of the segment
+    int n, kv, seg, head, token0;          // token0: first token of the tile
+    int first, last;                       // key blocks [first, last)
+    int whole;                             // all of the tile's: the result is final
+    int64_t slot;                          // of the partial result
+    int valid;
+};
+
+// ------------------------------------------------------------------ tensor core pieces (16-bit operands)
+
+template <bool BF16> __host__ __device__ constexpr uint32_t idesc16(int m, int n, bool b_n_major)
+{
+    return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((b_n_major ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// B read along its rows (N-major): panels of 64 columns `panel` bytes apart, eight keys (one swizzle atom) 1024.
+__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr, uint32_t panel)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void arrive_expect(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int token, int head, int page, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(token), "r"(head), "r"(page), "r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void lds16(uint32_t (&r)[4], uint32_t at)
+{
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Place of 16-byte piece c of row r in panels of 128 rows x 128 bytes.
+__device__ __forceinline__ uint32_t piece_at(int r, int c)
+{
+    return (uint32_t)((c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+template <bool BF16> __device__ __forceinline__ uint32_t pack16(float a, float b)
+{
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+template <bool BF16> __device__ __forceinline__ float2 unpack16(uint32_t u)
+{
+    if constexpr (BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+// Whether either half of a word of two 16-bit values is not finite.
+template <bool BF16> __device__ __forceinline__ bool odd2(uint32_t u)
+{
+    constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
+    return (u & e) == e || (u & (e << 16)) == (e << 16);
+}
+
+// Waits on the kernel's barriers that ran out on this device (each instance's unit has its own).
+static __device__ unsigned g_wait_timeouts;
+
+// ------------------------------------------------------------------ shapes
+
+template <int D> struct Shared {                               // beside queries and ring
+    uint64_t full[8], empty[8], landed[kCopyWarps];
+    uint64_t q_full[2], q_free[2], s_full[2][2], p_full[2], o_full[2], o_free, drain;
+    uint64_t item_full[kItems], item_empty[kItems];
+    Item item[kItems];
+    int64_t red[kThreads / 32][2];
+    uint32_t tmem;
+    int dead;
+    int poisoned[kItems];
+    uint32_t poison[kItems][D / 2];                            // 16 bits a column: which rows see a value that is not finite
+};
+
+template <int D, int PARTS> struct Shape {
+    static constexpr int kTiles = D <= 128 ? 2 : 1;            // row tiles of 128
+    static constexpr int kRows = 128 * kTiles;
+    static constexpr int kCols = D < 128 ? D : 128;            // columns of a stage
+    static constexpr int kHalves = D / kCols;                  // stages of a block of K, or V
+    static constexpr int kPanelBytes = kKeys * 128;
+    static constexpr int kStage = kKeys * kCols * 2;
+    static constexpr int kQTile = 128 * D * 2;                 // a row tile's queries, a part
+    static constexpr int kQBytes = kTiles * PARTS * kQTile;
+    static constexpr int kRoom = 224 * 1024 - kQBytes;
+    static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
+    static_assert(kStages >= 3, "K of a block and V of the one before, in part");
+    // Warps that fill the ring, in turn.  A warp that passes on from fill f knows that f - kStages is released; its next fill
+    // waits for f + kFillers - kStages, whose barrier tells that phase from the one before it only if f + kFillers - 2 kStages is.
+    static constexpr int kFillers = kStages < kCopyWarps ? kStages : kCopyWarps;
+    static_assert(kFillers <= kStages, "phases of a stage's barrier");
+    static constexpr int kSmem = kQBytes + kStages * kStage + (int)sizeof(Shared<D>);
+    static_assert(kSmem <= 227 * 1024, "a block's shared memory");
+    static constexpr int64_t kPart = (int64_t)kRows * (D + 2); // floats of a partial result: rows of O, then m and l of each
+};
+
+// A bounded wait; false (and from then on everywhere in the block) where the bound runs out.
+struct Wait {
+    volatile int *dead;
+    uint32_t limit;
+    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const
+    {
+        const uint32_t s = smem_addr(bar);
+        for (uint32_t i = 0; i < limit; ++i) {
+            uint32_t done;
+            asm volatile("{\n\t.reg .pred p;\n\t"
+                         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(done) : "r"(s), "r"(parity) : "memory");
+            if (done) return true;
+            if (*dead) return false;
+        }
+        if (atomicExch(const_cast<int *>(dead), 1) == 0) atomicAdd(&g_wait_timeouts, 1u);
+        return false;
+    }
+};
+// The same on the way out, whatever the others found: copies and products in flight end by themselves.
+__device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity)
+{
+    const uint32_t s = smem_addr(bar);
+    for (uint32_t i = 0; i < (1u << 22); ++i) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(s), "r"(parity) : "memory");
+        if (done) return;
+    }
+}
+
+// ------------------------------------------------------------------ softmax warps
+
+// Queries of a warp's 32 rows into shared memory, eight elements a lane, in PARTS 16-bit parts; returns what
+// the scores of this lane's row are to be multiplied by (fp16 products of a type with a wider range: the row's largest
+// element is brought to 2^14 .. 2^15).
+template <int D, bool BF16, int PARTS>
+__device__ __forceinline__ float load_queries(const FlashParams &p, const Item &it, int rows, int row0, uint32_t q_smem, int lane)
+{
+    using S = Shape<D, PARTS>;
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPasses = 32 / kPer;     // lanes of a row, rows of a pass
+    constexpr int kGo = 4;
+    const int col = (lane % kLanes) * 8;
+    const bool scaled = !BF16 && p.dtype != GDNA_F16;
+    float mine = 1.f;
+#pragma unroll 1
+    for (int pass = 0; pass < kPasses; pass += kGo) {
+        uint4 raw[kGo][2];
+#pragma unroll
+        for (int k = 0; k < kGo; ++k) {
+            const int r = row0 + (pass + k) * kPer + lane / kLanes;
+            raw[k][0] = raw[k][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (r >= rows || col >= p.d) continue;
+            const int t = (int)p.group_div.quotient((unsigned)r);
+            const int64_t from = (it.row0 + it.token0 + t) * p.q_stride + ((int64_t)it.head * p.group + (r - t * p.group)) * p.d + col;
+            if (p.q_vec) {
+                if (p.dtype == GDNA_F32) {
+                    const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const float *>(p.q) + from);
+                    raw[k][0] = at[0];
+                    raw[k][1] = at[1];
+                } else {
+                    raw[k][0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + from);
+                }
+            } else {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = col + j < p.d ? gdna::load_elem(p.q, from + j, p.dtype) : 0.f;
+                raw[k][0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+                raw[k][1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kGo; ++k) {
+            const int in_warp = (pass + k) * kPer + lane / kLanes;
+            float x[8];
+            if (!p.q_vec || p.dtype == GDNA_F32) {
+                x[0] = __uint_as_float(raw[k][0].x); x[1] = __uint_as_float(raw[k][0].y);
+                x[2] = __uint_as_float(raw[k][0].z); x[3] = __uint_as_float(raw[k][0].w);
+                x[4] = __uint_as_float(raw[k][1].x); x[5] = __uint_as_float(raw[k][1].y);
+                x[6] = __uint_as_float(raw[k][1].z); x[7] = __uint_as_float(raw[k][1].w);
+            } else {
+                const uint32_t u[4] = {raw[k][0].x, raw[k][0].y, raw[k][0].z, raw[k][0].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = p.dtype == GDNA_BF16 ? unpack16<true>(u[j]) : unpack16<false>(u[j]);
+                    x[2 * j] = f.x;
+                    x[2 * j + 1] = f.y;
+                }
+            }
+            if (scaled) {                              // (for the whole warp)
+                float top = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+#pragma unroll
+                for (int off = kLanes / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+                int e = (int)(__float_as_uint(top) >> 23) - 127;
+                e = top > 0.f && e < 128 ? max(e, -100) : 14;
+                const float up = __uint_as_float((unsigned)(127 + 14 - e) << 23);
+                const float back = __uint_as_float((unsigned)(127 - 14 + e) << 23);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] *= up;
+                const int which = lane - (pass + k) * kPer;            // this lane's row among the pass's
+                const float got = __shfl_sync(kFull, back, (which & (kPer - 1)) * kLanes);
+                if (which >= 0 && which < kPer) mine = got;
+            }
+            const uint32_t at = q_smem + piece_at((row0 & 127) + in_warp, lane % kLanes);
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+                uint32_t u[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    u[j] = pack16<BF16>(x[2 * j], x[2 * j + 1]);
+                    const float2 f = unpack16<BF16>(u[j]);
+                    x[2 * j] -= f.x;
+                    x[2 * j + 1] -= f.y;
+                }
+                sts16(at + part * S::kQTile, u[0], u[1], u[2], u[3]);
+            }
+        }
+    }
+    return mine;
+}
+
+__device__ __forceinline__ void fma2(float &a, float &b, float s, float c)        // a = a s + c, b = b s + c
+{
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(a), "+f"(b) : "f"(s), "f"(c));
+}
+__device__ __forceinline__ void add2(float &a, float &b, float c, float d)        // a += c, b += d
+{
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(a), "+f"(b) : "f"(c), "f"(d));
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D, bool BF16, int PARTS>
+__global__ void __launch_bounds__(kThreads, 1)
+flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+           const uint32_t polls)
+{
+    using S = Shape<D, PARTS>;
+    constexpr int TILES = S::kTiles;
+    // how far P may exceed 1 before O is rescaled (log2), and what fp16 weights are lifted by (log2): 2^(11 + 4) fits fp16
+    constexpr float kSlack = BF16 ? 8.f : 4.f, kLift = BF16 ? 0.f : 11.f;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    const uint32_t base = smem_addr(raw);
+    const uint32_t q_smem = base, ring = base + S::kQBytes;
+    Shared<D> &sh = *reinterpret_cast<Shared<D> *>(raw + S::kQBytes + S::kStages * S::kStage);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            tc::mbar_init(&sh.full[i], 1);
+            tc::mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < kCopyWarps; ++i) tc::mbar_init(&sh.landed[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sh.q_full[i], 4);
+            tc::mbar_init(&sh.q_free[i], 1);
+            tc::mbar_init(&sh.s_full[i][0], 1);
+            tc::mbar_init(&sh.s_full[i][1], 1);
+            tc::mbar_init(&sh.p_full[i], 4);
+            tc::mbar_init(&sh.o_full[i], 1);
+        }
+        tc::mbar_init(&sh.o_free, 4);
+        tc::mbar_init(&sh.drain, 1);
+        for (int i = 0; i < kItems; ++i) {
+            tc::mbar_init(&sh.item_full[i], 1);
+            tc::mbar_init(&sh.item_empty[i], 1 + kCopyWarps + 8);
+        }
+        sh.dead = (base & 1023u) != 0;                 // (dynamic shared memory starts where the swizzle can)
+        if (sh.dead) atomicAdd(&g_wait_timeouts, 1u);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) tc::tmem_alloc(&sh.tmem, 512);
+    const Totals all = totals(p, sh.red);              // (a barrier)
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const Wait wait{&sh.dead, sh.dead ? 0u : polls};
+    auto wait_warp = [&](uint64_t *bar, uint32_t parity) { return (bool)__all_sync(kFull, wait(bar, parity)); };
+    auto s_col = [&](int i) { return tmem + 128 * i; };                            // of S, and P
+    auto o_col = [&](int t) { return tmem + 256 + (TILES == 2 ? t * D : 0); };
+    auto rows_in = [&](const Item &it) {               // rows of a tile that are real
+        return min(p.tile_tokens, it.n - it.token0) * p.group;
+    };
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ---------------------------------------------------------------- softmax and output: a thread a row
+        const int wg = warp >> 2, quarter = warp & 3;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        uint32_t items = 0, blocks_all = 0, s_count[2] = {0, 0}, o_count = 0;
+        for (;; ++items) {
+            const int slot = items % kItems;
+            if (!wait_warp(&sh.item_full[slot], (items / kItems) & 1)) break;
+            const Item it = sh.item[slot];
+            if (!it.valid) break;
+            const int blocks = it.last - it.first, rows = rows_in(it);
+            const int row0 = (TILES == 2 ? wg * 128 : 0) + quarter * 32, r = row0 + lane;
+            const bool mine = TILES == 2 ? rows > wg * 128 : (items & 1) == (uint32_t)wg;
+            if (!mine) {
+                __syncwarp();
+                if (lane == 0) arrive(&sh.item_empty[slot]);
+                blocks_all += blocks;
+                continue;
+            }
+            const int t = (int)p.group_div.quotient((unsigned)r);
+            const bool real = r < rows;
+            int limit = p.causal ? it.kv - it.n + it.token0 + t + 1 : it.kv;       // keys that the row sees
+            if (!real || limit < 0) limit = 0;
+            float m = kNegInf, l0 = 0.f, l1 = 0.f, scale = p.scale2;
+            // (every phase of a barrier is waited for, in order: one that was skipped would be taken for the one after it)
+            if (TILES == 1 && items > 0 && !wait_warp(&sh.q_free[(items - 1) & 1], ((items - 1) >> 1) & 1)) break;
+            if (blocks > 0) {
+                scale *= load_queries<D, BF16, PARTS>(p, it, rows, row0, q_smem + (TILES == 2 ? wg * PARTS * S::kQTile : 0), lane);
+                tc::fence_smem_async();
+                __syncwarp();
+                if (lane == 0) arrive(&sh.q_full[wg]);
+            }
+            bool ok = true;
+            for (int j = 0; j < blocks; ++j) {
+                const int b = TILES == 2 ? 0 : (int)((blocks_all + j) & 1);
+                const int col = TILES == 2 ? wg : b;   // which S
+                ok = wait_warp(&sh.s_full[wg][b], s_count[b]++ & 1);
+                if (!ok) break;
+                tc::fence_after_sync();
+                float s[4][32];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) tc::tmem_ld32(s_col(col) + lanes + 32 * x, s[x]);
+                tc::ld_wait();
+                const int seen = limit - (it.first + j) * kKeys;
+                if (__any_sync(kFull, seen < kKeys)) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * x + i >= seen) s[x][i] = kNegInf;
+                }
+                float top[4] = {m, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) top[x] = fmaxf(top[x], fmaxf(s[x][i], s[x][i + 1]));
+                const float m_new = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                bool behind = TILES == 1 && j > 0;     // the last block's products are still to be waited for
+                if (__any_sync(kFull, (m_new - m) * scale > kSlack)) {
+                    const float f = m_new == m ? 1.f : ex2((m - m_new) * scale);
+                    if (j > 0) {
+                        // (two row tiles: the scores were asked for after the last block's products, so those are done)
+                        if (TILES == 1) {
+                            ok = wait_warp(&sh.o_full[wg], (o_count + j - 1) & 1);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            behind = false;
+                        }
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 32) {
+                            float o[32];
+                            tc::tmem_ld32(o_col(TILES == 2 ? wg : 0) + lanes + x, o);
+                            tc::ld_wait();
+                            uint32_t u[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
+                            tc::tmem_st32(o_col(TILES == 2 ? wg : 0) + lanes + x, u);
+                        }
+                    }
+                    l0 *= f;
+                    l1 *= f;
+                    m = m_new;
+                }
+                const float from = m == kNegInf ? 0.f : kLift - m * scale;
+#pragma unroll
+                for (int x = 0; x < 4; x += 2) {
+                    uint32_t u[32];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            float a = s[x + y][i], c = s[x + y][i + 1];
+                            fma2(a, c, scale, from);
+                            a = ex2(a);
+                            c = ex2(c);
+                            add2(l0, l1, a, c);
+                            u[16 * y + i / 2] = pack16<BF16>(a, c);
+                        }
+                    tc::tmem_st32(s_col(col) + lanes + 16 * x, u);
+                }
+                tc::st_wait();
+                if (behind) ok = wait_warp(&sh.o_full[wg], (o_count + j - 1) & 1);
+                if (!ok) break;
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) arrive(&sh.p_full[col]);
+            }
+            if (!ok) break;
+            // ---- the output
+            if (blocks > 0) {
+                const uint32_t last = TILES == 2 ? o_count++ : (o_count += blocks) - 1;
+                if (!wait_warp(&sh.o_full[wg], last & 1)) break;
+                tc::fence_after_sync();
+            }
+            const float l = l0 + l1;
+            const bool final_rows = it.whole && !p.all_parts;
+            const float norm = final_rows ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
+            const bool poisoned = blocks > 0 && *(volatile int *)&sh.poisoned[slot];
+            const int64_t row = it.row0 + it.token0 + t;
+            const int64_t head = (int64_t)it.head * p.group + (r - t * p.group);
+            float *part = p.parts + it.slot * S::kPart;
+            if (!final_rows && real)
+                *reinterpret_cast<float2 *>(part + S::kRows * D + 2 * r) = make_float2(m == kNegInf ? kNegInf : m * scale, l);
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+                float o[32];
+                if (blocks > 0) {
+                    tc::tmem_ld32(o_col(TILES == 2 ? wg : 0) + lanes + x, o);
+                    tc::ld_wait();
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                }
+                if (!real) continue;
+                if (poisoned) {
+                    const uint16_t *poison = reinterpret_cast<const uint16_t *>(sh.poison[slot]);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (limit > 0 && poison[x + i] <= (p.causal ? t : 0)) o[i] = __int_as_float(0x7fffffff);
+                }
+                if (!final_rows) {
+                    float4 *to = reinterpret_cast<float4 *>(part + (int64_t)r * D + x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    continue;
+                }
+                if (x >= p.d) continue;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= norm;
+                if (p.gate != nullptr) {
+                    const int64_t from = row * p.gate_stride + head * p.gate_head_stride + x;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        if (x + i >= p.d) break;
+                        float4 g;
+                        if (p.gate_vec) {
+                            g = gdna::got4(gdna::ask4(p.gate, from + i, p.dtype, true), p.dtype, true);
+                        } else {
+                            float e[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) e[k] = x + i + k < p.d ? gdna::load_elem(p.gate, from + i + k, p.dtype) : 0.f;
+                            g = make_float4(e[0], e[1], e[2], e[3]);
+                        }
+                        o[i] = __fdividef(o[i], 1.f + __expf(-g.x)); o[i + 1] = __fdividef(o[i + 1], 1.f + __expf(-g.y));
+                        o[i + 2] = __fdividef(o[i + 2], 1.f + __expf(-g.z)); o[i + 3] = __fdividef(o[i + 3], 1.f + __expf(-g.w));
+                    }
+                }
+                const int64_t to = row * p.out_stride + head * p.d + x;
+                if (p.out_vec) {
+                    uint4 *at = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + to);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (x + 8 * i >= p.d) break;
+                        uint32_t u[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float a = o[8 * i + 2 * k], b = o[8 * i + 2 * k + 1];
+                            u[k] = p.out_dtype == GDNA_BF16 ? pack16<true>(a, b) : pack16<false>(a, b);
+                        }
+                        at[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (x + i < p.d) gdna::store_elem(p.out, to + i, p.out_dtype, o[i]);
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (TILES == 1) arrive(&sh.o_free);
+                arrive(&sh.item_empty[slot]);
+            }
+            blocks_all += blocks;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 10) {
+            // ------------------------------------------------------------ work
+            uint32_t n = 0;
+            Item it{};
+            auto put = [&]() -> bool {
+                const int slot = n % kItems;
+                if (!wait_warp(&sh.item_empty[slot], ((n / kItems) & 1) ^ 1)) return false;
+                for (int i = lane; i < D / 2; i += 32) sh.poison[slot][i] = 0xffffffffu;
+                if (lane == 0) {
+                    sh.poisoned[slot] = 0;
+                    sh.item[slot] = it;
+                }
+                __syncwarp();
+                if (lane == 0) arrive(&sh.item_full[slot]);
+                ++n;
+                return true;
+            };
+            auto set = [&](const Place &at, int head, int64_t tau) {
+                const Segment s = segment(p, at.seg);
+                it.row0 = s.row0;
+                it.n = s.n;
+                it.kv = s.kv;
+                it.seg = at.seg;
+                it.head = head;
+                it.token0 = (int)(tau * p.tile_tokens);
+            };
+            const int g = p.grid, c = blockIdx.x;
+            bool ok = true;
+            it.valid = 1;
+            Place at{};
+            if (whole_tiles(p, all)) {
+                for (int64_t k = 0; ok; ++k) {
+                    const int64_t i = k * g + ((k & 1) ? g - 1 - c : c);
+                    if (i >= all.tiles) break;         // (and so is every later turn)
+                    at = find<false>(p, at.seg, at.cost, at.tiles, i);
+                    if (at.seg >= p.segs) break;
+                    const int64_t idx = i - at.tiles, tau = at.t.count - 1 - idx / p.nkv;
+                    set(at, (int)(idx % p.nkv), tau);
+                    it.first = 0;
+                    it.last = (int)(((int64_t)keys_of(p, at.t, tau) + kKeys - 1) / kKeys);
+                    it.whole = 1;
+                    ok = put();
+                }
+            } else {
+                const int64_t run = run_of(p, all), x0 = c * run;
+                const int64_t x1 = x0 + run < all.cost ? x0 + run : all.cost;
+                for (int64_t x = x0; ok && x < x1;) {
+                    at = find<true>(p, at.seg, at.cost, at.tiles, x);
+                    if (at.seg >= p.segs) break;
+                    const int head = (int)((x - at.cost) / at.t.cost);
+                    const int64_t y = x - at.cost - head * at.t.cost, tau = tile_at(at.t, y);
+                    const int64_t begin = x - y + cost_before(at.t, tau), end = begin + cost_of(p, at.t, tau);
+                    const int blocks = (int)(((int64_t)keys_of(p, at.t, tau) + kKeys - 1) / kKeys);
+                    it.first = x0 > begin ? blocks_before(x0 - begin, blocks) : 0;
+                    it.last = x1 < end ? blocks_before(x1 - begin, blocks) : blocks;
+                    // a tile without keys is the block's in which it begins
+                    if (it.first < it.last || (blocks == 0 && begin >= x0)) {
+                        set(at, head, tau);
+                        it.whole = it.first == 0 && it.last == blocks;
+                        it.slot = at.tiles + head * at.t.count + tau + c;
+                        ok = put();
+                    }
+                    x = end;
+                }
+            }
+            if (ok) {
+                it.valid = 0;
+                put();
+            }
+        } else if (warp == 8) {
+            // ------------------------------------------------------------ products, by one thread
+            if (lane == 0) {
+                constexpr uint32_t kQK = idesc16<BF16>(128, kKeys, false), kPV = idesc16<BF16>(128, S::kCols, true);
+                constexpr int kSteps = S::kCols / 16;  // of a stage's columns
+                uint32_t items = 0, fills = 0, blocks = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
+                bool ok = true;
+                auto stage_of = [&](uint32_t f) { return ring + (f % S::kStages) * S::kStage; };
+                auto wait_block = [&](uint32_t f) {    // the stages of a block of K, or V
+                    bool good = true;
+                    for (int h = 0; h < S::kHalves; ++h) good = good && wait(&sh.full[(f + h) % S::kStages], ((f + h) / S::kStages) & 1);
+                    return good;
+                };
+                auto release = [&](uint32_t f) {
+                    for (int h = 0; h < S::kHalves; ++h) tc::mma_commit(&sh.empty[(f + h) % S::kStages]);
+                };
+                auto qk = [&](int tile, int s, uint32_t f) {           // S s = Q of the tile . K^T, K in stages f ..
+#pragma unroll 1
+                    for (int i = 0; i < PARTS * S::kHalves; ++i) {
+                        const int part = i / S::kHalves, h = i % S::kHalves;
+                        const uint64_t a = tc::smem_desc_sw128(q_smem + (tile * PARTS + part) * S::kQTile + h * S::kStage);
+                        const uint64_t b = tc::smem_desc_sw128(stage_of(f + h));
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {             // (16 columns are 32 bytes of a panel: 2 in the descriptor)
+                            const uint64_t off = (k >> 2) * (S::kPanelBytes >> 4) + (k & 3) * 2;
+                            mma16_ss(s_col(s), a + off, b + off, kQK, i + k > 0);
+                        }
+                    }
+                };
+                auto pv = [&](int tile, int s, uint32_t f, bool acc) { // O of the tile += P . V
+#pragma unroll 1
+                    for (int h = 0; h < S::kHalves; ++h) {
+                        const uint64_t b = desc_n_major(stage_of(f + h), S::kPanelBytes);
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)           // (16 keys are 2048 bytes)
+                            mma16_ts(o_col(tile) + h * S::kCols, s_col(s) + 8 * k, b + k * (2048 >> 4), kPV, acc || k > 0);
+                    }
+                };
+                for (;; ++items) {
+                    const int slot = items % kItems;
+                    if (!wait(&sh.item_full[slot], (items / kItems) & 1)) break;
+                    const Item it = sh.item[slot];
+                    if (!it.valid) break;
+                    const int row_tiles = TILES == 2 && rows_in(it) > 128 ? 2 : 1;
+                    const uint32_t owner = items & 1;  // of a single row tile: the softmax warps take turns
+                    auto s_full = [&](int tile, uint32_t block) {
+                        return TILES == 2 ? &sh.s_full[tile][0] : &sh.s_full[owner][block & 1];
+                    };
+                    auto s_of = [&](int tile, uint32_t block) { return TILES == 2 ? tile : (int)(block & 1); };
+                    if (it.first < it.last) {
+                        uint32_t k_at = fills;
+                        fills += S::kHalves;
+                        ok = wait_block(k_at);
+                        for (int t = 0; ok && t < row_tiles; ++t) {
+                            const int q = TILES == 2 ? t : (int)owner;
+                            ok = wait(&sh.q_full[q], q_count[q]++ & 1);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            qk(t, s_of(t, blocks), k_at);
+                            tc::mma_commit(s_full(t, blocks));
+                        }
+                        if (ok) release(k_at);
+                        for (int j = it.first; ok && j < it.last; ++j, ++blocks) {
+                            const bool more = j + 1 < it.last, first = j == it.first;
+                            k_at = fills;
+                            if (more) fills += S::kHalves;
+                            const uint32_t v_at = fills;
+                            fills += S::kHalves;
+                            if (more) ok = wait_block(k_at);
+                            if (!ok) break;
+                            if constexpr (TILES == 1) {
+                                if (more) {
+                                    tc::fence_after_sync();
+                                    qk(0, s_of(0, blocks + 1), k_at);
+                                    tc::mma_commit(s_full(0, blocks + 1));
+                                    release(k_at);
+                                } else {
+                                    tc::mma_commit(&sh.q_free[owner]);
+                                }
+                                if (first && items > 0) ok = wait(&sh.o_free, (items - 1) & 1);
+                            }
+                            for (int t = 0; ok && t < row_tiles; ++t) {
+                                const int s = s_of(t, blocks);
+                                ok = wait(&sh.p_full[s], p_count[s]++ & 1) && (t > 0 || wait_block(v_at));
+                                if (!ok) break;
+                                tc::fence_after_sync();
+                                pv(t, s, v_at, !first);
+                                if (TILES == 1) {
+                                    tc::mma_commit(&sh.o_full[owner]);
+                                } else if (more) {
+                                    qk(t, s, k_at);
+                                    tc::mma_commit(s_full(t, 0));
+                                } else {
+                                    tc::mma_commit(&sh.o_full[t]);
+                                }
+                            }
+                            if (!ok) break;
+                            if (TILES == 2 && more) release(k_at);
+                            release(v_at);
+                        }
+                    } else if (TILES == 1) {
+                        tc::mma_commit(&sh.q_free[owner]);
+                        if (items > 0) ok = wait(&sh.o_free, (items - 1) & 1);
+                    }
+                    if (!ok) break;
+                    arrive(&sh.item_empty[slot]);
+                }
+                // products in flight end before tensor memory is given back
+                tc::mma_commit(&sh.drain);
+                wait_out(&sh.drain, 0);
+            }
+            __syncwarp();
+        } else if (warp >= 12) {
+            // ------------------------------------------------------------ the ring
+            constexpr int kPanels = S::kCols / 64, kPieces = S::kCols / 8;
+            const int me = warp - 12;
+            uint32_t items = 0, fills = 0, masked_count = 0;
+            int64_t flying[2] = {-1, -1};              // this warp's last tensor copies: stages' fills
+
+            // Fill f: the keys of block j, columns from h * kCols on, of K or V.
+            auto fill = [&](const Item &it, int slot, int j, int h, bool is_v) -> bool {
+                const uint32_t f = fills++;
+                if (f % S::kFillers != (uint32_t)me) return true;
+                const int st = f % S::kStages;
+                const uint32_t dst = ring + st * S::kStage, phase = ((f / S::kStages) & 1) ^ 1;
+                const int key0 = j * kKeys, keys = min(kKeys, it.kv - key0);       // (at least one)
+                // the tile's first token sees this many keys: a value from there on may be out of some row's sight
+                const int clear = p.causal ? it.kv - it.n + it.token0 + 1 : it.kv;
+                const bool masked = is_v && key0 + kKeys > clear;
+                // takes what is not finite out of a piece of eight values, noting which rows see it: those `rel` or more
+                // tokens behind the first
+                auto clean = [&](uint32_t (&u)[4], int row, int piece) -> bool {
+                    if (!(odd2<BF16>(u[0]) || odd2<BF16>(u[1]) || odd2<BF16>(u[2]) || odd2<BF16>(u[3]))) return false;
+                    const int key = key0 + row, rel = key < clear ? 0 : min(key - clear + 1, 0xfffe);
+#pragma unroll 1
+                    for (int e = 0; e < 8; ++e) {
+                        constexpr uint32_t x = BF16 ? 0x7f80u : 0x7c00u;
+                        const uint32_t word = e < 2 ? u[0] : e < 4 ? u[1] : e < 6 ? u[2] : u[3];
+                        if ((word >> (16 * (e & 1)) & x) != x) continue;
+                        const uint32_t keep = e & 1 ? 0x0000ffffu : 0xffff0000u;
+                        if (e < 2) u[0] &= keep; else if (e < 4) u[1] &= keep; else if (e < 6) u[2] &= keep; else u[3] &= keep;
+                        const int col = h * S::kCols + 8 * piece + e;
+                        uint32_t *at = &sh.poison[slot][col >> 1];
+                        const unsigned shift = (col & 1) * 16;
+                        uint32_t old = *reinterpret_cast<volatile uint32_t *>(at);
+                        while (((old >> shift) & 0xffffu) > (uint32_t)rel) {
+                            const uint32_t got = atomicCAS(at, old, (old & ~(0xffffu << shift)) | ((uint32_t)rel << shift));
+                            if (got == old) break;
+                            old = got;
+                        }
+                        *(volatile int *)&sh.poisoned[slot] = 1;
+                    }
+                    return true;
+                };
+                // all pieces of a stage that lies in shared memory: rows past the end to zeros, the others cleaned
+                auto clean_all = [&]() {
+#pragma unroll 4
+                    for (int i = lane; i < kKeys * kPieces; i += 32) {
+                        const int row = i / kPieces, piece = i % kPieces;
+                        const uint32_t a = dst + piece_at(row, piece);
+                        if (row >= keys) {
+                            sts16(a, 0u, 0u, 0u, 0u);
+                        } else {
+                            uint32_t u[4];
+                            lds16(u, a);
+                            if (clean(u, row, piece)) sts16(a, u[0], u[1], u[2], u[3]);
+                        }
+                    }
+                };
+                auto page_of = [&](int key, int &token) -> int {       // (key < kv)
+                    if (p.table == nullptr) {
+                        token = (int)it.row0 + key;
+                        return 0;
+                    }
+                    const unsigned q = p.page_div.quotient((unsigned)key);
+                    token = key - (int)q * p.cache.page_size;
+                    return p.table[(int64_t)it.seg * p.table_stride + q];
+                };
+
+                if (p.copy_mode == kTensorCopies) {
+                    const int per = p.copy_keys, count = (keys + per - 1) / per;   // keys of a copy; copies of a panel (16 at most)
+                    int page = 0, token = 0;
+                    if (lane < count) page = page_of(key0 + lane * per, token);    // before the stage is waited for
+                    if (!wait_warp(&sh.empty[st], phase)) return false;
+                    uint64_t *bar = masked ? &sh.landed[me] : &sh.full[st];
+                    if (lane == 0) arrive_expect(bar, (uint32_t)(count * kPanels * per * 128));
+                    __syncwarp();
+                    if (lane < count)
+#pragma unroll
+                        for (int x = 0; x < kPanels; ++x)
+                            copy_box(dst + x * S::kPanelBytes + lane * per * 128, is_v ? &v_map : &k_map, h * S::kCols + 64 * x, token,
+                                     it.head, page, bar);
+                    if (!masked) {
+                        flying[0] = flying[1];
+                        flying[1] = f;
+                        return true;
+                    }
+                    const uint32_t turn = masked_count++ & 1;
+                    if (!wait_warp(&sh.landed[me], turn)) {
+                        wait_out(&sh.landed[me], turn);
+                        return false;
+                    }
+                    clean_all();
+                    tc::fence_smem_async();
+                    __syncwarp();
+                    if (lane == 0) arrive(&sh.full[st]);
+                    return true;
+                }
+
+                // by loads: lane l has the places of keys l, l + 32, ..
+                int64_t place[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    place[i] = -1;
+                    const int row = lane + 32 * i;
+                    if (row < keys) {
+                        int token;
+                        const int page = page_of(key0 + row, token);
+                        if (page >= 0 && page < p.cache.pages)
+                            place[i] = (int64_t)page * p.cache.page_stride + (int64_t)token * p.cache.token_stride + (int64_t)it.head * p.cache.head_stride;
+                    }
+                }
+                if (!wait_warp(&sh.empty[st], phase)) return false;
+                const void *from = is_v ? p.v : p.k;
+                if (p.copy_mode == kLoads16) {
+                    // 16 bytes at a time, as they lie: E4M3 codes to the row's place in the last panel, to be widened there
+                    const bool codes = p.cache_dtype == GDNA_E4M3;
+                    const int elem = codes ? 1 : 2, each = 16 / elem, across = S::kCols / each;    // elements, pieces of a row
+                    const int shift = 31 - __clz(across);
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll 4
+                        for (int x = 0; x < across; ++x) {
+                            const int row = (x * 32 + lane) >> shift, piece = lane & (across - 1);
+                            const int64_t at = __shfl_sync(kFull, i == 0 ? place[0] : i == 1 ? place[1] : i == 2 ? place[2] : place[3], row);
+                            const int col = h * S::kCols + piece * each;
+                            const bool in = at >= 0 && col < p.d;
+                            const uint32_t to = dst + (codes ? (kPanels - 1) * S::kPanelBytes + (32 * i + row) * 128 + piece * 16
+                                                             : piece_at(32 * i + row, piece));
+                            const void *src = in ? static_cast<const uint8_t *>(from) + (at + col) * elem : from;
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(in ? 16 : 0) : "memory");
+                        }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    __syncwarp();
+                    if (codes) {
+                        // a row's codes are read by the lanes that write the row: 16 codes a lane
+                        constexpr int kLanes = S::kCols / 16, kPer = 32 / kLanes;
+#pragma unroll 2
+                        for (int row0 = 0; row0 < kKeys; row0 += kPer) {
+                            const int row = row0 + lane / kLanes, q = lane % kLanes;
+                            uint32_t u[4], a[4], b[4];
+                            lds16(u, dst + (kPanels - 1) * S::kPanelBytes + row * 128 + q * 16);
+                            auto widen = [](uint32_t x, uint32_t &lo, uint32_t &hi) {
+                                asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+                                    "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(x));
+                            };
+                            widen(u[0], a[0], a[1]); widen(u[1], a[2], a[3]);
+                            widen(u[2], b[0], b[1]); widen(u[3], b[2], b[3]);
+                            if (masked) {
+                                clean(a, row, 2 * q);
+                                clean(b, row, 2 * q + 1);
+                            }
+                            __syncwarp();
+                            sts16(dst + piece_at(row, 2 * q), a[0], a[1], a[2], a[3]);
+                            sts16(dst + piece_at(row, 2 * q + 1), b[0], b[1], b[2], b[3]);
+                        }
+                    } else if (masked) {
+                        clean_all();
+                    }
+                } else {
+                    // element by element: any alignment, any head size
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+                        for (int x = 0; x < kPieces; ++x) {
+                            const int row = (x * 32 + lane) / kPieces, piece = lane % kPieces;
+                            const int64_t at = __shfl_sync(kFull, i == 0 ? place[0] : i == 1 ? place[1] : i == 2 ? place[2] : place[3], row);
+                            const int col = h * S::kCols + piece * 8;
+                            float e[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) e[k] = at >= 0 && col + k < p.d ? gdna::load_elem(from, at + col + k, p.cache_dtype) : 0.f;
+                            uint32_t u[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) u[k] = pack16<BF16>(e[2 * k], e[2 * k + 1]);
+                            if (masked) clean(u, 32 * i + row, piece);
+                            sts16(dst + piece_at(32 * i + row, piece), u[0], u[1], u[2], u[3]);
+                        }
+                }
+                tc::fence_smem_async();
+                __syncwarp();
+                if (lane == 0) arrive(&sh.full[st]);
+                return true;
+            };
+            for (bool ok = true; ok; ++items) {
+                const int slot = items % kItems;
+                if (!wait_warp(&sh.item_full[slot], (items / kItems) & 1)) break;
+                const Item it = sh.item[slot];
+                if (!it.valid) break;
+                auto block = [&](int j, bool is_v) {
+                    for (int h = 0; ok && h < S::kHalves; ++h) ok = fill(it, slot, j, h, is_v);
+                };
+                // in the products' order: K of the first block, then K of the next and V of this one
+                if (it.first < it.last) block(it.first, false);
+                for (int j = it.first; ok && j < it.last; ++j) {
+                    if (j + 1 < it.last) block(j + 1, false);
+                    block(j, true);
+                }
+                __syncwarp();
+                if (ok && lane == 0) arrive(&sh.item_empty[slot]);
+            }
+            __syncwarp();
+            if (*(volatile int *)&sh.dead)             // copies in flight land before their memory is another block's
+                for (int i = 0; i < 2; ++i)
+                    if (flying[i] >= 0) wait_out(&sh.full[flying[i] % S::kStages], (uint32_t)(flying[i] / S::kStages) & 1);
+        }
+    }
+    __syncthreads();
+    if (warp == 8) tc::tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ launch
+
+// The map of K's or V's rows: element, token, head, page; box: 64 elements (a panel's 128 bytes) x `keys` tokens.  What
+// lies past a head, and in pages that are none, comes as zeros.  False where the encoder refuses the layout.
+inline bool rows_map(const FlashParams &p, const void *base, CUtensorMap *map)
+{
+    const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn::tensor_map_encoder());
+    if (encode == nullptr) return false;
+    const cuuint64_t size[4] = {(cuuint64_t)p.d, (cuuint64_t)(p.table != nullptr ? p.cache.page_size : p.rows), (cuuint64_t)p.nkv,
+                                (cuuint64_t)(p.table != nullptr ? p.cache.pages : 1)};
+    const int64_t strides[3] = {p.cache.token_stride, p.cache.head_stride, p.table != nullptr ? p.cache.page_stride : 64};
+    cuuint64_t stride[3];
+    for (int i = 0; i < 3; ++i) {
+        int64_t bytes = strides[i] * 2;
+        if (size[i + 1] == 1 && bytes <= 0) bytes = 16;        // (a dimension of one)
+        if (bytes <= 0 || bytes >= (int64_t{1} << 40)) return false;
+        stride[i] = (cuuint64_t)bytes;
+    }
+    const cuuint32_t box[4] = {64, (cuuint32_t)p.copy_keys, 1, 1}, step[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), size, stride, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF16, int PARTS> cudaError_t launch(FlashParams p, cudaStream_t s)
+{
+    using S = Shape<D, PARTS>;
+    CUtensorMap k_map{}, v_map{};
+    if (p.copy_mode == kTensorCopies && !(rows_map(p, p.k, &k_map) && rows_map(p, p.v, &v_map))) p.copy_mode = kLoads16;
+    const cudaError_t e = gdn::allow_dynamic_smem<&flash_rows<D, BF16, PARTS>>(S::kSmem);
+    if (e != cudaSuccess) return e;
+    flash_rows<D, BF16, PARTS><<<p.grid, kThreads, S::kSmem, s>>>(p, k_map, v_map, gdn::tc_copy_wait_polls());
+    return cudaGetLastError();
+}
+
+// 16-bit parts of a query: one where the products' type holds its type.
+template <int D> cudaError_t launch_by_type(const FlashParams &p, cudaStream_t s)
+{
+    const bool bf16 = p.cache_dtype == GDNA_BF16;
+    const bool one = p.dtype == GDNA_BF16 || (p.dtype == GDNA_F16 && !bf16);
+    if (bf16) return one ? launch<D, true, 1>(p, s) : launch<D, true, 2>(p, s);
+    return one ? launch<D, false, 1>(p, s) : launch<D, false, 2>(p, s);
+}
+
+template <int D> cudaError_t wait_timeouts(unsigned *count)
+{
+    return cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(unsigned));
+}
+
+}  // namespace flash
+
+// One unit each (gdnb_flash_64.cu ...).
+cudaError_t launch_flash_64(const FlashParams &p, cudaStream_t s);
+cudaError_t launch_flash_128(const FlashParams &p, cudaStream_t s);
+cudaError_t launch_flash_256(const FlashParams &p, cudaStream_t s);
+cudaError_t flash_timeouts_64(unsigned *count);
+cudaError_t flash_timeouts_128(unsigned *count);
+cudaError_t flash_timeouts_256(unsigned *count);
+
+}  // namespace gdnb

@@ -1,0 +1,244 @@
+// gdnb_norm.cu -- norm after a block, gate, residual scale and norm before the
+// next block in one pass (include/gdnb.h, gdnb_residual_norm).
+//
+//     u = post y / sqrt(mean y^2 + eps),  x' = x + scale gate u,  h = pre x' / sqrt(mean x'^2 + eps)
+//
+// Two sums over a row, the second of what the first decides, so a row stays in the registers
+// of one block: eight elements a thread (sixteen past 8192), the threads as many as the row
+// needs.  Bound by HBM for many rows and by the chain load, sum, sum, store for few.  A block
+// takes row after row and asks for the next one's elements before it adds up this one's, so
+// that the two barriers of a row are hidden by loads in flight; weights stay in registers.
+#include "gdnb_internal.cuh"
+
+namespace gdnb {
+namespace {
+
+using gdna::load_elem;
+using gdna::store_elem;
+
+// Eight elements as they lie in memory: 16 bytes of a 16-bit type, 32 of fp32 (WIDE).
+template <bool WIDE> struct Raw {
+    uint4 a[WIDE ? 2 : 1];
+};
+
+template <bool WIDE, bool VEC> struct Row8 {
+    Raw<WIDE> raw;
+    float one[VEC ? 1 : 8];
+
+    // elements 8t .. 8t+7 of a row (VEC), else t, t + step, ...
+    __device__ __forceinline__ void ask(const void *p, int64_t row, int first, int step, int c, int dtype, bool real)
+    {
+        if constexpr (VEC) {
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            const bool in = real && first < c;
+            if constexpr (WIDE) {
+                const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + row + first);
+                raw.a[0] = in ? at[0] : zero;
+                raw.a[1] = in ? at[1] : zero;
+            } else {
+                raw.a[0] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + row + first) : zero;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) one[j] = real && first + j * step < c ? load_elem(p, row + first + j * step, dtype) : 0.f;
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[8], int dtype) const
+    {
+        if constexpr (!VEC) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = one[j];
+        } else if constexpr (WIDE) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                x[4 * j] = __uint_as_float(raw.a[j].x); x[4 * j + 1] = __uint_as_float(raw.a[j].y);
+                x[4 * j + 2] = __uint_as_float(raw.a[j].z); x[4 * j + 3] = __uint_as_float(raw.a[j].w);
+            }
+        } else {
+            const unsigned u[4] = {raw.a[0].x, raw.a[0].y, raw.a[0].z, raw.a[0].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (dtype == GDNA_BF16) {
+                    x[2 * j] = __uint_as_float(u[j] << 16);
+                    x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[j]));
+                    x[2 * j] = f.x;
+                    x[2 * j + 1] = f.y;
+                }
+            }
+        }
+    }
+};
+
+template <bool VEC>
+__device__ __forceinline__ void put8(void *p, int64_t row, int first, int step, int c, int dtype, const float (&x)[8])
+{
+    if constexpr (VEC) {
+        if (first >= c) return;
+        if (dtype == GDNA_F32) {
+            float4 *at = reinterpret_cast<float4 *>(static_cast<float *>(p) + row + first);
+            at[0] = make_float4(x[0], x[1], x[2], x[3]);
+            at[1] = make_float4(x[4], x[5], x[6], x[7]);
+        } else {
+            unsigned u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (dtype == GDNA_BF16) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                    u[j] = *reinterpret_cast<const unsigned *>(&b);
+                } else {
+                    const __half2 b = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+                    u[j] = *reinterpret_cast<const unsigned *>(&b);
+                }
+            }
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + row + first) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (first + j * step < c) store_elem(p, row + first + j * step, dtype, x[j]);
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void weights8(const float *w, int first, int step, int c, float (&x)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = 1.f;
+    if (w == nullptr) return;
+    if constexpr (VEC) {
+        if (first >= c) return;
+        const float4 a = *reinterpret_cast<const float4 *>(w + first), b = *reinterpret_cast<const float4 *>(w + first + 4);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (first + j * step < c) x[j] = w[first + j * step];
+    }
+}
+
+// The block's sum of `x`, in the warps' order; `red` alternates between two buffers, so that one barrier a sum is enough.
+__device__ __forceinline__ float block_sum(float x, float *red)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    x = gdn::group_sum<32>(x);
+    if (warps == 1) return x;
+    if (lane == 0) red[warp] = x;
+    __syncthreads();
+    return gdn::group_sum<32>(lane < warps ? red[lane] : 0.f);
+}
+
+// XW, YW: x, y (and gate) are fp32.  K: groups of eight elements a thread.
+template <bool XW, bool YW, bool VEC, int K, int THREADS>
+__global__ void __launch_bounds__(THREADS) residual_norm(const NormParams p)
+{
+    __shared__ float red[2][32];
+    const int t = threadIdx.x, n = blockDim.x, c = p.c;
+    const int step = VEC ? 1 : n * K;                  // between a group's elements
+    auto first = [&](int k) { return VEC ? 8 * (t + k * n) : t + k * n; };
+    const float inv_c = 1.f / (float)c;
+    constexpr bool kAhead = K == 1;                    // the next row's elements and the weights in registers
+    float post[8], pre[8];
+    Row8<XW, VEC> x[K], x_next[kAhead ? 1 : 1];
+    Row8<YW, VEC> y[K], y_next[1], g[K], g_next[1];
+    const bool has_y = p.y != nullptr, has_gate = p.gate != nullptr;
+    auto ask = [&](int64_t row, int k, Row8<XW, VEC> &xr, Row8<YW, VEC> &yr, Row8<YW, VEC> &gr) {
+        const bool real = row < p.rows;
+        xr.ask(p.x, row * p.x_stride, first(k), step, c, p.x_dtype, real);
+        yr.ask(p.y, row * p.y_stride, first(k), step, c, p.y_dtype, real && has_y);
+        gr.ask(p.gate, row * p.gate_stride, first(k), step, c, p.y_dtype, real && has_gate);
+    };
+    int64_t row = blockIdx.x;
+    if constexpr (kAhead) {
+        ask(row, 0, x_next[0], y_next[0], g_next[0]);
+        weights8<VEC>(p.post, first(0), step, c, post);
+        weights8<VEC>(p.pre, first(0), step, c, pre);
+    }
+    for (; row < p.rows; row += gridDim.x) {
+        if constexpr (kAhead) {
+            x[0] = x_next[0]; y[0] = y_next[0]; g[0] = g_next[0];
+            ask(row + gridDim.x, 0, x_next[0], y_next[0], g_next[0]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k) ask(row, k, x[k], y[k], g[k]);
+        }
+        float factor = p.scale;
+        if (has_y && p.post != nullptr) {              // (for all threads alike)
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float v[8];
+                y[k].get(v, p.y_dtype);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
+            }
+            factor = p.scale / sqrtf(block_sum(sum, red[0]) * inv_c + p.eps);
+        }
+        float sum = 0.f, to[K][8];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            x[k].get(to[k], p.x_dtype);
+            if (has_y) {
+                float v[8], w[8];
+                y[k].get(v, p.y_dtype);
+                if constexpr (!kAhead) weights8<VEC>(p.post, first(k), step, c, post);
+                g[k].get(w, p.y_dtype);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float u = v[j] * factor * post[j];
+                    to[k][j] += has_gate ? u * w[j] : u;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum = fmaf(to[k][j], to[k][j], sum);
+            if (p.x_out != nullptr) put8<VEC>(p.x_out, row * p.x_out_stride, first(k), step, c, p.x_dtype, to[k]);
+        }
+        if (p.h == nullptr) {
+            // (the first sum's buffer is written again only after every thread has passed its barrier: two rows' barriers
+            // would otherwise meet in one buffer)
+            if (has_y && p.post != nullptr) __syncthreads();
+            continue;
+        }
+        const float norm = 1.f / sqrtf(block_sum(sum, red[1]) * inv_c + p.eps);
+        // without a first sum the same buffer is used row after row
+        if (!(has_y && p.post != nullptr)) __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if constexpr (!kAhead) weights8<VEC>(p.pre, first(k), step, c, pre);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) to[k][j] *= norm * pre[j];
+            put8<VEC>(p.h, row * p.h_stride, first(k), step, c, p.h_dtype, to[k]);
+        }
+    }
+}
+
+template <bool XW, bool YW, bool VEC>
+cudaError_t launch(const NormParams &p, cudaStream_t s)
+{
+    const int groups = (p.c + 7) / 8;
+    const int k = groups <= 1024 ? 1 : 2;
+    const int threads = ((groups + k - 1) / k + 31) / 32 * 32;
+    // as many blocks as are resident at once, and no more than rows
+    const int64_t resident = (int64_t)gdn::sm_count() * (threads >= 1024 || k == 2 ? 1 : threads <= 64 ? 16 : 1024 / threads);
+    const unsigned grid = (unsigned)(p.rows < resident ? p.rows : resident);
+    if (k == 2) residual_norm<XW, YW, VEC, 2, 1024><<<grid, threads, 0, s>>>(p);
+    else residual_norm<XW, YW, VEC, 1, 1024><<<grid, threads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <bool VEC> cudaError_t by_types(const NormParams &p, cudaStream_t s)
+{
+    const bool xw = p.x_dtype == GDNA_F32, yw = p.y != nullptr && p.y_dtype == GDNA_F32;
+    if (xw) return yw ? launch<true, true, VEC>(p, s) : launch<true, false, VEC>(p, s);
+    return yw ? launch<false, true, VEC>(p, s) : launch<false, false, VEC>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_residual_norm(const NormParams &p, bool vec, cudaStream_t s)
+{
+    return vec ? by_types<true>(p, s) : by_types<false>(p, s);
+}
+
+}  // namespace gdnb
