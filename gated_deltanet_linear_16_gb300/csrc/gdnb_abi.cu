@@ -25,7 +25,7 @@ void set_paths(gdnb::FlashParams &p, int64_t page_stride, int64_t token_stride, 
     p.copy_keys = size < 128 ? size : 128;
     p.copy_mode = !pieces ? gdnb::kElements : p.cache_dtype != GDNA_E4M3 && p.copy_keys >= 8 ? gdnb::kTensorCopies : gdnb::kLoads16;
     p.q_vec = p.d % 8 == 0 && rows_aligned(p.q, qe, 16, {p.q_stride, p.d});
-    p.gate_vec = p.d % 4 == 0 && rows_aligned(p.gate, qe, 4 * qe, {p.gate_stride, p.gate_head_stride});
+    p.gate_vec = p.d % 8 == 0 && rows_aligned(p.gate, qe, 16, {p.gate_stride, p.gate_head_stride});
     p.out_vec = p.d % 8 == 0 && rows_aligned(p.out, 2, 16, {p.out_stride, p.d});
 }
 

@@ -245,23 +245,28 @@ template <bool BF16> __host__ __device__ constexpr uint32_t idesc16(int m, int n
     return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((b_n_major ? 1u : 0u) << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
-// B read along its rows (N-major): panels of 64 columns `panel` bytes apart, eight keys (one swizzle atom) 1024.
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr, uint32_t panel)
+// A shared-memory descriptor's halves.  Low: the address in 16-byte units, and (N-major: B read along its rows) the distance
+// of the panels of 64 columns.  High: eight rows (one swizzle atom) 1024 bytes apart, descriptor version, 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t panel) { return ((addr & 0x3FFFFu) >> 4) | ((panel >> 4) << 16); }
+__device__ __forceinline__ void mma16_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
 {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHigh) : "memory");
 }
-__device__ __forceinline__ void mma16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kDescHigh) : "memory");
 }
-__device__ __forceinline__ void mma16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect()
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
 }
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void arrive(uint64_t *bar)
@@ -402,7 +407,7 @@ __device__ __forceinline__ float load_queries(const FlashParams &p, const Item &
 {
     using S = Shape<D, PARTS>;
     constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPasses = 32 / kPer;     // lanes of a row, rows of a pass
-    constexpr int kGo = 4;
+    constexpr int kGo = kPasses < 16 ? kPasses : 16;           // passes asked for at once
     const int col = (lane % kLanes) * 8;
     const bool scaled = !BF16 && p.dtype != GDNA_F16;
     float mine = 1.f;
@@ -495,6 +500,47 @@ __device__ __forceinline__ void add2(float &a, float &b, float c, float d)      
         "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(a), "+f"(b) : "f"(c), "f"(d));
 }
 
+// The output gates of 32 columns of a row: 16 bytes at a time where they are 16-bit elements that lie so, else when they are
+// applied.
+struct Gates {
+    uint4 raw[4];
+    __device__ __forceinline__ void ask(const FlashParams &p, int64_t row, int x, bool wanted)
+    {
+        if (!wanted || !p.gate_vec || p.dtype == GDNA_F32) return;
+        const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.gate) + row + x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (x + 8 * i < p.d) raw[i] = at[i];
+    }
+    __device__ __forceinline__ void apply(const FlashParams &p, int64_t row, int x, float (&o)[32]) const
+    {
+        const bool here = p.gate_vec && p.dtype != GDNA_F32;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (x + 8 * i >= p.d) break;
+            float g[8];
+            if (here) {
+                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = p.dtype == GDNA_BF16 ? unpack16<true>(u[k]) : unpack16<false>(u[k]);
+                    g[2 * k] = f.x;
+                    g[2 * k + 1] = f.y;
+                }
+            } else if (p.gate_vec) {
+                const float4 *at = reinterpret_cast<const float4 *>(static_cast<const float *>(p.gate) + row + x + 8 * i);
+                const float4 a = at[0], b = at[1];
+                g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w; g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) g[k] = x + 8 * i + k < p.d ? gdna::load_elem(p.gate, row + x + 8 * i + k, p.dtype) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[8 * i + k] = __fdividef(o[8 * i + k], 1.f + __expf(-g[k]));
+        }
+    }
+};
+
 // ------------------------------------------------------------------ the kernel
 
 template <int D, bool BF16, int PARTS>
@@ -556,6 +602,17 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
         const int wg = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         uint32_t items = 0, blocks_all = 0, s_count[2] = {0, 0}, o_count = 0;
+        // this warp's queries of an item into shared memory
+        auto queries = [&](const Item &it) {
+            const int rows = rows_in(it);
+            const float x = load_queries<D, BF16, PARTS>(p, it, rows, (TILES == 2 ? wg * 128 : 0) + quarter * 32,
+                                                         q_smem + (TILES == 2 ? wg * PARTS * S::kQTile : 0), lane);
+            tc::fence_smem_async();
+            __syncwarp();
+            if (lane == 0) arrive(&sh.q_full[wg]);
+            return x;
+        };
+        float ahead = 0.f;                             // the next item's queries are in already, with this scale
         for (;; ++items) {
             const int slot = items % kItems;
             if (!wait_warp(&sh.item_full[slot], (items / kItems) & 1)) break;
@@ -578,10 +635,8 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             // (every phase of a barrier is waited for, in order: one that was skipped would be taken for the one after it)
             if (TILES == 1 && items > 0 && !wait_warp(&sh.q_free[(items - 1) & 1], ((items - 1) >> 1) & 1)) break;
             if (blocks > 0) {
-                scale *= load_queries<D, BF16, PARTS>(p, it, rows, row0, q_smem + (TILES == 2 ? wg * PARTS * S::kQTile : 0), lane);
-                tc::fence_smem_async();
-                __syncwarp();
-                if (lane == 0) arrive(&sh.q_full[wg]);
+                scale *= ahead != 0.f ? ahead : queries(it);
+                ahead = 0.f;
             }
             bool ok = true;
             for (int j = 0; j < blocks; ++j) {
@@ -659,6 +714,14 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 if (lane == 0) arrive(&sh.p_full[col]);
             }
             if (!ok) break;
+            // two row tiles: the next item's queries first, so that its products run while this one's output is written (the
+            // scores of the last block are here, so nothing reads the old ones any more)
+            if (TILES == 2 && blocks > 0) {
+                const int after = (items + 1) % kItems;
+                if (!wait_warp(&sh.item_full[after], ((items + 1) / kItems) & 1)) break;
+                const Item &then = sh.item[after];
+                if (then.valid && then.first < then.last && rows_in(then) > wg * 128) ahead = queries(then);
+            }
             // ---- the output
             if (blocks > 0) {
                 const uint32_t last = TILES == 2 ? o_count++ : (o_count += blocks) - 1;
@@ -674,9 +737,16 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             float *part = p.parts + it.slot * S::kPart;
             if (!final_rows && real)
                 *reinterpret_cast<float2 *>(part + S::kRows * D + 2 * r) = make_float2(m == kNegInf ? kNegInf : m * scale, l);
+            // gates of 32 columns, asked for while the columns before them are written
+            const bool gated = p.gate != nullptr && final_rows && real;
+            const int64_t gate_row = row * p.gate_stride + head * p.gate_head_stride;
+            Gates gate, gate_next;
+            gate_next.ask(p, gate_row, 0, gated);
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 float o[32];
+                gate = gate_next;
+                gate_next.ask(p, gate_row, x + 32, gated && x + 32 < D);
                 if (blocks > 0) {
                     tc::tmem_ld32(o_col(TILES == 2 ? wg : 0) + lanes + x, o);
                     tc::ld_wait();
@@ -700,37 +770,19 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 if (x >= p.d) continue;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] *= norm;
-                if (p.gate != nullptr) {
-                    const int64_t from = row * p.gate_stride + head * p.gate_head_stride + x;
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        if (x + i >= p.d) break;
-                        float4 g;
-                        if (p.gate_vec) {
-                            g = gdna::got4(gdna::ask4(p.gate, from + i, p.dtype, true), p.dtype, true);
-                        } else {
-                            float e[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) e[k] = x + i + k < p.d ? gdna::load_elem(p.gate, from + i + k, p.dtype) : 0.f;
-                            g = make_float4(e[0], e[1], e[2], e[3]);
-                        }
-                        o[i] = __fdividef(o[i], 1.f + __expf(-g.x)); o[i + 1] = __fdividef(o[i + 1], 1.f + __expf(-g.y));
-                        o[i + 2] = __fdividef(o[i + 2], 1.f + __expf(-g.z)); o[i + 3] = __fdividef(o[i + 3], 1.f + __expf(-g.w));
-                    }
-                }
+                if (gated) gate.apply(p, gate_row, x, o);
                 const int64_t to = row * p.out_stride + head * p.d + x;
                 if (p.out_vec) {
                     uint4 *at = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + to);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (x + 8 * i >= p.d) break;
                         uint32_t u[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float a = o[8 * i + 2 * k], b = o[8 * i + 2 * k + 1];
                             u[k] = p.out_dtype == GDNA_BF16 ? pack16<true>(a, b) : pack16<false>(a, b);
                         }
-                        at[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                        if (x + 8 * i < p.d) at[i] = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 } else {
 #pragma unroll
@@ -818,116 +870,155 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 put();
             }
         } else if (warp == 8) {
-            // ------------------------------------------------------------ products, by one thread
-            if (lane == 0) {
-                constexpr uint32_t kQK = idesc16<BF16>(128, kKeys, false), kPV = idesc16<BF16>(128, S::kCols, true);
-                constexpr int kSteps = S::kCols / 16;  // of a stage's columns
-                uint32_t items = 0, fills = 0, blocks = 0, q_count[2] = {0, 0}, p_count[2] = {0, 0};
-                bool ok = true;
-                auto stage_of = [&](uint32_t f) { return ring + (f % S::kStages) * S::kStage; };
-                auto wait_block = [&](uint32_t f) {    // the stages of a block of K, or V
-                    bool good = true;
-                    for (int h = 0; h < S::kHalves; ++h) good = good && wait(&sh.full[(f + h) % S::kStages], ((f + h) / S::kStages) & 1);
-                    return good;
-                };
-                auto release = [&](uint32_t f) {
-                    for (int h = 0; h < S::kHalves; ++h) tc::mma_commit(&sh.empty[(f + h) % S::kStages]);
-                };
-                auto qk = [&](int tile, int s, uint32_t f) {           // S s = Q of the tile . K^T, K in stages f ..
-#pragma unroll 1
+            // ------------------------------------------------------------ products
+            // The whole warp walks along, with values that are the same in all lanes (from shuffles and votes), so that
+            // descriptors stay in uniform registers; one lane issues.  (One thread by itself: 120 cycles a product.)
+            constexpr uint32_t kQK = idesc16<BF16>(128, kKeys, false), kPV = idesc16<BF16>(128, S::kCols, true);
+            constexpr int kSteps = S::kCols / 16;      // of a stage's columns
+            const uint32_t t_base = __shfl_sync(kFull, tmem, 0), q_low = desc_low(__shfl_sync(kFull, q_smem, 0), 16);
+            const uint32_t ring_k = desc_low(__shfl_sync(kFull, ring, 0), 16), ring_v = desc_low(__shfl_sync(kFull, ring, 0), S::kPanelBytes);
+            const bool leader = elect();
+            uint32_t items = 0, blocks = 0, q_count = 0, p_count = 0;  // (parities of two barriers each)
+            // the ring's next stage, and its phase
+            uint32_t next = 0, phase = 0;
+            struct Stages {
+                uint32_t at[S::kHalves];
+            };
+            bool ok = true;
+            auto take = [&]() {                        // the stages of the next block of K, or V, once they are full
+                Stages x;
+#pragma unroll
+                for (int h = 0; h < S::kHalves; ++h) {
+                    ok = ok && wait_warp(&sh.full[next], phase);
+                    x.at[h] = next;
+                    if (++next == (uint32_t)S::kStages) { next = 0; phase ^= 1; }
+                }
+                return x;
+            };
+            auto release = [&](const Stages &x) {
+                if (leader)
+#pragma unroll
+                    for (int h = 0; h < S::kHalves; ++h) tc::mma_commit(&sh.empty[x.at[h]]);
+            };
+            auto qk = [&](int tile, uint32_t s, const Stages &x, uint64_t *bar) {  // S s = Q of the tile . K^T
+                const uint32_t d = t_base + 128 * s;
+                if (leader) {
+#pragma unroll
                     for (int i = 0; i < PARTS * S::kHalves; ++i) {
                         const int part = i / S::kHalves, h = i % S::kHalves;
-                        const uint64_t a = tc::smem_desc_sw128(q_smem + (tile * PARTS + part) * S::kQTile + h * S::kStage);
-                        const uint64_t b = tc::smem_desc_sw128(stage_of(f + h));
+                        const uint32_t a = q_low + (((tile * PARTS + part) * S::kQTile + h * S::kStage) >> 4);
+                        const uint32_t b = ring_k + x.at[h] * (S::kStage >> 4);
 #pragma unroll
-                        for (int k = 0; k < kSteps; ++k) {             // (16 columns are 32 bytes of a panel: 2 in the descriptor)
-                            const uint64_t off = (k >> 2) * (S::kPanelBytes >> 4) + (k & 3) * 2;
-                            mma16_ss(s_col(s), a + off, b + off, kQK, i + k > 0);
+                        for (int k = 0; k < kSteps; ++k) {             // (16 columns are 32 bytes of a panel)
+                            const uint32_t off = (k >> 2) * (S::kPanelBytes >> 4) + (k & 3) * 2;
+                            mma16_ss(d, a + off, b + off, kQK, i + k > 0);
                         }
                     }
-                };
-                auto pv = [&](int tile, int s, uint32_t f, bool acc) { // O of the tile += P . V
-#pragma unroll 1
+                    tc::mma_commit(bar);
+                }
+                __syncwarp();
+            };
+            auto pv = [&](int tile, uint32_t s, const Stages &x, uint32_t acc) {   // O of the tile += P . V
+                const uint32_t a = t_base + 128 * s, d = t_base + 256 + tile * D;
+                if (leader)
+#pragma unroll
                     for (int h = 0; h < S::kHalves; ++h) {
-                        const uint64_t b = desc_n_major(stage_of(f + h), S::kPanelBytes);
+                        const uint32_t b = ring_v + x.at[h] * (S::kStage >> 4);
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k)           // (16 keys are 2048 bytes)
-                            mma16_ts(o_col(tile) + h * S::kCols, s_col(s) + 8 * k, b + k * (2048 >> 4), kPV, acc || k > 0);
+                            mma16_ts(d + h * S::kCols, a + 8 * k, b + k * (2048 >> 4), kPV, k > 0 ? 1u : acc);
                     }
+                __syncwarp();
+            };
+            auto wait_q = [&](int i) {
+                const bool good = wait_warp(&sh.q_full[i], (q_count >> i) & 1);
+                q_count ^= 1u << i;
+                return good;
+            };
+            auto wait_p = [&](int i) {
+                const bool good = wait_warp(&sh.p_full[i], (p_count >> i) & 1);
+                p_count ^= 1u << i;
+                return good;
+            };
+            for (; ok; ++items) {
+                const int slot = items % kItems;
+                if (!wait_warp(&sh.item_full[slot], (items / kItems) & 1)) break;
+                const Item *it = &sh.item[slot];
+                if (!__shfl_sync(kFull, it->valid, 0)) break;
+                const int first_block = __shfl_sync(kFull, it->first, 0), last_block = __shfl_sync(kFull, it->last, 0);
+                const bool two = TILES == 2 && __shfl_sync(kFull, rows_in(*it), 0) > 128;
+                const uint32_t owner = items & 1;      // of a single row tile: the softmax warps take turns
+                __syncwarp();
+                if (leader) arrive(&sh.item_empty[slot]);
+                auto s_full = [&](int tile, uint32_t block) {
+                    return TILES == 2 ? &sh.s_full[tile][0] : &sh.s_full[owner][block & 1];
                 };
-                for (;; ++items) {
-                    const int slot = items % kItems;
-                    if (!wait(&sh.item_full[slot], (items / kItems) & 1)) break;
-                    const Item it = sh.item[slot];
-                    if (!it.valid) break;
-                    const int row_tiles = TILES == 2 && rows_in(it) > 128 ? 2 : 1;
-                    const uint32_t owner = items & 1;  // of a single row tile: the softmax warps take turns
-                    auto s_full = [&](int tile, uint32_t block) {
-                        return TILES == 2 ? &sh.s_full[tile][0] : &sh.s_full[owner][block & 1];
-                    };
-                    auto s_of = [&](int tile, uint32_t block) { return TILES == 2 ? tile : (int)(block & 1); };
-                    if (it.first < it.last) {
-                        uint32_t k_at = fills;
-                        fills += S::kHalves;
-                        ok = wait_block(k_at);
-                        for (int t = 0; ok && t < row_tiles; ++t) {
-                            const int q = TILES == 2 ? t : (int)owner;
-                            ok = wait(&sh.q_full[q], q_count[q]++ & 1);
+                auto s_of = [&](int tile, uint32_t block) { return TILES == 2 ? (uint32_t)tile : block & 1; };
+                if (first_block >= last_block) {
+                    if (TILES == 1) {
+                        if (leader) tc::mma_commit(&sh.q_free[owner]);
+                        __syncwarp();
+                        if (items > 0) ok = wait_warp(&sh.o_free, (items - 1) & 1);
+                    }
+                    continue;
+                }
+                Stages k_at = take();
+                ok = ok && wait_q(TILES == 2 ? 0 : (int)owner);
+                if (!ok) break;
+                tc::fence_after_sync();
+                qk(0, s_of(0, blocks), k_at, s_full(0, blocks));
+                if (two) {
+                    ok = wait_q(1);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    qk(1, 1, k_at, &sh.s_full[1][0]);
+                }
+                release(k_at);
+                for (int j = first_block; j < last_block; ++j, ++blocks) {
+                    const bool more = j + 1 < last_block;
+                    const uint32_t acc = j > first_block;
+                    if (more) k_at = take();
+                    if constexpr (TILES == 1) {
+                        if (!ok) break;
+                        if (more) {
+                            tc::fence_after_sync();
+                            qk(0, s_of(0, blocks + 1), k_at, s_full(0, blocks + 1));
+                            release(k_at);
+                        } else {
+                            if (leader) tc::mma_commit(&sh.q_free[owner]);
+                            __syncwarp();
+                        }
+                        if (acc == 0 && items > 0) ok = wait_warp(&sh.o_free, (items - 1) & 1);
+                    }
+                    const Stages v_at = take();
+                    const uint32_t s0 = s_of(0, blocks);
+                    ok = ok && wait_p(s0);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    pv(0, s0, v_at, acc);
+                    if constexpr (TILES == 1) {
+                        if (leader) tc::mma_commit(&sh.o_full[owner]);
+                    } else {
+                        if (more) qk(0, 0, k_at, &sh.s_full[0][0]);
+                        else if (leader) tc::mma_commit(&sh.o_full[0]);
+                        if (two) {
+                            ok = wait_p(1);
                             if (!ok) break;
                             tc::fence_after_sync();
-                            qk(t, s_of(t, blocks), k_at);
-                            tc::mma_commit(s_full(t, blocks));
+                            pv(1, 1, v_at, acc);
+                            if (more) qk(1, 1, k_at, &sh.s_full[1][0]);
+                            else if (leader) tc::mma_commit(&sh.o_full[1]);
                         }
-                        if (ok) release(k_at);
-                        for (int j = it.first; ok && j < it.last; ++j, ++blocks) {
-                            const bool more = j + 1 < it.last, first = j == it.first;
-                            k_at = fills;
-                            if (more) fills += S::kHalves;
-                            const uint32_t v_at = fills;
-                            fills += S::kHalves;
-                            if (more) ok = wait_block(k_at);
-                            if (!ok) break;
-                            if constexpr (TILES == 1) {
-                                if (more) {
-                                    tc::fence_after_sync();
-                                    qk(0, s_of(0, blocks + 1), k_at);
-                                    tc::mma_commit(s_full(0, blocks + 1));
-                                    release(k_at);
-                                } else {
-                                    tc::mma_commit(&sh.q_free[owner]);
-                                }
-                                if (first && items > 0) ok = wait(&sh.o_free, (items - 1) & 1);
-                            }
-                            for (int t = 0; ok && t < row_tiles; ++t) {
-                                const int s = s_of(t, blocks);
-                                ok = wait(&sh.p_full[s], p_count[s]++ & 1) && (t > 0 || wait_block(v_at));
-                                if (!ok) break;
-                                tc::fence_after_sync();
-                                pv(t, s, v_at, !first);
-                                if (TILES == 1) {
-                                    tc::mma_commit(&sh.o_full[owner]);
-                                } else if (more) {
-                                    qk(t, s, k_at);
-                                    tc::mma_commit(s_full(t, 0));
-                                } else {
-                                    tc::mma_commit(&sh.o_full[t]);
-                                }
-                            }
-                            if (!ok) break;
-                            if (TILES == 2 && more) release(k_at);
-                            release(v_at);
-                        }
-                    } else if (TILES == 1) {
-                        tc::mma_commit(&sh.q_free[owner]);
-                        if (items > 0) ok = wait(&sh.o_free, (items - 1) & 1);
+                        if (more) release(k_at);
                     }
-                    if (!ok) break;
-                    arrive(&sh.item_empty[slot]);
+                    release(v_at);
+                    __syncwarp();
                 }
-                // products in flight end before tensor memory is given back
-                tc::mma_commit(&sh.drain);
-                wait_out(&sh.drain, 0);
             }
+            // products in flight end before tensor memory is given back
+            __syncwarp();
+            if (leader) tc::mma_commit(&sh.drain);
+            wait_out(&sh.drain, 0);
             __syncwarp();
         } else if (warp >= 12) {
             // ------------------------------------------------------------ the ring

@@ -41,7 +41,7 @@ struct FlashParams {
     float scale2, v_scale;          // scores in units of log2
     // own keys of a shared call, to be joined
     const float *own, *own_lse;
-    int q_vec, gate_vec, out_vec;   // rows and heads start on boundaries of 16 bytes (out), four elements (gate), eight (q)
+    int q_vec, gate_vec, out_vec;   // rows and heads start on boundaries of 16 bytes, and are of eights
     int copy_mode, copy_keys;
     // set by the launcher
     int tile_tokens, tile_rows, grid;
