@@ -20,8 +20,9 @@
 // direction (N-major) for the second.
 //
 // Who does what (512 threads, one block an SM, persistent).  Warps 0-7: softmax, rescale, output, and the
-// queries' way into shared memory.  Warp 8 issues products, warp 10 deals out work, warps 12-15 fill
-// the ring, a stage each in turn, by tensor copies or by loads (E4M3, odd pages and layouts).
+// queries' way into shared memory.  Warps 8 and 9 issue the products of a row tile each, warp 10 deals out work, warps 12-15 fill
+// the ring, a stage each in turn, by tensor copies or by loads (E4M3, odd pages and layouts), and warp 11 looks at the values that
+// not every row sees.
 //
 // Work.  With many tiles a block takes every grid-th one, longest first within a sequence and in alternating
 // direction, so that neighbours read the same keys at the same time and loads even out.  With
@@ -58,7 +59,7 @@ constexpr int kMaxGrid = 160;              // blocks that share the work, at mos
 constexpr int kItems = 4;                  // slots of the work queue
 constexpr int kCopyWarps = 4;
 constexpr int kLead = 256;                 // what a tile costs beside its keys, in keys: queries, first products, output
-constexpr int kLeastChunk = 768;           // a block's run of the row of costs, at least
+constexpr int kLeastChunk = 768;           // a block's run of the row of costs, at least; tiles that cost less stay whole
 constexpr int kMostKeys = INT32_MAX - 4095;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -173,7 +174,7 @@ __device__ __forceinline__ Totals totals(const FlashParams &p, int64_t (*red)[2]
 }
 __device__ __forceinline__ bool whole_tiles(const FlashParams &p, const Totals &all)
 {
-    return !p.all_parts && (all.tiles >= 2 * (int64_t)p.grid || all.tiles > p.most_tiles);
+    return !p.all_parts && (all.tiles >= 2 * (int64_t)p.grid || all.tiles > p.most_tiles || all.cost <= all.tiles * kLeastChunk);
 }
 // Cost of a block's run.
 __device__ __forceinline__ int64_t run_of(const FlashParams &p, const Totals &all)
@@ -318,21 +319,14 @@ template <bool BF16> __device__ __forceinline__ float2 unpack16(uint32_t u)
     if constexpr (BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     else return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
-// Whether either half of a word of two 16-bit values is not finite.
-template <bool BF16> __device__ __forceinline__ bool odd2(uint32_t u)
-{
-    constexpr uint32_t e = BF16 ? 0x7f80u : 0x7c00u;
-    return (u & e) == e || (u & (e << 16)) == (e << 16);
-}
-
 // Waits on the kernel's barriers that ran out on this device (each instance's unit has its own).
 static __device__ unsigned g_wait_timeouts;
 
 // ------------------------------------------------------------------ shapes
 
 template <int D> struct Shared {                               // beside queries and ring
-    uint64_t full[8], empty[8], landed[kCopyWarps];
-    uint64_t q_full[2], q_free[2], s_full[2][2], p_full[2], o_full[2], o_free, drain;
+    uint64_t full[8], empty[8], landed[8];
+    uint64_t q_full[2], q_over[2], s_full[2][2], p_full[2], o_full[2], o_free, drain;
     uint64_t item_full[kItems], item_empty[kItems];
     Item item[kItems];
     int64_t red[kThreads / 32][2];
@@ -351,16 +345,21 @@ template <int D, int PARTS> struct Shape {
     static constexpr int kStage = kKeys * kCols * 2;
     static constexpr int kQTile = 128 * D * 2;                 // a row tile's queries, a part
     static constexpr int kQBytes = kTiles * PARTS * kQTile;
-    static constexpr int kRoom = 224 * 1024 - kQBytes;
+    // The softmax warps' room for 32 rows x 64 columns of output each, where a ring of four stages is left beside it; else
+    // they use their queries' place.
+    static constexpr int kOutWarp = 32 * 128;
+    static constexpr bool kOutRoom = kTiles == 2 && 224 * 1024 - kQBytes - 8 * kOutWarp >= 6 * kStage;
+    static constexpr int kOutBytes = kOutRoom ? 8 * kOutWarp : 0;
+    static constexpr int kRoom = 224 * 1024 - kQBytes - kOutBytes;
     static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
     static_assert(kStages >= 3, "K of a block and V of the one before, in part");
     // Warps that fill the ring, in turn.  A warp that passes on from fill f knows that f - kStages is released; its next fill
     // waits for f + kFillers - kStages, whose barrier tells that phase from the one before it only if f + kFillers - 2 kStages is.
     static constexpr int kFillers = kStages < kCopyWarps ? kStages : kCopyWarps;
     static_assert(kFillers <= kStages, "phases of a stage's barrier");
-    static constexpr int kSmem = kQBytes + kStages * kStage + (int)sizeof(Shared<D>);
+    static constexpr int kSmem = kQBytes + kOutBytes + kStages * kStage + (int)sizeof(Shared<D>);
     static_assert(kSmem <= 227 * 1024, "a block's shared memory");
-    static constexpr int64_t kPart = (int64_t)kRows * (D + 2); // floats of a partial result: rows of O, then m and l of each
+    static constexpr int64_t kPart = (int64_t)kRows * (D + 2); // floats of a partial result: O by fours of columns, row after row, then m and l of each row
 };
 
 // A bounded wait; false (and from then on everywhere in the block) where the bound runs out.
@@ -397,30 +396,99 @@ __device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity)
     }
 }
 
+// ------------------------------------------------------------------ values that some rows do not see
+
+// A stage of V's block in shared memory, columns from col0 on, taken over by a warp.  Its first `keys` keys are real; every row of the
+// tile sees those before `clear` (counted from the block's first).  Keys past the end become zeros; values from `clear` on that are
+// not finite do too, and which rows see them is noted: those `rel` or more tokens behind the tile's first.
+template <int D, bool BF16, int COLS>
+__device__ __forceinline__ void sanitize(Shared<D> &sh, int slot, uint32_t stage, int keys, int clear, int col0, int lane)
+{
+    constexpr int kPieces = COLS / 8;
+    const int from = max(clear, 0);
+    // x * 0 + .. is a NaN from the first value on that is not finite: four instructions for eight values
+    uint32_t odd = 0;
+    auto add = [&](uint32_t x) {
+        if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(x), "r"(0u));
+        else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(x), "r"(0u));
+    };
+#pragma unroll 8
+    for (int i = from * kPieces + lane; i < keys * kPieces; i += 32) {
+        uint32_t u[4];
+        lds16(u, stage + piece_at(i / kPieces, i % kPieces));
+        add(u[0]); add(u[1]); add(u[2]); add(u[3]);
+    }
+#pragma unroll 4
+    for (int i = keys * kPieces + lane; i < kKeys * kPieces; i += 32) sts16(stage + piece_at(i / kPieces, i % kPieces), 0u, 0u, 0u, 0u);
+    if (!__any_sync(kFull, (odd & 0x7fff7fffu) != 0)) return;
+#pragma unroll 1
+    for (int i = from * kPieces + lane; i < keys * kPieces; i += 32) {
+        const int row = i / kPieces, rel = min(row - clear + 1, 0xfffe);
+        const uint32_t piece = stage + piece_at(row, i % kPieces);
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+            constexpr uint32_t x = BF16 ? 0x7f80u : 0x7c00u;
+            uint32_t half;
+            asm volatile("{\n\t.reg .b16 h;\n\tld.shared.b16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(half) : "r"(piece + 2 * e) : "memory");
+            if ((half & x) != x) continue;
+            asm volatile("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tst.shared.b16 [%0], h;\n\t}" ::"r"(piece + 2 * e), "r"(0u) : "memory");
+            const int col = col0 + 8 * (i % kPieces) + e;
+            uint32_t *at = &sh.poison[slot][col >> 1];
+            const unsigned shift = (col & 1) * 16;
+            uint32_t old = *reinterpret_cast<volatile uint32_t *>(at);
+            while (((old >> shift) & 0xffffu) > (uint32_t)rel) {
+                const uint32_t got = atomicCAS(at, old, (old & ~(0xffffu << shift)) | ((uint32_t)rel << shift));
+                if (got == old) break;
+                old = got;
+            }
+            *(volatile int *)&sh.poisoned[slot] = 1;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ softmax warps
 
 // Queries of a warp's 32 rows into shared memory, eight elements a lane, in PARTS 16-bit parts; returns what
 // the scores of this lane's row are to be multiplied by (fp16 products of a type with a wider range: the row's largest
 // element is brought to 2^14 .. 2^15).
+template <int D, bool BF16, int PARTS> __device__ __forceinline__ bool as_they_lie(const FlashParams &p)
+{
+    return PARTS == 1 && p.q_vec && p.dtype == (BF16 ? GDNA_BF16 : GDNA_F16);
+}
 template <int D, bool BF16, int PARTS>
 __device__ __forceinline__ float load_queries(const FlashParams &p, const Item &it, int rows, int row0, uint32_t q_smem, int lane)
 {
     using S = Shape<D, PARTS>;
     constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPasses = 32 / kPer;     // lanes of a row, rows of a pass
-    constexpr int kGo = kPasses < 16 ? kPasses : 16;           // passes asked for at once
+    constexpr int kGo = 4;                                     // passes asked for at once
     const int col = (lane % kLanes) * 8;
     const bool scaled = !BF16 && p.dtype != GDNA_F16;
     float mine = 1.f;
+    // lane l has the place of the warp's row l
+    const int t_mine = (int)p.group_div.quotient((unsigned)(row0 + lane));
+    const int64_t place = (it.row0 + it.token0 + t_mine) * p.q_stride + ((int64_t)it.head * p.group + (row0 + lane - t_mine * p.group)) * p.d;
+    // queries of the products' type go as they lie, and are on their way on return
+    if (as_they_lie<D, BF16, PARTS>(p)) {
+#pragma unroll 4
+        for (int pass = 0; pass < kPasses; ++pass) {
+            const int in_warp = pass * kPer + lane / kLanes;
+            const int64_t from = __shfl_sync(kFull, place, in_warp) + col;
+            const bool in = row0 + in_warp < rows && col < p.d;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                         ::"r"(q_smem + piece_at((row0 & 127) + in_warp, lane % kLanes)),
+                           "l"(static_cast<const uint16_t *>(p.q) + (in ? from : 0)), "r"(in ? 16 : 0) : "memory");
+        }
+        return mine;
+    }
 #pragma unroll 1
     for (int pass = 0; pass < kPasses; pass += kGo) {
         uint4 raw[kGo][2];
 #pragma unroll
         for (int k = 0; k < kGo; ++k) {
-            const int r = row0 + (pass + k) * kPer + lane / kLanes;
+            const int in_warp = (pass + k) * kPer + lane / kLanes;
+            const int64_t from = __shfl_sync(kFull, place, in_warp) + col;
             raw[k][0] = raw[k][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (r >= rows || col >= p.d) continue;
-            const int t = (int)p.group_div.quotient((unsigned)r);
-            const int64_t from = (it.row0 + it.token0 + t) * p.q_stride + ((int64_t)it.head * p.group + (r - t * p.group)) * p.d + col;
+            if (row0 + in_warp >= rows || col >= p.d) continue;
             if (p.q_vec) {
                 if (p.dtype == GDNA_F32) {
                     const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const float *>(p.q) + from);
@@ -489,57 +557,36 @@ __device__ __forceinline__ float load_queries(const FlashParams &p, const Item &
     return mine;
 }
 
+// 1 / (1 + e^-x): both steps to two units in the last place, far below a 16-bit output's rounding.
+__device__ __forceinline__ float sigmoid(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + ex2(x * -1.4426950408889634f)));
+    return y;
+}
 __device__ __forceinline__ void fma2(float &a, float &b, float s, float c)        // a = a s + c, b = b s + c
 {
     asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
         "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(a), "+f"(b) : "f"(s), "f"(c));
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// 16 columns of this thread's lane.
+__device__ __forceinline__ void st16(uint32_t at, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                   "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
 __device__ __forceinline__ void add2(float &a, float &b, float c, float d)        // a += c, b += d
 {
     asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
         "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}" : "+f"(a), "+f"(b) : "f"(c), "f"(d));
 }
-
-// The output gates of 32 columns of a row: 16 bytes at a time where they are 16-bit elements that lie so, else when they are
-// applied.
-struct Gates {
-    uint4 raw[4];
-    __device__ __forceinline__ void ask(const FlashParams &p, int64_t row, int x, bool wanted)
-    {
-        if (!wanted || !p.gate_vec || p.dtype == GDNA_F32) return;
-        const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.gate) + row + x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (x + 8 * i < p.d) raw[i] = at[i];
-    }
-    __device__ __forceinline__ void apply(const FlashParams &p, int64_t row, int x, float (&o)[32]) const
-    {
-        const bool here = p.gate_vec && p.dtype != GDNA_F32;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (x + 8 * i >= p.d) break;
-            float g[8];
-            if (here) {
-                const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = p.dtype == GDNA_BF16 ? unpack16<true>(u[k]) : unpack16<false>(u[k]);
-                    g[2 * k] = f.x;
-                    g[2 * k + 1] = f.y;
-                }
-            } else if (p.gate_vec) {
-                const float4 *at = reinterpret_cast<const float4 *>(static_cast<const float *>(p.gate) + row + x + 8 * i);
-                const float4 a = at[0], b = at[1];
-                g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w; g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) g[k] = x + 8 * i + k < p.d ? gdna::load_elem(p.gate, row + x + 8 * i + k, p.dtype) : 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) o[8 * i + k] = __fdividef(o[8 * i + k], 1.f + __expf(-g[k]));
-        }
-    }
-};
 
 // ------------------------------------------------------------------ the kernel
 
@@ -550,33 +597,34 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
 {
     using S = Shape<D, PARTS>;
     constexpr int TILES = S::kTiles;
-    // how far P may exceed 1 before O is rescaled (log2), and what fp16 weights are lifted by (log2): 2^(11 + 4) fits fp16
-    constexpr float kSlack = BF16 ? 8.f : 4.f, kLift = BF16 ? 0.f : 11.f;
+    // how far P may exceed 1 before O is rescaled (log2), and what fp16 weights are lifted by (log2): 2^(8 + 7) fits fp16.
+    // (Slack 4 and lift 11: some row of 32 grew that far every few blocks, and a packed batch took 2070 us instead of 1735.)
+    constexpr float kSlack = 8.f, kLift = BF16 ? 0.f : 7.f;
     extern __shared__ __align__(1024) uint8_t raw[];
     const uint32_t base = smem_addr(raw);
-    const uint32_t q_smem = base, ring = base + S::kQBytes;
-    Shared<D> &sh = *reinterpret_cast<Shared<D> *>(raw + S::kQBytes + S::kStages * S::kStage);
+    const uint32_t q_smem = base, out_smem = base + S::kQBytes, ring = out_smem + S::kOutBytes;
+    Shared<D> &sh = *reinterpret_cast<Shared<D> *>(raw + S::kQBytes + S::kOutBytes + S::kStages * S::kStage);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             tc::mbar_init(&sh.full[i], 1);
-            tc::mbar_init(&sh.empty[i], 1);
+            tc::mbar_init(&sh.empty[i], TILES);
+            tc::mbar_init(&sh.landed[i], 1);
         }
-        for (int i = 0; i < kCopyWarps; ++i) tc::mbar_init(&sh.landed[i], 1);
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sh.q_full[i], 4);
-            tc::mbar_init(&sh.q_free[i], 1);
+            tc::mbar_init(&sh.q_over[i], 4);
             tc::mbar_init(&sh.s_full[i][0], 1);
             tc::mbar_init(&sh.s_full[i][1], 1);
             tc::mbar_init(&sh.p_full[i], 4);
             tc::mbar_init(&sh.o_full[i], 1);
         }
         tc::mbar_init(&sh.o_free, 4);
-        tc::mbar_init(&sh.drain, 1);
+        tc::mbar_init(&sh.drain, TILES);
         for (int i = 0; i < kItems; ++i) {
             tc::mbar_init(&sh.item_full[i], 1);
-            tc::mbar_init(&sh.item_empty[i], 1 + kCopyWarps + 8);
+            tc::mbar_init(&sh.item_empty[i], TILES + 1 + kCopyWarps + 8);
         }
         sh.dead = (base & 1023u) != 0;                 // (dynamic shared memory starts where the swizzle can)
         if (sh.dead) atomicAdd(&g_wait_timeouts, 1u);
@@ -596,21 +644,25 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
         return min(p.tile_tokens, it.n - it.token0) * p.group;
     };
 
+    // keys that a tile's first token sees: a value from there on may be out of some row's sight
+    auto clear_of = [&](const Item &it) { return p.causal ? it.kv - it.n + it.token0 + 1 : it.kv; };
+
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---------------------------------------------------------------- softmax and output: a thread a row
         const int wg = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         uint32_t items = 0, blocks_all = 0, s_count[2] = {0, 0}, o_count = 0;
-        // this warp's queries of an item into shared memory
-        auto queries = [&](const Item &it) {
-            const int rows = rows_in(it);
-            const float x = load_queries<D, BF16, PARTS>(p, it, rows, (TILES == 2 ? wg * 128 : 0) + quarter * 32,
-                                                         q_smem + (TILES == 2 ? wg * PARTS * S::kQTile : 0), lane);
+        // this warp's queries of an item on their way into shared memory, and the products told once they are there
+        auto ask_queries = [&](const Item &it) {
+            return load_queries<D, BF16, PARTS>(p, it, rows_in(it), (TILES == 2 ? wg * 128 : 0) + quarter * 32,
+                                                q_smem + (TILES == 2 ? wg * PARTS * S::kQTile : 0), lane);
+        };
+        auto tell_queries = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
             tc::fence_smem_async();
             __syncwarp();
             if (lane == 0) arrive(&sh.q_full[wg]);
-            return x;
         };
         float ahead = 0.f;                             // the next item's queries are in already, with this scale
         for (;; ++items) {
@@ -631,11 +683,15 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             const bool real = r < rows;
             int limit = p.causal ? it.kv - it.n + it.token0 + t + 1 : it.kv;       // keys that the row sees
             if (!real || limit < 0) limit = 0;
-            float m = kNegInf, l0 = 0.f, l1 = 0.f, scale = p.scale2;
+            float m = kNegInf, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f, scale = p.scale2;
             // (every phase of a barrier is waited for, in order: one that was skipped would be taken for the one after it)
-            if (TILES == 1 && items > 0 && !wait_warp(&sh.q_free[(items - 1) & 1], ((items - 1) >> 1) & 1)) break;
+            if (TILES == 1 && items > 0 && !wait_warp(&sh.q_over[(items - 1) & 1], ((items - 1) >> 1) & 1)) break;
             if (blocks > 0) {
-                scale *= ahead != 0.f ? ahead : queries(it);
+                if (ahead == 0.f) {
+                    ahead = ask_queries(it);
+                    tell_queries();
+                }
+                scale *= ahead;
                 ahead = 0.f;
             }
             bool ok = true;
@@ -645,67 +701,88 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 ok = wait_warp(&sh.s_full[wg][b], s_count[b]++ & 1);
                 if (!ok) break;
                 tc::fence_after_sync();
-                float s[4][32];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) tc::tmem_ld32(s_col(col) + lanes + 32 * x, s[x]);
-                tc::ld_wait();
+                const uint32_t s_at = s_col(col) + lanes;
                 const int seen = limit - (it.first + j) * kKeys;
-                if (__any_sync(kFull, seen < kKeys)) {
+                const bool masked = __any_sync(kFull, seen < kKeys);
+                float s[4][32];
+                auto scores = [&]() {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int x = 0; x < 4; ++x) tc::tmem_ld32(s_at + 32 * x, s[x]);
+                    tc::ld_wait();
+                    if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * x + i >= seen) s[x][i] = kNegInf;
-                }
-                float top[4] = {m, kNegInf, kNegInf, kNegInf};
+                        for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * x + i >= seen) s[x][i] = kNegInf;
+                    }
+                };
+                auto largest = [&](int x, float top) { // of 32 columns, and top
+                    float a = max3(top, s[x][0], s[x][1]), b = max3(s[x][2], s[x][3], s[x][4]);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) top[x] = fmaxf(top[x], fmaxf(s[x][i], s[x][i + 1]));
-                const float m_new = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    for (int i = 5; i < 29; i += 4) { a = max3(a, s[x][i], s[x][i + 1]); b = max3(b, s[x][i + 2], s[x][i + 3]); }
+                    return max3(max3(a, s[x][29], s[x][30]), b, s[x][31]);
+                };
+                // The weights by the maximum so far, with the block's maximum beside them: only where that is more than kSlack
+                // above (in the first blocks, as a rule) they are taken again.
                 bool behind = TILES == 1 && j > 0;     // the last block's products are still to be waited for
-                if (__any_sync(kFull, (m_new - m) * scale > kSlack)) {
-                    const float f = m_new == m ? 1.f : ex2((m - m_new) * scale);
+                uint32_t u[4][16];
+                float t0, t1, t2, t3;
+                for (bool fresh = j == 0;; fresh = false) {
+                    scores();
+                    if (fresh) {
+                        float top[2] = {kNegInf, kNegInf};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) top[x & 1] = largest(x, top[x & 1]);
+                        m = fmaxf(top[0], top[1]);
+                    }
+                    const float from = m == kNegInf ? 0.f : kLift - m * scale;
+                    float top[2] = {m, kNegInf};
+                    t0 = t1 = t2 = t3 = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        top[x & 1] = largest(x, top[x & 1]);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) fma2(s[x][i], s[x][i + 1], scale, from);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float a = ex2(s[x][i]), c = ex2(s[x][i + 1]);
+                            u[x][i / 2] = pack16<BF16>(a, c);
+                            if (i & 2) add2(t2, t3, a, c);
+                            else add2(t0, t1, a, c);
+                        }
+                    }
+                    const float m_new = fmaxf(top[0], top[1]);
+                    if (!__any_sync(kFull, (m_new - m) * scale > kSlack)) break;
+                    const float f = ex2((m - m_new) * scale);
                     if (j > 0) {
                         // (two row tiles: the scores were asked for after the last block's products, so those are done)
-                        if (TILES == 1) {
+                        if (behind) {
                             ok = wait_warp(&sh.o_full[wg], (o_count + j - 1) & 1);
                             if (!ok) break;
                             tc::fence_after_sync();
                             behind = false;
                         }
+                        const float keep = m_new == m ? 1.f : f;
 #pragma unroll 1
                         for (int x = 0; x < D; x += 32) {
                             float o[32];
                             tc::tmem_ld32(o_col(TILES == 2 ? wg : 0) + lanes + x, o);
                             tc::ld_wait();
-                            uint32_t u[32];
+                            uint32_t v[32];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
-                            tc::tmem_st32(o_col(TILES == 2 ? wg : 0) + lanes + x, u);
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(o[i] * keep);
+                            tc::tmem_st32(o_col(TILES == 2 ? wg : 0) + lanes + x, v);
                         }
+                        l0 *= keep; l1 *= keep; l2 *= keep; l3 *= keep;
                     }
-                    l0 *= f;
-                    l1 *= f;
                     m = m_new;
                 }
-                const float from = m == kNegInf ? 0.f : kLift - m * scale;
+                if (!ok) break;
 #pragma unroll
-                for (int x = 0; x < 4; x += 2) {
-                    uint32_t u[32];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            float a = s[x + y][i], c = s[x + y][i + 1];
-                            fma2(a, c, scale, from);
-                            a = ex2(a);
-                            c = ex2(c);
-                            add2(l0, l1, a, c);
-                            u[16 * y + i / 2] = pack16<BF16>(a, c);
-                        }
-                    tc::tmem_st32(s_col(col) + lanes + 16 * x, u);
-                }
+                for (int x = 0; x < 4; ++x) st16(s_at + 16 * x, u[x]);
+                add2(l0, l1, t0, t1);
+                add2(l2, l3, t2, t3);
                 tc::st_wait();
                 if (behind) ok = wait_warp(&sh.o_full[wg], (o_count + j - 1) & 1);
                 if (!ok) break;
@@ -714,86 +791,165 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 if (lane == 0) arrive(&sh.p_full[col]);
             }
             if (!ok) break;
-            // two row tiles: the next item's queries first, so that its products run while this one's output is written (the
+            // with room for the output: the next item's queries first, so that its products run while this one's output is written (the
             // scores of the last block are here, so nothing reads the old ones any more)
-            if (TILES == 2 && blocks > 0) {
+            if (S::kOutRoom && blocks > 0) {
                 const int after = (items + 1) % kItems;
                 if (!wait_warp(&sh.item_full[after], ((items + 1) / kItems) & 1)) break;
                 const Item &then = sh.item[after];
-                if (then.valid && then.first < then.last && rows_in(then) > wg * 128) ahead = queries(then);
+                if (as_they_lie<D, BF16, PARTS>(p) && then.valid && then.first < then.last && rows_in(then) > wg * 128) ahead = ask_queries(then);
             }
-            // ---- the output
+            // ---- the output: a row's 64 columns at a time out of its thread's lane, through shared memory, where lanes then
+            // take pieces of 16 bytes that lie side by side; gates the other way
+            const bool final_rows = it.whole && !p.all_parts;
+            const uint32_t stage = S::kOutRoom ? out_smem + warp * S::kOutWarp
+                                               : q_smem + (TILES == 2 ? wg * PARTS * S::kQTile : 0) + quarter * 32 * 128;
+            constexpr int kNext = S::kOutRoom ? 0 : S::kPanelBytes;    // from one panel of columns to the next
+            const bool gated = p.gate != nullptr && final_rows, gate_pieces = gated && p.gate_vec && p.dtype != GDNA_F32;
+            // lane l has the places of the warp's row l in the output and the gates; lanes take pieces of four rows at a time
+            const int64_t token_row = it.row0 + it.token0 + t, head_row = (int64_t)it.head * p.group + (r - t * p.group);
+            const int64_t out_row = token_row * p.out_stride + head_row * p.d;
+            const int64_t gate_row = token_row * p.gate_stride + head_row * p.gate_head_stride;
+            const unsigned reals = __ballot_sync(kFull, real);
+            auto place = [&](int row) { return (uint32_t)(row * 128 + (((lane & 7) ^ (row & 7)) << 4)); };
+            auto ask_gates = [&](int c) {
+                const int col = 64 * c + 8 * (lane & 7);
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) {
+                    const int from = 4 * i + (lane >> 3);
+                    const int64_t at = __shfl_sync(kFull, gate_row, from) + col;
+                    const bool in = (reals >> from & 1) && col < p.d;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                                 ::"r"(stage + c * kNext + place(from)), "l"(static_cast<const uint16_t *>(p.gate) + (in ? at : 0)), "r"(in ? 16 : 0) : "memory");
+                }
+            };
+            // eight columns of this thread's row, scaled, gated, rounded and put into their place; `plain`: gates and output
+            // are of the products' type, which the compiler then knows
+            const bool plain = p.out_dtype == (BF16 ? GDNA_BF16 : GDNA_F16) && (!gated || (gate_pieces && p.dtype == (BF16 ? GDNA_BF16 : GDNA_F16)));
+            if (gate_pieces)
+#pragma unroll 1
+                for (int c = 0; c < (S::kOutRoom ? 1 : D / 64); ++c) ask_gates(c);
             if (blocks > 0) {
                 const uint32_t last = TILES == 2 ? o_count++ : (o_count += blocks) - 1;
                 if (!wait_warp(&sh.o_full[wg], last & 1)) break;
                 tc::fence_after_sync();
+                if (ahead != 0.f) tell_queries();
             }
-            const float l = l0 + l1;
-            const bool final_rows = it.whole && !p.all_parts;
+            const float l = (l0 + l2) + (l1 + l3);
             const float norm = final_rows ? (l == 0.f ? 0.f : p.v_scale / l) : 1.f;
             const bool poisoned = blocks > 0 && *(volatile int *)&sh.poisoned[slot];
-            const int64_t row = it.row0 + it.token0 + t;
-            const int64_t head = (int64_t)it.head * p.group + (r - t * p.group);
             float *part = p.parts + it.slot * S::kPart;
             if (!final_rows && real)
                 *reinterpret_cast<float2 *>(part + S::kRows * D + 2 * r) = make_float2(m == kNegInf ? kNegInf : m * scale, l);
-            // gates of 32 columns, asked for while the columns before them are written
-            const bool gated = p.gate != nullptr && final_rows && real;
-            const int64_t gate_row = row * p.gate_stride + head * p.gate_head_stride;
-            Gates gate, gate_next;
-            gate_next.ask(p, gate_row, 0, gated);
 #pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
-                float o[32];
-                gate = gate_next;
-                gate_next.ask(p, gate_row, x + 32, gated && x + 32 < D);
-                if (blocks > 0) {
-                    tc::tmem_ld32(o_col(TILES == 2 ? wg : 0) + lanes + x, o);
-                    tc::ld_wait();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+            for (int c = 0; c < D / 64; ++c) {
+                const uint32_t here = stage + c * kNext;
+                if (gate_pieces) {
+                    if (S::kOutRoom && c > 0) ask_gates(c);
+                    if (S::kOutRoom || c == 0) asm volatile("cp.async.wait_all;" ::: "memory");
+                    __syncwarp();
                 }
-                if (!real) continue;
-                if (poisoned) {
-                    const uint16_t *poison = reinterpret_cast<const uint16_t *>(sh.poison[slot]);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {         // (rolled up: this code runs once an item, out of a cold cache)
+                    const int x = 64 * c + 32 * half;
+                    float o[32];
+                    if (blocks > 0) {
+                        tc::tmem_ld32(o_col(TILES == 2 ? wg : 0) + lanes + x, o);
+                        tc::ld_wait();
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (limit > 0 && poison[x + i] <= (p.causal ? t : 0)) o[i] = __int_as_float(0x7fffffff);
-                }
-                if (!final_rows) {
-                    float4 *to = reinterpret_cast<float4 *>(part + (int64_t)r * D + x);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    continue;
-                }
-                if (x >= p.d) continue;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] *= norm;
-                if (gated) gate.apply(p, gate_row, x, o);
-                const int64_t to = row * p.out_stride + head * p.d + x;
-                if (p.out_vec) {
-                    uint4 *at = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + to);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t u[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float a = o[8 * i + 2 * k], b = o[8 * i + 2 * k + 1];
-                            u[k] = p.out_dtype == GDNA_BF16 ? pack16<true>(a, b) : pack16<false>(a, b);
-                        }
-                        if (x + 8 * i < p.d) at[i] = make_uint4(u[0], u[1], u[2], u[3]);
+                        for (int i = 0; i < 32; ++i) o[i] = 0.f;
                     }
-                } else {
+                    if (poisoned) {
+                        const uint16_t *poison = reinterpret_cast<const uint16_t *>(sh.poison[slot]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (x + i < p.d) gdna::store_elem(p.out, to + i, p.out_dtype, o[i]);
+                        for (int i = 0; i < 32; ++i)
+                            if (poison[x + i] <= (p.causal ? t : 0)) o[i] = __int_as_float(0x7fffffff);
+                    }
+                    if (!final_rows) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (real)
+                                *reinterpret_cast<float4 *>(part + ((int64_t)(x / 4 + i) * S::kRows + r) * 4) =
+                                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        continue;
+                    }
+                    const uint32_t at0 = here + lane * 128;
+                    if (plain) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t at = at0 + (((4 * half + i) ^ (lane & 7)) << 4);
+                            uint32_t u[4];
+                            if (gated) lds16(u, at);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float y0 = o[8 * i + 2 * e] * norm, y1 = o[8 * i + 2 * e + 1] * norm;
+                                if (gated) {
+                                    const float2 g = unpack16<BF16>(u[e]);
+                                    y0 *= sigmoid(g.x);
+                                    y1 *= sigmoid(g.y);
+                                }
+                                u[e] = pack16<BF16>(y0, y1);
+                            }
+                            sts16(at, u[0], u[1], u[2], u[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t at = at0 + (((4 * half + i) ^ (lane & 7)) << 4);
+                            float g[8];
+                            if (gate_pieces) {
+                                uint32_t u[4];
+                                lds16(u, at);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 f = p.dtype == GDNA_BF16 ? unpack16<true>(u[e]) : unpack16<false>(u[e]);
+                                    g[2 * e] = f.x;
+                                    g[2 * e + 1] = f.y;
+                                }
+                            } else if (gated) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    g[e] = real && x + 8 * i + e < p.d ? gdna::load_elem(p.gate, gate_row + x + 8 * i + e, p.dtype) : 0.f;
+                            }
+                            float y[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = o[8 * i + e] * norm * (gated ? sigmoid(g[e]) : 1.f);
+                            uint32_t u[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                u[e] = p.out_dtype == GDNA_BF16 ? pack16<true>(y[2 * e], y[2 * e + 1]) : pack16<false>(y[2 * e], y[2 * e + 1]);
+                            sts16(at, u[0], u[1], u[2], u[3]);
+                        }
+                    }
                 }
+                if (!final_rows) continue;
+                __syncwarp();
+                const int col = 64 * c + 8 * (lane & 7);
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) {
+                    const int from = 4 * i + (lane >> 3);
+                    uint16_t *at = static_cast<uint16_t *>(p.out) + (__shfl_sync(kFull, out_row, from) + col);
+                    uint32_t u[4];
+                    lds16(u, here + place(from));
+                    if (!(reals >> from & 1) || col >= p.d) continue;
+                    if (p.out_vec) {
+                        *reinterpret_cast<uint4 *>(at) = make_uint4(u[0], u[1], u[2], u[3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (col + e < p.d) at[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+                    }
+                }
+                __syncwarp();
             }
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                if (TILES == 1) arrive(&sh.o_free);
+                if (TILES == 1) {
+                    arrive(&sh.o_free);
+                    arrive(&sh.q_over[wg]);
+                }
                 arrive(&sh.item_empty[slot]);
             }
             blocks_all += blocks;
@@ -869,16 +1025,18 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 it.valid = 0;
                 put();
             }
-        } else if (warp == 8) {
-            // ------------------------------------------------------------ products
+        } else if (warp < 8 + TILES) {
+            // ------------------------------------------------------------ products: a warp for each row tile
             // The whole warp walks along, with values that are the same in all lanes (from shuffles and votes), so that
-            // descriptors stay in uniform registers; one lane issues.  (One thread by itself: 120 cycles a product.)
+            // descriptors stay in uniform registers; one lane issues.  (One thread by itself: 120 cycles a product.)  Two
+            // warps, so that one's waits pass under the other's products.
+            const int tile = warp - 8;
             constexpr uint32_t kQK = idesc16<BF16>(128, kKeys, false), kPV = idesc16<BF16>(128, S::kCols, true);
             constexpr int kSteps = S::kCols / 16;      // of a stage's columns
             const uint32_t t_base = __shfl_sync(kFull, tmem, 0), q_low = desc_low(__shfl_sync(kFull, q_smem, 0), 16);
             const uint32_t ring_k = desc_low(__shfl_sync(kFull, ring, 0), 16), ring_v = desc_low(__shfl_sync(kFull, ring, 0), S::kPanelBytes);
             const bool leader = elect();
-            uint32_t items = 0, blocks = 0, q_count = 0, p_count = 0;  // (parities of two barriers each)
+            uint32_t items = 0, blocks = 0, q_count = 0, p_count = 0;  // (parities, of two barriers where there are two S)
             // the ring's next stage, and its phase
             uint32_t next = 0, phase = 0;
             struct Stages {
@@ -900,13 +1058,15 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
 #pragma unroll
                     for (int h = 0; h < S::kHalves; ++h) tc::mma_commit(&sh.empty[x.at[h]]);
             };
-            auto qk = [&](int tile, uint32_t s, const Stages &x, uint64_t *bar) {  // S s = Q of the tile . K^T
+            const uint32_t q_tile = q_low + ((tile * PARTS * S::kQTile) >> 4), o_tile = t_base + 256 + tile * D;
+            auto qk = [&](uint32_t s, const Stages &x, uint64_t *bar) {            // S s = Q . K^T
                 const uint32_t d = t_base + 128 * s;
+                tc::fence_after_sync();
                 if (leader) {
 #pragma unroll
                     for (int i = 0; i < PARTS * S::kHalves; ++i) {
                         const int part = i / S::kHalves, h = i % S::kHalves;
-                        const uint32_t a = q_low + (((tile * PARTS + part) * S::kQTile + h * S::kStage) >> 4);
+                        const uint32_t a = q_tile + ((part * S::kQTile + h * S::kStage) >> 4);
                         const uint32_t b = ring_k + x.at[h] * (S::kStage >> 4);
 #pragma unroll
                         for (int k = 0; k < kSteps; ++k) {             // (16 columns are 32 bytes of a panel)
@@ -918,27 +1078,21 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 }
                 __syncwarp();
             };
-            auto pv = [&](int tile, uint32_t s, const Stages &x, uint32_t acc) {   // O of the tile += P . V
-                const uint32_t a = t_base + 128 * s, d = t_base + 256 + tile * D;
+            auto pv = [&](uint32_t s, const Stages &x, uint32_t acc) {             // O += P . V
+                const uint32_t a = t_base + 128 * s;
+                ok = ok && wait_warp(&sh.p_full[s], (p_count >> s) & 1);
+                p_count ^= 1u << s;
+                if (!ok) return;
+                tc::fence_after_sync();
                 if (leader)
 #pragma unroll
                     for (int h = 0; h < S::kHalves; ++h) {
                         const uint32_t b = ring_v + x.at[h] * (S::kStage >> 4);
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k)           // (16 keys are 2048 bytes)
-                            mma16_ts(d + h * S::kCols, a + 8 * k, b + k * (2048 >> 4), kPV, k > 0 ? 1u : acc);
+                            mma16_ts(o_tile + h * S::kCols, a + 8 * k, b + k * (2048 >> 4), kPV, k > 0 ? 1u : acc);
                     }
                 __syncwarp();
-            };
-            auto wait_q = [&](int i) {
-                const bool good = wait_warp(&sh.q_full[i], (q_count >> i) & 1);
-                q_count ^= 1u << i;
-                return good;
-            };
-            auto wait_p = [&](int i) {
-                const bool good = wait_warp(&sh.p_full[i], (p_count >> i) & 1);
-                p_count ^= 1u << i;
-                return good;
             };
             for (; ok; ++items) {
                 const int slot = items % kItems;
@@ -946,70 +1100,55 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 const Item *it = &sh.item[slot];
                 if (!__shfl_sync(kFull, it->valid, 0)) break;
                 const int first_block = __shfl_sync(kFull, it->first, 0), last_block = __shfl_sync(kFull, it->last, 0);
-                const bool two = TILES == 2 && __shfl_sync(kFull, rows_in(*it), 0) > 128;
+                const bool rows_here = __shfl_sync(kFull, rows_in(*it), 0) > 128 * tile;
                 const uint32_t owner = items & 1;      // of a single row tile: the softmax warps take turns
                 __syncwarp();
                 if (leader) arrive(&sh.item_empty[slot]);
-                auto s_full = [&](int tile, uint32_t block) {
-                    return TILES == 2 ? &sh.s_full[tile][0] : &sh.s_full[owner][block & 1];
-                };
-                auto s_of = [&](int tile, uint32_t block) { return TILES == 2 ? (uint32_t)tile : block & 1; };
-                if (first_block >= last_block) {
-                    if (TILES == 1) {
-                        if (leader) tc::mma_commit(&sh.q_free[owner]);
+                if (!rows_here) {                      // the other tile's keys pass by
+                    for (int j = 2 * first_block; ok && j < 2 * last_block; ++j) {
+                        const Stages x = take();
+                        if (ok && leader)
+#pragma unroll
+                            for (int h = 0; h < S::kHalves; ++h) arrive(&sh.empty[x.at[h]]);
                         __syncwarp();
-                        if (items > 0) ok = wait_warp(&sh.o_free, (items - 1) & 1);
                     }
                     continue;
                 }
-                Stages k_at = take();
-                ok = ok && wait_q(TILES == 2 ? 0 : (int)owner);
-                if (!ok) break;
-                tc::fence_after_sync();
-                qk(0, s_of(0, blocks), k_at, s_full(0, blocks));
-                if (two) {
-                    ok = wait_q(1);
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    qk(1, 1, k_at, &sh.s_full[1][0]);
+                auto s_full = [&](uint32_t block) { return TILES == 2 ? &sh.s_full[tile][0] : &sh.s_full[owner][block & 1]; };
+                auto s_of = [&](uint32_t block) { return TILES == 2 ? (uint32_t)tile : block & 1; };
+                if (first_block >= last_block) {
+                    if (TILES == 1 && items > 0) ok = wait_warp(&sh.o_free, (items - 1) & 1);
+                    continue;
                 }
+                const int q = TILES == 2 ? tile : (int)owner;
+                Stages k_at = take();
+                ok = ok && wait_warp(&sh.q_full[q], (q_count >> q) & 1);
+                q_count ^= 1u << q;
+                if (!ok) break;
+                qk(s_of(blocks), k_at, s_full(blocks));
                 release(k_at);
                 for (int j = first_block; j < last_block; ++j, ++blocks) {
                     const bool more = j + 1 < last_block;
                     const uint32_t acc = j > first_block;
                     if (more) k_at = take();
+                    if (!ok) break;
                     if constexpr (TILES == 1) {
-                        if (!ok) break;
                         if (more) {
-                            tc::fence_after_sync();
-                            qk(0, s_of(0, blocks + 1), k_at, s_full(0, blocks + 1));
+                            qk(s_of(blocks + 1), k_at, s_full(blocks + 1));
                             release(k_at);
-                        } else {
-                            if (leader) tc::mma_commit(&sh.q_free[owner]);
-                            __syncwarp();
                         }
                         if (acc == 0 && items > 0) ok = wait_warp(&sh.o_free, (items - 1) & 1);
                     }
                     const Stages v_at = take();
-                    const uint32_t s0 = s_of(0, blocks);
-                    ok = ok && wait_p(s0);
+                    pv(s_of(blocks), v_at, acc);
                     if (!ok) break;
-                    tc::fence_after_sync();
-                    pv(0, s0, v_at, acc);
                     if constexpr (TILES == 1) {
                         if (leader) tc::mma_commit(&sh.o_full[owner]);
+                    } else if (more) {
+                        qk(tile, k_at, &sh.s_full[tile][0]);
+                        release(k_at);
                     } else {
-                        if (more) qk(0, 0, k_at, &sh.s_full[0][0]);
-                        else if (leader) tc::mma_commit(&sh.o_full[0]);
-                        if (two) {
-                            ok = wait_p(1);
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            pv(1, 1, v_at, acc);
-                            if (more) qk(1, 1, k_at, &sh.s_full[1][0]);
-                            else if (leader) tc::mma_commit(&sh.o_full[1]);
-                        }
-                        if (more) release(k_at);
+                        if (leader) tc::mma_commit(&sh.o_full[tile]);
                     }
                     release(v_at);
                     __syncwarp();
@@ -1020,11 +1159,43 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             if (leader) tc::mma_commit(&sh.drain);
             wait_out(&sh.drain, 0);
             __syncwarp();
+        } else if (warp == 11) {
+            // ------------------------------------------------------------ values that some rows do not see
+            uint32_t items = 0, fills = 0, turns = 0;  // (turns: a parity for each stage)
+            for (bool ok = true; ok; ++items) {
+                const int slot = items % kItems;
+                if (!wait_warp(&sh.item_full[slot], (items / kItems) & 1)) break;
+                const Item it = sh.item[slot];
+                if (!it.valid) break;
+                for (int j = it.first; ok && j < it.last; ++j) {
+                    // (the ring's order: K of the first block, then K of the next and V of this one)
+                    fills += (j == it.first ? S::kHalves : 0) + (j + 1 < it.last ? S::kHalves : 0);
+                    const int key0 = j * kKeys, clear = clear_of(it) - key0;
+                    if (p.copy_mode == kTensorCopies && clear < kKeys)
+                        for (int h = 0; ok && h < S::kHalves; ++h) {
+                            const int st = (fills + h) % S::kStages;
+                            const uint32_t turn = (turns >> st) & 1;
+                            turns ^= 1u << st;
+                            ok = wait_warp(&sh.landed[st], turn);
+                            if (!ok) {
+                                wait_out(&sh.landed[st], turn);
+                                break;
+                            }
+                            sanitize<D, BF16, S::kCols>(sh, slot, ring + st * S::kStage, min(kKeys, it.kv - key0), clear, h * S::kCols, lane);
+                            tc::fence_smem_async();
+                            __syncwarp();
+                            if (lane == 0) arrive(&sh.full[st]);
+                        }
+                    fills += S::kHalves;
+                }
+                __syncwarp();
+                if (ok && lane == 0) arrive(&sh.item_empty[slot]);
+            }
         } else if (warp >= 12) {
             // ------------------------------------------------------------ the ring
             constexpr int kPanels = S::kCols / 64, kPieces = S::kCols / 8;
             const int me = warp - 12;
-            uint32_t items = 0, fills = 0, masked_count = 0;
+            uint32_t items = 0, fills = 0;
             int64_t flying[2] = {-1, -1};              // this warp's last tensor copies: stages' fills
 
             // Fill f: the keys of block j, columns from h * kCols on, of K or V.
@@ -1034,49 +1205,8 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 const int st = f % S::kStages;
                 const uint32_t dst = ring + st * S::kStage, phase = ((f / S::kStages) & 1) ^ 1;
                 const int key0 = j * kKeys, keys = min(kKeys, it.kv - key0);       // (at least one)
-                // the tile's first token sees this many keys: a value from there on may be out of some row's sight
-                const int clear = p.causal ? it.kv - it.n + it.token0 + 1 : it.kv;
-                const bool masked = is_v && key0 + kKeys > clear;
-                // takes what is not finite out of a piece of eight values, noting which rows see it: those `rel` or more
-                // tokens behind the first
-                auto clean = [&](uint32_t (&u)[4], int row, int piece) -> bool {
-                    if (!(odd2<BF16>(u[0]) || odd2<BF16>(u[1]) || odd2<BF16>(u[2]) || odd2<BF16>(u[3]))) return false;
-                    const int key = key0 + row, rel = key < clear ? 0 : min(key - clear + 1, 0xfffe);
-#pragma unroll 1
-                    for (int e = 0; e < 8; ++e) {
-                        constexpr uint32_t x = BF16 ? 0x7f80u : 0x7c00u;
-                        const uint32_t word = e < 2 ? u[0] : e < 4 ? u[1] : e < 6 ? u[2] : u[3];
-                        if ((word >> (16 * (e & 1)) & x) != x) continue;
-                        const uint32_t keep = e & 1 ? 0x0000ffffu : 0xffff0000u;
-                        if (e < 2) u[0] &= keep; else if (e < 4) u[1] &= keep; else if (e < 6) u[2] &= keep; else u[3] &= keep;
-                        const int col = h * S::kCols + 8 * piece + e;
-                        uint32_t *at = &sh.poison[slot][col >> 1];
-                        const unsigned shift = (col & 1) * 16;
-                        uint32_t old = *reinterpret_cast<volatile uint32_t *>(at);
-                        while (((old >> shift) & 0xffffu) > (uint32_t)rel) {
-                            const uint32_t got = atomicCAS(at, old, (old & ~(0xffffu << shift)) | ((uint32_t)rel << shift));
-                            if (got == old) break;
-                            old = got;
-                        }
-                        *(volatile int *)&sh.poisoned[slot] = 1;
-                    }
-                    return true;
-                };
-                // all pieces of a stage that lies in shared memory: rows past the end to zeros, the others cleaned
-                auto clean_all = [&]() {
-#pragma unroll 4
-                    for (int i = lane; i < kKeys * kPieces; i += 32) {
-                        const int row = i / kPieces, piece = i % kPieces;
-                        const uint32_t a = dst + piece_at(row, piece);
-                        if (row >= keys) {
-                            sts16(a, 0u, 0u, 0u, 0u);
-                        } else {
-                            uint32_t u[4];
-                            lds16(u, a);
-                            if (clean(u, row, piece)) sts16(a, u[0], u[1], u[2], u[3]);
-                        }
-                    }
-                };
+                const int clear = clear_of(it) - key0;
+                const bool masked = is_v && clear < kKeys;
                 auto page_of = [&](int key, int &token) -> int {       // (key < kv)
                     if (p.table == nullptr) {
                         token = (int)it.row0 + key;
@@ -1092,7 +1222,8 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     int page = 0, token = 0;
                     if (lane < count) page = page_of(key0 + lane * per, token);    // before the stage is waited for
                     if (!wait_warp(&sh.empty[st], phase)) return false;
-                    uint64_t *bar = masked ? &sh.landed[me] : &sh.full[st];
+                    // (a masked stage goes on to the warp that looks at its values)
+                    uint64_t *bar = masked ? &sh.landed[st] : &sh.full[st];
                     if (lane == 0) arrive_expect(bar, (uint32_t)(count * kPanels * per * 128));
                     __syncwarp();
                     if (lane < count)
@@ -1103,17 +1234,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     if (!masked) {
                         flying[0] = flying[1];
                         flying[1] = f;
-                        return true;
                     }
-                    const uint32_t turn = masked_count++ & 1;
-                    if (!wait_warp(&sh.landed[me], turn)) {
-                        wait_out(&sh.landed[me], turn);
-                        return false;
-                    }
-                    clean_all();
-                    tc::fence_smem_async();
-                    __syncwarp();
-                    if (lane == 0) arrive(&sh.full[st]);
                     return true;
                 }
 
@@ -1166,16 +1287,10 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                             };
                             widen(u[0], a[0], a[1]); widen(u[1], a[2], a[3]);
                             widen(u[2], b[0], b[1]); widen(u[3], b[2], b[3]);
-                            if (masked) {
-                                clean(a, row, 2 * q);
-                                clean(b, row, 2 * q + 1);
-                            }
                             __syncwarp();
                             sts16(dst + piece_at(row, 2 * q), a[0], a[1], a[2], a[3]);
                             sts16(dst + piece_at(row, 2 * q + 1), b[0], b[1], b[2], b[3]);
                         }
-                    } else if (masked) {
-                        clean_all();
                     }
                 } else {
                     // element by element: any alignment, any head size
@@ -1192,9 +1307,12 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                             uint32_t u[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) u[k] = pack16<BF16>(e[2 * k], e[2 * k + 1]);
-                            if (masked) clean(u, 32 * i + row, piece);
                             sts16(dst + piece_at(32 * i + row, piece), u[0], u[1], u[2], u[3]);
                         }
+                }
+                if (masked) {
+                    __syncwarp();
+                    sanitize<D, BF16, S::kCols>(sh, slot, dst, keys, clear, h * S::kCols, lane);
                 }
                 tc::fence_smem_async();
                 __syncwarp();

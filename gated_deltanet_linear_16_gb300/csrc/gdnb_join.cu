@@ -3,8 +3,9 @@
 //
 //     o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i        M the largest m_i, in units of log2
 //
-// and with a request's own keys (o', lse') the two are weighted by 2^(lse2 - largest).  A block is eight
-// rows of a tile, a warp a row; all it reads has just been written, most of it is in the L2.
+// and with a request's own keys (o', lse') the two are weighted by 2^(lse2 - largest).  A block is 32 rows of a
+// tile: a lane a row, a warp every eighth four of columns, as the partial results lie; through shared memory the
+// output's lanes take pieces that lie side by side.  All it reads has just been written, most of it is in the L2.
 #include "gdnb_flash.cuh"
 
 namespace gdnb {
@@ -18,7 +19,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts(const FlashParams 
 {
     constexpr int kRows = D <= 128 ? 256 : 128;
     constexpr int64_t kPart = (int64_t)kRows * (D + 2);
-    constexpr int kQuads = D / 4, kEach = (kQuads + 31) / 32;  // groups of four columns, of a lane
+    constexpr int kMine = D / 4 / kJoinWarps;                  // a warp's fours of columns
+    __shared__ __align__(16) float sums[32][D + 4];
+    __shared__ float own_weight[32];
     __shared__ int64_t red[kJoinWarps][2];
     __shared__ int64_t first_slot;
     __shared__ Item item;
@@ -58,54 +61,61 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts(const FlashParams 
         const int n = parts;
         if (n == 0) continue;
         const int rows = min(p.tile_tokens, item.n - item.token0) * p.group;
-        for (int r = blockIdx.y * kJoinWarps + warp; r < rows; r += gridDim.y * kJoinWarps) {
+        for (int r0 = blockIdx.y * 32; r0 < rows; r0 += gridDim.y * 32) {
+            const int r = r0 + lane;
+            const bool real = r < rows;
             auto part = [&](int i) { return p.parts + (first_slot + i) * kPart; };
             auto ml = [&](int i) { return *reinterpret_cast<const float2 *>(part(i) + kRows * D + 2 * r); };
+            // every warp has all rows' maxima and sums for itself
             float top = kNegInf;
-            for (int i = lane; i < n; i += 32)
-                if (has[i]) top = fmaxf(top, ml(i).x);
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+            if (real)
+                for (int i = 0; i < n; ++i)
+                    if (has[i]) top = fmaxf(top, ml(i).x);
             const float from = top == kNegInf ? 0.f : top;
             float l = 0.f;
-            float4 o[kEach];
+            float4 o[kMine];
 #pragma unroll
-            for (int k = 0; k < kEach; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int i = 0; i < n; ++i) {
-                if (!has[i]) continue;
-                const float2 x = ml(i);
-                const float w = ex2(x.x - from);
-                l = fmaf(w, x.y, l);
+            for (int k = 0; k < kMine; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (real)
+#pragma unroll 2
+                for (int i = 0; i < n; ++i) {
+                    if (!has[i]) continue;
+                    const float2 x = ml(i);
+                    const float w = ex2(x.x - from);
+                    l = fmaf(w, x.y, l);
 #pragma unroll
-                for (int k = 0; k < kEach; ++k) {
-                    if (lane + 32 * k >= kQuads) continue;
-                    const float4 u = reinterpret_cast<const float4 *>(part(i) + (int64_t)r * D)[lane + 32 * k];
-                    o[k].x = fmaf(w, u.x, o[k].x); o[k].y = fmaf(w, u.y, o[k].y);
-                    o[k].z = fmaf(w, u.z, o[k].z); o[k].w = fmaf(w, u.w, o[k].w);
+                    for (int k = 0; k < kMine; ++k) {
+                        const float4 u = *reinterpret_cast<const float4 *>(part(i) + ((int64_t)(warp + kJoinWarps * k) * kRows + r) * 4);
+                        o[k].x = fmaf(w, u.x, o[k].x); o[k].y = fmaf(w, u.y, o[k].y);
+                        o[k].z = fmaf(w, u.z, o[k].z); o[k].w = fmaf(w, u.w, o[k].w);
+                    }
                 }
-            }
             const int t = r / p.group;
-            const int64_t row = item.row0 + item.token0 + t, head = (int64_t)item.head * p.group + (r - t * p.group);
             float norm = l == 0.f ? 0.f : p.v_scale / l, w_own = 0.f;
-            if (p.own != nullptr) {
-                const float mine = l == 0.f ? kNegInf : top + log2f(l) - (LIFTED ? 11.f : 0.f);
-                const float other = p.own_lse[row * p.nq + head] * 1.4426950408889634f;
+            if (p.own != nullptr && real) {
+                const float mine = l == 0.f ? kNegInf : top + log2f(l) - (LIFTED ? 7.f : 0.f);
+                const float other = p.own_lse[(item.row0 + item.token0 + t) * p.nq + (int64_t)item.head * p.group + (r - t * p.group)] * 1.4426950408889634f;
                 const float big = fmaxf(mine, other), w = big == kNegInf ? 0.f : ex2(mine - big);
                 w_own = big == kNegInf ? 0.f : ex2(other - big);
                 const float sum = w + w_own;
                 norm = sum == 0.f ? 0.f : norm * (w / sum);
                 w_own = sum == 0.f ? 0.f : w_own / sum;
             }
+            if (warp == 0) own_weight[lane] = w_own;
 #pragma unroll
-            for (int k = 0; k < kEach; ++k) {
-                const int col = 4 * (lane + 32 * k);
-                if (col >= p.d) continue;
-                float a[4] = {o[k].x * norm, o[k].y * norm, o[k].z * norm, o[k].w * norm};
-                const int64_t to = row * p.out_stride + head * p.d + col;
+            for (int k = 0; k < kMine; ++k)
+                *reinterpret_cast<float4 *>(&sums[lane][4 * (warp + kJoinWarps * k)]) =
+                    make_float4(o[k].x * norm, o[k].y * norm, o[k].z * norm, o[k].w * norm);
+            __syncthreads();
+            for (int x = tid; x < 32 * (D / 4); x += 32 * kJoinWarps) {
+                const int row_in = x / (D / 4), col = 4 * (x % (D / 4)), rr = r0 + row_in;
+                if (rr >= rows || col >= p.d) continue;
+                const int tt = rr / p.group;
+                const int64_t row = item.row0 + item.token0 + tt, head = (int64_t)item.head * p.group + (rr - tt * p.group);
+                const float4 y = *reinterpret_cast<const float4 *>(&sums[row_in][col]);
+                float a[4] = {y.x, y.y, y.z, y.w}, g[4] = {0.f, 0.f, 0.f, 0.f};
                 const int64_t g_at = row * p.gate_stride + head * p.gate_head_stride + col;
                 const int64_t own_at = (row * p.nq + head) * p.d + col;
-                float g[4] = {0.f, 0.f, 0.f, 0.f};
                 if (p.gate != nullptr) {
                     if (p.gate_vec) {
                         const float4 u = gdna::got4(gdna::ask4(p.gate, g_at, p.dtype, true), p.dtype, true);
@@ -115,11 +125,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts(const FlashParams 
                         for (int e = 0; e < 4; ++e) g[e] = col + e < p.d ? gdna::load_elem(p.gate, g_at + e, p.dtype) : 0.f;
                     }
                 }
+                const float w = p.own != nullptr ? own_weight[row_in] : 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if (p.own != nullptr && w_own != 0.f && col + e < p.d) a[e] = fmaf(w_own, p.own[own_at + e], a[e]);
+                    if (w != 0.f && col + e < p.d) a[e] = fmaf(w, p.own[own_at + e], a[e]);
                     if (p.gate != nullptr) a[e] = a[e] / (1.f + expf(-g[e]));
                 }
+                const int64_t to = row * p.out_stride + head * p.d + col;
                 if (p.out_vec) {
                     gdna::store4(p.out, to, p.out_dtype, true, make_float4(a[0], a[1], a[2], a[3]));
                 } else {
@@ -128,14 +140,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts(const FlashParams 
                         if (col + e < p.d) gdna::store_elem(p.out, to + e, p.out_dtype, a[e]);
                 }
             }
+            __syncthreads();
         }
     }
 }
 
 template <int D> cudaError_t launch_join(const FlashParams &p, unsigned tiles, cudaStream_t s)
 {
-    // eight rows a block at once; a split tile's rows over as many blocks
-    const dim3 grid(tiles, (unsigned)((p.tile_rows < (D <= 128 ? 256 : 128) ? p.tile_rows : (D <= 128 ? 256 : 128)) + kJoinWarps - 1) / kJoinWarps);
+    // 32 rows a block at once; a split tile's rows over as many blocks
+    const dim3 grid(tiles, (unsigned)((p.tile_rows < (D <= 128 ? 256 : 128) ? p.tile_rows : (D <= 128 ? 256 : 128)) + 31) / 32);
     if (p.cache_dtype == GDNA_BF16) join_parts<D, false><<<grid, 32 * kJoinWarps, 0, s>>>(p);
     else join_parts<D, true><<<grid, 32 * kJoinWarps, 0, s>>>(p);
     return cudaGetLastError();

@@ -103,7 +103,7 @@ GDN_API int64_t gdnb_attn_prompt_workspace(int64_t rows, int batch, int nq, int 
  *   queries in one part where that type holds theirs, else in two (an F32 query
  *   keeps 16 bits over a BF16 cache, 22 over the others), and the weights in one
  *   part: to 2^-8 of themselves over a BF16 cache; over the others to 2^-11 of
- *   themselves or 2^-36 of the row's largest, whichever is more.
+ *   themselves or 2^-32 of the row's largest, whichever is more.
  *   A value or key that is not finite shows (as NaN or infinity) in the rows that see
  *   it, and in no other.  Results do not depend on timing.
  *   Caches (bases and strides) on 16-byte boundaries with pages of a multiple of 8
