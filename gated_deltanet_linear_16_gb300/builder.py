@@ -31,7 +31,8 @@ SOURCES = ["gdn_abi.cu", "gdn_decode.cu", "gdn_chunk2.cu", "gdn_conv_norm.cu", "
            "gdn_noalloc.cu", "gdn_norm.cu", "gdn_prefill_tc.cu",
            "gdna_abi.cu", "gdna_pages.cu", "gdna_rope.cu", "gdna_attn.cu",
            "gdna_attn_f16.cu", "gdna_attn_bf16.cu", "gdna_attn_e4m3.cu",
-           "gdnb_abi.cu", "gdnb_norm.cu", "gdnb_join.cu", "gdnb_flash_64.cu", "gdnb_flash_128.cu", "gdnb_flash_256.cu"]
+           "gdnb_abi.cu", "gdnb_norm.cu", "gdnb_join.cu", "gdnb_flash_64_f16.cu", "gdnb_flash_64_bf16.cu",
+           "gdnb_flash_128_f16.cu", "gdnb_flash_128_bf16.cu", "gdnb_flash_256_f16.cu", "gdnb_flash_256_bf16.cu"]
 
 
 def nvcc() -> str:

@@ -23,7 +23,8 @@ void set_paths(gdnb::FlashParams &p, int64_t page_stride, int64_t token_stride, 
     const bool pieces = p.d * e % 16 == 0 && rows_aligned(p.k, e, 16, {page_stride, token_stride, head_stride}) && aligned(p.v, 16);
     const int size = p.table != nullptr ? p.cache.page_size & -p.cache.page_size : 128;
     p.copy_keys = size < 128 ? size : 128;
-    p.copy_mode = !pieces ? gdnb::kElements : p.cache_dtype != GDNA_E4M3 && p.copy_keys >= 8 ? gdnb::kTensorCopies : gdnb::kLoads16;
+    // (32 copies a stage at most, and eight rows of a swizzle together)
+    p.copy_mode = !pieces ? gdnb::kElements : p.copy_keys >= (p.cache_dtype == GDNA_E4M3 ? 4 : 8) ? gdnb::kTensorCopies : gdnb::kPieces16;
     p.q_vec = p.d % 8 == 0 && rows_aligned(p.q, qe, 16, {p.q_stride, p.d});
     p.gate_vec = p.d % 8 == 0 && rows_aligned(p.gate, qe, 16, {p.gate_stride, p.gate_head_stride});
     p.out_vec = p.d % 8 == 0 && rows_aligned(p.out, 2, 16, {p.out_stride, p.d});
@@ -147,7 +148,7 @@ GDN_API int gdnb_attn_prompt(const void *q, gdna_dtype dtype, const void *gate,
     if (!aligned(workspace, 16)) return GDN_ERR_ALIGN;
 
     p.q = q; p.gate = gate; p.k = k_cache; p.v = v_cache; p.table = table; p.row_start = row_start; p.kv_len = kv_len;
-    p.out = out; p.parts = static_cast<float *>(workspace);
+    p.out = out; p.workspace = workspace;
     p.rows = rows; p.table_stride = table_stride; p.q_stride = q_stride; p.gate_stride = gate_stride;
     p.gate_head_stride = gate_head_stride; p.out_stride = out_stride;
     p.dtype = dtype; p.cache_dtype = cache_dtype; p.out_dtype = out_dtype;
@@ -234,7 +235,7 @@ GDN_API int gdnb_attn_shared(const void *q, gdna_dtype dtype, const void *gate,
     gdnb::FlashParams p{};
     p.cache = cache;
     p.q = q; p.gate = gate; p.k = k_cache; p.v = v_cache; p.table = shared_table; p.row_start = group_start; p.kv_len = shared_len;
-    p.out = out; p.parts = reinterpret_cast<float *>(at + space.decode + space.own + space.lse);
+    p.out = out; p.workspace = at + space.decode + space.own + space.lse;
     p.rows = rows; p.table_stride = shared_stride; p.q_stride = q_stride; p.gate_stride = gate_stride;
     p.gate_head_stride = gate_head_stride; p.out_stride = out_stride;
     p.dtype = dtype; p.cache_dtype = cache_dtype; p.out_dtype = out_dtype;

@@ -229,6 +229,15 @@ __device__ __forceinline__ Place find(const FlashParams &p, int seg, int64_t cos
     return none;
 }
 
+// Where a split tile's partial results are, for the join: a header with the number of tiles, then a record each.
+struct Record {
+    int64_t row0, first_slot;
+    int n, head, token0;
+    int parts;                             // 0: the result is final already
+};
+__device__ __forceinline__ int64_t *record_count(const FlashParams &p) { return reinterpret_cast<int64_t *>(p.records); }
+__device__ __forceinline__ Record *records(const FlashParams &p) { return reinterpret_cast<Record *>(static_cast<uint8_t *>(p.records) + 64); }
+
 // A block's piece of work: some key blocks of a tile.
 struct Item {
     int64_t row0;                          // first row of the segment
@@ -356,7 +365,11 @@ template <int D, int PARTS> struct Shape {
     // Warps that fill the ring, in turn.  A warp that passes on from fill f knows that f - kStages is released; its next fill
     // waits for f + kFillers - kStages, whose barrier tells that phase from the one before it only if f + kFillers - 2 kStages is.
     static constexpr int kFillers = kStages < kCopyWarps ? kStages : kCopyWarps;
-    static_assert(kFillers <= kStages, "phases of a stage's barrier");
+    // E4M3 codes come by tensor copies to the last panel of their stage and are widened there.  A warp asks for its next stage's
+    // before it widens this one's, so a stage's release must not wait for the one behind it: K's may (V of the block
+    // before is the next fill), hence the two less.
+    static constexpr bool kCodes = kCols == 128;
+    static constexpr int kWideners = kStages - 2 < kCopyWarps ? kStages - 2 : kCopyWarps;
     static constexpr int kSmem = kQBytes + kOutBytes + kStages * kStage + (int)sizeof(Shared<D>);
     static_assert(kSmem <= 227 * 1024, "a block's shared memory");
     static constexpr int64_t kPart = (int64_t)kRows * (D + 2); // floats of a partial result: O by fours of columns, row after row, then m and l of each row
@@ -590,7 +603,8 @@ __device__ __forceinline__ void add2(float &a, float &b, float c, float d)      
 
 // ------------------------------------------------------------------ the kernel
 
-template <int D, bool BF16, int PARTS>
+// COPY: how keys come in.  (A template argument, for the registers of the warps that fill the ring.)
+template <int D, bool BF16, int PARTS, int COPY>
 __global__ void __launch_bounds__(kThreads, 1)
 flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
            const uint32_t polls)
@@ -631,6 +645,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) tc::tmem_alloc(&sh.tmem, 512);
+    gdn::early_start<true>(nullptr, 0);                // (nothing of other kernels' is read or written before)
     const Totals all = totals(p, sh.red);              // (a barrier)
     tc::fence_before_sync();
     __syncthreads();
@@ -986,7 +1001,9 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             bool ok = true;
             it.valid = 1;
             Place at{};
-            if (whole_tiles(p, all)) {
+            const bool whole = whole_tiles(p, all);
+            if (c == 0 && lane == 0) *record_count(p) = whole ? 0 : all.tiles;
+            if (whole) {
                 for (int64_t k = 0; ok; ++k) {
                     const int64_t i = k * g + ((k & 1) ? g - 1 - c : c);
                     if (i >= all.tiles) break;         // (and so is every later turn)
@@ -1011,11 +1028,22 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     const int blocks = (int)(((int64_t)keys_of(p, at.t, tau) + kKeys - 1) / kKeys);
                     it.first = x0 > begin ? blocks_before(x0 - begin, blocks) : 0;
                     it.last = x1 < end ? blocks_before(x1 - begin, blocks) : blocks;
+                    // the block in which a tile begins tells which have a part of it
+                    const int64_t tile = at.tiles + head * at.t.count + tau;
+                    if (begin >= x0 && lane == 0) {
+                        const int64_t b = (end - 1) / run;     // the last one; an end may come before its first keys
+                        const bool mine = it.last > 0 || blocks == 0;
+                        const bool theirs = b > c && blocks_before(b * run - begin, blocks) < blocks;
+                        const int64_t first = mine ? c : c + 1, last = b > c && !theirs ? b - 1 : b;
+                        const bool one = first == last && !p.all_parts;
+                        const Segment s = segment(p, at.seg);
+                        records(p)[tile] = Record{s.row0, tile + first, s.n, head, (int)(tau * p.tile_tokens), one ? 0 : (int)(last - first + 1)};
+                    }
                     // a tile without keys is the block's in which it begins
                     if (it.first < it.last || (blocks == 0 && begin >= x0)) {
                         set(at, head, tau);
                         it.whole = it.first == 0 && it.last == blocks;
-                        it.slot = at.tiles + head * at.t.count + tau + c;
+                        it.slot = tile + c;
                         ok = put();
                     }
                     x = end;
@@ -1171,7 +1199,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     // (the ring's order: K of the first block, then K of the next and V of this one)
                     fills += (j == it.first ? S::kHalves : 0) + (j + 1 < it.last ? S::kHalves : 0);
                     const int key0 = j * kKeys, clear = clear_of(it) - key0;
-                    if (p.copy_mode == kTensorCopies && clear < kKeys)
+                    if (COPY == kTensorCopies && clear < kKeys)
                         for (int h = 0; ok && h < S::kHalves; ++h) {
                             const int st = (fills + h) % S::kStages;
                             const uint32_t turn = (turns >> st) & 1;
@@ -1198,15 +1226,68 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             uint32_t items = 0, fills = 0;
             int64_t flying[2] = {-1, -1};              // this warp's last tensor copies: stages' fills
 
+            const bool codes = COPY == kCodeCopies || (COPY == kLoads && p.cache_dtype == GDNA_E4M3);
+            constexpr bool ahead = COPY == kCodeCopies;
+            constexpr uint32_t fillers = ahead ? S::kWideners : S::kFillers;
+
+            // E4M3 codes of a stage, a row's where its last panel begins, to fp16: the lanes that read a row's write the row
+            auto widen_stage = [&](uint32_t dst) {
+                constexpr int kLanes = S::kCols / 16, kPer = 32 / kLanes, kGo = 4;
+                const int q = lane % kLanes;
+#pragma unroll 1
+                for (int row0 = lane / kLanes; row0 < kKeys; row0 += kGo * kPer) {
+                    uint32_t u[kGo][4];
+#pragma unroll
+                    for (int k = 0; k < kGo; ++k) lds16(u[k], dst + (kPanels - 1) * S::kPanelBytes + (row0 + k * kPer) * 128 + q * 16);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < kGo; ++k) {
+                        uint32_t a[4], b[4];
+                        auto widen = [](uint32_t x, uint32_t &lo, uint32_t &hi) {
+                            asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+                                "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(x));
+                        };
+                        widen(u[k][0], a[0], a[1]); widen(u[k][1], a[2], a[3]);
+                        widen(u[k][2], b[0], b[1]); widen(u[k][3], b[2], b[3]);
+                        sts16(dst + piece_at(row0 + k * kPer, 2 * q), a[0], a[1], a[2], a[3]);
+                        sts16(dst + piece_at(row0 + k * kPer, 2 * q + 1), b[0], b[1], b[2], b[3]);
+                    }
+                }
+            };
+            // a stage filled by this warp's own hand goes to the products
+            auto hand_over = [&](int slot, int st, bool masked, int keys, int clear, int h) {
+                __syncwarp();
+                if (masked) sanitize<D, BF16, S::kCols>(sh, slot, ring + st * S::kStage, keys, clear, h * S::kCols, lane);
+                tc::fence_smem_async();
+                __syncwarp();
+                if (lane == 0) arrive(&sh.full[st]);
+            };
+            // the stage whose codes are on their way
+            int w_slot = 0, w_fill = -1, w_keys = 0, w_clear = 0, w_h = 0;
+            auto widen_last = [&]() -> bool {
+                if (w_fill < 0) return true;
+                const int st = w_fill % S::kStages;
+                const uint32_t parity = (uint32_t)(w_fill / S::kStages) & 1;
+                const bool masked = w_clear < kKeys;
+                w_fill = -1;
+                if (!wait_warp(&sh.landed[st], parity)) {
+                    wait_out(&sh.landed[st], parity);
+                    return false;
+                }
+                widen_stage(ring + st * S::kStage);
+                hand_over(w_slot, st, masked, w_keys, w_clear, w_h);
+                return true;
+            };
+
             // Fill f: the keys of block j, columns from h * kCols on, of K or V.
             auto fill = [&](const Item &it, int slot, int j, int h, bool is_v) -> bool {
                 const uint32_t f = fills++;
-                if (f % S::kFillers != (uint32_t)me) return true;
+                if (f % fillers != (uint32_t)me) return true;
                 const int st = f % S::kStages;
                 const uint32_t dst = ring + st * S::kStage, phase = ((f / S::kStages) & 1) ^ 1;
                 const int key0 = j * kKeys, keys = min(kKeys, it.kv - key0);       // (at least one)
-                const int clear = clear_of(it) - key0;
-                const bool masked = is_v && clear < kKeys;
+                const int clear = is_v ? clear_of(it) - key0 : kKeys;
+                const bool masked = clear < kKeys;
                 auto page_of = [&](int key, int &token) -> int {       // (key < kv)
                     if (p.table == nullptr) {
                         token = (int)it.row0 + key;
@@ -1217,11 +1298,21 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     return p.table[(int64_t)it.seg * p.table_stride + q];
                 };
 
-                if (p.copy_mode == kTensorCopies) {
-                    const int per = p.copy_keys, count = (keys + per - 1) / per;   // keys of a copy; copies of a panel (16 at most)
+                if constexpr (COPY != kLoads) {
+                    const int per = p.copy_keys, count = (keys + per - 1) / per;   // keys of a copy; copies of a panel (32 at most)
                     int page = 0, token = 0;
                     if (lane < count) page = page_of(key0 + lane * per, token);    // before the stage is waited for
                     if (!wait_warp(&sh.empty[st], phase)) return false;
+                    if constexpr (ahead) {
+                        if (lane == 0) arrive_expect(&sh.landed[st], (uint32_t)(count * per * 128));
+                        __syncwarp();
+                        if (lane < count)
+                            copy_box(dst + (kPanels - 1) * S::kPanelBytes + lane * per * 128, is_v ? &v_map : &k_map, h * S::kCols, token, it.head,
+                                     page, &sh.landed[st]);
+                        const bool good = widen_last();
+                        w_slot = slot; w_fill = (int)f; w_keys = keys; w_clear = clear; w_h = h;
+                        return good;
+                    }
                     // (a masked stage goes on to the warp that looks at its values)
                     uint64_t *bar = masked ? &sh.landed[st] : &sh.full[st];
                     if (lane == 0) arrive_expect(bar, (uint32_t)(count * kPanels * per * 128));
@@ -1236,7 +1327,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                         flying[1] = f;
                     }
                     return true;
-                }
+                } else {
 
                 // by loads: lane l has the places of keys l, l + 32, ..
                 int64_t place[4];
@@ -1253,9 +1344,8 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 }
                 if (!wait_warp(&sh.empty[st], phase)) return false;
                 const void *from = is_v ? p.v : p.k;
-                if (p.copy_mode == kLoads16) {
+                if (p.copy_mode == kPieces16) {
                     // 16 bytes at a time, as they lie: E4M3 codes to the row's place in the last panel, to be widened there
-                    const bool codes = p.cache_dtype == GDNA_E4M3;
                     const int elem = codes ? 1 : 2, each = 16 / elem, across = S::kCols / each;    // elements, pieces of a row
                     const int shift = 31 - __clz(across);
 #pragma unroll 1
@@ -1273,25 +1363,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                         }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     __syncwarp();
-                    if (codes) {
-                        // a row's codes are read by the lanes that write the row: 16 codes a lane
-                        constexpr int kLanes = S::kCols / 16, kPer = 32 / kLanes;
-#pragma unroll 2
-                        for (int row0 = 0; row0 < kKeys; row0 += kPer) {
-                            const int row = row0 + lane / kLanes, q = lane % kLanes;
-                            uint32_t u[4], a[4], b[4];
-                            lds16(u, dst + (kPanels - 1) * S::kPanelBytes + row * 128 + q * 16);
-                            auto widen = [](uint32_t x, uint32_t &lo, uint32_t &hi) {
-                                asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-                                    "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(x));
-                            };
-                            widen(u[0], a[0], a[1]); widen(u[1], a[2], a[3]);
-                            widen(u[2], b[0], b[1]); widen(u[3], b[2], b[3]);
-                            __syncwarp();
-                            sts16(dst + piece_at(row, 2 * q), a[0], a[1], a[2], a[3]);
-                            sts16(dst + piece_at(row, 2 * q + 1), b[0], b[1], b[2], b[3]);
-                        }
-                    }
+                    if (codes) widen_stage(dst);
                 } else {
                     // element by element: any alignment, any head size
 #pragma unroll 1
@@ -1310,14 +1382,9 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                             sts16(dst + piece_at(32 * i + row, piece), u[0], u[1], u[2], u[3]);
                         }
                 }
-                if (masked) {
-                    __syncwarp();
-                    sanitize<D, BF16, S::kCols>(sh, slot, dst, keys, clear, h * S::kCols, lane);
-                }
-                tc::fence_smem_async();
-                __syncwarp();
-                if (lane == 0) arrive(&sh.full[st]);
+                hand_over(slot, st, masked, keys, clear, h);
                 return true;
+                }
             };
             for (bool ok = true; ok; ++items) {
                 const int slot = items % kItems;
@@ -1333,10 +1400,12 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     if (j + 1 < it.last) block(j + 1, false);
                     block(j, true);
                 }
+                if (ahead && ok) ok = widen_last();    // (what it notes goes by the item's slot)
                 __syncwarp();
                 if (ok && lane == 0) arrive(&sh.item_empty[slot]);
             }
             __syncwarp();
+            if (ahead && w_fill >= 0) wait_out(&sh.landed[w_fill % S::kStages], (uint32_t)(w_fill / S::kStages) & 1);
             if (*(volatile int *)&sh.dead)             // copies in flight land before their memory is another block's
                 for (int i = 0; i < 2; ++i)
                     if (flying[i] >= 0) wait_out(&sh.full[flying[i] % S::kStages], (uint32_t)(flying[i] / S::kStages) & 1);
@@ -1348,61 +1417,78 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
 
 // ------------------------------------------------------------------ launch
 
-// The map of K's or V's rows: element, token, head, page; box: 64 elements (a panel's 128 bytes) x `keys` tokens.  What
+// The map of K's or V's rows: element, token, head, page; box: 128 bytes (a panel's 64 elements, or E4M3 codes) x `copy_keys` tokens.  What
 // lies past a head, and in pages that are none, comes as zeros.  False where the encoder refuses the layout.
 inline bool rows_map(const FlashParams &p, const void *base, CUtensorMap *map)
 {
     const auto encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(gdn::tensor_map_encoder());
     if (encode == nullptr) return false;
+    const bool codes = p.cache_dtype == GDNA_E4M3;
     const cuuint64_t size[4] = {(cuuint64_t)p.d, (cuuint64_t)(p.table != nullptr ? p.cache.page_size : p.rows), (cuuint64_t)p.nkv,
                                 (cuuint64_t)(p.table != nullptr ? p.cache.pages : 1)};
     const int64_t strides[3] = {p.cache.token_stride, p.cache.head_stride, p.table != nullptr ? p.cache.page_stride : 64};
     cuuint64_t stride[3];
     for (int i = 0; i < 3; ++i) {
-        int64_t bytes = strides[i] * 2;
+        int64_t bytes = strides[i] * (codes ? 1 : 2);
         if (size[i + 1] == 1 && bytes <= 0) bytes = 16;        // (a dimension of one)
         if (bytes <= 0 || bytes >= (int64_t{1} << 40)) return false;
         stride[i] = (cuuint64_t)bytes;
     }
-    const cuuint32_t box[4] = {64, (cuuint32_t)p.copy_keys, 1, 1}, step[4] = {1, 1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), size, stride, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t box[4] = {codes ? 128u : 64u, (cuuint32_t)p.copy_keys, 1, 1}, step[4] = {1, 1, 1, 1};
+    return encode(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(base), size, stride, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF16, int PARTS, int COPY>
+cudaError_t launch_copy(const FlashParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, cudaStream_t s)
+{
+    using S = Shape<D, PARTS>;
+    const cudaError_t e = gdn::allow_dynamic_smem<&flash_rows<D, BF16, PARTS, COPY>>(S::kSmem);
+    if (e != cudaSuccess) return e;
+    return gdn::launch_early(flash_rows<D, BF16, PARTS, COPY>, dim3(p.grid), kThreads, S::kSmem, s, true, p, k_map, v_map, gdn::tc_copy_wait_polls());
 }
 
 template <int D, bool BF16, int PARTS> cudaError_t launch(FlashParams p, cudaStream_t s)
 {
-    using S = Shape<D, PARTS>;
     CUtensorMap k_map{}, v_map{};
-    if (p.copy_mode == kTensorCopies && !(rows_map(p, p.k, &k_map) && rows_map(p, p.v, &v_map))) p.copy_mode = kLoads16;
-    const cudaError_t e = gdn::allow_dynamic_smem<&flash_rows<D, BF16, PARTS>>(S::kSmem);
-    if (e != cudaSuccess) return e;
-    flash_rows<D, BF16, PARTS><<<p.grid, kThreads, S::kSmem, s>>>(p, k_map, v_map, gdn::tc_copy_wait_polls());
-    return cudaGetLastError();
+    const bool codes = p.cache_dtype == GDNA_E4M3;
+    // (heads of up to 64 codes do not fill a row of a stage: by loads)
+    if (p.copy_mode == kTensorCopies && ((codes && !Shape<D, PARTS>::kCodes) || !(rows_map(p, p.k, &k_map) && rows_map(p, p.v, &v_map))))
+        p.copy_mode = kPieces16;
+    if (p.copy_mode != kTensorCopies) return launch_copy<D, BF16, PARTS, kLoads>(p, k_map, v_map, s);
+    if constexpr (!BF16 && Shape<D, PARTS>::kCodes)
+        if (codes) return launch_copy<D, BF16, PARTS, kCodeCopies>(p, k_map, v_map, s);
+    return launch_copy<D, BF16, PARTS, kTensorCopies>(p, k_map, v_map, s);
 }
 
-// 16-bit parts of a query: one where the products' type holds its type.
-template <int D> cudaError_t launch_by_type(const FlashParams &p, cudaStream_t s)
+// 16-bit parts of a query: one where the products' type holds its type; and one for an F32 query in fp16 products where the
+// output is bf16, whose rounding hides what the 11 bits leave out (one part for two: half the first product's work, two more stages).
+template <int D, bool BF16> cudaError_t launch_by_type(const FlashParams &p, cudaStream_t s)
 {
-    const bool bf16 = p.cache_dtype == GDNA_BF16;
-    const bool one = p.dtype == GDNA_BF16 || (p.dtype == GDNA_F16 && !bf16);
-    if (bf16) return one ? launch<D, true, 1>(p, s) : launch<D, true, 2>(p, s);
-    return one ? launch<D, false, 1>(p, s) : launch<D, false, 2>(p, s);
+    const bool one = p.dtype == GDNA_BF16 || (!BF16 && (p.dtype == GDNA_F16 || p.out_dtype == GDNA_BF16));
+    return one ? launch<D, BF16, 1>(p, s) : launch<D, BF16, 2>(p, s);
 }
 
-template <int D> cudaError_t wait_timeouts(unsigned *count)
+template <int UNIT> cudaError_t wait_timeouts(unsigned *count)
 {
     return cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(unsigned));
 }
 
 }  // namespace flash
 
-// One unit each (gdnb_flash_64.cu ...).
-cudaError_t launch_flash_64(const FlashParams &p, cudaStream_t s);
-cudaError_t launch_flash_128(const FlashParams &p, cudaStream_t s);
-cudaError_t launch_flash_256(const FlashParams &p, cudaStream_t s);
-cudaError_t flash_timeouts_64(unsigned *count);
-cudaError_t flash_timeouts_128(unsigned *count);
-cudaError_t flash_timeouts_256(unsigned *count);
+// One unit each (gdnb_flash_64_f16.cu ...).
+cudaError_t launch_flash_64_f16(const FlashParams &p, cudaStream_t s);
+cudaError_t flash_timeouts_64_f16(unsigned *count);
+cudaError_t launch_flash_64_bf16(const FlashParams &p, cudaStream_t s);
+cudaError_t flash_timeouts_64_bf16(unsigned *count);
+cudaError_t launch_flash_128_f16(const FlashParams &p, cudaStream_t s);
+cudaError_t flash_timeouts_128_f16(unsigned *count);
+cudaError_t launch_flash_128_bf16(const FlashParams &p, cudaStream_t s);
+cudaError_t flash_timeouts_128_bf16(unsigned *count);
+cudaError_t launch_flash_256_f16(const FlashParams &p, cudaStream_t s);
+cudaError_t flash_timeouts_256_f16(unsigned *count);
+cudaError_t launch_flash_256_bf16(const FlashParams &p, cudaStream_t s);
+cudaError_t flash_timeouts_256_bf16(unsigned *count);
 
 }  // namespace gdnb

@@ -1,0 +1,7 @@
+// gdnb_flash_256_bf16.cu -- attention of many query rows: the instances for head sizes up to 256, bf16 products.
+#include "gdnb_flash.cuh"
+
+namespace gdnb {
+cudaError_t launch_flash_256_bf16(const FlashParams &p, cudaStream_t s) { return flash::launch_by_type<256, true>(p, s); }
+cudaError_t flash_timeouts_256_bf16(unsigned *count) { return flash::wait_timeouts<256>(count); }
+}  // namespace gdnb

@@ -19,8 +19,9 @@ struct NormParams {
     float scale, eps;
 };
 
-// How keys come into shared memory.
-enum CopyMode { kTensorCopies = 0, kLoads16 = 1, kElements = 2 };
+// How keys come into shared memory: 16-bit rows by tensor copies, E4M3 codes by tensor copies, or loads (16 bytes at a time, or
+// element by element).
+enum CopyMode { kTensorCopies = 0, kCodeCopies = 1, kLoads = 2, kPieces16 = 2, kElements = 3 };
 
 // Attention of segments: runs of query rows with one list of keys each (the sequences of a prompt
 // call; the groups of a shared prefix).
@@ -30,9 +31,11 @@ struct FlashParams {
     const int32_t *row_start;       // [segs + 1] (NULL: one segment), times row_mult
     const int32_t *kv_len;          // [segs], or NULL
     void *out;
-    float *parts;                   // partial results (Deal::slot)
+    void *records;                  // of split tiles, and their partial results: the workspace (set by the launcher)
+    float *parts;
+    void *workspace;
     int64_t rows, table_stride, q_stride, gate_stride, gate_head_stride, out_stride;
-    int64_t most_tiles;             // that segments which do not overlap can make (set by the launcher)
+    int64_t most_tiles, slots;      // that segments which do not overlap can make; partial results (set by the launcher)
     CacheLayout cache;
     int dtype, cache_dtype, out_dtype;
     int segs, row_mult, nq, nkv, group, d, max_pages;

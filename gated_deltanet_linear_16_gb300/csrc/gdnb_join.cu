@@ -13,79 +13,51 @@ namespace flash {
 namespace {
 
 constexpr int kJoinWarps = 8;
+constexpr int kJoinCols = 64;              // columns of a block
 
 template <int D, bool LIFTED>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_parts(const FlashParams p)
 {
     constexpr int kRows = D <= 128 ? 256 : 128;
     constexpr int64_t kPart = (int64_t)kRows * (D + 2);
-    constexpr int kMine = D / 4 / kJoinWarps;                  // a warp's fours of columns
-    __shared__ __align__(16) float sums[32][D + 4];
+    constexpr int kMine = kJoinCols / 4 / kJoinWarps;          // a warp's fours of columns
+    __shared__ __align__(16) float sums[32][kJoinCols + 4];
     __shared__ float own_weight[32];
-    __shared__ int64_t red[kJoinWarps][2];
-    __shared__ int64_t first_slot;
-    __shared__ Item item;
-    __shared__ int parts, has[kMaxGrid];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Totals all = totals(p, red);
-    if (whole_tiles(p, all)) return;
-    for (int64_t tile = blockIdx.x; tile < all.tiles; tile += gridDim.x) {
-        __syncthreads();
-        if (warp == 0) {
-            const Place at = find<false>(p, 0, 0, 0, tile);
-            const int64_t idx = tile - at.tiles;
-            const int head = (int)(idx / at.t.count);
-            const int64_t tau = idx - head * at.t.count;
-            const int64_t begin = at.cost + head * at.t.cost + cost_before(at.t, tau), end = begin + cost_of(p, at.t, tau);
-            const int blocks = (int)(((int64_t)keys_of(p, at.t, tau) + kKeys - 1) / kKeys);
-            const int64_t run = run_of(p, all), c0 = begin / run, c1 = (end - 1) / run;
-            int full = 0;
-            for (int c = (int)c0 + lane; c <= (int)c1; c += 32) {
-                const int b0 = c * run > begin ? blocks_before(c * run - begin, blocks) : 0;
-                const int b1 = (c + 1) * run < end ? blocks_before((c + 1) * run - begin, blocks) : blocks;
-                has[c - c0] = b0 < b1 || (blocks == 0 && c == c0);
-                full |= b0 == 0 && b1 == blocks && has[c - c0];
-            }
-            full = __any_sync(kFull, full);
-            if (lane == 0) {
-                const Segment s = segment(p, at.seg);
-                item.row0 = s.row0;
-                item.n = s.n;
-                item.head = head;
-                item.token0 = (int)(tau * p.tile_tokens);
-                first_slot = tile + c0;
-                parts = full && !p.all_parts ? 0 : (int)(c1 - c0 + 1);         // 0: the result is final
-            }
-        }
-        __syncthreads();
-        const int n = parts;
-        if (n == 0) continue;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, col0 = blockIdx.z * kJoinCols;
+    gdn::early_start<true>(nullptr, 0);
+    const int64_t tiles = *record_count(p);
+    for (int64_t tile = blockIdx.x; tile < tiles && tile < p.most_tiles; tile += gridDim.x) {
+        const Record item = records(p)[tile];
+        const int n = item.parts;
+        // (a record is whole unless its block gave up: then it may be anything)
+        if (n <= 0 || n > kMaxGrid || item.first_slot < 0 || item.first_slot + n > p.slots || item.row0 < 0 || item.n <= 0 ||
+            item.row0 + item.n > p.rows || item.token0 < 0 || item.token0 >= item.n || item.head < 0 || item.head >= p.nkv)
+            continue;
         const int rows = min(p.tile_tokens, item.n - item.token0) * p.group;
         for (int r0 = blockIdx.y * 32; r0 < rows; r0 += gridDim.y * 32) {
             const int r = r0 + lane;
             const bool real = r < rows;
-            auto part = [&](int i) { return p.parts + (first_slot + i) * kPart; };
-            auto ml = [&](int i) { return *reinterpret_cast<const float2 *>(part(i) + kRows * D + 2 * r); };
+            const float *first = p.parts + item.first_slot * kPart;
+            auto ml = [&](int i) { return *reinterpret_cast<const float2 *>(first + i * kPart + kRows * D + 2 * r); };
             // every warp has all rows' maxima and sums for itself
             float top = kNegInf;
             if (real)
-                for (int i = 0; i < n; ++i)
-                    if (has[i]) top = fmaxf(top, ml(i).x);
+#pragma unroll 8
+                for (int i = 0; i < n; ++i) top = fmaxf(top, ml(i).x);
             const float from = top == kNegInf ? 0.f : top;
             float l = 0.f;
             float4 o[kMine];
 #pragma unroll
             for (int k = 0; k < kMine; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (real)
-#pragma unroll 2
+#pragma unroll 4
                 for (int i = 0; i < n; ++i) {
-                    if (!has[i]) continue;
                     const float2 x = ml(i);
                     const float w = ex2(x.x - from);
                     l = fmaf(w, x.y, l);
 #pragma unroll
                     for (int k = 0; k < kMine; ++k) {
-                        const float4 u = *reinterpret_cast<const float4 *>(part(i) + ((int64_t)(warp + kJoinWarps * k) * kRows + r) * 4);
+                        const float4 u = *reinterpret_cast<const float4 *>(first + i * kPart + ((int64_t)(col0 / 4 + warp + kJoinWarps * k) * kRows + r) * 4);
                         o[k].x = fmaf(w, u.x, o[k].x); o[k].y = fmaf(w, u.y, o[k].y);
                         o[k].z = fmaf(w, u.z, o[k].z); o[k].w = fmaf(w, u.w, o[k].w);
                     }
@@ -107,12 +79,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts(const FlashParams 
                 *reinterpret_cast<float4 *>(&sums[lane][4 * (warp + kJoinWarps * k)]) =
                     make_float4(o[k].x * norm, o[k].y * norm, o[k].z * norm, o[k].w * norm);
             __syncthreads();
-            for (int x = tid; x < 32 * (D / 4); x += 32 * kJoinWarps) {
-                const int row_in = x / (D / 4), col = 4 * (x % (D / 4)), rr = r0 + row_in;
+            for (int x = tid; x < 32 * (kJoinCols / 4); x += 32 * kJoinWarps) {
+                const int row_in = x / (kJoinCols / 4), in_cols = 4 * (x % (kJoinCols / 4)), col = col0 + in_cols, rr = r0 + row_in;
                 if (rr >= rows || col >= p.d) continue;
                 const int tt = rr / p.group;
                 const int64_t row = item.row0 + item.token0 + tt, head = (int64_t)item.head * p.group + (rr - tt * p.group);
-                const float4 y = *reinterpret_cast<const float4 *>(&sums[row_in][col]);
+                const float4 y = *reinterpret_cast<const float4 *>(&sums[row_in][in_cols]);
                 float a[4] = {y.x, y.y, y.z, y.w}, g[4] = {0.f, 0.f, 0.f, 0.f};
                 const int64_t g_at = row * p.gate_stride + head * p.gate_head_stride + col;
                 const int64_t own_at = (row * p.nq + head) * p.d + col;
@@ -145,13 +117,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts(const FlashParams 
     }
 }
 
-template <int D> cudaError_t launch_join(const FlashParams &p, unsigned tiles, cudaStream_t s)
+template <int D> cudaError_t launch_join(const FlashParams &p, int64_t tiles, cudaStream_t s)
 {
-    // 32 rows a block at once; a split tile's rows over as many blocks
-    const dim3 grid(tiles, (unsigned)((p.tile_rows < (D <= 128 ? 256 : 128) ? p.tile_rows : (D <= 128 ? 256 : 128)) + 31) / 32);
-    if (p.cache_dtype == GDNA_BF16) join_parts<D, false><<<grid, 32 * kJoinWarps, 0, s>>>(p);
-    else join_parts<D, true><<<grid, 32 * kJoinWarps, 0, s>>>(p);
-    return cudaGetLastError();
+    const int64_t rows = p.rows * p.group < p.tile_rows ? p.rows * p.group : p.tile_rows;  // of a tile
+    const dim3 grid((unsigned)(tiles < 65536 ? tiles : 65536), (unsigned)((rows + 31) / 32), D / kJoinCols);
+    if (p.cache_dtype == GDNA_BF16) return gdn::launch_early(join_parts<D, false>, grid, 32 * kJoinWarps, 0, s, true, p);
+    return gdn::launch_early(join_parts<D, true>, grid, 32 * kJoinWarps, 0, s, true, p);
 }
 
 int width_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
@@ -169,11 +140,14 @@ int64_t most_tiles(int64_t rows, int segs, int group, int nkv, int d)
 
 using namespace flash;
 
+// Tiles that may be split, and the bytes of their records (with the header).
+static int64_t split_tiles(int64_t most, bool all_parts) { return !all_parts && most > 2 * kMaxGrid ? 2 * kMaxGrid : most; }
+static int64_t record_bytes(int64_t tiles) { return (64 + tiles * (int64_t)sizeof(Record) + 255) / 256 * 256; }
+
 int64_t flash_parts_bytes(int64_t rows, int segs, int group, int nkv, int d, bool all_parts)
 {
-    int64_t tiles = most_tiles(rows, segs, group, nkv, d);
-    if (!all_parts && tiles > 2 * kMaxGrid) tiles = 2 * kMaxGrid;      // (more are not split)
-    return (tiles + kMaxGrid) * rows_of(d) * (width_of(d) + 2) * (int64_t)sizeof(float);
+    const int64_t tiles = split_tiles(most_tiles(rows, segs, group, nkv, d), all_parts);
+    return record_bytes(tiles) + (tiles + kMaxGrid) * rows_of(d) * (width_of(d) + 2) * (int64_t)sizeof(float);
 }
 
 cudaError_t launch_flash(FlashParams p, cudaStream_t s)
@@ -185,24 +159,30 @@ cudaError_t launch_flash(FlashParams p, cudaStream_t s)
     p.group_div = Divisor::of((unsigned)p.group);
     p.page_div = Divisor::of((unsigned)(p.table != nullptr ? p.cache.page_size : 1));
     p.most_tiles = most_tiles(p.rows, p.segs, p.group, p.nkv, p.d);
-    cudaError_t e = p.d <= 64 ? launch_flash_64(p, s) : p.d <= 128 ? launch_flash_128(p, s) : launch_flash_256(p, s);
+    const int64_t tiles = split_tiles(p.most_tiles, p.all_parts != 0);
+    p.slots = tiles + kMaxGrid;
+    p.records = p.workspace;
+    p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + record_bytes(tiles));
+    const bool bf16 = p.cache_dtype == GDNA_BF16;
+    const cudaError_t e = p.d <= 64    ? (bf16 ? launch_flash_64_bf16(p, s) : launch_flash_64_f16(p, s))
+                          : p.d <= 128 ? (bf16 ? launch_flash_128_bf16(p, s) : launch_flash_128_f16(p, s))
+                                       : (bf16 ? launch_flash_256_bf16(p, s) : launch_flash_256_f16(p, s));
     if (e != cudaSuccess) return e;
-    int64_t tiles = p.most_tiles;
-    if (!p.all_parts && tiles > 2 * p.grid) tiles = 2 * p.grid;
-    if (tiles > 65536) tiles = 65536;
-    if (p.rows < p.tile_tokens) p.tile_rows = (int)p.rows * p.group;   // (rows of a tile, for the join's grid)
-    return p.d <= 64 ? launch_join<64>(p, (unsigned)tiles, s) : p.d <= 128 ? launch_join<128>(p, (unsigned)tiles, s)
-                                                                           : launch_join<256>(p, (unsigned)tiles, s);
+    return p.d <= 64 ? launch_join<64>(p, tiles, s) : p.d <= 128 ? launch_join<128>(p, tiles, s) : launch_join<256>(p, tiles, s);
 }
 
 cudaError_t flash_wait_timeouts(unsigned *count)
 {
-    unsigned n[3] = {0, 0, 0};
-    cudaError_t e = flash_timeouts_64(&n[0]);
-    if (e == cudaSuccess) e = flash_timeouts_128(&n[1]);
-    if (e == cudaSuccess) e = flash_timeouts_256(&n[2]);
-    *count = n[0] + n[1] + n[2];
-    return e;
+    cudaError_t (*const units[])(unsigned *) = {flash_timeouts_64_f16, flash_timeouts_64_bf16, flash_timeouts_128_f16,
+                                                flash_timeouts_128_bf16, flash_timeouts_256_f16, flash_timeouts_256_bf16};
+    *count = 0;
+    for (const auto unit : units) {
+        unsigned n = 0;
+        const cudaError_t e = unit(&n);
+        if (e != cudaSuccess) return e;
+        *count += n;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace gdnb

@@ -4,58 +4,62 @@
 //     u = post y / sqrt(mean y^2 + eps),  x' = x + scale gate u,  h = pre x' / sqrt(mean x'^2 + eps)
 //
 // Two sums over a row, the second of what the first decides, so a row stays in the registers
-// of one block: eight elements a thread (sixteen past 8192), the threads as many as the row
-// needs.  Bound by HBM for many rows and by the chain load, sum, sum, store for few.  A block
-// takes row after row and asks for the next one's elements before it adds up this one's, so
-// that the two barriers of a row are hidden by loads in flight; weights stay in registers.
+// of one block: eight or sixteen elements a thread, the threads as many as the row needs.
+// Bound by HBM for many rows and by the chain load, sum, sum, store for few: with many rows sixteen elements, so that
+// an SM has more rows in hand, with few eight, so that the chain is short.  A block takes row after row and asks for the
+// next one's elements before it adds up this one's (16-bit rows), so that loads are in flight behind a row's two barriers.
 #include "gdnb_internal.cuh"
 
 namespace gdnb {
 namespace {
 
-using gdna::load_elem;
 using gdna::store_elem;
 
-// Eight elements as they lie in memory: 16 bytes of a 16-bit type, 32 of fp32 (WIDE).
-template <bool WIDE> struct Raw {
-    uint4 a[WIDE ? 2 : 1];
-};
-
+// Eight elements of a row as they lie in memory (WIDE: fp32, else 16 bits), so that all are on their way before the first is
+// looked at: elements first .. first + 7 (VEC: 16 bytes at a time), else first, first + step, ...
 template <bool WIDE, bool VEC> struct Row8 {
-    Raw<WIDE> raw;
-    float one[VEC ? 1 : 8];
+    uint4 a[VEC ? (WIDE ? 2 : 1) : 1];
+    uint32_t one[VEC ? 1 : (WIDE ? 8 : 4)];
 
-    // elements 8t .. 8t+7 of a row (VEC), else t, t + step, ...
-    __device__ __forceinline__ void ask(const void *p, int64_t row, int first, int step, int c, int dtype, bool real)
+    __device__ __forceinline__ void ask(const void *p, int64_t row, int first, int step, int c, bool real)
     {
         if constexpr (VEC) {
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
             const bool in = real && first < c;
             if constexpr (WIDE) {
                 const uint4 *at = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + row + first);
-                raw.a[0] = in ? at[0] : zero;
-                raw.a[1] = in ? at[1] : zero;
+                a[0] = in ? at[0] : zero;
+                a[1] = in ? at[1] : zero;
             } else {
-                raw.a[0] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + row + first) : zero;
+                a[0] = in ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + row + first) : zero;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) one[j] = real && first + j * step < c ? load_elem(p, row + first + j * step, dtype) : 0.f;
+            for (int j = 0; j < 8; ++j) {
+                const bool in = real && first + j * step < c;
+                if constexpr (WIDE) {
+                    one[j] = in ? static_cast<const uint32_t *>(p)[row + first + j * step] : 0u;
+                } else {
+                    const uint32_t x = in ? static_cast<const uint16_t *>(p)[row + first + j * step] : 0u;
+                    one[j / 2] = j & 1 ? one[j / 2] | x << 16 : x;
+                }
+            }
         }
     }
     __device__ __forceinline__ void get(float (&x)[8], int dtype) const
     {
+        uint32_t u[WIDE ? 8 : 4];
         if constexpr (!VEC) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = one[j];
-        } else if constexpr (WIDE) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                x[4 * j] = __uint_as_float(raw.a[j].x); x[4 * j + 1] = __uint_as_float(raw.a[j].y);
-                x[4 * j + 2] = __uint_as_float(raw.a[j].z); x[4 * j + 3] = __uint_as_float(raw.a[j].w);
-            }
+            for (int j = 0; j < (WIDE ? 8 : 4); ++j) u[j] = one[j];
         } else {
-            const unsigned u[4] = {raw.a[0].x, raw.a[0].y, raw.a[0].z, raw.a[0].w};
+#pragma unroll
+            for (int j = 0; j < (WIDE ? 2 : 1); ++j) { u[4 * j] = a[j].x; u[4 * j + 1] = a[j].y; u[4 * j + 2] = a[j].z; u[4 * j + 3] = a[j].w; }
+        }
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(u[j]);
+        } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (dtype == GDNA_BF16) {
@@ -130,38 +134,44 @@ __device__ __forceinline__ float block_sum(float x, float *red)
 }
 
 // XW, YW: x, y (and gate) are fp32.  K: groups of eight elements a thread.
-template <bool XW, bool YW, bool VEC, int K, int THREADS>
-__global__ void __launch_bounds__(THREADS) residual_norm(const NormParams p)
+template <bool XW, bool YW, bool VEC, int K, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) residual_norm(const NormParams p)
 {
     __shared__ float red[2][32];
     const int t = threadIdx.x, n = blockDim.x, c = p.c;
     const int step = VEC ? 1 : n * K;                  // between a group's elements
     auto first = [&](int k) { return VEC ? 8 * (t + k * n) : t + k * n; };
     const float inv_c = 1.f / (float)c;
-    constexpr bool kAhead = K == 1;                    // the next row's elements and the weights in registers
+    constexpr bool kAhead = !XW && !YW && VEC;         // the next row's elements in registers
+    constexpr bool kKeep = K == 1;                     // and the weights
     float post[8], pre[8];
-    Row8<XW, VEC> x[K], x_next[kAhead ? 1 : 1];
-    Row8<YW, VEC> y[K], y_next[1], g[K], g_next[1];
+    Row8<XW, VEC> x[K], x_next[kAhead ? K : 1];
+    Row8<YW, VEC> y[K], y_next[kAhead ? K : 1], g[K];
     const bool has_y = p.y != nullptr, has_gate = p.gate != nullptr;
-    auto ask = [&](int64_t row, int k, Row8<XW, VEC> &xr, Row8<YW, VEC> &yr, Row8<YW, VEC> &gr) {
+    auto ask = [&](int64_t row, int k, Row8<XW, VEC> &xr, Row8<YW, VEC> &yr) {
         const bool real = row < p.rows;
-        xr.ask(p.x, row * p.x_stride, first(k), step, c, p.x_dtype, real);
-        yr.ask(p.y, row * p.y_stride, first(k), step, c, p.y_dtype, real && has_y);
-        gr.ask(p.gate, row * p.gate_stride, first(k), step, c, p.y_dtype, real && has_gate);
+        xr.ask(p.x, row * p.x_stride, first(k), step, c, real);
+        yr.ask(p.y, row * p.y_stride, first(k), step, c, real && has_y);
     };
     int64_t row = blockIdx.x;
     if constexpr (kAhead) {
-        ask(row, 0, x_next[0], y_next[0], g_next[0]);
+#pragma unroll
+        for (int k = 0; k < K; ++k) ask(row, k, x_next[k], y_next[k]);
+    }
+    if constexpr (kKeep) {
         weights8<VEC>(p.post, first(0), step, c, post);
         weights8<VEC>(p.pre, first(0), step, c, pre);
     }
     for (; row < p.rows; row += gridDim.x) {
-        if constexpr (kAhead) {
-            x[0] = x_next[0]; y[0] = y_next[0]; g[0] = g_next[0];
-            ask(row + gridDim.x, 0, x_next[0], y_next[0], g_next[0]);
-        } else {
 #pragma unroll
-            for (int k = 0; k < K; ++k) ask(row, k, x[k], y[k], g[k]);
+        for (int k = 0; k < K; ++k) {
+            g[k].ask(p.gate, row * p.gate_stride, first(k), step, c, has_gate);
+            if constexpr (kAhead) {
+                x[k] = x_next[k]; y[k] = y_next[k];
+                ask(row + gridDim.x, k, x_next[k], y_next[k]);
+            } else {
+                ask(row, k, x[k], y[k]);
+            }
         }
         float factor = p.scale;
         if (has_y && p.post != nullptr) {              // (for all threads alike)
@@ -182,7 +192,7 @@ __global__ void __launch_bounds__(THREADS) residual_norm(const NormParams p)
             if (has_y) {
                 float v[8], w[8];
                 y[k].get(v, p.y_dtype);
-                if constexpr (!kAhead) weights8<VEC>(p.post, first(k), step, c, post);
+                if constexpr (!kKeep) weights8<VEC>(p.post, first(k), step, c, post);
                 g[k].get(w, p.y_dtype);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -205,7 +215,7 @@ __global__ void __launch_bounds__(THREADS) residual_norm(const NormParams p)
         if (!(has_y && p.post != nullptr)) __syncthreads();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if constexpr (!kAhead) weights8<VEC>(p.pre, first(k), step, c, pre);
+            if constexpr (!kKeep) weights8<VEC>(p.pre, first(k), step, c, pre);
 #pragma unroll
             for (int j = 0; j < 8; ++j) to[k][j] *= norm * pre[j];
             put8<VEC>(p.h, row * p.h_stride, first(k), step, c, p.h_dtype, to[k]);
@@ -216,14 +226,18 @@ __global__ void __launch_bounds__(THREADS) residual_norm(const NormParams p)
 template <bool XW, bool YW, bool VEC>
 cudaError_t launch(const NormParams &p, cudaStream_t s)
 {
-    const int groups = (p.c + 7) / 8;
-    const int k = groups <= 1024 ? 1 : 2;
-    const int threads = ((groups + k - 1) / k + 31) / 32 * 32;
-    // as many blocks as are resident at once, and no more than rows
-    const int64_t resident = (int64_t)gdn::sm_count() * (threads >= 1024 || k == 2 ? 1 : threads <= 64 ? 16 : 1024 / threads);
-    const unsigned grid = (unsigned)(p.rows < resident ? p.rows : resident);
-    if (k == 2) residual_norm<XW, YW, VEC, 2, 1024><<<grid, threads, 0, s>>>(p);
-    else residual_norm<XW, YW, VEC, 1, 1024><<<grid, threads, 0, s>>>(p);
+    const int groups = (p.c + 7) / 8, sms = gdn::sm_count();
+    // Sixteen elements a thread where the row needs them, or where there are rows for it: four or more an SM.
+    const bool wide = groups > 1024 || (groups > 128 && p.rows >= 4 * (int64_t)sms);
+    const int threads = ((wide ? (groups + 1) / 2 : groups) + 31) / 32 * 32;
+    auto grid = [&](int resident) {                    // as many blocks as are resident at once, and no more than rows
+        const int64_t most = (int64_t)sms * resident;
+        return (unsigned)(p.rows < most ? p.rows : most);
+    };
+    const int some = threads >= 1024 ? 1 : threads <= 64 ? 16 : 1024 / threads;
+    if (!wide) residual_norm<XW, YW, VEC, 1, 1024, 1><<<grid(some), threads, 0, s>>>(p);
+    else if (threads <= 256) residual_norm<XW, YW, VEC, 2, 256, 4><<<grid(some), threads, 0, s>>>(p);
+    else residual_norm<XW, YW, VEC, 2, 1024, 1><<<grid(some), threads, 0, s>>>(p);
     return cudaGetLastError();
 }
 

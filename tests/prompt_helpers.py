@@ -3,7 +3,7 @@
 Bounds, with e = 2^-24, S the largest sum |q_i k_i| * scale of a row and vmax the largest |v| it sees.  A score is a sum of D
 exact products in fp32 (8 sqrt(D) e S, as independent roundings; tcgen05 adds 16 at a time and cuts instead of rounding,
 D / 16 cuts of 2 e S at most, which is less), of queries that hold 16 bits (fp32 over a bf16 cache: 2^-16 S), 22 (fp32 over the
-others: 2^-22 S) or all of theirs; its own error and its maximum's enter a weight.  A weight enters its product rounded
+others: 2^-22 S; 11 with a bf16 output: 2^-11 S) or all of theirs; its own error and its maximum's enter a weight.  A weight enters its product rounded
 once, to 2^-8 (bf16) or 2^-11 (fp16, or 2^-32 of the largest, which n keys make n 2^-32) of itself; the sum of weights is of unrounded ones,
 so all of that scales vmax.  Sums over n keys add 8 sqrt(n) e, the exponentials and rescales 32 e more.  The output's type adds
 half a unit in its last place, the gate a few e of the output."""
@@ -38,7 +38,7 @@ def attention_rows(q, keys, values, seen, scale):
 
 
 def tolerance(want, size, vmax, n, d, dtype, cache, out_type):
-    part_q = 0.0 if dtype != "f32" else 2.0 ** -16 if cache == "bf16" else 2.0 ** -22
+    part_q = 0.0 if dtype != "f32" else 2.0 ** -16 if cache == "bf16" else 2.0 ** -11 if out_type == "bf16" else 2.0 ** -22
     score = (8 * np.sqrt(d) * E32 + part_q) * size
     part = 2.0 ** -8 if cache == "bf16" else 2.0 ** -11 + n * 2.0 ** -32
     return (vmax * (2 * score + part + (8 * np.sqrt(max(n, 1)) + 32) * E32) * 1.01 + HALF_ULP[out_type] * 1.001 * want.abs()
