@@ -340,7 +340,7 @@ template <int D> struct Shared {                               // beside queries
     Item item[kItems];
     int64_t red[kThreads / 32][2];
     uint32_t tmem;
-    int dead;
+    int dead, turn;                                            // turn: a product warp issues, the other waits
     int poisoned[kItems];
     uint32_t poison[kItems][D / 2];                            // 16 bits a column: which rows see a value that is not finite
 };
@@ -357,7 +357,7 @@ template <int D, int PARTS> struct Shape {
     // The softmax warps' room for 32 rows x 64 columns of output each, where a ring of four stages is left beside it; else
     // they use their queries' place.
     static constexpr int kOutWarp = 32 * 128;
-    static constexpr bool kOutRoom = kTiles == 2 && 224 * 1024 - kQBytes - 8 * kOutWarp >= 6 * kStage;
+    static constexpr bool kOutRoom = kTiles == 2 && 224 * 1024 - kQBytes - 8 * kOutWarp >= 4 * kStage;
     static constexpr int kOutBytes = kOutRoom ? 8 * kOutWarp : 0;
     static constexpr int kRoom = 224 * 1024 - kQBytes - kOutBytes;
     static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
@@ -473,7 +473,7 @@ __device__ __forceinline__ float load_queries(const FlashParams &p, const Item &
 {
     using S = Shape<D, PARTS>;
     constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPasses = 32 / kPer;     // lanes of a row, rows of a pass
-    constexpr int kGo = 4;                                     // passes asked for at once
+    constexpr int kGo = 8;                                     // passes asked for at once
     const int col = (lane % kLanes) * 8;
     const bool scaled = !BF16 && p.dtype != GDNA_F16;
     float mine = 1.f;
@@ -640,6 +640,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             tc::mbar_init(&sh.item_full[i], 1);
             tc::mbar_init(&sh.item_empty[i], TILES + 1 + kCopyWarps + 8);
         }
+        sh.turn = 0;
         sh.dead = (base & 1023u) != 0;                 // (dynamic shared memory starts where the swizzle can)
         if (sh.dead) atomicAdd(&g_wait_timeouts, 1u);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -864,8 +865,9 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     if (S::kOutRoom || c == 0) asm volatile("cp.async.wait_all;" ::: "memory");
                     __syncwarp();
                 }
+                // (rolled up: this code runs once an item, out of a cold instruction cache; unrolled it took longer)
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {         // (rolled up: this code runs once an item, out of a cold cache)
+                for (int half = 0; half < 2; ++half) {
                     const int x = 64 * c + 32 * half;
                     float o[32];
                     if (blocks > 0) {
@@ -922,6 +924,14 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                                     g[2 * e] = f.x;
                                     g[2 * e + 1] = f.y;
                                 }
+                            } else if (gated && p.gate_vec) {          // (fp32)
+                                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+                                if (real && x + 8 * i < p.d) {
+                                    const float4 *from = reinterpret_cast<const float4 *>(static_cast<const float *>(p.gate) + gate_row + x + 8 * i);
+                                    a = from[0];
+                                    b = from[1];
+                                }
+                                g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w; g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
                             } else if (gated) {
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
@@ -1106,11 +1116,26 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 }
                 __syncwarp();
             };
+            // A tile's P V and Q K go to the tensor core in one piece: with the two tiles' products between one another, both tiles'
+            // scores were ready at once, and no softmax ran under products (period of a block 4700 cycles against 3500).  (Heads
+            // of 64: the products are bound by their issue, which two warps do side by side: 283 us against 236.)
+            constexpr bool kTurns = TILES == 2 && D == 128;
+            auto mine_now = [&]() {
+                if (!kTurns) return;
+                if (leader)
+                    for (uint32_t i = 0; i < (1u << 20); ++i)          // (the other holds it while it issues, and waits for nothing)
+                        if (atomicCAS(&sh.turn, 0, 1) == 0) break;
+                __syncwarp();
+            };
+            auto yours = [&]() {
+                if (kTurns && leader) atomicExch(&sh.turn, 0);
+            };
             auto pv = [&](uint32_t s, const Stages &x, uint32_t acc) {             // O += P . V
                 const uint32_t a = t_base + 128 * s;
                 ok = ok && wait_warp(&sh.p_full[s], (p_count >> s) & 1);
                 p_count ^= 1u << s;
                 if (!ok) return;
+                mine_now();
                 tc::fence_after_sync();
                 if (leader)
 #pragma unroll
@@ -1174,8 +1199,10 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                         if (leader) tc::mma_commit(&sh.o_full[owner]);
                     } else if (more) {
                         qk(tile, k_at, &sh.s_full[tile][0]);
+                        yours();
                         release(k_at);
                     } else {
+                        yours();
                         if (leader) tc::mma_commit(&sh.o_full[tile]);
                     }
                     release(v_at);
@@ -1470,10 +1497,8 @@ template <int D, bool BF16> cudaError_t launch_by_type(const FlashParams &p, cud
     return one ? launch<D, BF16, 1>(p, s) : launch<D, BF16, 2>(p, s);
 }
 
-template <int UNIT> cudaError_t wait_timeouts(unsigned *count)
-{
-    return cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(unsigned));
-}
+// (each unit's own: internal linkage, as the counter has)
+static inline cudaError_t wait_timeouts(unsigned *count) { return cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(unsigned)); }
 
 }  // namespace flash
 

@@ -3,5 +3,5 @@
 
 namespace gdnb {
 cudaError_t launch_flash_128_f16(const FlashParams &p, cudaStream_t s) { return flash::launch_by_type<128, false>(p, s); }
-cudaError_t flash_timeouts_128_f16(unsigned *count) { return flash::wait_timeouts<128>(count); }
+cudaError_t flash_timeouts_128_f16(unsigned *count) { return flash::wait_timeouts(count); }
 }  // namespace gdnb

@@ -3,5 +3,5 @@
 
 namespace gdnb {
 cudaError_t launch_flash_256_f16(const FlashParams &p, cudaStream_t s) { return flash::launch_by_type<256, false>(p, s); }
-cudaError_t flash_timeouts_256_f16(unsigned *count) { return flash::wait_timeouts<256>(count); }
+cudaError_t flash_timeouts_256_f16(unsigned *count) { return flash::wait_timeouts(count); }
 }  // namespace gdnb
