@@ -60,6 +60,8 @@ constexpr int kItems = 4;                  // slots of the work queue
 constexpr int kCopyWarps = 4;
 constexpr int kLead = 256;                 // what a tile costs beside its keys, in keys: queries, first products, output
 constexpr int kLeastChunk = 768;           // a block's run of the row of costs, at least; tiles that cost less stay whole
+constexpr int kLeastPart = 256;            // the same where every result is a partial one: a block of keys or two (four requests, one
+                                           // prefix of 3000: 43 us against 49)
 constexpr int kMostKeys = INT32_MAX - 4095;
 constexpr float kNegInf = -__builtin_huge_valf();
 
@@ -180,7 +182,8 @@ __device__ __forceinline__ bool whole_tiles(const FlashParams &p, const Totals &
 __device__ __forceinline__ int64_t run_of(const FlashParams &p, const Totals &all)
 {
     const int64_t even = (all.cost + p.grid - 1) / p.grid;
-    return even < kLeastChunk ? kLeastChunk : even;
+    const int64_t least = p.all_parts ? kLeastPart : kLeastChunk;
+    return even < least ? least : even;
 }
 
 // A segment's place in the row of all (costs and tiles before it), found 32 at a time by one warp.
@@ -345,7 +348,7 @@ template <int D> struct Shared {                               // beside queries
     uint32_t poison[kItems][D / 2];                            // 16 bits a column: which rows see a value that is not finite
 };
 
-template <int D, int PARTS> struct Shape {
+template <int D, int PARTS, int COPY> struct Shape {
     static constexpr int kTiles = D <= 128 ? 2 : 1;            // row tiles of 128
     static constexpr int kRows = 128 * kTiles;
     static constexpr int kCols = D < 128 ? D : 128;            // columns of a stage
@@ -355,9 +358,9 @@ template <int D, int PARTS> struct Shape {
     static constexpr int kQTile = 128 * D * 2;                 // a row tile's queries, a part
     static constexpr int kQBytes = kTiles * PARTS * kQTile;
     // The softmax warps' room for 32 rows x 64 columns of output each, where a ring of four stages is left beside it; else
-    // they use their queries' place.
+    // they use their queries' place.  (E4M3 codes would have a warp less to widen them: 326 us against 311.)
     static constexpr int kOutWarp = 32 * 128;
-    static constexpr bool kOutRoom = kTiles == 2 && 224 * 1024 - kQBytes - 8 * kOutWarp >= 4 * kStage;
+    static constexpr bool kOutRoom = kTiles == 2 && COPY != kCodeCopies && 224 * 1024 - kQBytes - 8 * kOutWarp >= 4 * kStage;
     static constexpr int kOutBytes = kOutRoom ? 8 * kOutWarp : 0;
     static constexpr int kRoom = 224 * 1024 - kQBytes - kOutBytes;
     static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
@@ -365,11 +368,8 @@ template <int D, int PARTS> struct Shape {
     // Warps that fill the ring, in turn.  A warp that passes on from fill f knows that f - kStages is released; its next fill
     // waits for f + kFillers - kStages, whose barrier tells that phase from the one before it only if f + kFillers - 2 kStages is.
     static constexpr int kFillers = kStages < kCopyWarps ? kStages : kCopyWarps;
-    // E4M3 codes come by tensor copies to the last panel of their stage and are widened there.  A warp asks for its next stage's
-    // before it widens this one's, so a stage's release must not wait for the one behind it: K's may (V of the block
-    // before is the next fill), hence the two less.
-    static constexpr bool kCodes = kCols == 128;
-    static constexpr int kWideners = kStages - 2 < kCopyWarps ? kStages - 2 : kCopyWarps;
+    // (E4M3 codes come by tensor copies to the last panel of their stage and are widened there; a warp asks for its next stage's
+    // before it widens this one's where that stage is free already, and else after.)
     static constexpr int kSmem = kQBytes + kOutBytes + kStages * kStage + (int)sizeof(Shared<D>);
     static_assert(kSmem <= 227 * 1024, "a block's shared memory");
     static constexpr int64_t kPart = (int64_t)kRows * (D + 2); // floats of a partial result: O by fours of columns, row after row, then m and l of each row
@@ -395,18 +395,21 @@ struct Wait {
         return false;
     }
 };
+// Whether it is over already.
+__device__ __forceinline__ bool test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return done != 0;
+}
 // The same on the way out, whatever the others found: copies and products in flight end by themselves.
 __device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity)
 {
-    const uint32_t s = smem_addr(bar);
-    for (uint32_t i = 0; i < (1u << 22); ++i) {
-        uint32_t done;
-        asm volatile("{\n\t.reg .pred p;\n\t"
-                     "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                     "selp.u32 %0, 1, 0, p;\n\t}"
-                     : "=r"(done) : "r"(s), "r"(parity) : "memory");
-        if (done) return;
-    }
+    for (uint32_t i = 0; i < (1u << 22); ++i)
+        if (test(bar, parity)) return;
 }
 
 // ------------------------------------------------------------------ values that some rows do not see
@@ -468,10 +471,10 @@ template <int D, bool BF16, int PARTS> __device__ __forceinline__ bool as_they_l
 {
     return PARTS == 1 && p.q_vec && p.dtype == (BF16 ? GDNA_BF16 : GDNA_F16);
 }
-template <int D, bool BF16, int PARTS>
+template <int D, bool BF16, int PARTS, int COPY>
 __device__ __forceinline__ float load_queries(const FlashParams &p, const Item &it, int rows, int row0, uint32_t q_smem, int lane)
 {
-    using S = Shape<D, PARTS>;
+    using S = Shape<D, PARTS, COPY>;
     constexpr int kLanes = D / 8, kPer = 32 / kLanes, kPasses = 32 / kPer;     // lanes of a row, rows of a pass
     constexpr int kGo = 8;                                     // passes asked for at once
     const int col = (lane % kLanes) * 8;
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
            const uint32_t polls)
 {
-    using S = Shape<D, PARTS>;
+    using S = Shape<D, PARTS, COPY>;
     constexpr int TILES = S::kTiles;
     // how far P may exceed 1 before O is rescaled (log2), and what fp16 weights are lifted by (log2): 2^(8 + 7) fits fp16.
     // (Slack 4 and lift 11: some row of 32 grew that far every few blocks, and a packed batch took 2070 us instead of 1735.)
@@ -671,7 +674,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
         uint32_t items = 0, blocks_all = 0, s_count[2] = {0, 0}, o_count = 0;
         // this warp's queries of an item on their way into shared memory, and the products told once they are there
         auto ask_queries = [&](const Item &it) {
-            return load_queries<D, BF16, PARTS>(p, it, rows_in(it), (TILES == 2 ? wg * 128 : 0) + quarter * 32,
+            return load_queries<D, BF16, PARTS, COPY>(p, it, rows_in(it), (TILES == 2 ? wg * 128 : 0) + quarter * 32,
                                                 q_smem + (TILES == 2 ? wg * PARTS * S::kQTile : 0), lane);
         };
         auto tell_queries = [&]() {
@@ -1255,7 +1258,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
 
             const bool codes = COPY == kCodeCopies || (COPY == kLoads && p.cache_dtype == GDNA_E4M3);
             constexpr bool ahead = COPY == kCodeCopies;
-            constexpr uint32_t fillers = ahead ? S::kWideners : S::kFillers;
+            constexpr uint32_t fillers = S::kFillers;
 
             // E4M3 codes of a stage, a row's where its last panel begins, to fp16: the lanes that read a row's write the row
             auto widen_stage = [&](uint32_t dst) {
@@ -1329,6 +1332,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     const int per = p.copy_keys, count = (keys + per - 1) / per;   // keys of a copy; copies of a panel (32 at most)
                     int page = 0, token = 0;
                     if (lane < count) page = page_of(key0 + lane * per, token);    // before the stage is waited for
+                    if (ahead && !__all_sync(kFull, test(&sh.empty[st], phase)) && !widen_last()) return false;
                     if (!wait_warp(&sh.empty[st], phase)) return false;
                     if constexpr (ahead) {
                         if (lane == 0) arrive_expect(&sh.landed[st], (uint32_t)(count * per * 128));
@@ -1470,7 +1474,7 @@ inline bool rows_map(const FlashParams &p, const void *base, CUtensorMap *map)
 template <int D, bool BF16, int PARTS, int COPY>
 cudaError_t launch_copy(const FlashParams &p, const CUtensorMap &k_map, const CUtensorMap &v_map, cudaStream_t s)
 {
-    using S = Shape<D, PARTS>;
+    using S = Shape<D, PARTS, COPY>;
     const cudaError_t e = gdn::allow_dynamic_smem<&flash_rows<D, BF16, PARTS, COPY>>(S::kSmem);
     if (e != cudaSuccess) return e;
     return gdn::launch_early(flash_rows<D, BF16, PARTS, COPY>, dim3(p.grid), kThreads, S::kSmem, s, true, p, k_map, v_map, gdn::tc_copy_wait_polls());
@@ -1481,10 +1485,10 @@ template <int D, bool BF16, int PARTS> cudaError_t launch(FlashParams p, cudaStr
     CUtensorMap k_map{}, v_map{};
     const bool codes = p.cache_dtype == GDNA_E4M3;
     // (heads of up to 64 codes do not fill a row of a stage: by loads)
-    if (p.copy_mode == kTensorCopies && ((codes && !Shape<D, PARTS>::kCodes) || !(rows_map(p, p.k, &k_map) && rows_map(p, p.v, &v_map))))
+    if (p.copy_mode == kTensorCopies && ((codes && !(D >= 128)) || !(rows_map(p, p.k, &k_map) && rows_map(p, p.v, &v_map))))
         p.copy_mode = kPieces16;
     if (p.copy_mode != kTensorCopies) return launch_copy<D, BF16, PARTS, kLoads>(p, k_map, v_map, s);
-    if constexpr (!BF16 && Shape<D, PARTS>::kCodes)
+    if constexpr (!BF16 && (D >= 128))
         if (codes) return launch_copy<D, BF16, PARTS, kCodeCopies>(p, k_map, v_map, s);
     return launch_copy<D, BF16, PARTS, kTensorCopies>(p, k_map, v_map, s);
 }

@@ -133,10 +133,12 @@ __device__ __forceinline__ float block_sum(float x, float *red)
     return gdn::group_sum<32>(lane < warps ? red[lane] : 0.f);
 }
 
-// XW, YW: x, y (and gate) are fp32.  K: groups of eight elements a thread.
-template <bool XW, bool YW, bool VEC, int K, int THREADS, int BLOCKS>
+// XW, YW: x, y (and gate) are fp32.  K: groups of eight elements a thread.  EARLY: launched early, where all rows are in hand at
+// once.
+template <bool XW, bool YW, bool VEC, int K, int THREADS, int BLOCKS, bool EARLY>
 __global__ void __launch_bounds__(THREADS, BLOCKS) residual_norm(const NormParams p)
 {
+    gdn::early_start<EARLY>(nullptr, 0);
     __shared__ float red[2][32];
     const int t = threadIdx.x, n = blockDim.x, c = p.c;
     const int step = VEC ? 1 : n * K;                  // between a group's elements
@@ -235,9 +237,15 @@ cudaError_t launch(const NormParams &p, cudaStream_t s)
         return (unsigned)(p.rows < most ? p.rows : most);
     };
     const int some = threads >= 1024 ? 1 : threads <= 64 ? 16 : 1024 / threads;
-    if (!wide) residual_norm<XW, YW, VEC, 1, 1024, 1><<<grid(some), threads, 0, s>>>(p);
-    else if (threads <= 256) residual_norm<XW, YW, VEC, 2, 256, 4><<<grid(some), threads, 0, s>>>(p);
-    else residual_norm<XW, YW, VEC, 2, 1024, 1><<<grid(some), threads, 0, s>>>(p);
+    const unsigned blocks = grid(some);
+    if (!wide) {
+        if (blocks == p.rows) return gdn::launch_early(residual_norm<XW, YW, VEC, 1, 1024, 1, true>, blocks, threads, 0, s, true, p);
+        residual_norm<XW, YW, VEC, 1, 1024, 1, false><<<blocks, threads, 0, s>>>(p);
+    } else if (threads <= 256) {
+        residual_norm<XW, YW, VEC, 2, 256, 4, false><<<blocks, threads, 0, s>>>(p);
+    } else {
+        residual_norm<XW, YW, VEC, 2, 1024, 1, false><<<blocks, threads, 0, s>>>(p);
+    }
     return cudaGetLastError();
 }
 
