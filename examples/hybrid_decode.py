@@ -4,6 +4,7 @@ A hybrid language model interleaves gated-delta-rule layers, whose cache is a fi
 layers, whose cache grows by one key and value a token and lives in pages.  This walks a handful of requests of
 different lengths through a few steps, one layer of each kind a step, with random weights:
 
+    gdnb_attn_prompt, gdnb_residual_norm   the prompts, packed: their attention, and the residual and norm behind it
     gdna_page_assign                       which cache slot each request's new token gets (once a step)
     gdn_decode_norm                        the gated-delta-rule layer: state update, readout, gated norm
     gdna_qk_norm_rope, gdna_attn_decode    the attention layer: head norms, rotation, cache rows; attention, output gate
@@ -62,7 +63,7 @@ class Requests:
         gdn.gdna_page_assign(self.lens[turn], fresh, self.table, self.free_pages, self.head[turn], self.lens[1 - turn],
                              row_start, slots, positions, self.head[1 - turn], self.unserved, batch=self.batch, rows=rows,
                              page_size=PAGE, max_pages=MAX_PAGES)
-        return slots, positions
+        return slots, positions, row_start
 
     def store(self, qkv, slots, positions):
         """Head norms, rotation and cache rows of a projection [rows, (q | gate) heads, k heads, v heads]; returns q."""
@@ -97,10 +98,24 @@ def rand(r, *shape):
 
 
 def prompts(r, lengths):
-    """The prompts' keys and values into the cache (their attention and states are left out here)."""
-    rows = sum(lengths)
-    slots, positions = r.assign(0, torch.tensor(lengths, dtype=torch.int32, device="cuda"), rows)
-    r.store(rand(r, rows, (2 * NQ + 2 * NKV) * HD), slots, positions)
+    """The prompts, packed: their keys and values into the cache, their attention, and the norm that the next block reads.
+    (Their delta-rule states are left out here.)  Returns how far the last tokens' attention is off float64."""
+    rows, width = sum(lengths), NQ * HD
+    slots, positions, row_start = r.assign(0, torch.tensor(lengths, dtype=torch.int32, device="cuda"), rows)
+    qkv = rand(r, rows, (2 * NQ + 2 * NKV) * HD)
+    q = r.store(qkv, slots, positions)
+    mixed = torch.empty((rows, width), dtype=torch.bfloat16, device="cuda")
+    need = gdn.gdnb_attn_prompt_workspace(rows=rows, batch=r.batch, nq=NQ, nkv=NKV, d=HD)
+    gdn.gdnb_attn_prompt(q, r.k_cache, r.v_cache, row_start, r.lens[1], mixed, torch.empty(need, dtype=torch.uint8, device="cuda"),
+                         gate=qkv[:, HD:], rows=rows, batch=r.batch, nq=NQ, nkv=NKV, d=HD, table=r.table, pages=r.pages, page_size=PAGE,
+                         max_pages=MAX_PAGES, gate_stride=qkv.shape[1], gate_head_stride=2 * HD)
+    stream, normed = rand(r, rows, width), torch.empty((rows, width), dtype=torch.bfloat16, device="cuda")
+    weight = torch.ones(width, device="cuda")
+    gdn.gdnb_residual_norm(stream, mixed, stream, normed, post=weight, pre=weight, rows=rows, c=width)
+    assert torch.isfinite(stream).all() and torch.isfinite(normed.float()).all()
+    last = row_start[1:].long() - 1
+    want = expected(r, r.lens[1], qkv[last], positions[last])
+    return ((mixed[last].double() - want).norm() / want.norm()).item()
 
 
 def expected(r, lens, qkv, positions):
@@ -124,13 +139,13 @@ def expected(r, lens, qkv, positions):
 
 def main(lengths=(5, 200, 16, 1, 333), steps=20):
     r = Requests(lengths)
-    prompts(r, list(lengths))
+    first_off = prompts(r, list(lengths))
     one = torch.ones(r.batch, dtype=torch.int32, device="cuda")
     qkv = torch.empty((r.batch, (2 * NQ + 2 * NKV) * HD), device="cuda")
     x = torch.empty((r.batch, (2 * NK + 2 * NV) * D), device="cuda")
 
     def step(turn):
-        slots, positions = r.assign(turn, one, r.batch)
+        slots, positions, _ = r.assign(turn, one, r.batch)
         mixed = r.delta_rule(x)
         q = r.store(qkv, slots, positions)
         return mixed, r.attend(turn, qkv, q), positions
@@ -160,8 +175,8 @@ def main(lengths=(5, 200, 16, 1, 333), steps=20):
     want = expected(r, lens, qkv, second[2])
     off = ((second[1].double() - want).norm() / want.norm()).item()
     print(f"{steps // 2 * 2} steps of {r.batch} requests, lengths now {lens.tolist()}: the attention layer is {off:.1e} off "
-          f"float64 (bf16 output), the delta-rule layer's output has norm {second[0].float().norm().item():.1f}")
-    assert off < 4e-3 and all(torch.isfinite(t.float()).all() for t in first[:2] + second[:2])
+          f"float64 (bf16 output; {first_off:.1e} in the prompts), the delta-rule layer's output has norm {second[0].float().norm().item():.1f}")
+    assert max(off, first_off) < 4e-3 and all(torch.isfinite(t.float()).all() for t in first[:2] + second[:2])
     return off
 
 

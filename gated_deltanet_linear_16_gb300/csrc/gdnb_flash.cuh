@@ -60,6 +60,7 @@ constexpr int kItems = 4;                  // slots of the work queue
 constexpr int kCopyWarps = 4;
 constexpr int kLead = 256;                 // what a tile costs beside its keys, in keys: queries, first products, output
 constexpr int kLeastChunk = 768;           // a block's run of the row of costs, at least; tiles that cost less stay whole
+static_assert(kLeastChunk >= kKeys, "every block between a tile's first and last has keys of it");
 constexpr int kLeastPart = 256;            // the same where every result is a partial one: a block of keys or two (four requests, one
                                            // prefix of 3000: 43 us against 49)
 constexpr int kMostKeys = INT32_MAX - 4095;
@@ -1044,10 +1045,14 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     // the block in which a tile begins tells which have a part of it
                     const int64_t tile = at.tiles + head * at.t.count + tau;
                     if (begin >= x0 && lane == 0) {
-                        const int64_t b = (end - 1) / run;     // the last one; an end may come before its first keys
-                        const bool mine = it.last > 0 || blocks == 0;
-                        const bool theirs = b > c && blocks_before(b * run - begin, blocks) < blocks;
-                        const int64_t first = mine ? c : c + 1, last = b > c && !theirs ? b - 1 : b;
+                        // from the block in whose run the first keys end to that in whose run the last ones begin (a run is longer
+                        // than a block of keys, so those between all have some)
+                        int64_t first = (begin + kLead + kKeys + run - 1) / run - 1, last = (begin + kLead + (int64_t)kKeys * blocks - 1) / run;
+                        const int64_t final_block = (end - 1) / run;
+                        if (first < c) first = c;
+                        if (first > final_block) first = final_block;
+                        if (last > final_block) last = final_block;
+                        if (blocks == 0) first = last = c;
                         const bool one = first == last && !p.all_parts;
                         const Segment s = segment(p, at.seg);
                         records(p)[tile] = Record{s.row0, tile + first, s.n, head, (int)(tau * p.tile_tokens), one ? 0 : (int)(last - first + 1)};

@@ -97,6 +97,13 @@ def test_few_rows_over_many_keys(cuda_lib, d, gated):
     check_prompt(make_prompt([33, 1, 90], [9000, 20000, 5000], 6, 2, d, page=64, seed=d), gated=gated)
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_split_anywhere(cuda_lib, seed):
+    """Lengths at which a tile's keys begin and end anywhere in a block's share of the work."""
+    cached = [900 + (seed * 1213 + i * (389 + 17 * seed)) % 5000 for i in range(5)]
+    check_prompt(make_prompt([1 + (5 * seed + i) % 70 for i in range(5)], cached, 2, 1, 64, page=64, seed=seed))
+
+
 @pytest.mark.parametrize("d,cache", [(64, "bf16"), (128, "f16"), (128, "e4m3"), (256, "bf16"), (256, "f16")])
 def test_many_tiles(cuda_lib, d, cache):
     """More tiles than two a block of the grid: every block takes one after the other."""

@@ -98,6 +98,13 @@ def test_several_tokens(cuda_lib, q_len, d, group):
     check_shared(make_shared([1000, 77, 128], [4, 1, 5], [9, 0, 2, 1, 40, 128, 3, 0, 5, 200], 2 * group, 2, d, q_len=q_len, seed=q_len))
 
 
+@pytest.mark.parametrize("seed", range(12))
+def test_prefix_lengths(cuda_lib, seed):
+    """Prefixes of lengths at which a tile's keys begin and end anywhere in a block's share of the work."""
+    lens = [1 + (seed * 613 + i * (89 + 7 * seed)) % 2300 for i in range(7)]
+    check_shared(make_shared(lens, [1] * 7, [i for i in range(7)], 4, 2, 64, page=64, seed=seed))
+
+
 def test_a_long_prefix(cuda_lib):
     check_shared(make_shared([30011], [40], [(37 * i) % 400 for i in range(40)], 12, 4, 128, page=64, seed=2), gated=8)
 
