@@ -33,13 +33,19 @@ void set_paths(gdnb::FlashParams &p, int64_t page_stride, int64_t token_stride, 
 // Scratch of a shared call: the own attention's, its output and log-sums, the prefix's partial results.
 struct SharedSpace {
     int64_t decode, own, lse, parts;       // bytes
+    bool together;                         // own keys by the prefix's kernel
     int64_t all() const { return decode + own + lse + parts; }
 };
+// Requests whose own keys go through the prefix's kernel with the prefix: as many as make about a tile for each SM.  That saves two
+// launches and their latencies (four requests of up to 400 own keys, 4 key heads of 256: 33 us against 44; 38 of them: 43
+// against 51; 96 requests of up to 2500, 8 heads of 128, by gdna_attn_decode's kernel: 57 us of 235).
+constexpr int64_t kTogether = 152;
 SharedSpace shared_space(int batch, int groups, int q_len, int nq, int nkv, int d)
 {
-    const int64_t rows = (int64_t)batch * q_len;
+    const int64_t rows = (int64_t)batch * q_len, own_tiles = gdnb::flash_tiles(q_len, batch, nq / nkv, nkv, d);
+    if (own_tiles <= kTogether) return SharedSpace{0, 0, 0, gdnb::flash_parts_bytes(rows, groups, nq / nkv, nkv, d, true, own_tiles), true};
     return SharedSpace{round256(attn_workspace_bytes((int64_t)q_len * (nq / nkv), d)), round256(rows * nq * d * 4), round256(rows * nq * 4),
-                       gdnb::flash_parts_bytes(rows, groups, nq / nkv, nkv, d, true)};
+                       gdnb::flash_parts_bytes(rows, groups, nq / nkv, nkv, d, true), false};
 }
 
 }  // namespace
@@ -216,21 +222,23 @@ GDN_API int gdnb_attn_shared(const void *q, gdna_dtype dtype, const void *gate,
 
     uint8_t *at = static_cast<uint8_t *>(workspace);
     float *own = reinterpret_cast<float *>(at + space.decode), *own_lse = reinterpret_cast<float *>(at + space.decode + space.own);
-    // each request's own keys
-    AttnParams a{};
-    a.cache = cache;
-    a.q = q; a.k = k_cache; a.v = v_cache; a.table = table; a.kv_len = kv_len;
-    a.out = own; a.lse = own_lse; a.workspace = workspace;
-    a.table_stride = table_stride; a.q_stride = q_stride; a.gate_stride = hq; a.gate_head_stride = d; a.out_stride = hq;
-    a.dtype = dtype; a.cache_dtype = cache_dtype; a.out_dtype = GDNA_F32;
-    a.batch = batch; a.q_len = q_len; a.nq = nq; a.nkv = nkv; a.group = nq / nkv; a.d = d; a.max_pages = max_pages;
-    a.scale = scale2; a.v_scale = v_scale;
-    a.q_vec = rows_aligned(q, elem_size(dtype), 4 * elem_size(dtype), {q_stride, d});
-    a.out_vec = d % 4 == 0 && aligned(own, 16);
-    const int64_t e = elem_size(cache_dtype);
-    const bool fast = d * e % 16 == 0 && rows_aligned(k_cache, e, 16, {page_stride, token_stride, head_stride}) && aligned(v_cache, 16);
-    st = gdn::report_cuda_error(launch_attn_decode(a, fast, (cudaStream_t)stream));
-    if (st != GDN_OK) return st;
+    if (!space.together) {
+        // each request's own keys
+        AttnParams a{};
+        a.cache = cache;
+        a.q = q; a.k = k_cache; a.v = v_cache; a.table = table; a.kv_len = kv_len;
+        a.out = own; a.lse = own_lse; a.workspace = workspace;
+        a.table_stride = table_stride; a.q_stride = q_stride; a.gate_stride = hq; a.gate_head_stride = d; a.out_stride = hq;
+        a.dtype = dtype; a.cache_dtype = cache_dtype; a.out_dtype = GDNA_F32;
+        a.batch = batch; a.q_len = q_len; a.nq = nq; a.nkv = nkv; a.group = nq / nkv; a.d = d; a.max_pages = max_pages;
+        a.scale = scale2; a.v_scale = v_scale;
+        a.q_vec = rows_aligned(q, elem_size(dtype), 4 * elem_size(dtype), {q_stride, d});
+        a.out_vec = d % 4 == 0 && aligned(own, 16);
+        const int64_t e = elem_size(cache_dtype);
+        const bool fast = d * e % 16 == 0 && rows_aligned(k_cache, e, 16, {page_stride, token_stride, head_stride}) && aligned(v_cache, 16);
+        st = gdn::report_cuda_error(launch_attn_decode(a, fast, (cudaStream_t)stream));
+        if (st != GDN_OK) return st;
+    }
     // the prefix, and both joined
     gdnb::FlashParams p{};
     p.cache = cache;
@@ -240,7 +248,13 @@ GDN_API int gdnb_attn_shared(const void *q, gdna_dtype dtype, const void *gate,
     p.gate_head_stride = gate_head_stride; p.out_stride = out_stride;
     p.dtype = dtype; p.cache_dtype = cache_dtype; p.out_dtype = out_dtype;
     p.segs = groups; p.row_mult = q_len; p.nq = nq; p.nkv = nkv; p.group = nq / nkv; p.d = d; p.max_pages = max_shared_pages;
-    p.all_parts = 1; p.scale2 = scale2; p.v_scale = v_scale; p.own = own; p.own_lse = own_lse;
+    p.all_parts = 1; p.scale2 = scale2; p.v_scale = v_scale;
+    if (space.together) {
+        p.segs += batch;
+        p.own_segs = batch; p.own_table = table; p.own_table_stride = table_stride; p.own_kv_len = kv_len; p.own_max_pages = max_pages;
+    } else {
+        p.own = own; p.own_lse = own_lse;
+    }
     set_paths(p, page_stride, token_stride, head_stride);
     return gdn::report_cuda_error(gdnb::launch_flash(p, (cudaStream_t)stream));
 }

@@ -71,21 +71,37 @@ constexpr float kNegInf = -__builtin_huge_valf();
 struct Segment {
     int64_t row0;
     int n, kv;                             // tokens, keys
+    bool causal;                           // the t-th of n tokens sees n - 1 - t keys less than the last; else all see all
+    const int32_t *pages;                  // its row of the block table
 };
 
 __device__ __forceinline__ Segment segment(const FlashParams &p, int b)
 {
     Segment s;
-    int64_t r0 = 0, r1 = p.rows;
-    if (p.row_start != nullptr) {
-        r0 = min(max((int64_t)p.row_start[b] * p.row_mult, (int64_t)0), p.rows);
-        r1 = min(max((int64_t)p.row_start[b + 1] * p.row_mult, r0), p.rows);
+    int64_t r0 = 0, r1 = p.rows, most;
+    const int32_t *len = p.kv_len;
+    int at = b;
+    if (b >= p.segs - p.own_segs) {        // a request's own keys
+        at = b - (p.segs - p.own_segs);
+        r0 = (int64_t)at * p.row_mult;
+        r1 = r0 + p.row_mult;
+        len = p.own_kv_len;
+        most = (int64_t)p.own_max_pages * p.cache.page_size;
+        s.causal = true;
+        s.pages = p.own_table + at * p.own_table_stride;
+    } else {
+        if (p.row_start != nullptr) {
+            r0 = min(max((int64_t)p.row_start[b] * p.row_mult, (int64_t)0), p.rows);
+            r1 = min(max((int64_t)p.row_start[b + 1] * p.row_mult, r0), p.rows);
+        }
+        most = p.table == nullptr ? r1 - r0 : (int64_t)p.max_pages * p.cache.page_size;
+        s.causal = p.causal != 0;
+        s.pages = p.table == nullptr ? nullptr : p.table + b * p.table_stride;
     }
     s.row0 = r0;
     s.n = (int)(r1 - r0);
-    int64_t most = p.table == nullptr ? (int64_t)s.n : (int64_t)p.max_pages * p.cache.page_size;
     if (most > kMostKeys) most = kMostKeys;
-    s.kv = p.kv_len == nullptr ? (int)most : (int)min((int64_t)max(p.kv_len[b], 0), most);
+    s.kv = len == nullptr ? (int)most : (int)min((int64_t)max(len[at], 0), most);
     return s;
 }
 
@@ -103,10 +119,10 @@ __device__ __forceinline__ Tiles tiles_of(const FlashParams &p, const Segment &s
     t.n = s.n;
     t.kv = s.kv;
     t.count = ((int64_t)s.n + p.tile_tokens - 1) / p.tile_tokens;
-    t.step = p.causal ? p.tile_tokens : 0;
-    t.base = kLead + (p.causal ? max(s.kv - s.n, 0) : s.kv);
+    t.step = s.causal ? p.tile_tokens : 0;
+    t.base = kLead + (s.causal ? max(s.kv - s.n, 0) : s.kv);
     t.cost = t.count * t.base;
-    if (p.causal && t.count > 0) t.cost += (int64_t)t.step * (t.count * (t.count - 1) / 2) + s.n;
+    if (s.causal && t.count > 0) t.cost += (int64_t)t.step * (t.count * (t.count - 1) / 2) + s.n;
     return t;
 }
 __device__ __forceinline__ int64_t cost_before(const Tiles &t, int64_t tau)       // of tiles [0, tau), tau < count
@@ -115,12 +131,12 @@ __device__ __forceinline__ int64_t cost_before(const Tiles &t, int64_t tau)     
 }
 __device__ __forceinline__ int64_t cost_of(const FlashParams &p, const Tiles &t, int64_t tau)
 {
-    return t.base + (p.causal ? min((tau + 1) * t.step, (int64_t)t.n) : 0);
+    return t.base + (t.step != 0 ? min((tau + 1) * t.step, (int64_t)t.n) : 0);
 }
 // Keys that tile tau's last token sees, and its blocks.
 __device__ __forceinline__ int keys_of(const FlashParams &p, const Tiles &t, int64_t tau)
 {
-    if (!p.causal) return t.kv;
+    if (t.step == 0) return t.kv;
     const int64_t k = t.kv - (int64_t)t.n + min((tau + 1) * (int64_t)p.tile_tokens, (int64_t)t.n);
     return k < 0 ? 0 : (int)k;
 }
@@ -245,9 +261,12 @@ __device__ __forceinline__ Record *records(const FlashParams &p) { return reinte
 // A block's piece of work: some key blocks of a tile.
 struct Item {
     int64_t row0;                          // first row of the segment
-    int n, kv, seg, head, token0;          // token0: first token of the tile
+    int n, kv, head, token0;               // token0: first token of the tile
     int first, last;                       // key blocks [first, last)
     int whole;                             // all of the tile's: the result is final
+    int causal;
+    int clear;                             // keys that its first token sees: a value from there on may be out of some row's sight
+    const int32_t *pages;
     int64_t slot;                          // of the partial result
     int valid;
 };
@@ -664,9 +683,6 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
         return min(p.tile_tokens, it.n - it.token0) * p.group;
     };
 
-    // keys that a tile's first token sees: a value from there on may be out of some row's sight
-    auto clear_of = [&](const Item &it) { return p.causal ? it.kv - it.n + it.token0 + 1 : it.kv; };
-
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---------------------------------------------------------------- softmax and output: a thread a row
@@ -701,7 +717,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             }
             const int t = (int)p.group_div.quotient((unsigned)r);
             const bool real = r < rows;
-            int limit = p.causal ? it.kv - it.n + it.token0 + t + 1 : it.kv;       // keys that the row sees
+            int limit = it.causal ? it.clear + t : it.clear;       // keys that the row sees
             if (!real || limit < 0) limit = 0;
             float m = kNegInf, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f, scale = p.scale2;
             // (every phase of a barrier is waited for, in order: one that was skipped would be taken for the one after it)
@@ -885,7 +901,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                         const uint16_t *poison = reinterpret_cast<const uint16_t *>(sh.poison[slot]);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (poison[x + i] <= (p.causal ? t : 0)) o[i] = __int_as_float(0x7fffffff);
+                            if (poison[x + i] <= (it.causal ? t : 0)) o[i] = __int_as_float(0x7fffffff);
                     }
                     if (!final_rows) {
 #pragma unroll
@@ -1007,16 +1023,19 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 it.row0 = s.row0;
                 it.n = s.n;
                 it.kv = s.kv;
-                it.seg = at.seg;
+                it.causal = s.causal;
+                it.pages = s.pages;
                 it.head = head;
                 it.token0 = (int)(tau * p.tile_tokens);
+                it.clear = s.causal ? s.kv - s.n + it.token0 + 1 : s.kv;
             };
             const int g = p.grid, c = blockIdx.x;
             bool ok = true;
             it.valid = 1;
             Place at{};
             const bool whole = whole_tiles(p, all);
-            if (c == 0 && lane == 0) *record_count(p) = whole ? 0 : all.tiles;
+            // (a request's own keys are joined with its prefix's: their records stand behind the others)
+            if (c == 0 && lane == 0) *record_count(p) = whole || all.tiles == 0 ? 0 : all.tiles - p.own_tiles;
             if (whole) {
                 for (int64_t k = 0; ok; ++k) {
                     const int64_t i = k * g + ((k & 1) ? g - 1 - c : c);
@@ -1233,7 +1252,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 for (int j = it.first; ok && j < it.last; ++j) {
                     // (the ring's order: K of the first block, then K of the next and V of this one)
                     fills += (j == it.first ? S::kHalves : 0) + (j + 1 < it.last ? S::kHalves : 0);
-                    const int key0 = j * kKeys, clear = clear_of(it) - key0;
+                    const int key0 = j * kKeys, clear = it.clear - key0;
                     if (COPY == kTensorCopies && clear < kKeys)
                         for (int h = 0; ok && h < S::kHalves; ++h) {
                             const int st = (fills + h) % S::kStages;
@@ -1321,16 +1340,16 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 const int st = f % S::kStages;
                 const uint32_t dst = ring + st * S::kStage, phase = ((f / S::kStages) & 1) ^ 1;
                 const int key0 = j * kKeys, keys = min(kKeys, it.kv - key0);       // (at least one)
-                const int clear = is_v ? clear_of(it) - key0 : kKeys;
+                const int clear = is_v ? it.clear - key0 : kKeys;
                 const bool masked = clear < kKeys;
                 auto page_of = [&](int key, int &token) -> int {       // (key < kv)
-                    if (p.table == nullptr) {
+                    if (it.pages == nullptr) {
                         token = (int)it.row0 + key;
                         return 0;
                     }
                     const unsigned q = p.page_div.quotient((unsigned)key);
                     token = key - (int)q * p.cache.page_size;
-                    return p.table[(int64_t)it.seg * p.table_stride + q];
+                    return it.pages[q];
                 };
 
                 if constexpr (COPY != kLoads) {

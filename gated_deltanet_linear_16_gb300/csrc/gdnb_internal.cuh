@@ -42,8 +42,12 @@ struct FlashParams {
     int causal;
     int all_parts;                  // every result is a partial one
     float scale2, v_scale;          // scores in units of log2
-    // own keys of a shared call, to be joined
+    // a shared call's requests' own keys: their attention, to be joined; or the last own_segs segments, row_mult tokens each
     const float *own, *own_lse;
+    const int32_t *own_table, *own_kv_len;
+    int64_t own_table_stride;
+    int own_segs, own_max_pages;
+    int64_t own_tiles;              // (set by the launcher)
     int q_vec, gate_vec, out_vec;   // rows and heads start on boundaries of 16 bytes, and are of eights
     int copy_mode, copy_keys;
     // set by the launcher
@@ -54,7 +58,9 @@ struct FlashParams {
 cudaError_t launch_residual_norm(const NormParams &p, bool vec, cudaStream_t s);
 cudaError_t launch_flash(FlashParams p, cudaStream_t s);
 // Partial results: bytes that `segs` segments of `rows` rows need (prompt calls: a bound whatever the rows).
-int64_t flash_parts_bytes(int64_t rows, int segs, int group, int nkv, int d, bool all_parts);
+int64_t flash_parts_bytes(int64_t rows, int segs, int group, int nkv, int d, bool all_parts, int64_t own_tiles = 0);
+// Tiles of `tokens` tokens of each of `segs` segments.
+int64_t flash_tiles(int tokens, int segs, int group, int nkv, int d);
 cudaError_t flash_wait_timeouts(unsigned *count);
 
 }  // namespace gdnb

@@ -15,6 +15,12 @@ namespace {
 constexpr int kJoinWarps = 8;
 constexpr int kJoinCols = 64;              // columns of a block
 
+__device__ __forceinline__ bool sound(const FlashParams &p, const Record &x)
+{
+    return x.parts > 0 && x.parts <= kMaxGrid && x.first_slot >= 0 && x.first_slot + x.parts <= p.slots && x.row0 >= 0 && x.n > 0 &&
+           x.row0 + x.n <= p.rows && x.token0 >= 0 && x.token0 < x.n && x.head >= 0 && x.head < p.nkv;
+}
+
 template <int D, bool LIFTED>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_parts(const FlashParams p)
 {
@@ -28,41 +34,56 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts(const FlashParams 
     const int64_t tiles = *record_count(p);
     for (int64_t tile = blockIdx.x; tile < tiles && tile < p.most_tiles; tile += gridDim.x) {
         const Record item = records(p)[tile];
-        const int n = item.parts;
         // (a record is whole unless its block gave up: then it may be anything)
-        if (n <= 0 || n > kMaxGrid || item.first_slot < 0 || item.first_slot + n > p.slots || item.row0 < 0 || item.n <= 0 ||
-            item.row0 + item.n > p.rows || item.token0 < 0 || item.token0 >= item.n || item.head < 0 || item.head >= p.nkv)
-            continue;
+        if (!sound(p, item)) continue;
         const int rows = min(p.tile_tokens, item.n - item.token0) * p.group;
         for (int r0 = blockIdx.y * 32; r0 < rows; r0 += gridDim.y * 32) {
-            const int r = r0 + lane;
+            const int r = r0 + lane, t = r / p.group;
             const bool real = r < rows;
-            const float *first = p.parts + item.first_slot * kPart;
-            auto ml = [&](int i) { return *reinterpret_cast<const float2 *>(first + i * kPart + kRows * D + 2 * r); };
+            // the row's partial results: of its tile, and of its request's own
+            struct Parts {
+                const float *first;
+                int n, row;
+            } lists[2] = {{p.parts + item.first_slot * kPart, real ? item.parts : 0, r}, {nullptr, 0, 0}};
+            if (p.own_segs > 0 && real) {
+                const int64_t row = item.row0 + item.token0 + t, request = row / p.row_mult;
+                const int token = (int)(row - request * p.row_mult), tau = token / p.tile_tokens;
+                const int each = (p.row_mult + p.tile_tokens - 1) / p.tile_tokens;
+                const int64_t at = tiles + (request * p.nkv + item.head) * each + tau;
+                if (request < p.own_segs && at < p.most_tiles) {
+                    const Record own = records(p)[at];
+                    if (sound(p, own))
+                        lists[1] = {p.parts + own.first_slot * kPart, own.parts, (token - tau * p.tile_tokens) * p.group + (r - t * p.group)};
+                }
+            }
+            auto ml = [&](const Parts &x, int i) { return *reinterpret_cast<const float2 *>(x.first + i * kPart + kRows * D + 2 * x.row); };
             // every warp has all rows' maxima and sums for itself
             float top = kNegInf;
-            if (real)
+#pragma unroll
+            for (int which = 0; which < 2; ++which)
 #pragma unroll 8
-                for (int i = 0; i < n; ++i) top = fmaxf(top, ml(i).x);
+                for (int i = 0; i < lists[which].n; ++i) top = fmaxf(top, ml(lists[which], i).x);
             const float from = top == kNegInf ? 0.f : top;
             float l = 0.f;
             float4 o[kMine];
 #pragma unroll
             for (int k = 0; k < kMine; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (real)
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                const Parts x = lists[which];
 #pragma unroll 4
-                for (int i = 0; i < n; ++i) {
-                    const float2 x = ml(i);
-                    const float w = ex2(x.x - from);
-                    l = fmaf(w, x.y, l);
+                for (int i = 0; i < x.n; ++i) {
+                    const float2 y = ml(x, i);
+                    const float w = ex2(y.x - from);
+                    l = fmaf(w, y.y, l);
 #pragma unroll
                     for (int k = 0; k < kMine; ++k) {
-                        const float4 u = *reinterpret_cast<const float4 *>(first + i * kPart + ((int64_t)(col0 / 4 + warp + kJoinWarps * k) * kRows + r) * 4);
+                        const float4 u = *reinterpret_cast<const float4 *>(x.first + i * kPart + ((int64_t)(col0 / 4 + warp + kJoinWarps * k) * kRows + x.row) * 4);
                         o[k].x = fmaf(w, u.x, o[k].x); o[k].y = fmaf(w, u.y, o[k].y);
                         o[k].z = fmaf(w, u.z, o[k].z); o[k].w = fmaf(w, u.w, o[k].w);
                     }
                 }
-            const int t = r / p.group;
+            }
             float norm = l == 0.f ? 0.f : p.v_scale / l, w_own = 0.f;
             if (p.own != nullptr && real) {
                 const float mine = l == 0.f ? kNegInf : top + log2f(l) - (LIFTED ? 7.f : 0.f);
@@ -144,9 +165,15 @@ using namespace flash;
 static int64_t split_tiles(int64_t most, bool all_parts) { return !all_parts && most > 2 * kMaxGrid ? 2 * kMaxGrid : most; }
 static int64_t record_bytes(int64_t tiles) { return (64 + tiles * (int64_t)sizeof(Record) + 255) / 256 * 256; }
 
-int64_t flash_parts_bytes(int64_t rows, int segs, int group, int nkv, int d, bool all_parts)
+int64_t flash_tiles(int tokens, int segs, int group, int nkv, int d)
 {
-    const int64_t tiles = split_tiles(most_tiles(rows, segs, group, nkv, d), all_parts);
+    const int tile = rows_of(d) / group;
+    return (int64_t)segs * ((tokens + tile - 1) / tile) * nkv;
+}
+
+int64_t flash_parts_bytes(int64_t rows, int segs, int group, int nkv, int d, bool all_parts, int64_t own_tiles)
+{
+    const int64_t tiles = split_tiles(most_tiles(rows, segs, group, nkv, d) + own_tiles, all_parts);
     return record_bytes(tiles) + (tiles + kMaxGrid) * rows_of(d) * (width_of(d) + 2) * (int64_t)sizeof(float);
 }
 
@@ -158,9 +185,12 @@ cudaError_t launch_flash(FlashParams p, cudaStream_t s)
     p.tile_rows = p.tile_tokens * p.group;
     p.group_div = Divisor::of((unsigned)p.group);
     p.page_div = Divisor::of((unsigned)(p.table != nullptr ? p.cache.page_size : 1));
-    p.most_tiles = most_tiles(p.rows, p.segs, p.group, p.nkv, p.d);
+    p.own_tiles = flash_tiles(p.row_mult, p.own_segs, p.group, p.nkv, p.d);
+    const int64_t joined = most_tiles(p.rows, p.segs - p.own_segs, p.group, p.nkv, p.d);
+    p.most_tiles = joined + p.own_tiles;
     const int64_t tiles = split_tiles(p.most_tiles, p.all_parts != 0);
     p.slots = tiles + kMaxGrid;
+    const int64_t to_join = joined < tiles ? joined : tiles;   // (a request's own tiles are joined with its prefix's)
     p.records = p.workspace;
     p.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + record_bytes(tiles));
     const bool bf16 = p.cache_dtype == GDNA_BF16;
@@ -168,7 +198,7 @@ cudaError_t launch_flash(FlashParams p, cudaStream_t s)
                           : p.d <= 128 ? (bf16 ? launch_flash_128_bf16(p, s) : launch_flash_128_f16(p, s))
                                        : (bf16 ? launch_flash_256_bf16(p, s) : launch_flash_256_f16(p, s));
     if (e != cudaSuccess) return e;
-    return p.d <= 64 ? launch_join<64>(p, tiles, s) : p.d <= 128 ? launch_join<128>(p, tiles, s) : launch_join<256>(p, tiles, s);
+    return p.d <= 64 ? launch_join<64>(p, to_join, s) : p.d <= 128 ? launch_join<128>(p, to_join, s) : launch_join<256>(p, to_join, s);
 }
 
 cudaError_t flash_wait_timeouts(unsigned *count)

@@ -145,8 +145,8 @@ GDN_API int64_t gdnb_attn_shared_workspace(int batch, int groups, int q_len, int
  *                shared_stride.  shared_len [groups] int32.  Both as table and kv_len
  *                below.
  *   table, max_pages, table_stride, kv_len: the requests' own pages and lengths.
- *   The other arguments, limits and precisions are gdnb_attn_prompt's (own keys:
- *   gdna_attn_decode's), with batch * q_len <= 2^31 - 4096 and the limits of
+ *   The other arguments, limits and precisions are gdnb_attn_prompt's (own keys of
+ *   many requests: gdna_attn_decode's), with batch * q_len <= 2^31 - 4096 and the limits of
  *   gdna_attn_decode.
  */
 GDN_API int gdnb_attn_shared(const void *q, gdna_dtype dtype, const void *gate,

@@ -86,16 +86,21 @@ def test_head_sizes(cuda_lib, d, nq, nkv):
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("out", ["f16", "bf16"])
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_types(cuda_lib, cache, dtype, out, d):
-    check_shared(make_shared([400], [5], [5, 0, 33, 1, 64], 6, 2, d, dtype=dtype, cache=cache, seed=1, scale8=0.125 if cache == "e4m3" else 1.0),
+@pytest.mark.parametrize("times", [1, 16])
+def test_types(cuda_lib, cache, dtype, out, d, times):
+    """Few requests, whose own keys go with the prefix, and many."""
+    check_shared(make_shared([400], [5 * times], [5, 0, 33, 1, 64] * times, 6, 2, d, dtype=dtype, cache=cache, seed=1, scale8=0.125 if cache == "e4m3" else 1.0),
                  out, gated=1)
 
 
 @pytest.mark.parametrize("q_len", [1, 2, 3, 5])
-@pytest.mark.parametrize("d,group", [(128, 3), (256, 8), (64, 16)])
-def test_several_tokens(cuda_lib, q_len, d, group):
-    """Tokens of a request see fewer own keys the earlier they come; some see the prefix alone."""
-    check_shared(make_shared([1000, 77, 128], [4, 1, 5], [9, 0, 2, 1, 40, 128, 3, 0, 5, 200], 2 * group, 2, d, q_len=q_len, seed=q_len))
+@pytest.mark.parametrize("d,group", [(128, 3), (256, 8), (64, 16), (256, 60)])
+@pytest.mark.parametrize("times", [1, 8])
+def test_several_tokens(cuda_lib, q_len, d, group, times):
+    """Tokens of a request see fewer own keys the earlier they come; some see the prefix alone.  (60 heads on a key head: a
+    request's tokens make more than one tile.)"""
+    check_shared(make_shared([1000, 77, 128], [4 * times, times, 5 * times], [9, 0, 2, 1, 40, 128, 3, 0, 5, 200] * times, 2 * group, 2, d,
+                             q_len=q_len, seed=q_len))
 
 
 @pytest.mark.parametrize("seed", range(12))
