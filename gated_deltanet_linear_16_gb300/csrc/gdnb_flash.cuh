@@ -147,15 +147,20 @@ __device__ __forceinline__ int blocks_before(int64_t x, int blocks)
     const int64_t b = (x - kLead) / kKeys;
     return b < blocks ? (int)b : blocks;
 }
+// a / b of what is not negative: most of it has 32 bits, whose division is a fifth of the 64-bit one.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b)
+{
+    return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // The tile in which place `y` of a head's costs lies.
 __device__ __forceinline__ int64_t tile_at(const Tiles &t, int64_t y)
 {
     int64_t tau;
     if (t.step == 0) {
-        tau = y / t.base;
-    } else {                               // tau (base + step/2) + step/2 tau^2 <= y
-        const double h = 0.5 * t.step, b = (double)t.base + h;
-        tau = (int64_t)((sqrt(b * b + 4.0 * h * (double)y) - b) / (2.0 * h));
+        tau = quotient(y, t.base);
+    } else {                               // tau (base + step/2) + step/2 tau^2 <= y: near enough in fp32, then step by step
+        const float h = 0.5f * (float)t.step, b = (float)t.base + h;
+        tau = (int64_t)(2.f * (float)y / (sqrtf(b * b + 4.f * h * (float)y) + b));
     }
     if (tau < 0) tau = 0;
     if (tau > t.count - 1) tau = t.count - 1;
@@ -203,51 +208,43 @@ __device__ __forceinline__ int64_t run_of(const FlashParams &p, const Totals &al
     return even < least ? least : even;
 }
 
-// A segment's place in the row of all (costs and tiles before it), found 32 at a time by one warp.
-struct Place {
-    int seg;                               // p.segs: none
-    int64_t cost, tiles;                   // before the segment, over all heads
+// 32 segments in the lanes of a warp, with the costs and tiles up to and with each (over all heads).
+struct Window {
+    int first;                             // segment of lane 0
+    Segment s;
     Tiles t;
-};
-// The segment in which place x of the costs (BY_COST; else tile x) lies, from segment `seg` on, before which `cost`
-// and `tiles` stand.
-template <bool BY_COST>
-__device__ __forceinline__ Place find(const FlashParams &p, int seg, int64_t cost, int64_t tiles, int64_t x)
-{
-    const int lane = threadIdx.x & 31;
-    for (; seg < p.segs; seg += 32) {
-        Tiles t{};
-        if (seg + lane < p.segs) t = tiles_of(p, segment(p, seg + lane));
-        int64_t c = t.cost * p.nkv, n = t.count * p.nkv;
-        const int64_t c0 = c, n0 = n;
+    int64_t cost, tiles;
+    __device__ __forceinline__ void load(const FlashParams &p, int seg, int64_t cost0, int64_t tiles0)
+    {
+        const int lane = threadIdx.x & 31;
+        first = seg;
+        s = Segment{};
+        t = Tiles{};
+        if (seg + lane < p.segs) {
+            s = segment(p, seg + lane);
+            t = tiles_of(p, s);
+        }
+        cost = t.cost * p.nkv;
+        tiles = t.count * p.nkv;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t u = __shfl_up_sync(kFull, c, off), v = __shfl_up_sync(kFull, n, off);
-            if (lane >= off) { c += u; n += v; }
+            const int64_t u = __shfl_up_sync(kFull, cost, off), v = __shfl_up_sync(kFull, tiles, off);
+            if (lane >= off) { cost += u; tiles += v; }
         }
-        const bool past = BY_COST ? cost + c > x : tiles + n > x;
-        const unsigned hit = __ballot_sync(kFull, past);
-        const int at = hit ? __ffs(hit) - 1 : 31;
-        if (hit) {
-            Place r;
-            r.seg = seg + at;
-            r.cost = cost + __shfl_sync(kFull, c - c0, at);
-            r.tiles = tiles + __shfl_sync(kFull, n - n0, at);
-            r.t.count = __shfl_sync(kFull, t.count, at);
-            r.t.base = __shfl_sync(kFull, t.base, at);
-            r.t.cost = __shfl_sync(kFull, t.cost, at);
-            r.t.step = __shfl_sync(kFull, t.step, at);
-            r.t.n = __shfl_sync(kFull, t.n, at);
-            r.t.kv = __shfl_sync(kFull, t.kv, at);
-            return r;
-        }
-        cost += __shfl_sync(kFull, c, 31);
-        tiles += __shfl_sync(kFull, n, 31);
+        cost += cost0;
+        tiles += tiles0;
     }
-    Place none{};
-    none.seg = p.segs;
-    return none;
-}
+    // The lane whose segment has place x of the costs (BY_COST; else tile x), windows further on if need be; -1: none.
+    template <bool BY_COST> __device__ __forceinline__ int find(const FlashParams &p, int64_t x)
+    {
+        for (;;) {
+            const unsigned hit = __ballot_sync(kFull, (BY_COST ? cost : tiles) > x);
+            if (hit) return __ffs(hit) - 1;
+            if (first + 32 >= p.segs) return -1;
+            load(p, first + 32, __shfl_sync(kFull, cost, 31), __shfl_sync(kFull, tiles, 31));
+        }
+    }
+};
 
 // Where a split tile's partial results are, for the join: a header with the number of tiles, then a record each.
 struct Record {
@@ -1003,36 +1000,41 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 10) {
             // ------------------------------------------------------------ work
+            // Each lane has a segment; the one whose turn it is works out the item and writes it.
             uint32_t n = 0;
-            Item it{};
-            auto put = [&]() -> bool {
+            auto room = [&]() -> bool {                // for the next item, with nothing noted against it
                 const int slot = n % kItems;
                 if (!wait_warp(&sh.item_empty[slot], ((n / kItems) & 1) ^ 1)) return false;
                 for (int i = lane; i < D / 2; i += 32) sh.poison[slot][i] = 0xffffffffu;
-                if (lane == 0) {
-                    sh.poisoned[slot] = 0;
-                    sh.item[slot] = it;
-                }
-                __syncwarp();
-                if (lane == 0) arrive(&sh.item_full[slot]);
-                ++n;
+                if (lane == 0) sh.poisoned[slot] = 0;
                 return true;
             };
-            auto set = [&](const Place &at, int head, int64_t tau) {
-                const Segment s = segment(p, at.seg);
-                it.row0 = s.row0;
-                it.n = s.n;
-                it.kv = s.kv;
-                it.causal = s.causal;
-                it.pages = s.pages;
+            auto tell = [&]() {
+                __syncwarp();
+                if (lane == 0) arrive(&sh.item_full[n % kItems]);
+                ++n;
+            };
+            Window win;
+            win.load(p, 0, 0, 0);
+            auto write = [&](int head, int64_t tau, int first, int last, bool whole, int64_t slot) {
+                Item &it = sh.item[n % kItems];
+                const int token0 = (int)(tau * p.tile_tokens);
+                it.row0 = win.s.row0;
+                it.n = win.s.n;
+                it.kv = win.s.kv;
                 it.head = head;
-                it.token0 = (int)(tau * p.tile_tokens);
-                it.clear = s.causal ? s.kv - s.n + it.token0 + 1 : s.kv;
+                it.token0 = token0;
+                it.first = first;
+                it.last = last;
+                it.whole = whole;
+                it.causal = win.s.causal;
+                it.clear = win.s.causal ? win.s.kv - win.s.n + token0 + 1 : win.s.kv;
+                it.pages = win.s.pages;
+                it.slot = slot;
+                it.valid = 1;
             };
             const int g = p.grid, c = blockIdx.x;
             bool ok = true;
-            it.valid = 1;
-            Place at{};
             const bool whole = whole_tiles(p, all);
             // (a request's own keys are joined with its prefix's: their records stand behind the others)
             if (c == 0 && lane == 0) *record_count(p) = whole || all.tiles == 0 ? 0 : all.tiles - p.own_tiles;
@@ -1040,55 +1042,60 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 for (int64_t k = 0; ok; ++k) {
                     const int64_t i = k * g + ((k & 1) ? g - 1 - c : c);
                     if (i >= all.tiles) break;         // (and so is every later turn)
-                    at = find<false>(p, at.seg, at.cost, at.tiles, i);
-                    if (at.seg >= p.segs) break;
-                    const int64_t idx = i - at.tiles, tau = at.t.count - 1 - idx / p.nkv;
-                    set(at, (int)(idx % p.nkv), tau);
-                    it.first = 0;
-                    it.last = (int)(((int64_t)keys_of(p, at.t, tau) + kKeys - 1) / kKeys);
-                    it.whole = 1;
-                    ok = put();
+                    const int at = win.find<false>(p, i);
+                    if (at < 0) break;
+                    ok = room();
+                    if (ok && lane == at) {
+                        const int64_t idx = i - (win.tiles - win.t.count * p.nkv), row = quotient(idx, p.nkv), tau = win.t.count - 1 - row;
+                        write((int)(idx - row * p.nkv), tau, 0, (int)(((int64_t)keys_of(p, win.t, tau) + kKeys - 1) / kKeys), true, 0);
+                    }
+                    if (ok) tell();
                 }
             } else {
                 const int64_t run = run_of(p, all), x0 = c * run;
                 const int64_t x1 = x0 + run < all.cost ? x0 + run : all.cost;
                 for (int64_t x = x0; ok && x < x1;) {
-                    at = find<true>(p, at.seg, at.cost, at.tiles, x);
-                    if (at.seg >= p.segs) break;
-                    const int head = (int)((x - at.cost) / at.t.cost);
-                    const int64_t y = x - at.cost - head * at.t.cost, tau = tile_at(at.t, y);
-                    const int64_t begin = x - y + cost_before(at.t, tau), end = begin + cost_of(p, at.t, tau);
-                    const int blocks = (int)(((int64_t)keys_of(p, at.t, tau) + kKeys - 1) / kKeys);
-                    it.first = x0 > begin ? blocks_before(x0 - begin, blocks) : 0;
-                    it.last = x1 < end ? blocks_before(x1 - begin, blocks) : blocks;
-                    // the block in which a tile begins tells which have a part of it
-                    const int64_t tile = at.tiles + head * at.t.count + tau;
-                    if (begin >= x0 && lane == 0) {
-                        // from the block in whose run the first keys end to that in whose run the last ones begin (a run is longer
-                        // than a block of keys, so those between all have some)
-                        int64_t first = (begin + kLead + kKeys + run - 1) / run - 1, last = (begin + kLead + (int64_t)kKeys * blocks - 1) / run;
-                        const int64_t final_block = (end - 1) / run;
-                        if (first < c) first = c;
-                        if (first > final_block) first = final_block;
-                        if (last > final_block) last = final_block;
-                        if (blocks == 0) first = last = c;
-                        const bool one = first == last && !p.all_parts;
-                        const Segment s = segment(p, at.seg);
-                        records(p)[tile] = Record{s.row0, tile + first, s.n, head, (int)(tau * p.tile_tokens), one ? 0 : (int)(last - first + 1)};
+                    const int at = win.find<true>(p, x);
+                    if (at < 0) break;
+                    int64_t end = 0, tile = 0, tau = 0;
+                    int head = 0, first = 0, last = 0, blocks = 0, some = 0;
+                    if (lane == at) {
+                        const int64_t before = win.cost - win.t.cost * p.nkv;
+                        head = (int)quotient(x - before, win.t.cost);
+                        const int64_t y = x - before - head * win.t.cost;
+                        tau = tile_at(win.t, y);
+                        const int64_t begin = x - y + cost_before(win.t, tau);
+                        end = begin + cost_of(p, win.t, tau);
+                        blocks = (int)(((int64_t)keys_of(p, win.t, tau) + kKeys - 1) / kKeys);
+                        first = x0 > begin ? blocks_before(x0 - begin, blocks) : 0;
+                        last = x1 < end ? blocks_before(x1 - begin, blocks) : blocks;
+                        tile = win.tiles - win.t.count * p.nkv + head * win.t.count + tau;
+                        // a tile without keys is the block's in which it begins
+                        some = first < last || (blocks == 0 && begin >= x0);
+                        // and that block tells which have a part of the tile: from the one in whose run the first keys end to that in
+                        // whose run the last ones begin (a run is longer than a block of keys, so those between all have some)
+                        if (begin >= x0) {
+                            int64_t b0 = quotient(begin + kLead + kKeys + run - 1, run) - 1, b1 = quotient(begin + kLead + (int64_t)kKeys * blocks - 1, run);
+                            const int64_t most = quotient(end - 1, run);
+                            if (b0 < c) b0 = c;
+                            if (b0 > most) b0 = most;
+                            if (b1 > most) b1 = most;
+                            if (blocks == 0) b0 = b1 = c;
+                            const bool one = b0 == b1 && !p.all_parts;
+                            records(p)[tile] = Record{win.s.row0, tile + b0, win.s.n, head, (int)(tau * p.tile_tokens), one ? 0 : (int)(b1 - b0 + 1)};
+                        }
                     }
-                    // a tile without keys is the block's in which it begins
-                    if (it.first < it.last || (blocks == 0 && begin >= x0)) {
-                        set(at, head, tau);
-                        it.whole = it.first == 0 && it.last == blocks;
-                        it.slot = tile + c;
-                        ok = put();
+                    if (__shfl_sync(kFull, some, at)) {
+                        ok = room();
+                        if (ok && lane == at) write(head, tau, first, last, first == 0 && last == blocks, tile + c);
+                        if (ok) tell();
                     }
-                    x = end;
+                    x = __shfl_sync(kFull, end, at);
                 }
             }
-            if (ok) {
-                it.valid = 0;
-                put();
+            if (ok && room()) {
+                if (lane == 0) sh.item[n % kItems].valid = 0;
+                tell();
             }
         } else if (warp < 8 + TILES) {
             // ------------------------------------------------------------ products: a warp for each row tile
