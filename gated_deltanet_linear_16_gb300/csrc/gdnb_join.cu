@@ -141,7 +141,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_parts(const FlashParams 
 template <int D> cudaError_t launch_join(const FlashParams &p, int64_t tiles, cudaStream_t s)
 {
     const int64_t rows = p.rows * p.group < p.tile_rows ? p.rows * p.group : p.tile_rows;  // of a tile
-    const dim3 grid((unsigned)(tiles < 65536 ? tiles : 65536), (unsigned)((rows + 31) / 32), D / kJoinCols);
+    // eight blocks an SM, which take tile after tile: often nothing is split, and what is launched only ends
+    const int64_t each = (rows + 31) / 32 * (D / kJoinCols), most = (8 * (int64_t)p.grid + each - 1) / each;
+    const dim3 grid((unsigned)(tiles < most ? tiles : most), (unsigned)((rows + 31) / 32), D / kJoinCols);
     if (p.cache_dtype == GDNA_BF16) return gdn::launch_early(join_parts<D, false>, grid, 32 * kJoinWarps, 0, s, true, p);
     return gdn::launch_early(join_parts<D, true>, grid, 32 * kJoinWarps, 0, s, true, p);
 }

@@ -13,7 +13,6 @@
 namespace gdnb {
 namespace {
 
-using gdna::store_elem;
 
 // Eight elements of a row as they lie in memory (WIDE: fp32, else 16 bits), so that all are on their way before the first is
 // looked at: elements first .. first + 7 (VEC: 16 bytes at a time), else first, first + step, ...
@@ -38,9 +37,9 @@ template <bool WIDE, bool VEC> struct Row8 {
             for (int j = 0; j < 8; ++j) {
                 const bool in = real && first + j * step < c;
                 if constexpr (WIDE) {
-                    one[j] = in ? static_cast<const uint32_t *>(p)[row + first + j * step] : 0u;
+                    one[j] = in ? (static_cast<const uint32_t *>(p) + row + first)[j * step] : 0u;
                 } else {
-                    const uint32_t x = in ? static_cast<const uint16_t *>(p)[row + first + j * step] : 0u;
+                    const uint32_t x = in ? (static_cast<const uint16_t *>(p) + row + first)[j * step] : 0u;
                     one[j / 2] = j & 1 ? one[j / 2] | x << 16 : x;
                 }
             }
@@ -99,9 +98,20 @@ __device__ __forceinline__ void put8(void *p, int64_t row, int first, int step, 
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + row + first) = make_uint4(u[0], u[1], u[2], u[3]);
         }
     } else {
+        // (the type decided once, not for each element)
+        if (dtype == GDNA_F32) {
+            float *at = static_cast<float *>(p) + row + first;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (first + j * step < c) store_elem(p, row + first + j * step, dtype, x[j]);
+            for (int j = 0; j < 8; ++j)
+                if (first + j * step < c) at[j * step] = x[j];
+        } else {
+            uint16_t *at = static_cast<uint16_t *>(p) + row + first;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint16_t h = dtype == GDNA_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x[j])) : __half_as_ushort(__float2half_rn(x[j]));
+                if (first + j * step < c) at[j * step] = h;
+            }
+        }
     }
 }
 
