@@ -39,6 +39,14 @@
 // What a row does not see.  Masked scores are replaced.  In blocks where some row does not see all
 // keys, values that are not finite are taken out of V (0 x NaN) and the first such key of each column is noted: the rows
 // that see it come out NaN in that column, the others clean.  Keys past the end count as zeros.
+//
+// What bounds it (GB300, device time).  Long lists of keys: 512 rows over 60000 keys of 8 heads of 128 take 373 us, 1357 TFLOP/s or
+// 0.71 of the measured rate; there shared memory is full: Q and K of the first product take its 128 bytes a cycle by themselves,
+// and the copies come on top.  Prompts: eight of 4096, 24/4 heads of 256, 1741 us (948 TFLOP/s), a packed batch at 128 1526 us (1108): what a
+// tile costs beside its keys, some 16000 cycles of queries, first scores and output to 19 blocks of 4000.  Heads of 64: 226 us (389
+// TFLOP/s), the softmax warps' issue slots.  E4M3: 223 us for 107 GFLOP, the widening (one conversion of two codes takes a quarter of the
+// schedulers' time).  Short calls: 25 us for one prompt of 180 tokens: 2 us until sums of lengths are there, 3 until the first item is
+// dealt, then a chain of copies, products, softmax, output, in code that no cache holds yet.
 #pragma once
 
 #include <cuda.h>
@@ -674,6 +682,9 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
     const uint32_t tmem = sh.tmem;
     const Wait wait{&sh.dead, sh.dead ? 0u : polls};
     auto wait_warp = [&](uint64_t *bar, uint32_t parity) { return (bool)__all_sync(kFull, wait(bar, parity)); };
+    // for the end of another's item, which may have a million keys: 256 times the bound (a wait that runs out elsewhere ends these too)
+    const Wait patient{&sh.dead, wait.limit < (1u << 24) ? wait.limit << 8 : 0xffffffffu};
+    auto wait_long = [&](uint64_t *bar, uint32_t parity) { return (bool)__all_sync(kFull, patient(bar, parity)); };
     auto s_col = [&](int i) { return tmem + 128 * i; };                            // of S, and P
     auto o_col = [&](int t) { return tmem + 256 + (TILES == 2 ? t * D : 0); };
     auto rows_in = [&](const Item &it) {               // rows of a tile that are real
@@ -700,7 +711,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
         float ahead = 0.f;                             // the next item's queries are in already, with this scale
         for (;; ++items) {
             const int slot = items % kItems;
-            if (!wait_warp(&sh.item_full[slot], (items / kItems) & 1)) break;
+            if (!wait_long(&sh.item_full[slot], (items / kItems) & 1)) break;
             const Item it = sh.item[slot];
             if (!it.valid) break;
             const int blocks = it.last - it.first, rows = rows_in(it);
@@ -718,7 +729,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             if (!real || limit < 0) limit = 0;
             float m = kNegInf, l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f, scale = p.scale2;
             // (every phase of a barrier is waited for, in order: one that was skipped would be taken for the one after it)
-            if (TILES == 1 && items > 0 && !wait_warp(&sh.q_over[(items - 1) & 1], ((items - 1) >> 1) & 1)) break;
+            if (TILES == 1 && items > 0 && !wait_long(&sh.q_over[(items - 1) & 1], ((items - 1) >> 1) & 1)) break;
             if (blocks > 0) {
                 if (ahead == 0.f) {
                     ahead = ask_queries(it);
@@ -828,7 +839,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             // scores of the last block are here, so nothing reads the old ones any more)
             if (S::kOutRoom && blocks > 0) {
                 const int after = (items + 1) % kItems;
-                if (!wait_warp(&sh.item_full[after], ((items + 1) / kItems) & 1)) break;
+                if (!wait_long(&sh.item_full[after], ((items + 1) / kItems) & 1)) break;
                 const Item &then = sh.item[after];
                 if (as_they_lie<D, BF16, PARTS>(p) && then.valid && then.first < then.last && rows_in(then) > wg * 128) ahead = ask_queries(then);
             }
@@ -1004,7 +1015,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             uint32_t n = 0;
             auto room = [&]() -> bool {                // for the next item, with nothing noted against it
                 const int slot = n % kItems;
-                if (!wait_warp(&sh.item_empty[slot], ((n / kItems) & 1) ^ 1)) return false;
+                if (!wait_long(&sh.item_empty[slot], ((n / kItems) & 1) ^ 1)) return false;
                 for (int i = lane; i < D / 2; i += 32) sh.poison[slot][i] = 0xffffffffu;
                 if (lane == 0) sh.poisoned[slot] = 0;
                 return true;
@@ -1183,7 +1194,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             };
             for (; ok; ++items) {
                 const int slot = items % kItems;
-                if (!wait_warp(&sh.item_full[slot], (items / kItems) & 1)) break;
+                if (!wait_long(&sh.item_full[slot], (items / kItems) & 1)) break;
                 const Item *it = &sh.item[slot];
                 if (!__shfl_sync(kFull, it->valid, 0)) break;
                 const int first_block = __shfl_sync(kFull, it->first, 0), last_block = __shfl_sync(kFull, it->last, 0);
@@ -1253,7 +1264,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             uint32_t items = 0, fills = 0, turns = 0;  // (turns: a parity for each stage)
             for (bool ok = true; ok; ++items) {
                 const int slot = items % kItems;
-                if (!wait_warp(&sh.item_full[slot], (items / kItems) & 1)) break;
+                if (!wait_long(&sh.item_full[slot], (items / kItems) & 1)) break;
                 const Item it = sh.item[slot];
                 if (!it.valid) break;
                 for (int j = it.first; ok && j < it.last; ++j) {
@@ -1450,7 +1461,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             };
             for (bool ok = true; ok; ++items) {
                 const int slot = items % kItems;
-                if (!wait_warp(&sh.item_full[slot], (items / kItems) & 1)) break;
+                if (!wait_long(&sh.item_full[slot], (items / kItems) & 1)) break;
                 const Item it = sh.item[slot];
                 if (!it.valid) break;
                 auto block = [&](int j, bool is_v) {

@@ -8,6 +8,9 @@
 // Bound by HBM for many rows and by the chain load, sum, sum, store for few: with many rows sixteen elements, so that
 // an SM has more rows in hand, with few eight, so that the chain is short.  A block takes row after row and asks for the
 // next one's elements before it adds up this one's (16-bit rows), so that loads are in flight behind a row's two barriers.
+// 32768 rows of 4096, bf16: 194 us, 5.5 TB/s (eight elements a thread: 250); fp32 throughout, 16384 rows: 171 us, 0.93 of the copy
+// rate; one row: 6 us, the call.  Rows that are not of eights on 16-byte boundaries go element by element, four times slower
+// (16384 rows of 4095: 400 us): bound by its instructions.
 #include "gdnb_internal.cuh"
 
 namespace gdnb {
