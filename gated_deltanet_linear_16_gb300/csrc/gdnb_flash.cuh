@@ -674,6 +674,10 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) tc::tmem_alloc(&sh.tmem, 512);
+    if (COPY != kLoads && tid == 32 * 12) {            // (the first copies would wait for them)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
+    }
     gdn::early_start<true>(nullptr, 0);                // (nothing of other kernels' is read or written before)
     const Totals all = totals(p, sh.red);              // (a barrier)
     tc::fence_before_sync();
