@@ -925,23 +925,22 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     }
                     const uint32_t at0 = here + lane * 128;
                     if (plain) {
+                        uint32_t u[4][4];              // (all gates first, so that the four chains of latencies run side by side)
+                        if (gated) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t at = at0 + (((4 * half + i) ^ (lane & 7)) << 4);
-                            uint32_t u[4];
-                            if (gated) lds16(u, at);
+                            for (int i = 0; i < 4; ++i) lds16(u[i], at0 + (((4 * half + i) ^ (lane & 7)) << 4));
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float y0 = o[8 * i + 2 * e] * norm, y1 = o[8 * i + 2 * e + 1] * norm;
-                                if (gated) {
-                                    const float2 g = unpack16<BF16>(u[e]);
-                                    y0 *= sigmoid(g.x);
-                                    y1 *= sigmoid(g.y);
-                                }
-                                u[e] = pack16<BF16>(y0, y1);
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 g = unpack16<BF16>(u[i / 4][i % 4]);
+                                o[2 * i] *= sigmoid(g.x);
+                                o[2 * i + 1] *= sigmoid(g.y);
                             }
-                            sts16(at, u[0], u[1], u[2], u[3]);
                         }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) u[i / 4][i % 4] = pack16<BF16>(o[2 * i] * norm, o[2 * i + 1] * norm);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sts16(at0 + (((4 * half + i) ^ (lane & 7)) << 4), u[i][0], u[i][1], u[i][2], u[i][3]);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -983,19 +982,30 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 if (!final_rows) continue;
                 __syncwarp();
                 const int col = 64 * c + 8 * (lane & 7);
-#pragma unroll 2
-                for (int i = 0; i < 8; ++i) {
-                    const int from = 4 * i + (lane >> 3);
-                    uint16_t *at = static_cast<uint16_t *>(p.out) + (__shfl_sync(kFull, out_row, from) + col);
-                    uint32_t u[4];
-                    lds16(u, here + place(from));
-                    if (!(reals >> from & 1) || col >= p.d) continue;
-                    if (p.out_vec) {
-                        *reinterpret_cast<uint4 *>(at) = make_uint4(u[0], u[1], u[2], u[3]);
-                    } else {
+#pragma unroll 1
+                for (int i0 = 0; i0 < 8; i0 += 4) {
+                    uint16_t *at[4];
+                    uint32_t u[4][4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (col + e < p.d) at[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+                    for (int i = 0; i < 4; ++i) {
+                        const int from = 4 * (i0 + i) + (lane >> 3);
+                        at[i] = static_cast<uint16_t *>(p.out) + (__shfl_sync(kFull, out_row, from) + col);
+                        lds16(u[i], here + place(from));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int from = 4 * (i0 + i) + (lane >> 3);
+                        if (!(reals >> from & 1) || col >= p.d) continue;
+                        if (p.out_vec) {
+                            *reinterpret_cast<uint4 *>(at[i]) = make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]);
+                        } else {                       // element by element
+#pragma unroll 1
+                            for (int e = 0; e < 8 && col + e < p.d; ++e) {
+                                uint16_t x;
+                                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(here + place(from) + 2 * e) : "memory");
+                                at[i][e] = x;
+                            }
+                        }
                     }
                 }
                 __syncwarp();
