@@ -749,6 +749,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 ok = wait_warp(&sh.s_full[wg][b], s_count[b]++ & 1);
                 if (!ok) break;
                 tc::fence_after_sync();
+                if (TILES == 1 && j + 1 == blocks && lane == 0) arrive(&sh.q_over[wg]);    // nothing reads these queries any more
                 const uint32_t s_at = s_col(col) + lanes;
                 const int seen = limit - (it.first + j) * kKeys;
                 const bool masked = __any_sync(kFull, seen < kKeys);
@@ -839,6 +840,10 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 if (lane == 0) arrive(&sh.p_full[col]);
             }
             if (!ok) break;
+            if (TILES == 1 && blocks == 0) {
+                __syncwarp();
+                if (lane == 0) arrive(&sh.q_over[wg]);
+            }
             // with room for the output: the next item's queries first, so that its products run while this one's output is written (the
             // scores of the last block are here, so nothing reads the old ones any more)
             if (S::kOutRoom && blocks > 0) {
@@ -874,9 +879,21 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             // eight columns of this thread's row, scaled, gated, rounded and put into their place; `plain`: gates and output
             // are of the products' type, which the compiler then knows
             const bool plain = p.out_dtype == (BF16 ? GDNA_BF16 : GDNA_F16) && (!gated || (gate_pieces && p.dtype == (BF16 ? GDNA_BF16 : GDNA_F16)));
-            if (gate_pieces)
+            if (TILES == 2 && gate_pieces)
 #pragma unroll 1
                 for (int c = 0; c < (S::kOutRoom ? 1 : D / 64); ++c) ask_gates(c);
+            // (a single row tile: a lane writes its own row)
+            const uint4 *gate_at = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.gate) + gate_row);
+            uint4 ahead_g[8];
+            auto ask_row = [&](int x) {                // 64 columns of the row's gates
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    ahead_g[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (real && x + 8 * i < p.d) ahead_g[i] = gate_at[x / 8 + i];
+                }
+            };
+            const bool wide = plain && p.out_vec;
+            if (TILES == 1 && wide && gated) ask_row(0);
             if (blocks > 0) {
                 const uint32_t last = TILES == 2 ? o_count++ : (o_count += blocks) - 1;
                 if (!wait_warp(&sh.o_full[wg], last & 1)) break;
@@ -889,134 +906,218 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             float *part = p.parts + it.slot * S::kPart;
             if (!final_rows && real)
                 *reinterpret_cast<float2 *>(part + S::kRows * D + 2 * r) = make_float2(m == kNegInf ? kNegInf : m * scale, l);
+            if constexpr (TILES == 1) {
 #pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-                const uint32_t here = stage + c * kNext;
-                if (gate_pieces) {
-                    if (S::kOutRoom && c > 0) ask_gates(c);
-                    if (S::kOutRoom || c == 0) asm volatile("cp.async.wait_all;" ::: "memory");
-                    __syncwarp();
-                }
-                // (rolled up: this code runs once an item, out of a cold instruction cache; unrolled it took longer)
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const int x = 64 * c + 32 * half;
-                    float o[32];
+                for (int x = 0; x < (wide || !final_rows ? D : 0); x += 64) {
+                    float o[2][32];
                     if (blocks > 0) {
-                        tc::tmem_ld32(o_col(TILES == 2 ? wg : 0) + lanes + x, o);
+                        tc::tmem_ld32(o_col(0) + lanes + x, o[0]);
+                        tc::tmem_ld32(o_col(0) + lanes + x + 32, o[1]);
                         tc::ld_wait();
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                        for (int i = 0; i < 64; ++i) o[i / 32][i % 32] = 0.f;
                     }
                     if (poisoned) {
                         const uint16_t *poison = reinterpret_cast<const uint16_t *>(sh.poison[slot]);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (poison[x + i] <= (it.causal ? t : 0)) o[i] = __int_as_float(0x7fffffff);
+                        for (int i = 0; i < 64; ++i)
+                            if (poison[x + i] <= (it.causal ? t : 0)) o[i / 32][i % 32] = __int_as_float(0x7fffffff);
                     }
                     if (!final_rows) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
+                        for (int i = 0; i < 16; ++i)
                             if (real)
                                 *reinterpret_cast<float4 *>(part + ((int64_t)(x / 4 + i) * S::kRows + r) * 4) =
-                                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                                    make_float4(o[i / 8][4 * i % 32], o[i / 8][4 * i % 32 + 1], o[i / 8][4 * i % 32 + 2], o[i / 8][4 * i % 32 + 3]);
                         continue;
                     }
-                    const uint32_t at0 = here + lane * 128;
-                    if (plain) {
-                        uint32_t u[4][4];              // (all gates first, so that the four chains of latencies run side by side)
-                        if (gated) {
+                    if (gated) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) lds16(u[i], at0 + (((4 * half + i) ^ (lane & 7)) << 4));
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t u[4] = {ahead_g[i].x, ahead_g[i].y, ahead_g[i].z, ahead_g[i].w};
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float2 g = unpack16<BF16>(u[i / 4][i % 4]);
-                                o[2 * i] *= sigmoid(g.x);
-                                o[2 * i + 1] *= sigmoid(g.y);
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 g = unpack16<BF16>(u[e]);
+                                o[i / 4][8 * i % 32 + 2 * e] *= sigmoid(g.x);
+                                o[i / 4][8 * i % 32 + 2 * e + 1] *= sigmoid(g.y);
                             }
                         }
+                        if (x + 64 < D) ask_row(x + 64);
+                    }
+                    uint4 *out_at = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + out_row + x);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) u[i / 4][i % 4] = pack16<BF16>(o[2 * i] * norm, o[2 * i + 1] * norm);
+                    for (int i = 0; i < 8; ++i) {
+                        const float *y = &o[i / 4][8 * i % 32];
+                        if (real && x + 8 * i < p.d)
+                            out_at[i] = make_uint4(pack16<BF16>(y[0] * norm, y[1] * norm), pack16<BF16>(y[2] * norm, y[3] * norm),
+                                                   pack16<BF16>(y[4] * norm, y[5] * norm), pack16<BF16>(y[6] * norm, y[7] * norm));
+                    }
+                }
+                // other types, and rows that do not begin at 16 bytes
+#pragma unroll 1
+                for (int x = 0; x < (wide || !final_rows ? 0 : p.d); x += 8) {
+                    float o[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sts16(at0 + (((4 * half + i) ^ (lane & 7)) << 4), u[i][0], u[i][1], u[i][2], u[i][3]);
+                    for (int i = 0; i < 8; ++i) o[i] = 0.f;
+                    if (blocks > 0) {
+                        tc::tmem_ld8(o_col(0) + lanes + x, o);
+                        tc::ld_wait();
+                    }
+                    float g[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) g[i] = 0.f;
+                    if (gated && p.gate_vec && real) {
+                        const uint4 u = gdna::ask4(p.gate, gate_row + x, p.dtype, true), v = gdna::ask4(p.gate, gate_row + x + 4, p.dtype, true);
+                        const float4 a = gdna::got4(u, p.dtype, true), b = gdna::got4(v, p.dtype, true);
+                        g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w; g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
+                    } else if (gated && real) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (x + i < p.d) g[i] = gdna::load_elem(p.gate, gate_row + x + i, p.dtype);
+                    }
+                    const uint16_t *poison = reinterpret_cast<const uint16_t *>(sh.poison[slot]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (poisoned && poison[x + i] <= (it.causal ? t : 0)) o[i] = __int_as_float(0x7fffffff);
+                        o[i] *= norm * (gated ? sigmoid(g[i]) : 1.f);
+                    }
+                    if (p.out_vec && real) {
+                        gdna::store4(p.out, out_row + x, p.out_dtype, true, make_float4(o[0], o[1], o[2], o[3]));
+                        gdna::store4(p.out, out_row + x + 4, p.out_dtype, true, make_float4(o[4], o[5], o[6], o[7]));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t at = at0 + (((4 * half + i) ^ (lane & 7)) << 4);
-                            float g[8];
-                            if (gate_pieces) {
+                        for (int i = 0; i < 8; ++i)
+                            if (real && x + i < p.d) gdna::store_elem(p.out, out_row + x + i, p.out_dtype, o[i]);
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint32_t here = stage + c * kNext;
+                    if (gate_pieces) {
+                        if (S::kOutRoom && c > 0) ask_gates(c);
+                        if (S::kOutRoom || c == 0) asm volatile("cp.async.wait_all;" ::: "memory");
+                        __syncwarp();
+                    }
+                    // (rolled up: this code runs once an item, out of a cold instruction cache; unrolled it took longer)
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        const int x = 64 * c + 32 * half;
+                        float o[32];
+                        if (blocks > 0) {
+                            tc::tmem_ld32(o_col(wg) + lanes + x, o);
+                            tc::ld_wait();
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+                        }
+                        if (poisoned) {
+                            const uint16_t *poison = reinterpret_cast<const uint16_t *>(sh.poison[slot]);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (poison[x + i] <= (it.causal ? t : 0)) o[i] = __int_as_float(0x7fffffff);
+                        }
+                        if (!final_rows) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (real)
+                                    *reinterpret_cast<float4 *>(part + ((int64_t)(x / 4 + i) * S::kRows + r) * 4) =
+                                        make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            continue;
+                        }
+                        const uint32_t at0 = here + lane * 128;
+                        if (plain) {
+                            uint32_t u[4][4];              // (all gates first, so that the four chains of latencies run side by side)
+                            if (gated) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) lds16(u[i], at0 + (((4 * half + i) ^ (lane & 7)) << 4));
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float2 g = unpack16<BF16>(u[i / 4][i % 4]);
+                                    o[2 * i] *= sigmoid(g.x);
+                                    o[2 * i + 1] *= sigmoid(g.y);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) u[i / 4][i % 4] = pack16<BF16>(o[2 * i] * norm, o[2 * i + 1] * norm);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                sts16(at0 + (((4 * half + i) ^ (lane & 7)) << 4), u[i][0], u[i][1], u[i][2], u[i][3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t at = at0 + (((4 * half + i) ^ (lane & 7)) << 4);
+                                float g[8];
+                                if (gate_pieces) {
+                                    uint32_t u[4];
+                                    lds16(u, at);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float2 f = p.dtype == GDNA_BF16 ? unpack16<true>(u[e]) : unpack16<false>(u[e]);
+                                        g[2 * e] = f.x;
+                                        g[2 * e + 1] = f.y;
+                                    }
+                                } else if (gated && p.gate_vec) {          // (fp32)
+                                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+                                    if (real && x + 8 * i < p.d) {
+                                        const float4 *from = reinterpret_cast<const float4 *>(static_cast<const float *>(p.gate) + gate_row + x + 8 * i);
+                                        a = from[0];
+                                        b = from[1];
+                                    }
+                                    g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w; g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
+                                } else if (gated) {
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e)
+                                        g[e] = real && x + 8 * i + e < p.d ? gdna::load_elem(p.gate, gate_row + x + 8 * i + e, p.dtype) : 0.f;
+                                }
+                                float y[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) y[e] = o[8 * i + e] * norm * (gated ? sigmoid(g[e]) : 1.f);
                                 uint32_t u[4];
-                                lds16(u, at);
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float2 f = p.dtype == GDNA_BF16 ? unpack16<true>(u[e]) : unpack16<false>(u[e]);
-                                    g[2 * e] = f.x;
-                                    g[2 * e + 1] = f.y;
-                                }
-                            } else if (gated && p.gate_vec) {          // (fp32)
-                                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-                                if (real && x + 8 * i < p.d) {
-                                    const float4 *from = reinterpret_cast<const float4 *>(static_cast<const float *>(p.gate) + gate_row + x + 8 * i);
-                                    a = from[0];
-                                    b = from[1];
-                                }
-                                g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w; g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
-                            } else if (gated) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    g[e] = real && x + 8 * i + e < p.d ? gdna::load_elem(p.gate, gate_row + x + 8 * i + e, p.dtype) : 0.f;
-                            }
-                            float y[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) y[e] = o[8 * i + e] * norm * (gated ? sigmoid(g[e]) : 1.f);
-                            uint32_t u[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                u[e] = p.out_dtype == GDNA_BF16 ? pack16<true>(y[2 * e], y[2 * e + 1]) : pack16<false>(y[2 * e], y[2 * e + 1]);
-                            sts16(at, u[0], u[1], u[2], u[3]);
-                        }
-                    }
-                }
-                if (!final_rows) continue;
-                __syncwarp();
-                const int col = 64 * c + 8 * (lane & 7);
-#pragma unroll 1
-                for (int i0 = 0; i0 < 8; i0 += 4) {
-                    uint16_t *at[4];
-                    uint32_t u[4][4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int from = 4 * (i0 + i) + (lane >> 3);
-                        at[i] = static_cast<uint16_t *>(p.out) + (__shfl_sync(kFull, out_row, from) + col);
-                        lds16(u[i], here + place(from));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int from = 4 * (i0 + i) + (lane >> 3);
-                        if (!(reals >> from & 1) || col >= p.d) continue;
-                        if (p.out_vec) {
-                            *reinterpret_cast<uint4 *>(at[i]) = make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]);
-                        } else {                       // element by element
-#pragma unroll 1
-                            for (int e = 0; e < 8 && col + e < p.d; ++e) {
-                                uint16_t x;
-                                asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(here + place(from) + 2 * e) : "memory");
-                                at[i][e] = x;
+                                for (int e = 0; e < 4; ++e)
+                                    u[e] = p.out_dtype == GDNA_BF16 ? pack16<true>(y[2 * e], y[2 * e + 1]) : pack16<false>(y[2 * e], y[2 * e + 1]);
+                                sts16(at, u[0], u[1], u[2], u[3]);
                             }
                         }
                     }
+                    if (!final_rows) continue;
+                    __syncwarp();
+                    const int col = 64 * c + 8 * (lane & 7);
+#pragma unroll 1
+                    for (int i0 = 0; i0 < 8; i0 += 4) {
+                        uint16_t *at[4];
+                        uint32_t u[4][4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int from = 4 * (i0 + i) + (lane >> 3);
+                            at[i] = static_cast<uint16_t *>(p.out) + (__shfl_sync(kFull, out_row, from) + col);
+                            lds16(u[i], here + place(from));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int from = 4 * (i0 + i) + (lane >> 3);
+                            if (!(reals >> from & 1) || col >= p.d) continue;
+                            if (p.out_vec) {
+                                *reinterpret_cast<uint4 *>(at[i]) = make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]);
+                            } else {                       // element by element
+#pragma unroll 1
+                                for (int e = 0; e < 8 && col + e < p.d; ++e) {
+                                    uint16_t x;
+                                    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(here + place(from) + 2 * e) : "memory");
+                                    at[i][e] = x;
+                                }
+                            }
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                if (TILES == 1) {
-                    arrive(&sh.o_free);
-                    arrive(&sh.q_over[wg]);
-                }
+                if (TILES == 1) arrive(&sh.o_free);
                 arrive(&sh.item_empty[slot]);
             }
             blocks_all += blocks;
