@@ -17,6 +17,8 @@ struct NormParams {
     int64_t rows, x_stride, y_stride, gate_stride, x_out_stride, h_stride;
     int x_dtype, y_dtype, h_dtype, c;
     float scale, eps;
+    int phase;                      // elements from a boundary of eight to the first row (set by the launcher)
+    bool gate_pieces;               // the gate's rows begin where the others do
 };
 
 // How keys come into shared memory: 16-bit rows by tensor copies, E4M3 codes by tensor copies, or loads (16 bytes at a time, or

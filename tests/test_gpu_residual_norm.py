@@ -104,6 +104,29 @@ def test_alignment(cuda_lib, pad, before):
     check(30, 1024, "bf16", "bf16", "f32", gate="rows", pad=pad, before=before)
 
 
+@pytest.mark.parametrize("c", [63, 65, 71, 1023, 1030, 4095, 8191, 16369, 16370, 16371])
+@pytest.mark.parametrize("rows", [9, 1300])
+@pytest.mark.parametrize("gate", ["rows", "one"])
+def test_rows_that_begin_anywhere(cuda_lib, c, rows, gate):
+    """Odd widths side by side: every phase of eight elements, first and last groups of a row in part; one row a block and many."""
+    check(rows, c, "bf16", "bf16", "bf16", gate=gate, pad=0, seed=c)
+    check(rows, c, "f32", "f16", "f32", gate=gate, pad=2, post=gate == "one", pre=gate == "rows", seed=c)
+
+
+@pytest.mark.parametrize("before", [0, 1, 3, 7])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_first_row_anywhere(cuda_lib, before, x):
+    check(300, 2881, x, h=x, with_y=False, pad=0, before=before)
+    check(2000, 777, x, h=x, with_y=False, with_x=False, pad=1, before=before)
+    check(1500, 999, x, x, x, in_place=True, pad=0, before=before)
+
+
+@pytest.mark.parametrize("c,rows", [(2881, 1500), (513, 3000), (12001, 400)])
+def test_odd_widths_in_place(cuda_lib, c, rows):
+    check(rows, c, "bf16", "bf16", "bf16", gate="rows", in_place=True, pad=0)
+    check(rows, c, "f32", "f32", "f32", gate="one", in_place=True, pad=0)
+
+
 def test_zeros_and_large_values(cuda_lib):
     check(5, 640, "f32", "f32", "f32", size=0.0, eps=1e-6)
     check(5, 640, "f32", "bf16", "f32", size=1e12, eps=0.0)
