@@ -42,10 +42,11 @@
 //
 // What bounds it (GB300, device time).  Long lists of keys: 512 rows over 60000 keys of 8 heads of 128 take 373 us, 1357 TFLOP/s or
 // 0.71 of the measured rate; there shared memory is full: Q and K of the first product take its 128 bytes a cycle by themselves,
-// and the copies come on top.  Prompts: eight of 4096, 24/4 heads of 256, 1741 us (948 TFLOP/s), a packed batch at 128 1526 us (1108): what a
-// tile costs beside its keys, some 16000 cycles of queries, first scores and output to 19 blocks of 4000.  Heads of 64: 226 us (389
+// and the copies come on top.  Prompts: eight of 4096, 24/4 heads of 256, 1560 us (1057 TFLOP/s): 128 KB of keys and values a block of 4000
+// cycles from L2, through a ring that holds 1.25 blocks; the next tile's queries and first scores come while a tile's output is written.
+// A packed batch at 128 1526 us (1108): what a tile costs beside its keys, queries, first scores and output.  Heads of 64: 215 us (408
 // TFLOP/s), the softmax warps' issue slots.  E4M3: 223 us for 107 GFLOP, the widening (one conversion of two codes takes a quarter of the
-// schedulers' time).  Short calls: 25 us for one prompt of 180 tokens: 2 us until sums of lengths are there, 3 until the first item is
+// schedulers' time).  Short calls: 23 us for one prompt of 180 tokens: 2 us until sums of lengths are there, 3 until the first item is
 // dealt, then a chain of copies, products, softmax, output, in code that no cache holds yet.
 #pragma once
 
