@@ -40,10 +40,10 @@
 // keys, values that are not finite are taken out of V (0 x NaN) and the first such key of each column is noted: the rows
 // that see it come out NaN in that column, the others clean.  Keys past the end count as zeros.
 //
-// What bounds it (GB300, device time).  Long lists of keys: 512 rows over 60000 keys of 8 heads of 128 take 373 us, 1357 TFLOP/s or
-// 0.71 of the measured rate; there shared memory is full: Q and K of the first product take its 128 bytes a cycle by themselves,
-// and the copies come on top.  Prompts: eight of 4096, 24/4 heads of 256, 1560 us (1057 TFLOP/s): 128 KB of keys and values a block of 4000
-// cycles from L2, through a ring that holds 1.25 blocks; the next tile's queries and first scores come while a tile's output is written.
+// What bounds it (GB300, device time).  Long lists of keys: 512 rows over 60000 keys of 8 heads of 128 take 334 us, 1511 TFLOP/s or
+// 0.79 of the measured rate; there shared memory is full: Q and K of the first product take its 128 bytes a cycle by themselves,
+// and the copies come on top.  Prompts: eight of 4096, 24/4 heads of 256, 1564 us (1055 TFLOP/s; two of 16384
+// 1305): what a tile costs beside its 16 blocks, gates and output (without gates 1406); the next one's queries and first scores come meanwhile.
 // A packed batch at 128 1526 us (1108): what a tile costs beside its keys, queries, first scores and output.  Heads of 64: 215 us (408
 // TFLOP/s), the softmax warps' issue slots.  E4M3: 223 us for 107 GFLOP, the widening (one conversion of two codes takes a quarter of the
 // schedulers' time).  Short calls: 23 us for one prompt of 180 tokens: 2 us until sums of lengths are there, 3 until the first item is
@@ -69,6 +69,7 @@ constexpr int kItems = 4;                  // slots of the work queue
 constexpr int kCopyWarps = 4;
 constexpr int kLead = 256;                 // what a tile costs beside its keys, in keys: queries, first products, output
 constexpr int kLeastChunk = 768;           // a block's run of the row of costs, at least; tiles that cost less stay whole
+constexpr int kLongItem = 32;               // blocks from which on the order of an item's keys is chosen
 static_assert(kLeastChunk >= kKeys, "every block between a tile's first and last has keys of it");
 constexpr int kLeastPart = 256;            // the same where every result is a partial one: a block of keys or two (four requests, one
                                            // prefix of 3000: 43 us against 49)
@@ -269,6 +270,7 @@ struct Item {
     int64_t row0;                          // first row of the segment
     int n, kv, head, token0;               // token0: first token of the tile
     int first, last;                       // key blocks [first, last)
+    int turned, by;                        // of which [first, turned), which all rows see, come from first + by on, then from first on
     int whole;                             // all of the tile's: the result is final
     int causal;
     int clear;                             // keys that its first token sees: a value from there on may be out of some row's sight
@@ -276,6 +278,13 @@ struct Item {
     int64_t slot;                          // of the partial result
     int valid;
 };
+// The block that is copied as the j-th (`turned` and `by` matter to the copies alone: rows see all of any block before `turned`).
+__device__ __forceinline__ int block_at(const Item &it, int j)
+{
+    if (j >= it.turned) return j;
+    j += it.by;
+    return j < it.turned ? j : j - (it.turned - it.first);
+}
 
 // ------------------------------------------------------------------ tensor core pieces (16-bit operands)
 
@@ -1143,7 +1152,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             };
             Window win;
             win.load(p, 0, 0, 0);
-            auto write = [&](int head, int64_t tau, int first, int last, bool whole, int64_t slot) {
+            auto write = [&](int head, int64_t tau, int first, int last, bool whole, int64_t slot, int turned, int by) {
                 Item &it = sh.item[n % kItems];
                 const int token0 = (int)(tau * p.tile_tokens);
                 it.row0 = win.s.row0;
@@ -1153,6 +1162,8 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 it.token0 = token0;
                 it.first = first;
                 it.last = last;
+                it.turned = turned;
+                it.by = by;
                 it.whole = whole;
                 it.causal = win.s.causal;
                 it.clear = win.s.causal ? win.s.kv - win.s.n + token0 + 1 : win.s.kv;
@@ -1174,7 +1185,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     ok = room();
                     if (ok && lane == at) {
                         const int64_t idx = i - (win.tiles - win.t.count * p.nkv), row = quotient(idx, p.nkv), tau = win.t.count - 1 - row;
-                        write((int)(idx - row * p.nkv), tau, 0, (int)(((int64_t)keys_of(p, win.t, tau) + kKeys - 1) / kKeys), true, 0);
+                        write((int)(idx - row * p.nkv), tau, 0, (int)(((int64_t)keys_of(p, win.t, tau) + kKeys - 1) / kKeys), true, 0, 0, 0);
                     }
                     if (ok) tell();
                 }
@@ -1214,7 +1225,20 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     }
                     if (__shfl_sync(kFull, some, at)) {
                         ok = room();
-                        if (ok && lane == at) write(head, tau, first, last, first == 0 && last == blocks, tile + c);
+                        if (ok && lane == at) {
+                            // Runs of one head's tiles begin at different keys, and what one block has read the others would
+                            // read again long after.  So a long item's keys are taken in an order by which all blocks are at
+                            // equal keys, modulo a run, at equal times: 512 rows over 60000 keys 375 -> 334 us, heads of 256 895 -> 589.
+                            int turned = 0, by = 0;
+                            if (last - first >= kLongItem) {
+                                const int64_t period = run / kKeys, late = ((x - x0) / kKeys - first) % period;
+                                const int clear = win.s.causal ? win.s.kv - win.s.n + (int)(tau * p.tile_tokens) + 1 : win.s.kv;
+                                turned = min(last, clear / kKeys);
+                                by = (int)(late < 0 ? late + period : late);
+                                if (first + by >= turned) turned = by = 0;
+                            }
+                            write(head, tau, first, last, first == 0 && last == blocks, tile + c, turned, by);
+                        }
                         if (ok) tell();
                     }
                     x = __shfl_sync(kFull, end, at);
@@ -1252,6 +1276,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 }
                 return x;
             };
+            // (in the ring's order, which the copying warps count on: K of the next block before V of this one)
             auto release = [&](const Stages &x) {
                 if (leader)
 #pragma unroll
@@ -1473,7 +1498,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 if (f % fillers != (uint32_t)me) return true;
                 const int st = f % S::kStages;
                 const uint32_t dst = ring + st * S::kStage, phase = ((f / S::kStages) & 1) ^ 1;
-                const int key0 = j * kKeys, keys = min(kKeys, it.kv - key0);       // (at least one)
+                const int key0 = block_at(it, j) * kKeys, keys = min(kKeys, it.kv - key0);       // (at least one)
                 const int clear = is_v ? it.clear - key0 : kKeys;
                 const bool masked = clear < kKeys;
                 auto page_of = [&](int key, int &token) -> int {       // (key < kv)

@@ -300,6 +300,12 @@ def test_waits_that_run_out(cuda_lib, d):
     check_prompt(s)
 
 
+@pytest.mark.parametrize("d,cache", [(64, "bf16"), (128, "f16"), (128, "e4m3"), (256, "bf16")])
+def test_long_items(cuda_lib, d, cache):
+    """Tiles split into runs of some 40 blocks, whose keys are not taken from the first on."""
+    check_prompt(make_prompt([300, 2], [90000, 30011], 4, 4, d, cache=cache, page=24, seed=d, scale8=0.25 if cache == "e4m3" else 1.0), gated=8)
+
+
 def test_a_long_cache(cuda_lib):
     """Places in the cache beyond 2^31 elements."""
     d, nkv, page, n = 128, 2, 256, 5000
