@@ -120,19 +120,23 @@ struct Tiles {
     int64_t count;                         // tiles
     int64_t base;                          // cost of a tile beside its own tokens
     int64_t cost;                          // of all
-    int step;                              // tokens a tile adds (0: every tile sees all keys)
+    int step;                              // tokens a tile adds (0: every tile costs the same)
     int n, kv;
+    bool causal;
 };
 __device__ __forceinline__ Tiles tiles_of(const FlashParams &p, const Segment &s)
 {
     Tiles t;
     t.n = s.n;
     t.kv = s.kv;
+    t.causal = s.causal;
     t.count = ((int64_t)s.n + p.tile_tokens - 1) / p.tile_tokens;
-    t.step = s.causal ? p.tile_tokens : 0;
-    t.base = kLead + (s.causal ? max(s.kv - s.n, 0) : s.kv);
+    // Of more tokens than keys the first see none, and all tiles cost what the last does: no tile's cost may pass kLead and its
+    // segment's keys, which is what the launcher goes by (never_split).
+    t.step = s.causal && s.n <= s.kv ? p.tile_tokens : 0;
+    t.base = kLead + (t.step != 0 ? s.kv - s.n : s.kv);
     t.cost = t.count * t.base;
-    if (s.causal && t.count > 0) t.cost += (int64_t)t.step * (t.count * (t.count - 1) / 2) + s.n;
+    if (t.step != 0 && t.count > 0) t.cost += (int64_t)t.step * (t.count * (t.count - 1) / 2) + s.n;
     return t;
 }
 __device__ __forceinline__ int64_t cost_before(const Tiles &t, int64_t tau)       // of tiles [0, tau), tau < count
@@ -146,7 +150,7 @@ __device__ __forceinline__ int64_t cost_of(const FlashParams &p, const Tiles &t,
 // Keys that tile tau's last token sees, and its blocks.
 __device__ __forceinline__ int keys_of(const FlashParams &p, const Tiles &t, int64_t tau)
 {
-    if (t.step == 0) return t.kv;
+    if (!t.causal) return t.kv;
     const int64_t k = t.kv - (int64_t)t.n + min((tau + 1) * (int64_t)p.tile_tokens, (int64_t)t.n);
     return k < 0 ? 0 : (int)k;
 }
@@ -210,6 +214,8 @@ __device__ __forceinline__ bool whole_tiles(const FlashParams &p, const Totals &
 {
     return !p.all_parts && (all.tiles >= 2 * (int64_t)p.grid || all.tiles > p.most_tiles || all.cost <= all.tiles * kLeastChunk);
 }
+// Whether whole_tiles() is sure to hold, whatever the lengths, where no segment has more than `keys` keys: then nothing is to be joined.
+inline bool never_split(const FlashParams &p, int64_t keys) { return !p.all_parts && keys + kLead <= kLeastChunk; }
 // Cost of a block's run.
 __device__ __forceinline__ int64_t run_of(const FlashParams &p, const Totals &all)
 {

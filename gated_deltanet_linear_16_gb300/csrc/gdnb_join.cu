@@ -200,9 +200,8 @@ cudaError_t launch_flash(FlashParams p, cudaStream_t s)
                           : p.d <= 128 ? (bf16 ? launch_flash_128_bf16(p, s) : launch_flash_128_f16(p, s))
                                        : (bf16 ? launch_flash_256_bf16(p, s) : launch_flash_256_f16(p, s));
     if (e != cudaSuccess) return e;
-    // lists of keys so short that no tile is split (as the kernel has it): nothing to join
     const int64_t keys = p.table != nullptr ? (int64_t)p.max_pages * p.cache.page_size : p.rows;
-    if (!p.all_parts && keys + kLead <= kLeastChunk) return cudaSuccess;
+    if (never_split(p, keys)) return cudaSuccess;
     return p.d <= 64 ? launch_join<64>(p, to_join, s) : p.d <= 128 ? launch_join<128>(p, to_join, s) : launch_join<256>(p, to_join, s);
 }
 
