@@ -385,6 +385,8 @@ template <int D> struct Shared {                               // beside queries
     int64_t red[kThreads / 32][2];
     uint32_t tmem;
     int dead, turn;                                            // turn: a product warp issues, the other waits
+    uint8_t landed_turn[8];                                    // parity of a stage's next copy that lands before it is looked at
+    uint8_t flying[kCopyWarps][2];                             // a copying warp's last two tensor copies: 128, 16: landed, 8: parity, stage
     int poisoned[kItems];
     uint32_t poison[kItems][D / 2];                            // 16 bits a column: which rows see a value that is not finite
 };
@@ -669,6 +671,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             tc::mbar_init(&sh.full[i], 1);
             tc::mbar_init(&sh.empty[i], TILES);
             tc::mbar_init(&sh.landed[i], 1);
+            sh.landed_turn[i] = 0;
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&sh.q_full[i], 4);
@@ -685,6 +688,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             tc::mbar_init(&sh.item_empty[i], TILES + 1 + kCopyWarps + 8);
         }
         sh.turn = 0;
+        for (int i = 0; i < kCopyWarps; ++i) sh.flying[i][0] = sh.flying[i][1] = 0;
         sh.dead = (base & 1023u) != 0;                 // (dynamic shared memory starts where the swizzle can)
         if (sh.dead) atomicAdd(&g_wait_timeouts, 1u);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1424,10 +1428,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                             const uint32_t turn = (turns >> st) & 1;
                             turns ^= 1u << st;
                             ok = wait_warp(&sh.landed[st], turn);
-                            if (!ok) {
-                                wait_out(&sh.landed[st], turn);
-                                break;
-                            }
+                            if (!ok) break;
                             sanitize<D, BF16, S::kCols>(sh, slot, ring + st * S::kStage, min(kKeys, it.kv - key0), clear, h * S::kCols, lane);
                             tc::fence_smem_async();
                             __syncwarp();
@@ -1443,7 +1444,6 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             constexpr int kPanels = S::kCols / 64, kPieces = S::kCols / 8;
             const int me = warp - 12;
             uint32_t items = 0, fills = 0;
-            int64_t flying[2] = {-1, -1};              // this warp's last tensor copies: stages' fills
 
             const bool codes = COPY == kCodeCopies || (COPY == kLoads && p.cache_dtype == GDNA_E4M3);
             constexpr bool ahead = COPY == kCodeCopies;
@@ -1535,6 +1535,13 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                     }
                     // (a masked stage goes on to the warp that looks at its values)
                     uint64_t *bar = masked ? &sh.landed[st] : &sh.full[st];
+                    uint32_t parity = phase ^ 1;
+                    if (masked) {
+                        parity = *(volatile uint8_t *)&sh.landed_turn[st];
+                        __syncwarp();
+                        if (lane == 0) *(volatile uint8_t *)&sh.landed_turn[st] = (uint8_t)(parity ^ 1);
+                    }
+                    if (lane == 0) sh.flying[me][f / fillers & 1] = (uint8_t)(128u | (masked ? 16u : 0u) | parity << 3 | st);
                     if (lane == 0) arrive_expect(bar, (uint32_t)(count * kPanels * per * 128));
                     __syncwarp();
                     if (lane < count)
@@ -1542,10 +1549,6 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                         for (int x = 0; x < kPanels; ++x)
                             copy_box(dst + x * S::kPanelBytes + lane * per * 128, is_v ? &v_map : &k_map, h * S::kCols + 64 * x, token,
                                      it.head, page, bar);
-                    if (!masked) {
-                        flying[0] = flying[1];
-                        flying[1] = f;
-                    }
                     return true;
                 } else {
 
@@ -1626,13 +1629,20 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             }
             __syncwarp();
             if (ahead && w_fill >= 0) wait_out(&sh.landed[w_fill % S::kStages], (uint32_t)(w_fill / S::kStages) & 1);
-            if (*(volatile int *)&sh.dead)             // copies in flight land before their memory is another block's
-                for (int i = 0; i < 2; ++i)
-                    if (flying[i] >= 0) wait_out(&sh.full[flying[i] % S::kStages], (uint32_t)(flying[i] / S::kStages) & 1);
         }
     }
     __syncthreads();
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
+    // Where a wait ran out, anywhere in the block: copies in flight land before their memory is another block's.  (Asked here, as
+    // the warp whose copies they are may have had nothing to wait for.  Two a warp: its third is asked for only after its first has
+    // been used.)
+    if (*(volatile int *)&sh.dead == 0) return;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (COPY == kTensorCopies && warp >= 12)
+        for (int i = 0; i < 2; ++i) {
+            const unsigned x = *(volatile uint8_t *)&sh.flying[warp - 12][i];
+            if (x != 0) wait_out(x & 16 ? &sh.landed[x & 7] : &sh.full[x & 7], x >> 3 & 1);
+        }
 }
 
 // ------------------------------------------------------------------ launch

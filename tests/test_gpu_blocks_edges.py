@@ -4,7 +4,8 @@ import pytest
 import torch
 
 import gated_deltanet_linear_16_gb300 as gdn
-from tests.prompt_helpers import check_prompt, make_prompt
+from tests.attn_layers_helpers import guarded, intact
+from tests.prompt_helpers import call_prompt, check_prompt, make_prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -28,7 +29,6 @@ def test_lengths_beyond_the_table(cuda_lib, d):
     lens = torch.tensor([1300, 1 << 30], dtype=torch.int32, device="cuda")
     whole = torch.full((s["rows"], 6 * d), 77.0, dtype=torch.bfloat16, device="cuda")
     want = whole.clone()
-    from tests.prompt_helpers import call_prompt
     call_prompt(s, want, max_pages=8)
     pages = s["pages"]
     k, v = pages.store.addresses()
@@ -38,3 +38,23 @@ def test_lengths_beyond_the_table(cuda_lib, d):
                          table_stride=pages.table.stride(0), max_pages=8, **pages.store.args())
     torch.cuda.synchronize()
     assert torch.equal(whole, want)
+
+
+@pytest.mark.parametrize("d,cache,page", [(64, "bf16", 16), (128, "bf16", 24), (128, "e4m3", 16), (128, "f16", 5), (256, "bf16", 64),
+                                          (256, "e4m3", 32)])
+@pytest.mark.parametrize("polls", [1, 2, 4, 8, 16, 40, 100, 300])
+def test_waits_that_run_out_on_the_way(cuda_lib, d, cache, page, polls):
+    """Too few polls for some of the waits: blocks give up with copies and products in flight, and wait those out before they
+    end.  What is right is not asked of this call but of the next."""
+    s = make_prompt([200, 10, 700], [300, 5000, 0], 4, 2, d, cache=cache, page=page, seed=3, scale8=0.25 if cache == "e4m3" else 1.0)
+    whole, out = guarded(s["rows"], 4 * d, 4 * d + 8, "bf16", before=8)
+    gdn.gdn_set_wait_polls(polls)
+    try:
+        for _ in range(3):
+            call_prompt(s, out)
+            torch.cuda.synchronize()
+    finally:
+        gdn.gdn_set_wait_polls(gdn.GDN_DEFAULT_WAIT_POLLS)
+    gdn.gdn_device_wait_timeouts()
+    assert intact(whole, out)
+    check_prompt(s)
