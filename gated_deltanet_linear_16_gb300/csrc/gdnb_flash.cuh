@@ -766,7 +766,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             for (int j = 0; j < blocks; ++j) {
                 const int b = TILES == 2 ? 0 : (int)((blocks_all + j) & 1);
                 const int col = TILES == 2 ? wg : b;   // which S
-                ok = wait_warp(&sh.s_full[wg][b], s_count[b]++ & 1);
+                ok = wait_long(&sh.s_full[wg][b], s_count[b]++ & 1);   // (the first of a second row tile: while another item is without one)
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (TILES == 1 && j + 1 == blocks && lane == 0) arrive(&sh.q_over[wg]);    // nothing reads these queries any more
@@ -1427,7 +1427,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                             const int st = (fills + h) % S::kStages;
                             const uint32_t turn = (turns >> st) & 1;
                             turns ^= 1u << st;
-                            ok = wait_warp(&sh.landed[st], turn);
+                            ok = wait_long(&sh.landed[st], turn);  // (the first: while all other blocks pass)
                             if (!ok) break;
                             sanitize<D, BF16, S::kCols>(sh, slot, ring + st * S::kStage, min(kKeys, it.kv - key0), clear, h * S::kCols, lane);
                             tc::fence_smem_async();

@@ -110,7 +110,8 @@ GDN_API int64_t gdnb_attn_prompt_workspace(int64_t rows, int batch, int nq, int 
  *   tokens are brought in by tensor copies; other pages, types and layouts by
  *   loads, slower where the GPU waits for them.
  *   The kernels' waits for their own copies and products are bounded
- *   (gdn_set_wait_polls); where one runs out, that block's rows are incomplete and
+ *   (gdn_set_wait_polls; a wait that lasts as long as a sequence's keys by 256 times
+ *   the polls); where one runs out, that block's rows are incomplete and
  *   gdn_device_wait_timeouts counts it.
  */
 GDN_API int gdnb_attn_prompt(const void *q, gdna_dtype dtype, const void *gate,

@@ -4,8 +4,8 @@ import pytest
 import torch
 
 import gated_deltanet_linear_16_gb300 as gdn
-from tests.attn_layers_helpers import guarded, intact
-from tests.prompt_helpers import call_prompt, check_prompt, make_prompt
+from tests.attn_layers_helpers import TYPES, guarded, intact
+from tests.prompt_helpers import Pages, call_prompt, check_prompt, make_prompt, rand, starts_of, tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,42 @@ def test_waits_that_run_out_on_the_way(cuda_lib, d, cache, page, polls):
     gdn.gdn_device_wait_timeouts()
     assert intact(whole, out)
     check_prompt(s)
+
+
+@pytest.mark.parametrize("d,cache", [(64, "bf16"), (128, "bf16"), (128, "e4m3"), (256, "f16")])
+def test_waits_as_long_as_an_item(cuda_lib, d, cache):
+    """Few polls a wait, and items of a million keys: a warp that has nothing to do until the next item, or until the last keys
+    of this one, has polls enough.  (First an item of one row a block, then one of both row tiles: the second tile's warps
+    wait for the first item's end.)  The list of keys is four pages again and again."""
+    page, times, short, long = 64, 4096, torch.cuda.get_device_properties(0).multi_processor_count, 200
+    n, cycle, batch = 4 * page * times, 4 * page, 2 * short
+    gen = torch.Generator().manual_seed(d)
+    store = Pages([cycle], 1, d, cache, page, scale=0.25 if cache == "e4m3" else 1.0, gen=gen)
+    at = store.where[0][0][::page].to(torch.int32)
+    table = at.repeat(times).repeat(batch, 1).cuda()
+    fresh = [1] * short + [long] * short
+    starts = torch.tensor(starts_of(fresh), dtype=torch.int32, device="cuda")
+    rows = sum(fresh)
+    q = rand(gen, rows, d).to(TYPES["f16" if cache != "bf16" else "bf16"]).cuda()
+    whole, out = guarded(rows, d, d + 8, "bf16", before=8)
+    lens = torch.full((batch,), n, dtype=torch.int32, device="cuda")
+    ws = torch.empty(gdn.gdnb_attn_prompt_workspace(rows=rows, batch=batch, nq=1, nkv=1, d=d), dtype=torch.uint8, device="cuda")
+    k, v = store.store.addresses()
+    scale8 = store.scale
+    before = gdn.gdn_device_wait_timeouts()
+    gdn.gdn_set_wait_polls(40)
+    try:
+        gdn.gdnb_attn_prompt(q, k, v, starts, lens, out, ws, rows=rows, batch=batch, nq=1, nkv=1, d=d, table=table, max_pages=4 * times,
+                             k_scale=scale8, v_scale=scale8, out_stride=out.stride(0), **store.store.args())
+        torch.cuda.synchronize()
+    finally:
+        gdn.gdn_set_wait_polls(gdn.GDN_DEFAULT_WAIT_POLLS)
+    assert gdn.gdn_device_wait_timeouts() == before
+    behind = torch.cat([torch.full((f,), f - 1) - torch.arange(f) for f in fresh]).cuda()      # keys at the end that a row does not see
+    count = times - (torch.arange(cycle, device="cuda")[None] >= cycle - behind[:, None]).double()
+    keys, values = store.keys[0][:, 0].double(), store.values[0][:, 0].double()
+    s = q.double() @ keys.T * d ** -0.5
+    want = torch.softmax(s + torch.log(count), -1) @ values
+    size = (q.double().abs() @ keys.abs().T * d ** -0.5).amax(-1, keepdim=True)
+    tol = tolerance(want, size, values.abs().amax(), n, d, "bf16", cache, "bf16")
+    assert ((out.double() - want).abs() <= tol).all() and intact(whole, out)
