@@ -47,6 +47,20 @@ SharedSpace shared_space(int batch, int groups, int q_len, int nq, int nkv, int 
     return SharedSpace{round256(attn_workspace_bytes((int64_t)q_len * (nq / nkv), d)), round256(rows * nq * d * 4), round256(rows * nq * 4),
                        gdnb::flash_parts_bytes(rows, groups, nq / nkv, nkv, d, true), false};
 }
+// What a caller has to bring: never less for more requests, groups or tokens, so that scratch for a server's largest step serves the
+// smaller ones.  A step whose own keys go with the prefix needs a partial result for each of their tiles, more than a somewhat larger
+// step by the other way, so the largest such steps within this one count too: of so many tiles a request, all tokens that those
+// hold, and as many requests as go together.
+int64_t shared_bytes(int batch, int groups, int q_len, int nq, int nkv, int d)
+{
+    int64_t most = shared_space(batch, groups, q_len, nq, nkv, d).all();
+    const int64_t tile = gdnb::flash_tile_tokens(nq / nkv, d);
+    for (int64_t each = 1; each * nkv <= kTogether && (each - 1) * tile < q_len; ++each) {
+        const int64_t tokens = std::min<int64_t>(q_len, each * tile), requests = std::min<int64_t>(batch, kTogether / (each * nkv));
+        most = std::max(most, shared_space((int)requests, groups, (int)tokens, nq, nkv, d).all());
+    }
+    return most;
+}
 
 }  // namespace
 
@@ -169,7 +183,7 @@ GDN_API int64_t gdnb_attn_shared_workspace(int batch, int groups, int q_len, int
     if (batch < 0 || q_len < 0 || groups < 1 || groups > kMostSegments || !heads_ok(nq, nkv, d) || !countable(batch, q_len, nq) ||
         (int64_t)batch * q_len > kMostRows)
         return 0;
-    return shared_space(batch, groups, q_len, nq, nkv, d).all();
+    return shared_bytes(batch, groups, q_len, nq, nkv, d);
 }
 
 GDN_API int gdnb_attn_shared(const void *q, gdna_dtype dtype, const void *gate,
@@ -199,11 +213,12 @@ GDN_API int gdnb_attn_shared(const void *q, gdna_dtype dtype, const void *gate,
     if (most > 4e18) return GDN_ERR_UNSUPPORTED;
     if (k_cache == nullptr || v_cache == nullptr || shared_table == nullptr || shared_len == nullptr) return GDN_ERR_ARG;
     const SharedSpace space = shared_space(batch, groups, q_len, nq, nkv, d);
+    const int64_t need = shared_bytes(batch, groups, q_len, nq, nkv, d);
     const CacheLayout cache{page_stride, token_stride, head_stride, pages, page_size};
     Operand ops[12];
     int n = 0;
     ops[n++] = {out, rows, hq, out_stride, 2};
-    ops[n++] = {workspace, 1, space.all(), space.all(), 1};
+    ops[n++] = {workspace, 1, need, need, 1};
     const int n_out = n;
     int st = check_cache(k_cache, v_cache, cache_dtype, cache, nkv, d, &ops[n], &ops[n + 1]);
     if (st != GDN_OK && st != GDN_ERR_ALIAS) return st;
@@ -217,7 +232,7 @@ GDN_API int gdnb_attn_shared(const void *q, gdna_dtype dtype, const void *gate,
     if (gate != nullptr) ops[n++] = {gate, rows, heads_len(nq, gate_head_stride, d), gate_stride, elem_size(dtype)};
     st = check_operands(ops, n, n_out);
     if (st != GDN_OK) return st;
-    if (workspace_bytes < space.all()) return GDN_ERR_ARG;
+    if (workspace_bytes < need) return GDN_ERR_ARG;
     if (!aligned(workspace, 16)) return GDN_ERR_ALIGN;
 
     uint8_t *at = static_cast<uint8_t *>(workspace);

@@ -61,7 +61,8 @@ cudaError_t launch_residual_norm(const NormParams &p, bool vec, cudaStream_t s);
 cudaError_t launch_flash(FlashParams p, cudaStream_t s);
 // Partial results: bytes that `segs` segments of `rows` rows need (prompt calls: a bound whatever the rows).
 int64_t flash_parts_bytes(int64_t rows, int segs, int group, int nkv, int d, bool all_parts, int64_t own_tiles = 0);
-// Tiles of `tokens` tokens of each of `segs` segments.
+// Tokens of a tile; tiles of `tokens` tokens of each of `segs` segments.
+int flash_tile_tokens(int group, int d);
 int64_t flash_tiles(int tokens, int segs, int group, int nkv, int d);
 cudaError_t flash_wait_timeouts(unsigned *count);
 

@@ -154,8 +154,7 @@ int rows_of(int d) { return d <= 128 ? 256 : 128; }
 // Tiles that `rows` rows in `segs` segments make, at most.
 int64_t most_tiles(int64_t rows, int segs, int group, int nkv, int d)
 {
-    const int64_t tokens = rows_of(d) / group;
-    return (rows / tokens + (rows < segs ? rows : segs)) * nkv;
+    return (rows / (rows_of(d) / group) + (rows < segs ? rows : segs)) * nkv;
 }
 
 }  // namespace
@@ -167,9 +166,10 @@ using namespace flash;
 static int64_t split_tiles(int64_t most, bool all_parts) { return !all_parts && most > 2 * kMaxGrid ? 2 * kMaxGrid : most; }
 static int64_t record_bytes(int64_t tiles) { return (64 + tiles * (int64_t)sizeof(Record) + 255) / 256 * 256; }
 
+int flash_tile_tokens(int group, int d) { return rows_of(d) / group; }
 int64_t flash_tiles(int tokens, int segs, int group, int nkv, int d)
 {
-    const int tile = rows_of(d) / group;
+    const int tile = flash_tile_tokens(group, d);
     return (int64_t)segs * ((tokens + tile - 1) / tile) * nkv;
 }
 
@@ -183,7 +183,7 @@ cudaError_t launch_flash(FlashParams p, cudaStream_t s)
 {
     const int sms = gdn::sm_count();
     p.grid = sms < kMaxGrid ? sms : kMaxGrid;
-    p.tile_tokens = rows_of(p.d) / p.group;
+    p.tile_tokens = flash_tile_tokens(p.group, p.d);
     p.tile_rows = p.tile_tokens * p.group;
     p.group_div = Divisor::of((unsigned)p.group);
     p.page_div = Divisor::of((unsigned)(p.table != nullptr ? p.cache.page_size : 1));

@@ -57,8 +57,8 @@ GDN_API int gdnb_residual_norm(const void *x, gdna_dtype x_dtype, const void *y,
 
 /*
  * gdnb_attn_prompt_workspace -- bytes of scratch that gdnb_attn_prompt needs for a
- * shape on any GPU this library runs on; 0 if the shape is not supported.  Makes
- * no CUDA call.
+ * shape on any GPU this library runs on (never more for fewer rows or sequences);
+ * 0 if the shape is not supported.  Makes no CUDA call.
  */
 GDN_API int64_t gdnb_attn_prompt_workspace(int64_t rows, int batch, int nq, int nkv, int d);
 
@@ -127,7 +127,8 @@ GDN_API int gdnb_attn_prompt(const void *q, gdna_dtype dtype, const void *gate,
 
 /*
  * gdnb_attn_shared_workspace -- bytes of scratch that gdnb_attn_shared needs for a
- * shape; 0 if the shape is not supported.  Makes no CUDA call.
+ * shape on any GPU this library runs on (never more for fewer requests, groups or
+ * tokens); 0 if the shape is not supported.  Makes no CUDA call.
  */
 GDN_API int64_t gdnb_attn_shared_workspace(int batch, int groups, int q_len, int nq, int nkv, int d);
 

@@ -6,6 +6,7 @@ import torch
 import gated_deltanet_linear_16_gb300 as gdn
 from tests.attn_layers_helpers import TYPES, guarded, intact
 from tests.prompt_helpers import Pages, call_prompt, check_prompt, make_prompt, rand, starts_of, tolerance
+from tests.test_gpu_attn_shared import check_shared, make_shared
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +98,13 @@ def test_waits_as_long_as_an_item(cuda_lib, d, cache):
     size = (q.double().abs() @ keys.abs().T * d ** -0.5).amax(-1, keepdim=True)
     tol = tolerance(want, size, values.abs().amax(), n, d, "bf16", cache, "bf16")
     assert ((out.double() - want).abs() <= tol).all() and intact(whole, out)
+
+
+def test_scratch_of_the_largest_step(cuda_lib):
+    """Scratch allocated once, for the largest batch, serves steps of fewer requests and tokens, whichever way their own keys go."""
+    nq, nkv, d, most = 16, 4, 128, 60
+    ws = torch.full((gdn.gdnb_attn_shared_workspace(batch=most, groups=3, q_len=3, nq=nq, nkv=nkv, d=d),), 255, dtype=torch.uint8, device="cuda")
+    for batch, q_len, prefixes in ((60, 3, [300, 70, 9]), (39, 1, [200]), (38, 3, [500, 40]), (38, 1, [100, 30, 7]), (5, 2, [1000]), (1, 1, [40])):
+        n = len(prefixes)
+        groups = [batch * (g + 1) // n - batch * g // n for g in range(n)]
+        check_shared(make_shared(prefixes, groups, [(7 * b) % 45 for b in range(batch)], nq, nkv, d, q_len=q_len, seed=batch), ws=ws)
