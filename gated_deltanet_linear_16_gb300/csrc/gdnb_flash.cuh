@@ -45,8 +45,8 @@
 // and the copies come on top.  Prompts: eight of 4096, 24/4 heads of 256, 1564 us (1055 TFLOP/s; two of 16384
 // 1305): what a tile costs beside its 16 blocks, gates and output (without gates 1406); the next one's queries and first scores come meanwhile.
 // A packed batch at 128 1526 us (1108): what a tile costs beside its keys, queries, first scores and output.  Heads of 64: 215 us (408
-// TFLOP/s), the softmax warps' issue slots.  E4M3: 223 us for 107 GFLOP, the widening (one conversion of two codes takes a quarter of the
-// schedulers' time).  Short calls: 23 us for one prompt of 180 tokens: 2 us until sums of lengths are there, 3 until the first item is
+// TFLOP/s), the softmax warps' issue slots.  E4M3, fp32 queries in two parts: 362 us for 107 GFLOP, a ring of
+// three stages (a query in one part: 217, five stages) and the widening (a conversion of two codes takes a quarter of the schedulers' time).  Short calls: 23 us for one prompt of 180 tokens: 2 us until sums of lengths are there, 3 until the first item is
 // dealt, then a chain of copies, products, softmax, output, in code that no cache holds yet.
 #pragma once
 
@@ -1692,11 +1692,12 @@ template <int D, bool BF16, int PARTS> cudaError_t launch(FlashParams p, cudaStr
     return launch_copy<D, BF16, PARTS, kTensorCopies>(p, k_map, v_map, s);
 }
 
-// 16-bit parts of a query: one where the products' type holds its type; and one for an F32 query in fp16 products where the
-// output is bf16, whose rounding hides what the 11 bits leave out (one part for two: half the first product's work, two more stages).
+// 16-bit parts of a query: one where the products' type holds its type (fp16 holds a row of bf16's once that is scaled), else two.  (One
+// for an F32 query in fp16 products and a bf16 output would halve the first product, but a score is off by what the query
+// leaves out times the score itself: with 11 bits scores of a hundred by up to 0.05, weights by 5 %, which no output's type hides.)
 template <int D, bool BF16> cudaError_t launch_by_type(const FlashParams &p, cudaStream_t s)
 {
-    const bool one = p.dtype == GDNA_BF16 || (!BF16 && (p.dtype == GDNA_F16 || p.out_dtype == GDNA_BF16));
+    const bool one = p.dtype == GDNA_BF16 || (!BF16 && p.dtype == GDNA_F16);
     return one ? launch<D, BF16, 1>(p, s) : launch<D, BF16, 2>(p, s);
 }
 

@@ -101,7 +101,7 @@ GDN_API int64_t gdnb_attn_prompt_workspace(int64_t rows, int batch, int nq, int 
  *   Scores, softmax sums and outputs are held in fp32.  The products are of 16-bit
  *   operands, bf16 over a BF16 cache, else fp16: the keys and values exactly, the
  *   queries in one part where that type holds theirs, else in two (an F32 query
- *   keeps 16 bits over a BF16 cache, 22 over the others, 11 there with a BF16 out), and the weights in one
+ *   keeps 16 bits over a BF16 cache, 22 over the others), and the weights in one
  *   part: to 2^-8 of themselves over a BF16 cache; over the others to 2^-11 of
  *   themselves or 2^-32 of the row's largest, whichever is more.
  *   A value or key that is not finite shows (as NaN or infinity) in the rows that see

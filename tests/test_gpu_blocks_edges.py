@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import gated_deltanet_linear_16_gb300 as gdn
-from tests.attn_layers_helpers import TYPES, guarded, intact
+from tests.attn_layers_helpers import E32, HALF_ULP, TYPES, guarded, intact
 from tests.prompt_helpers import Pages, call_prompt, check_prompt, make_prompt, rand, starts_of, tolerance
 from tests.test_gpu_attn_shared import check_shared, make_shared
 
@@ -108,3 +108,31 @@ def test_scratch_of_the_largest_step(cuda_lib):
         n = len(prefixes)
         groups = [batch * (g + 1) // n - batch * g // n for g in range(n)]
         check_shared(make_shared(prefixes, groups, [(7 * b) % 45 for b in range(batch)], nq, nkv, d, q_len=q_len, seed=batch), ws=ws)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cache", ["f16", "e4m3", "bf16"])
+@pytest.mark.parametrize("out", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [2, 4000])
+def test_all_that_an_fp32_query_holds(cuda_lib, d, cache, out, n):
+    """Two keys whose scores of a hundred and more differ by what lies beyond the first 11 (8) bits of half a query's elements, all
+    the same way: rounded to those the two weights would be equal.  The bound is the one of two parts whatever the output."""
+    h, c = d // 2, 28.0 if cache == "e4m3" else 40.0
+    s = make_prompt([1], [n - 1], 2, 1, d, dtype="f32", cache=cache, page=64, seed=1)
+    at, tok = s["pages"].where[0]
+    key, value = torch.full((n, 1, d), -c), torch.zeros((n, 1, d))
+    key[:2] = 0.0
+    key[0, 0, :h], key[1, 0, h:] = c, c
+    value[0], value[1] = 1.0, -1.0
+    store = s["pages"].store
+    s["keys"][0] = torch.tensor(store.put("k", at, tok, key), device="cuda")
+    s["values"][0] = torch.tensor(store.put("v", at, tok, value), device="cuda")
+    q = torch.ones((s["rows"], 2, d))
+    q[:, :, :h] += 0.9 * (2.0 ** -8 if cache == "bf16" else 2.0 ** -11)
+    s["q"] = q.reshape(-1, 2 * d).cuda()
+    got, want, _ = check_prompt(s, out)
+    got, want = got[s["starts"][0]], want[s["starts"][0]]
+    size = 2 * c * h * d ** -0.5                                  # of the other keys, as large as it gets
+    bound = (2 * ((2.0 ** -16 if cache == "bf16" else 2.0 ** -22) + 8 * d ** 0.5 * E32) * size + (8 * n ** 0.5 + 32) * E32
+             + (2.0 ** -8 if cache == "bf16" else 2.0 ** -11 + n * 2.0 ** -32) + HALF_ULP[out] * want.abs())
+    assert (want.abs() > 0.02).all() and ((got - want).abs() <= bound).all()
