@@ -216,8 +216,9 @@ GDN_API int64_t gdna_attn_workspace(int batch, int q_len, int nq, int nkv, int d
  *   BF16 and lse NULL, else all 24; a weight over an F16 or E4M3 cache is held to
  *   2^-22 of itself or 2^-40 of its row's largest, whichever is more, over a BF16
  *   cache to 2^-16 of itself (F32 out: 2^-24).
- *   A value or key that is not finite shows in the rows that see it.  Results do
- *   not depend on timing.
+ *   A value or key that is not finite shows in the rows that see it; but a key
+ *   whose score with a row is -inf has weight 0 there, and a row of no other key
+ *   gives 0.  Results do not depend on timing.
  *   The tensor-core kernels' waits for their own copies are bounded
  *   (gdn_set_wait_polls); where one runs out the rows of that block come out NaN
  *   and gdn_device_wait_timeouts counts it.

@@ -105,7 +105,10 @@ GDN_API int64_t gdnb_attn_prompt_workspace(int64_t rows, int batch, int nq, int 
  *   part: to 2^-8 of themselves over a BF16 cache; over the others to 2^-11 of
  *   themselves or 2^-32 of the row's largest, whichever is more.
  *   A value or key that is not finite shows (as NaN or infinity) in the rows that see
- *   it, and in no other.  Results do not depend on timing.
+ *   it, and in no other; but a key whose score with a row is -inf (an infinite one
+ *   whose sign there is the query's opposite) has weight 0 there, and a row of no
+ *   other key gives 0.  (An F32 query's two parts may make that score NaN.)
+ *   Results do not depend on timing.
  *   Caches (bases and strides) on 16-byte boundaries with pages of a multiple of 8
  *   tokens are brought in by tensor copies; other pages, types and layouts by
  *   loads, slower where the GPU waits for them.

@@ -5,8 +5,9 @@ import torch
 
 import gated_deltanet_linear_16_gb300 as gdn
 from tests.attn_layers_helpers import E32, HALF_ULP, TYPES, guarded, intact
-from tests.prompt_helpers import Pages, call_prompt, check_prompt, make_prompt, rand, starts_of, tolerance
-from tests.test_gpu_attn_shared import check_shared, make_shared
+from tests.prompt_helpers import (Pages, attention_rows, call_prompt, check_prompt, make_prompt, prompt64, rand, starts_of,
+                                  tolerance)
+from tests.test_gpu_attn_shared import call_shared, check_shared, make_shared
 
 pytestmark = pytest.mark.gpu
 
@@ -136,3 +137,55 @@ def test_all_that_an_fp32_query_holds(cuda_lib, d, cache, out, n):
     bound = (2 * ((2.0 ** -16 if cache == "bf16" else 2.0 ** -22) + 8 * d ** 0.5 * E32) * size + (8 * n ** 0.5 + 32) * E32
              + (2.0 ** -8 if cache == "bf16" else 2.0 ** -11 + n * 2.0 ** -32) + HALF_ULP[out] * want.abs())
     assert (want.abs() > 0.02).all() and ((got - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cache", ["f16", "bf16"])
+@pytest.mark.parametrize("cached", [0, 5000])
+def test_infinite_keys(cuda_lib, d, cache, cached):
+    """An infinite key's score is +inf, and the row NaN, or -inf, and the key's weight 0; a row of no other key gives 0."""
+    n, col = 40, 5
+    s = make_prompt([n, 1, 1], [cached, 0, 0], 6, 1, d, dtype=cache, cache=cache, page=64, seed=d)
+    bad = [(0, cached + 10, 1.0), (1, 0, 1.0), (2, 0, -1.0)]
+    for b, j, sign in bad:
+        at, tok = s["pages"].where[b]
+        s["pages"].store.k[at[j], tok[j], 0, col] = sign * float("inf")
+        s["keys"][b][j, 0, col] = 0.0
+    want, size, vmax = prompt64(s)
+    s["keys"][0][cached + 10, 0, col] = 1e30                      # a weight of 0 where the query's element is below 0
+    without = prompt64(s)[0]
+    got, _, _ = check_prompt(s, cache, finite=False)
+    tol = tolerance(without, size, vmax, n + cached, d, cache, cache, cache)
+    q5 = s["q"].view(-1, 6, d)[:, :, col].double()
+    r0 = s["starts"][0]
+    for r in range(n):
+        up = (q5[r0 + r] > 0) & (r >= 10)
+        assert torch.isnan(got[r0 + r][up]).all()
+        assert ((got[r0 + r] - without[r0 + r]).abs() <= tol[r0 + r])[~up].all()
+    for b, _, sign in bad[1:]:
+        r = s["starts"][b]
+        up = sign * q5[r] > 0
+        assert torch.isnan(got[r][up]).all() and (got[r][~up] == 0).all()
+
+
+@pytest.mark.parametrize("times", [1, 30])
+@pytest.mark.parametrize("cache", ["f16", "bf16"])
+def test_infinite_keys_of_a_prefix(cuda_lib, times, cache):
+    nq, nkv, d, col = 4, 2, 128, 7
+    s = make_shared([300], [5 * times], [5, 0, 33, 1, 64] * times, nq, nkv, d, dtype=cache, cache=cache, seed=3)
+    pages = s["pages"]
+    at, tok = pages.where[0]
+    pages.store.k[at[200], tok[200], 1, col] = float("-inf")
+    out = torch.zeros((s["rows"], nq * d), dtype=TYPES[cache], device="cuda")
+    call_shared(s, out)
+    torch.cuda.synchronize()
+    got, q = out.double().view(-1, nq, d), s["q"].double().view(-1, nq, d)
+    for r, m in enumerate(s["lens"]):
+        keys, values = (torch.cat([x[0], x[1 + r]]) for x in (pages.keys, pages.values))
+        keys[200, 1, col] = 0.0
+        _, size, vmax = attention_rows(q[r:r + 1], keys, values, torch.tensor([300 + m]), s["scale"])
+        keys[200, 1, col] = -1e30
+        want = attention_rows(q[r:r + 1], keys, values, torch.tensor([300 + m]), s["scale"])[0]
+        up = (q[r, :, col] < 0) & (torch.arange(nq, device="cuda") >= nq // nkv)
+        tol = tolerance(want, size, vmax, 300 + m, d, cache, cache, cache)
+        assert torch.isnan(got[r][up]).all() and ((got[r] - want[0]).abs() <= tol[0])[~up].all()
