@@ -87,7 +87,8 @@ GDN_API int64_t gdnb_attn_prompt_workspace(int64_t rows, int batch, int nq, int 
  *                F16 or BF16.
  *   row_start    [batch + 1] int32.  Values are cut to [0, rows], and an end to its
  *                start.  Rows of no sequence are left as they were.  Where starts go
- *                back, so that sequences overlap, either's result may be kept.
+ *                back, so that sequences overlap, each element of a row of several
+ *                is of one of their results, and may be of another in the next call.
  *   kv_len       [batch] int32.  Below 0 counts as 0; above max_pages * page_size (or
  *                2^31 - 4096) as that.  NULL with table NULL (the rows' number);
  *                given with it, cut to the rows' number.

@@ -189,3 +189,70 @@ def test_infinite_keys_of_a_prefix(cuda_lib, times, cache):
         up = (q[r, :, col] < 0) & (torch.arange(nq, device="cuda") >= nq // nkv)
         tol = tolerance(want, size, vmax, 300 + m, d, cache, cache, cache)
         assert torch.isnan(got[r][up]).all() and ((got[r] - want[0]).abs() <= tol[0])[~up].all()
+
+
+def owners(starts, rows):
+    """For each row the sequences (or groups) it belongs to, and where those end: starts are cut to the rows, ends to their starts."""
+    mine = [[] for _ in range(rows)]
+    for b, (x, y) in enumerate(zip(starts, starts[1:])):
+        lo = min(max(x, 0), rows)
+        hi = min(max(y, lo), rows)
+        for r in range(lo, hi):
+            mine[r].append((b, hi))
+    return mine
+
+
+def random_starts(seed, n, rows):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randint(-20, rows + 20, (n + 1,), generator=gen).tolist()
+
+
+@pytest.mark.parametrize("starts", [[-5, 30, 80, 1000], [60, 40, 90, 90], [0, 50, 20, 70], [-5, 30, 1000, 80], [10, 10, 60, 61], [95, 99, 120, 130],
+                                    1, 2, 3, 4])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("cached", [5, 3000])
+def test_starts_out_of_range(cuda_lib, starts, d, cached):
+    """Starts are cut to the rows; rows of no sequence stay as they were; elements of rows of several hold one of their results."""
+    nq = 4
+    s = make_prompt([30, 30, 30], [cached, cached, cached], nq, 2, d, behind=0)
+    rows = s["rows"]
+    starts = random_starts(starts, 3, rows) if isinstance(starts, int) else starts
+    whole, out = guarded(rows, nq * d, nq * d + 8, "bf16", before=8)
+    before = gdn.gdn_device_wait_timeouts()
+    call_prompt(dict(s, starts=starts), out)
+    torch.cuda.synchronize()
+    assert gdn.gdn_device_wait_timeouts() == before and intact(whole, out)
+    got, q = out.double().view(rows, nq, d), s["q"].double().view(rows, nq, d)
+    for r, mine in enumerate(owners(starts, rows)):
+        fits = (got[r] == 77) if not mine else torch.zeros_like(got[r], dtype=torch.bool)
+        for b, end in mine:
+            n = s["lens"][b]
+            want, size, vmax = attention_rows(q[r:r + 1], s["keys"][b], s["values"][b], torch.tensor([n - (end - 1 - r)]), s["scale"])
+            fits |= (got[r] - want[0]).abs() <= tolerance(want, size, vmax, n, d, "bf16", "bf16", "bf16")[0]
+        assert fits.all(), (r, mine)
+
+
+@pytest.mark.parametrize("start", [[0, 5, 2], [4, 2, 6], [-3, 2, 900], [6, 9, 12], [1, 1, 4], [0, 5, 2, 6], [2, 6, -1, 3]])
+@pytest.mark.parametrize("times", [1, 30])
+def test_groups_out_of_range(cuda_lib, start, times):
+    """As above; where groups overlap nothing may be written at all."""
+    nq, nkv, d, n = 4, 2, 128, len(start) - 1
+    s = make_shared([100, 50, 300][:n], [6 * times] + [0] * (n - 1), [5, 6, 7, 8, 9, 10] * times, nq, nkv, d, seed=6)
+    start = [x if x < 0 or x == 900 else x * times for x in start]
+    batch, pages = 6 * times, s["pages"]
+    whole, out = guarded(s["rows"], nq * d, nq * d + 8, "bf16", before=8)
+    before = gdn.gdn_device_wait_timeouts()
+    call_shared(dict(s, start=start), out)
+    torch.cuda.synchronize()
+    assert gdn.gdn_device_wait_timeouts() == before and intact(whole, out)
+    got, q = out.double().view(-1, nq, d), s["q"].double().view(-1, nq, d)
+    mine = owners(start, batch)
+    apart = max(len(x) for x in mine) <= 1
+    for r in range(batch):
+        fits = (got[r] == 77) if not mine[r] or not apart else torch.zeros_like(got[r], dtype=torch.bool)
+        for g, _ in mine[r]:
+            keys, values = (torch.cat([x[g], x[n + r]]) for x in (pages.keys, pages.values))
+            m = keys.shape[0]
+            want, size, vmax = attention_rows(q[r:r + 1], keys, values, torch.tensor([m]), s["scale"])
+            fits |= (got[r] - want[0]).abs() <= tolerance(want, size, vmax, m, d, "bf16", "bf16", "bf16")[0]
+        assert fits.all(), (r, mine[r])
