@@ -1137,7 +1137,8 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                if (TILES == 1) arrive(&sh.o_free);
+                // (an item without blocks has no O: its arrival would stand for one of a warp that is not done with the item before)
+                if (TILES == 1 && blocks > 0) arrive(&sh.o_free);
                 arrive(&sh.item_empty[slot]);
             }
             blocks_all += blocks;
@@ -1270,6 +1271,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
             const uint32_t ring_k = desc_low(__shfl_sync(kFull, ring, 0), 16), ring_v = desc_low(__shfl_sync(kFull, ring, 0), S::kPanelBytes);
             const bool leader = elect();
             uint32_t items = 0, blocks = 0, q_count = 0, p_count = 0;  // (parities, of two barriers where there are two S)
+            uint32_t o_turn = 0;                       // items that had blocks
             // the ring's next stage, and its phase
             uint32_t next = 0, phase = 0;
             struct Stages {
@@ -1365,10 +1367,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                 }
                 auto s_full = [&](uint32_t block) { return TILES == 2 ? &sh.s_full[tile][0] : &sh.s_full[owner][block & 1]; };
                 auto s_of = [&](uint32_t block) { return TILES == 2 ? (uint32_t)tile : block & 1; };
-                if (first_block >= last_block) {
-                    if (TILES == 1 && items > 0) ok = wait_warp(&sh.o_free, (items - 1) & 1);
-                    continue;
-                }
+                if (first_block >= last_block) continue;
                 const int q = TILES == 2 ? tile : (int)owner;
                 Stages k_at = take();
                 ok = ok && wait_warp(&sh.q_full[q], (q_count >> q) & 1);
@@ -1386,7 +1385,7 @@ flash_rows(const FlashParams p, const __grid_constant__ CUtensorMap k_map, const
                             qk(s_of(blocks + 1), k_at, s_full(blocks + 1));
                             release(k_at);
                         }
-                        if (acc == 0 && items > 0) ok = wait_warp(&sh.o_free, (items - 1) & 1);
+                        if (acc == 0 && o_turn++ > 0) ok = wait_warp(&sh.o_free, o_turn & 1);      // (of the last item with blocks)
                     }
                     const Stages v_at = take();
                     pv(s_of(blocks), v_at, acc);

@@ -256,3 +256,15 @@ def test_groups_out_of_range(cuda_lib, start, times):
             want, size, vmax = attention_rows(q[r:r + 1], keys, values, torch.tensor([m]), s["scale"])
             fits |= (got[r] - want[0]).abs() <= tolerance(want, size, vmax, m, d, "bf16", "bf16", "bf16")[0]
         assert fits.all(), (r, mine[r])
+
+
+@pytest.mark.parametrize("d,pad,dtype", [(256, 8, "bf16"), (256, 5, "f16"), (255, 5, "f32"), (200, 5, "bf16"), (128, 5, "bf16"), (64, 8, "f16")])
+@pytest.mark.parametrize("keys", [[2, 2, 0], [300, 0, 0, 0, 0, 0, 0], [1, 0, 1, 1, 0, 0, 1, 0, 0, 0]])
+@pytest.mark.parametrize("times", [1, 40, 110])
+def test_sequences_without_a_key_among_others(cuda_lib, d, pad, dtype, keys, times):
+    """Rows that see nothing, in the blocks that also have rows of few keys: their output does not count as the others'."""
+    fresh = [2 if n else 1 for n in keys] * times
+    cached = [n - f for n, f in zip(keys * times, fresh)]
+    cache = "f16" if dtype == "f16" else "bf16"
+    s = make_prompt(fresh, cached, 6, 2, d, dtype=dtype, cache=cache, page=16, seed=len(keys))
+    check_prompt(s, cache, gated=1, pad=pad)
