@@ -268,3 +268,46 @@ def test_sequences_without_a_key_among_others(cuda_lib, d, pad, dtype, keys, tim
     cache = "f16" if dtype == "f16" else "bf16"
     s = make_prompt(fresh, cached, 6, 2, d, dtype=dtype, cache=cache, page=16, seed=len(keys))
     check_prompt(s, cache, gated=1, pad=pad)
+
+
+@pytest.mark.parametrize("d,nq", [(128, 32), (256, 16)])
+def test_rows_beyond_2_31_elements(cuda_lib, d, nq):
+    """Queries, gates, outputs and dense keys behind the 2^31st element."""
+    nkv, each, batch = 2, 100, 5300
+    rows = each * batch
+    assert rows * nq * d > 1 << 31
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    kv = torch.randn((rows, 2 * nkv * d), device="cuda", generator=gen, dtype=torch.bfloat16)
+    q = torch.empty((rows, nq * d), device="cuda", dtype=torch.bfloat16)
+    for i in range(0, rows, each * 100):
+        q[i:i + each * 100] = torch.randn((min(each * 100, rows - i), nq * d), device="cuda", generator=gen, dtype=torch.bfloat16)
+    out = torch.zeros_like(q)
+    starts = torch.arange(batch + 1, dtype=torch.int32, device="cuda") * each
+    ws = torch.empty(gdn.gdnb_attn_prompt_workspace(rows=rows, batch=batch, nq=nq, nkv=nkv, d=d), dtype=torch.uint8, device="cuda")
+    gdn.gdnb_attn_prompt(q, kv, kv[:, nkv * d:], starts, None, out, ws, rows=rows, batch=batch, nq=nq, nkv=nkv, d=d,
+                         token_stride=2 * nkv * d, gate=q)
+    torch.cuda.synchronize()
+    for b in (0, 1, batch // 2, batch - 1):
+        r = slice(b * each, (b + 1) * each)
+        q64, k64, v64 = q[r].double().view(each, nq, d), kv[r, :nkv * d].double().view(each, nkv, d), kv[r, nkv * d:].double().view(each, nkv, d)
+        want, size, vmax = attention_rows(q64, k64, v64, 1 + torch.arange(each), d ** -0.5)
+        tol = tolerance(want, size, vmax, each, d, "bf16", "bf16", "bf16")
+        want = want * torch.sigmoid(q64)
+        assert ((out[r].double().view(each, nq, d) - want).abs() <= tol + HALF_ULP["bf16"] * want.abs()).all(), b
+
+
+@pytest.mark.parametrize("c", [8192, 8191])
+def test_norm_rows_beyond_2_31_elements(cuda_lib, c):
+    rows = (1 << 31) // c + 500
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.zeros((rows, c), dtype=torch.bfloat16, device="cuda")
+    x[-700:] = torch.randn((700, c), device="cuda", generator=gen)
+    y = torch.zeros_like(x)
+    y[-700:] = torch.randn((700, c), device="cuda", generator=gen)
+    want = x[-700:].double() + 0.5 * y[-700:].double()
+    gdn.gdnb_residual_norm(x, y, x, y, rows=rows, c=c, scale=0.5)
+    torch.cuda.synchronize()
+    assert ((x[-700:].double() - want).abs() <= (HALF_ULP["bf16"] + 4 * E32) * want.abs() + 4 * E32).all()
+    normed = want / (want.square().mean(-1, keepdim=True) + 1e-6).sqrt()
+    assert ((y[-700:].double() - normed).abs() <= (HALF_ULP["bf16"] + 40 * E32) * normed.abs() + 4 * E32).all()
+    assert (x[:1000] == 0).all() and (y[:1000] == 0).all()
