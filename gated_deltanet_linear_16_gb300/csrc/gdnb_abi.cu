@@ -37,8 +37,10 @@ struct SharedSpace {
     int64_t all() const { return decode + own + lse + parts; }
 };
 // Requests whose own keys go through the prefix's kernel with the prefix: as many as make about a tile for each SM.  That saves two
-// launches and their latencies (four requests of up to 400 own keys, 4 key heads of 256: 33 us against 44; 38 of them: 43
-// against 51; 96 requests of up to 2500, 8 heads of 128, by gdna_attn_decode's kernel: 57 us of 235).
+// launches and their latencies, and a tile of a few rows costs as much as a full one.  Both ways, us: 24/4 heads of 256, own keys to
+// 100 and to 3000, 16 tiles 28 and 32 against 42 and 44, 152 tiles 36 and 59 against 49 and 68, 304 tiles 49 and 83 against 56 and
+// 92; 48/8 of 128 at 304 tiles, own keys to 3000, 66 against 62; over E4M3 at 200 tiles, own keys to 900, 106 against 89; 768 tiles of
+// 128, own keys to 2500, 260 against 227.
 constexpr int64_t kTogether = 152;
 SharedSpace shared_space(int batch, int groups, int q_len, int nq, int nkv, int d)
 {

@@ -40,13 +40,14 @@
 // keys, values that are not finite are taken out of V (0 x NaN) and the first such key of each column is noted: the rows
 // that see it come out NaN in that column, the others clean.  Keys past the end count as zeros.
 //
-// What bounds it (GB300, device time).  Long lists of keys: 512 rows over 60000 keys of 8 heads of 128 take 334 us, 1511 TFLOP/s or
-// 0.79 of the measured rate; there shared memory is full: Q and K of the first product take its 128 bytes a cycle by themselves,
-// and the copies come on top.  Prompts: eight of 4096, 24/4 heads of 256, 1564 us (1055 TFLOP/s; two of 16384
-// 1305): what a tile costs beside its 16 blocks, gates and output (without gates 1406); the next one's queries and first scores come meanwhile.
-// A packed batch at 128 1526 us (1108): what a tile costs beside its keys, queries, first scores and output.  Heads of 64: 215 us (408
-// TFLOP/s), the softmax warps' issue slots.  E4M3, fp32 queries in two parts: 362 us for 107 GFLOP, a ring of
-// three stages (a query in one part: 217, five stages) and the widening (a conversion of two codes takes a quarter of the schedulers' time).  Short calls: 23 us for one prompt of 180 tokens: 2 us until sums of lengths are there, 3 until the first item is
+// What bounds it (GB300, device time).  Long lists of keys: 512 rows over 60000 keys of 8 heads of 128 take 335 us, 1510 TFLOP/s or
+// 0.79 of the measured rate (360 from call to call with cold keys, 1400); there shared memory is full: Q and K of the first product take
+// its 128 bytes a cycle by themselves, and the copies come on top.  Prompts: eight of 4096, 24/4 heads of 256, 1580 us (1044 TFLOP/s; two
+// of 16384 1305): what a tile costs beside its 16 blocks, gates and output (without gates 1431); the next one's queries and first scores
+// come meanwhile.  A packed batch at 128 1519 us (1113): what a tile costs beside its keys, queries, first scores and output.  Heads of
+// 64: 220 us (400 TFLOP/s), the softmax warps' issue slots, and tiles dealt unevenly: the busiest block has 1.2 times the mean.  E4M3, fp32 queries in two parts: 362 us for 107 GFLOP, a ring of
+// three stages (a query in one part: 217, five stages), the widening (a conversion of two codes takes a quarter of the schedulers' time),
+// and tiles dealt unevenly (1.4).  Short calls: 23 us for one prompt of 180 tokens: 2 us until sums of lengths are there, 3 until the first item is
 // dealt, then a chain of copies, products, softmax, output, in code that no cache holds yet.
 #pragma once
 

@@ -47,7 +47,10 @@ extern "C" {
  *   unrounded x').  An output overlapping any other operand is GDN_ERR_ALIAS; rows
  *   of one stride that lie side by side do not overlap.
  *   1 <= C <= 16384 (GDN_ERR_UNSUPPORTED).  Rows and strides on 16-byte boundaries
- *   with C a multiple of 8 run a vector kernel, any other call a scalar one.
+ *   with C a multiple of 8 are taken 16 bytes at a time; so are rows that all begin
+ *   equally far behind a boundary of eight elements (an odd C, rows side by side, 64
+ *   <= C <= 16370) but for their ends, at about half the rate; any other call goes
+ *   element by element, at half of that.
  */
 GDN_API int gdnb_residual_norm(const void *x, gdna_dtype x_dtype, const void *y, gdna_dtype y_dtype,
                                const void *gate, const float *post, const float *pre, float scale, float eps,
@@ -111,8 +114,9 @@ GDN_API int64_t gdnb_attn_prompt_workspace(int64_t rows, int batch, int nq, int 
  *   other key gives 0.  (An F32 query's two parts may make that score NaN.)
  *   Results do not depend on timing.
  *   Caches (bases and strides) on 16-byte boundaries with pages of a multiple of 8
- *   tokens are brought in by tensor copies; other pages, types and layouts by
- *   loads, slower where the GPU waits for them.
+ *   tokens (E4M3: 4, and heads above 64) are brought in by tensor copies; other pages
+ *   by loads of 16 bytes, up to three times slower; heads of no multiple of 16 bytes
+ *   and unaligned caches element by element, up to eight times slower.
  *   The kernels' waits for their own copies and products are bounded
  *   (gdn_set_wait_polls; a wait that lasts as long as a sequence's keys by 256 times
  *   the polls); where one runs out, that block's rows are incomplete and
